@@ -25,6 +25,9 @@ __all__ = [
     "ra_ring_fwd", "ra_ring_fwd_workspace_bytes", "ra_ring_bwd", "ra_ring_bwd_workspace_bytes",
     "ra_ring_fwd_noalloc", "ra_ring_fwd_varlen", "ra_ring_bwd_varlen", "ra_ring_step_host",
     "ra_ring_step_host_workspace_bytes", "ra_ffn_workspace_bytes", "ra_ffn_fwd", "ra_ffn_bwd",
+    "ra_xent_fwd_workspace_bytes", "ra_xent_fwd", "ra_xent_bwd_workspace_bytes", "ra_xent_bwd",
+    "ra_newton_schulz_workspace_bytes", "ra_newton_schulz", "ffn_fwd", "ffn_bwd", "xent_fwd", "xent_bwd",
+    "newton_schulz",
     "ra_sync_status", "ra_last_error", "ra_launch_count", "ra_selftest_timeout", "ra_debug_visit_log",
     "ra_kernel_timing", "ra_kernel_timing_read",
     "ring_attention_fwd", "ring_attention_bwd", "RA_F32", "RA_BF16", "RA_F16",
@@ -80,6 +83,12 @@ def _load():
         "ra_ffn_workspace_bytes": (sz, [i, ctypes.c_longlong, i, i, i, i]),
         "ra_ffn_fwd": (i, [vp, vp, vp, i, ctypes.c_longlong, i, i, i, vp, i, vp, sz, vp]),
         "ra_ffn_bwd": (i, [vp, vp, vp, vp, i, ctypes.c_longlong, i, i, i, vp, i, vp, vp, vp, sz, vp]),
+        "ra_xent_fwd_workspace_bytes": (sz, [i, ll, i, i]),
+        "ra_xent_fwd": (i, [vp, vp, i, ll, i, i, ll, ll, vp, ll, vp, vp, vp, sz, vp]),
+        "ra_xent_bwd_workspace_bytes": (sz, [i, i, ll, i, i, i]),
+        "ra_xent_bwd": (i, [vp, vp, i, ll, i, i, ll, ll, vp, ll, vp, vp, i, vp, i, vp, i, vp, sz, vp]),
+        "ra_newton_schulz_workspace_bytes": (sz, [i, i, i]),
+        "ra_newton_schulz": (i, [vp, i, i, i, i, ll, ll, ctypes.POINTER(f), i, f, vp, i, ll, ll, vp, sz, vp]),
         "ra_ring_bwd_varlen": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, vp, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd_workspace_bytes": (sz, [i, i, sh, i]),
@@ -199,6 +208,7 @@ def empty_like_layout(t, dtype=None):
 
 RA_KERNEL_FWD_TC, RA_KERNEL_BWD_TC, RA_KERNEL_FWD_F32, RA_KERNEL_BWD_F32, RA_KERNEL_GEMM_TC = 0, 1, 2, 3, 4
 RA_COPY_H2D, RA_COPY_D2H = 5, 6
+RA_KERNEL_PAIR_TC = 7
 
 
 def ra_kernel_timing(enable):
@@ -400,6 +410,139 @@ def ffn_bwd(x, w1, w2, dy, block=None, dx_dtype=torch.float32, stream=None):
     ws = _workspace(ra_ffn_workspace_bytes(_dt(x), T, dm, dh, block, True), x.device)
     ra_ffn_bwd(x, w1, w2, dy, block, dx, dw1, dw2, ws, stream)
     return dx, dw1, dw2
+
+
+def _on_device(ref, **tensors):
+    """Every tensor lies on ref's device, and that is the current one (the
+    stream and the library's kernels belong to it)."""
+    if not ref.is_cuda or ref.device.index != torch.cuda.current_device():
+        raise RAError(1, f"tensors must be on the current CUDA device (got {ref.device})")
+    for name, t in tensors.items():
+        if t is not None and t.device != ref.device:
+            raise RAError(1, f"{name} is on {t.device}, not on {ref.device}")
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """Row stride of a 2-D tensor with contiguous rows (0 where it has one row
+    or is packed)."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise RAError(1, f"{name} must be {list(shape) if shape else '2-D'} (got {list(t.shape)})")
+    if dtype is not None and t.dtype != dtype:
+        raise RAError(1, f"{name} must be {dtype} (got {t.dtype})")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise RAError(1, f"{name} must have contiguous rows (strides {t.stride()})")
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
+def _vector(t, name, T, dtype):
+    if t.dim() != 1 or t.shape[0] != T or t.dtype != dtype or not t.is_contiguous():
+        raise RAError(1, f"{name} must be a contiguous {dtype} tensor [{T}] (got {t.dtype} {list(t.shape)})")
+
+
+def _xent_check(x, w, targets):
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
+        raise RAError(1, f"x [T, D] and w [V, D] must have one D and one dtype (got {list(x.shape)} {x.dtype}, "
+                         f"{list(w.shape)} {w.dtype})")
+    T, D = x.shape
+    _vector(targets, "targets", T, torch.int64)
+    return T, D, w.shape[0], _rows(x, "x"), _rows(w, "w")
+
+
+def ra_xent_fwd_workspace_bytes(dtype, T, D, V):
+    return int(_lib().ra_xent_fwd_workspace_bytes(dtype, int(T), int(D), int(V)))
+
+
+def ra_xent_bwd_workspace_bytes(dtype, dx_dtype, T, D, V, block):
+    return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), int(block)))
+
+
+def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
+    """loss and lse [T] fp32 of the softmax cross entropy of x w^T [T, V] against
+    targets [T] int64, without the logits.  See include/ra.h."""
+    T, D, V, xs, ws = _xent_check(x, w, targets)
+    for t, name in ((loss, "loss"), (lse, "lse")):
+        _vector(t, name, T, torch.float32)
+    _on_device(x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
+    _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
+                              int(ignore_index), loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index=-100, stream=None):
+    """Gradients of sum(dloss * loss): dx [T, D] and dw [V, D] (packed,
+    overwritten), `block` vocabulary entries at a time."""
+    T, D, V, xs, ws = _xent_check(x, w, targets)
+    for t, name in ((lse, "lse"), (dloss, "dloss")):
+        _vector(t, name, T, torch.float32)
+    for t, name, shape in ((dx, "dx", (T, D)), (dw, "dw", (V, D))):
+        if tuple(t.shape) != shape or not t.is_contiguous():
+            raise RAError(1, f"{name} must be a packed {list(shape)} tensor")
+    _on_device(x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
+    _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
+                              int(ignore_index), lse.data_ptr(), dloss.data_ptr(), int(block), dx.data_ptr(), _dt(dx),
+                              dw.data_ptr(), _dt(dw), workspace.data_ptr(),
+                              workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def xent_fwd(x, w, targets, ignore_index=-100, stream=None):
+    """Convenience wrapper: allocates loss, lse and the workspace."""
+    T, D, V, _, _ = _xent_check(x, w, targets)
+    loss, lse = torch.empty(2, T, dtype=torch.float32, device=x.device)
+    ws = _workspace(ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), x.device)
+    ra_xent_fwd(x, w, targets, loss, lse, ws, ignore_index, stream)
+    return loss, lse
+
+
+def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_dtype=torch.float32,
+             ignore_index=-100, stream=None):
+    """Convenience wrapper: allocates dx, dw and the workspace (block: the whole
+    vocabulary by default)."""
+    T, D, V, _, _ = _xent_check(x, w, targets)
+    block = V if block is None else block
+    dx = torch.empty(T, D, dtype=dx_dtype, device=x.device)
+    dw = torch.empty(V, D, dtype=dw_dtype, device=x.device)
+    ws = _workspace(ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), x.device)
+    ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, ws, ignore_index, stream)
+    return dx, dw
+
+
+def ra_newton_schulz_workspace_bytes(batch, rows, cols):
+    return int(_lib().ra_newton_schulz_workspace_bytes(int(batch), int(rows), int(cols)))
+
+
+def _ns_layout(t, name):
+    """(batch, rows, cols, batch stride, row stride) of a [rows, cols] or
+    [batch, rows, cols] tensor with contiguous rows."""
+    if t.dim() not in (2, 3):
+        raise RAError(1, f"{name} must be [rows, cols] or [batch, rows, cols] (got {list(t.shape)})")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise RAError(1, f"{name} must have contiguous rows (strides {t.stride()})")
+    rows, cols = t.shape[-2:]
+    batch = t.shape[0] if t.dim() == 3 else 1
+    return (batch, rows, cols, t.stride(0) if t.dim() == 3 and batch > 1 else 0,
+            t.stride(-2) if rows > 1 else 0)
+
+
+def ra_newton_schulz(g, out, workspace, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, stream=None):
+    """out <- `steps` Newton-Schulz steps on g / (|g| + eps), each matrix of a
+    batch by itself.  See include/ra.h."""
+    batch, rows, cols, gb, gr = _ns_layout(g, "g")
+    if tuple(out.shape) != tuple(g.shape):
+        raise RAError(1, f"out must have the shape of g ({list(out.shape)} vs {list(g.shape)})")
+    _, _, _, ob, orr = _ns_layout(out, "out")
+    _on_device(g, out=out, workspace=workspace)
+    _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), batch, rows, cols, gb, gr, (ctypes.c_float * 3)(*coeffs),
+                                   int(steps), float(eps), out.data_ptr(), _dt(out), ob, orr, workspace.data_ptr(),
+                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out_dtype=None, stream=None):
+    """Convenience wrapper: allocates out (g's dtype by default) and the workspace."""
+    batch, rows, cols, _, _ = _ns_layout(g, "g")
+    out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
+    ws = _workspace(ra_newton_schulz_workspace_bytes(batch, rows, cols), g.device)
+    ra_newton_schulz(g, out, ws, steps, coeffs, eps, stream)
+    return out
 
 
 def ra_ring_bwd_workspace_bytes(dtype, grad_dtype, shape, P):

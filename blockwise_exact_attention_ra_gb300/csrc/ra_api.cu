@@ -186,6 +186,28 @@ int make_map_2d(CUtensorMap* m, const void* base, int is_bf16, long long rows, l
 
 namespace {
 
+// Batch of row-major matrices [batch, rows, cols]: dims (cols, rows, batch), any
+// box; cols and rows may be of any size, ld and bstride (elements) multiples of
+// 16 bytes.
+int make_map_3d(CUtensorMap* m, const void* base, int dtype, long long cols, long long rows, long long batch,
+                long long ld, long long bstride, int box_cols, int box_rows, bool swizzle) {
+  EncodeTiledFn fn;
+  int rc = encoder(&fn);
+  if (rc) return rc;
+  const cuuint64_t es = dtype == RA_F32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  cuuint64_t strides[2] = {(cuuint64_t)ld * es, (cuuint64_t)(batch > 1 ? bstride : ld) * es};
+  cuuint32_t box[3] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(m, dtype == RA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                     : dtype == RA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                  3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", (int)r);
+  return RA_OK;
+}
+
 // -------------------------------------------------------------- validation
 size_t dtype_size(int dt) { return dt == RA_F32 ? 4 : 2; }
 bool valid_dtype(int dt) { return dt == RA_F32 || dt == RA_BF16 || dt == RA_F16; }
@@ -401,6 +423,7 @@ int ra_sync_status(void* stream) {
     if (e != cudaSuccess) return cuda_fail(e, "clear status word");
     return fail(v, v == RA_ERR_RANGE ? "an operand exceeded the fp16 range"
                                      : v == RA_ERR_TIMEOUT ? "a bounded wait on the device gave up"
+                                     : v == RA_ERR_INVALID_ARG ? "a target lies outside the vocabulary"
                                                            : "device reported status %d",
                 v);
   }
@@ -1214,6 +1237,461 @@ int ra_ring_step_host(const void* q, const void* k, const void* v, const void* d
       return cuda_fail(e, "gradient download");
   }
   if ((e = cudaStreamWaitEvent(main_st, ev.e[3], 0)) != cudaSuccess) return cuda_fail(e, "join O download");
+  return RA_OK;
+}
+
+#pragma GCC visibility pop
+}  // extern "C"
+
+// ------------------------------------------------ cross entropy of a vocabulary
+namespace ra {
+namespace {
+
+// One CTA-pair product: fills in the operands' maps and picks the tile width.
+struct PairPlan {
+  cudaStream_t st;
+  int* status;
+  int sms;
+
+  // Tiles are 256 rows by 256 or 128 columns.  The wide tile moves fewer operand
+  // bytes per product, the narrow one splits the work finer: the rule takes the one
+  // whose waves over the pairs cost less, a narrow tile counted as 0.56 of a wide
+  // one (half the products, 12% slower per product).
+  int tile_cols(const PairArgs& a) const {
+    const long long pairs = sms / 2;
+    const long long w256 = ((long long)pair_tiles(a, 256) * a.batch + pairs - 1) / pairs;
+    const long long w128 = ((long long)pair_tiles(a, 128) * a.batch + pairs - 1) / pairs;
+    return 0.56 * (double)w128 < (double)w256 ? 128 : 256;
+  }
+  // a: everything but the operands' maps and the fields set here.  Operands are
+  // matrices of `rows` x `cols` (as stored) with leading dimension ld.
+  struct Operand {
+    const void* p;
+    long long rows, cols, ld, bstride;
+  };
+  int run(PairArgs& a, int bn, const Operand& A, const Operand& B, int dtype) const {
+    int rc;
+    if ((rc = make_map_3d(&a.tm_a, A.p, dtype, A.cols, A.rows, a.batch, A.ld, A.bstride, 64, a.a_mn ? 64 : 128, true)) ||
+        (rc = make_map_3d(&a.tm_b, B.p, dtype, B.cols, B.rows, a.batch, B.ld, B.bstride, 64, a.b_mn ? 64 : bn / 2, true)))
+      return rc;
+    a.ab_bf16 = dtype == RA_BF16;
+    a.status = status;
+    a.wait_limit_ns = wait_limit_ns();
+    // the pairs at work together cover all columns of a few tile rows, or 16 tile
+    // rows where the columns are many
+    const int tn = (a.N + bn - 1) / bn, pairs = sms / 2 > 0 ? sms / 2 : 1;
+    a.group_m = tn < 5 ? (pairs + tn - 1) / tn : 16;
+    TimedLaunch tl(RA_KERNEL_PAIR_TC, st);
+    const cudaError_t e = launch_tc_pair(a, bn, sms, st);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "CTA-pair product launch");
+  }
+};
+
+struct XentShape {
+  long long T, xs, ws;
+  int D, V, block;
+};
+
+int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, long long w_rstride, int block,
+               XentShape* out) {
+  if (dtype != RA_BF16 && dtype != RA_F16)
+    return fail(RA_ERR_UNSUPPORTED, "the cross entropy takes bf16 or fp16 operands");
+  if (T < 1 || D < 1 || V < 1 || block < 1)
+    return fail(RA_ERR_INVALID_ARG, "non-positive cross-entropy size (T=%lld D=%d V=%d block=%d)", T, D, V, block);
+  if (D % 8) return fail(RA_ERR_UNSUPPORTED, "D must be a multiple of 8 (got %d)", D);
+  if (T > (1 << 30) || V > (1 << 30) || D > (1 << 20)) return fail(RA_ERR_INVALID_ARG, "cross-entropy size too large");
+  if (x_rstride == 0) x_rstride = D;
+  if (w_rstride == 0) w_rstride = D;
+  if (x_rstride < D || w_rstride < D || x_rstride > (1ll << 32) || w_rstride > (1ll << 32))
+    return fail(RA_ERR_INVALID_ARG, "row strides (%lld, %lld) must be 0 or at least D=%d", x_rstride, w_rstride, D);
+  if (x_rstride % 8 || w_rstride % 8)
+    return fail(RA_ERR_INVALID_ARG, "row strides must be multiples of 8 elements (got %lld, %lld)", x_rstride, w_rstride);
+  *out = XentShape{T, x_rstride, w_rstride, D, V, block < V ? block : V};
+  return RA_OK;
+}
+
+// forward: target logits [T] fp32 | statistics [column parts][T] (max, sum); the
+// parts are at most ceil(V / 64)
+struct XentFwdWs {
+  size_t target, stats, total;
+};
+XentFwdWs xent_fwd_layout(const XentShape& s) {
+  XentFwdWs w{};
+  w.stats = align256((size_t)s.T * 4);
+  w.total = w.stats + align256((size_t)((s.V + 63) / 64) * s.T * 8);
+  return w;
+}
+
+// backward: scale (256 bytes) | gradient of one block's logits [T][ld] 16-bit | fp32
+// sum of dx [T, D] (16-bit dx and more than one block)
+struct XentBwdWs {
+  size_t scale, d, acc, total;
+  long long ld;
+};
+XentBwdWs xent_bwd_layout(const XentShape& s, int dx_dtype) {
+  XentBwdWs w{};
+  w.ld = (s.block + 63) / 64 * 64;
+  w.d = 256;
+  w.acc = w.d + align256((size_t)s.T * w.ld * 2);
+  w.total = w.acc + (dx_dtype != RA_F32 && s.block < s.V ? align256((size_t)s.T * s.D * 4) : 0);
+  return w;
+}
+
+int check_targets(const long long* targets) {
+  if (!targets || (reinterpret_cast<uintptr_t>(targets) & 7u))
+    return fail(RA_ERR_INVALID_ARG, "targets must be a non-NULL, 8-byte aligned device array of 64-bit integers");
+  return RA_OK;
+}
+int check_floats(const void* p, const char* name) {
+  if (!p || (reinterpret_cast<uintptr_t>(p) & 3u))
+    return fail(RA_ERR_INVALID_ARG, "%s must be a non-NULL, 4-byte aligned device array", name);
+  return RA_OK;
+}
+int check_workspace(const void* workspace, size_t ws_bytes, size_t need) {
+  if (!workspace || ws_bytes < need)
+    return fail(RA_ERR_INVALID_ARG, "workspace of %zu bytes needed (got %zu)", need, ws_bytes);
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(RA_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
+  return RA_OK;
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+size_t ra_xent_fwd_workspace_bytes(ra_dtype dtype, long long T, int D, int V) {
+  XentShape s;
+  if (check_xent(dtype, T, D, V, 0, 0, V, &s)) return 0;
+  return xent_fwd_layout(s).total;
+}
+
+size_t ra_xent_bwd_workspace_bytes(ra_dtype dtype, ra_dtype dx_dtype, long long T, int D, int V, int block) {
+  XentShape s;
+  if (check_xent(dtype, T, D, V, 0, 0, block, &s) || !valid_dtype(dx_dtype)) return 0;
+  return xent_bwd_layout(s, dx_dtype).total;
+}
+
+int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V, long long x_rstride,
+                long long w_rstride, const long long* targets, long long ignore_index, float* loss, float* lse,
+                void* workspace, size_t ws_bytes, void* stream) {
+  XentShape s;
+  int rc;
+  if ((rc = check_xent(dtype, T, D, V, x_rstride, w_rstride, V, &s))) return rc;
+  if ((rc = check_ptr(x, "x")) || (rc = check_ptr(w, "w")) || (rc = check_targets(targets)) ||
+      (rc = check_floats(loss, "loss")) || (rc = check_floats(lse, "lse")))
+    return rc;
+  const XentFwdWs l = xent_fwd_layout(s);
+  if ((rc = check_workspace(workspace, ws_bytes, l.total))) return rc;
+  int* st;
+  if ((rc = status_ptr(&st))) return rc;
+  if (!device_is_sm103()) return fail(RA_ERR_UNSUPPORTED, "tensor-core kernels are built for sm_103a only");
+  char* base = static_cast<char*>(workspace);
+  PairPlan plan{static_cast<cudaStream_t>(stream), st, device_sms()};
+  PairArgs a;
+  memset(&a, 0, sizeof a);
+  a.epi = PAIR_STATS;
+  a.M = (int)s.T; a.N = s.V; a.K = s.D; a.batch = 1;
+  a.targets = targets;
+  a.ignore = ignore_index;
+  a.vocab = s.V;
+  a.stats = reinterpret_cast<float2*>(base + l.stats);
+  a.target_logit = reinterpret_cast<float*>(base);
+  const int bn = plan.tile_cols(a);
+  if ((rc = plan.run(a, bn, {x, s.T, s.D, s.xs, 0}, {w, s.V, s.D, s.ws, 0}, dtype))) return rc;
+  const cudaError_t e = launch_xent_finish(a.stats, (s.V + bn / 2 - 1) / (bn / 2), a.target_logit, targets,
+                                           ignore_index, s.V, s.T, loss, lse, st, plan.st);
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy reduction launch");
+}
+
+int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V, long long x_rstride,
+                long long w_rstride, const long long* targets, long long ignore_index, const float* lse,
+                const float* dloss, int block, void* dx, ra_dtype dx_dtype, void* dw, ra_dtype dw_dtype,
+                void* workspace, size_t ws_bytes, void* stream) {
+  XentShape s;
+  int rc;
+  if ((rc = check_xent(dtype, T, D, V, x_rstride, w_rstride, block, &s))) return rc;
+  if (!valid_dtype(dx_dtype) || !valid_dtype(dw_dtype)) return fail(RA_ERR_INVALID_ARG, "bad gradient dtype");
+  if ((rc = check_ptr(x, "x")) || (rc = check_ptr(w, "w")) || (rc = check_targets(targets)) ||
+      (rc = check_floats(lse, "lse")) || (rc = check_floats(dloss, "dloss")) || (rc = check_ptr(dx, "dx")) ||
+      (rc = check_ptr(dw, "dw")))
+    return rc;
+  const XentBwdWs l = xent_bwd_layout(s, dx_dtype);
+  if ((rc = check_workspace(workspace, ws_bytes, l.total))) return rc;
+  int* st;
+  if ((rc = status_ptr(&st))) return rc;
+  if (!device_is_sm103()) return fail(RA_ERR_UNSUPPORTED, "tensor-core kernels are built for sm_103a only");
+  char* base = static_cast<char*>(workspace);
+  PairPlan plan{static_cast<cudaStream_t>(stream), st, device_sms()};
+  float* scale = nullptr;
+  if (dtype == RA_F16) {
+    scale = reinterpret_cast<float*>(base);
+    const cudaError_t e = launch_xent_scale(dloss, targets, ignore_index, s.V, s.T, scale, plan.st);
+    if (e != cudaSuccess) return cuda_fail(e, "gradient scale launch");
+  }
+  void* d = base + l.d;
+  void* acc = dx_dtype == RA_F32 ? dx : base + l.acc;
+  for (int v0 = 0; v0 < s.V; v0 += s.block) {
+    const int C = s.V - v0 < s.block ? s.V - v0 : s.block;
+    const bool first = v0 == 0, last = v0 + C == s.V;
+    const char* wb = static_cast<const char*>(w) + (size_t)v0 * s.ws * 2;
+    PairArgs a;
+    memset(&a, 0, sizeof a);
+    a.batch = 1;
+    a.scale = scale;
+    // d = gradient of this block's logits, recomputed from x and w
+    a.epi = PAIR_DLOGITS;
+    a.M = (int)s.T; a.N = C; a.K = s.D;
+    a.targets = targets;
+    a.ignore = ignore_index;
+    a.vocab = s.V;
+    a.col_off = v0;
+    a.lse = lse;
+    a.grad = dloss;
+    if ((rc = make_map_3d(&a.tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32, true))) return rc;
+    if ((rc = plan.run(a, plan.tile_cols(a), {x, s.T, s.D, s.xs, 0}, {wb, C, s.D, s.ws, 0}, dtype))) return rc;
+    // dx += d W  (W's rows as [K, N]: MN-major); summed over blocks in fp32
+    const int cdt = last && dx_dtype != RA_F32 ? dx_dtype : RA_F32;
+    void* c = cdt == RA_F32 ? acc : dx;
+    a.epi = PAIR_STORE;
+    a.M = (int)s.T; a.N = s.D; a.K = C;
+    a.b_mn = 1;
+    a.c_dtype = cdt;
+    a.c_accumulate = cdt == RA_F32 && !first;
+    a.c_add = cdt != RA_F32 && !first ? static_cast<const float*>(acc) : nullptr;
+    if ((rc = make_map_3d(&a.tm_c, c, cdt, s.D, s.T, 1, s.D, 0, cdt == RA_F32 ? 32 : 64, 32, true))) return rc;
+    if ((rc = plan.run(a, plan.tile_cols(a), {d, s.T, C, l.ld, 0}, {wb, C, s.D, s.ws, 0}, dtype))) return rc;
+    // dw of this block = d^T x  (both MN-major)
+    a.M = C; a.N = s.D; a.K = (int)s.T;
+    a.a_mn = 1;
+    a.c_dtype = dw_dtype;
+    a.c_accumulate = 0;
+    a.c_add = nullptr;
+    void* dwb = static_cast<char*>(dw) + (size_t)v0 * s.D * dtype_size(dw_dtype);
+    if ((rc = make_map_3d(&a.tm_c, dwb, dw_dtype, s.D, C, 1, s.D, 0, dw_dtype == RA_F32 ? 32 : 64, 32, true))) return rc;
+    if ((rc = plan.run(a, plan.tile_cols(a), {d, s.T, C, l.ld, 0}, {x, s.T, s.D, s.xs, 0}, dtype))) return rc;
+  }
+  return RA_OK;
+}
+
+#pragma GCC visibility pop
+}  // extern "C"
+
+// ------------------------------------------------ Newton-Schulz orthogonalisation
+namespace ra {
+namespace {
+
+struct NsShape {
+  int batch, rows, cols, m;  // m: the smaller side
+  long long ld, ldm;         // padded rows of X and of the m x m matrices
+  double sx, sa, sb;         // powers of two by which X, A' and B' are held in fp16
+};
+
+// The largest |p(s)| over s in [0, top], p(s) = a s + b s^3 + c s^5: at top or at a
+// root of p'(s) = a + 3 b s^2 + 5 c s^4.
+double ns_bound(double a, double b, double c, double top) {
+  auto p = [&](double s) { return fabs(s * (a + s * s * (b + c * s * s))); };
+  double best = p(top);
+  double roots[2] = {-1.0, -1.0};
+  if (c == 0.0) {
+    if (b != 0.0) roots[0] = -a / (3.0 * b);
+  } else {
+    const double disc = 9.0 * b * b - 20.0 * a * c;
+    if (disc >= 0.0) {
+      roots[0] = (-3.0 * b + sqrt(disc)) / (10.0 * c);
+      roots[1] = (-3.0 * b - sqrt(disc)) / (10.0 * c);
+    }
+  }
+  for (double r : roots)
+    if (r > 0.0 && r < top * top && p(sqrt(r)) > best) best = p(sqrt(r));
+  return best;
+}
+double pow2_below(double x) { return ldexp(1.0, ilogb(x)); }
+
+int check_ns(int batch, int rows, int cols, const float* coeffs, int steps, float eps, NsShape* out) {
+  if (batch < 1 || rows < 1 || cols < 1 || steps < 1)
+    return fail(RA_ERR_INVALID_ARG, "non-positive Newton-Schulz size (batch=%d rows=%d cols=%d steps=%d)", batch, rows,
+                cols, steps);
+  if (rows > 65536 || cols > 65536 || batch > 65535 || steps > 100)
+    return fail(RA_ERR_INVALID_ARG, "Newton-Schulz size too large (batch=%d rows=%d cols=%d steps=%d)", batch, rows,
+                cols, steps);
+  if (!coeffs) return fail(RA_ERR_INVALID_ARG, "coeffs is NULL");
+  for (int i = 0; i < 3; ++i)
+    if (!isfinite(coeffs[i])) return fail(RA_ERR_INVALID_ARG, "coeffs must be finite");
+  if (!(eps >= 0.f) || !isfinite(eps)) return fail(RA_ERR_INVALID_ARG, "eps must be finite and >= 0 (got %g)", (double)eps);
+  NsShape s{};
+  s.batch = batch; s.rows = rows; s.cols = cols;
+  s.m = rows < cols ? rows : cols;
+  s.ld = (cols + 63) / 64 * 64;
+  s.ldm = (s.m + 63) / 64 * 64;
+  // Singular values start at or below 1 and stay below `top`; from that follow the
+  // largest entries of X, A' and B', which must fit fp16 times their powers of two.
+  const double a = coeffs[0], b = coeffs[1], c = coeffs[2];
+  double top = 1.0, cur = 1.0;
+  for (int i = 0; i < steps; ++i) {
+    cur = ns_bound(a, b, c, cur);
+    if (!(cur < 64.0))
+      return fail(RA_ERR_UNSUPPORTED, "coeffs (%g, %g, %g) let singular values grow past 64", a, b, c);
+    if (cur > top) top = cur;
+  }
+  const double t2 = top * top, room = 32768.0;
+  const double bmax = (fabs(b) + 2.0 * fabs(c) * t2) * t2 + fabs(c) * t2 * t2;
+  s.sa = pow2_below(room / t2);
+  s.sb = pow2_below(room / (bmax > 1.0 ? bmax : 1.0));
+  const double most = pow2_below(room / top), want = pow2_below(sqrt((double)rows * cols));
+  s.sx = want < most ? want : most;
+  *out = s;
+  return RA_OK;
+}
+
+// norm parts | sums of X's squares (two buffers) | X high terms (two buffers) | X low terms | A' | B'
+struct NsWs {
+  size_t parts, sums[2], hi[2], lo, a, b, total;
+};
+int ns_sums(const NsShape& s) {
+  // 16 partial sums per tile; narrow tiles bound the count
+  return 16 * ((s.rows + 255) / 256) * ((s.cols + 127) / 128);
+}
+NsWs ns_layout(const NsShape& s) {
+  NsWs w{};
+  size_t off = 0;
+  auto take = [&off](size_t bytes) {
+    const size_t at = off;
+    off += align256(bytes);
+    return at;
+  };
+  const size_t x = (size_t)s.batch * s.rows * s.ld * 2, g = (size_t)s.batch * s.m * s.ldm * 2;
+  w.parts = take((size_t)s.batch * kNsParts * 3 * 4);
+  for (size_t& at : w.sums) at = take((size_t)s.batch * ns_sums(s) * 4);
+  w.hi[0] = take(x);
+  w.hi[1] = take(x);
+  w.lo = take(x);
+  w.a = take(g);
+  w.b = take(g);
+  w.total = off;
+  return w;
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+size_t ra_newton_schulz_workspace_bytes(int batch, int rows, int cols) {
+  NsShape s;
+  const float none[3] = {1.f, 0.f, 0.f};
+  if (check_ns(batch, rows, cols, none, 1, 0.f, &s)) return 0;
+  return ns_layout(s).total;
+}
+
+int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int cols, long long g_bstride,
+                     long long g_rstride, const float* coeffs, int steps, float eps, void* out, ra_dtype out_dtype,
+                     long long out_bstride, long long out_rstride, void* workspace, size_t ws_bytes, void* stream) {
+  NsShape s;
+  int rc;
+  if ((rc = check_ns(batch, rows, cols, coeffs, steps, eps, &s))) return rc;
+  if (!valid_dtype(g_dtype) || !valid_dtype(out_dtype)) return fail(RA_ERR_INVALID_ARG, "bad dtype");
+  struct Side {
+    const char* name;
+    const void* p;
+    int dtype;
+    long long *bs, *rs;
+  };
+  for (const Side& d : {Side{"g", g, g_dtype, &g_bstride, &g_rstride}, Side{"out", out, out_dtype, &out_bstride, &out_rstride}}) {
+    if (!d.p || (reinterpret_cast<uintptr_t>(d.p) & (dtype_size(d.dtype) - 1)))
+      return fail(RA_ERR_INVALID_ARG, "%s is NULL or not aligned to its elements", d.name);
+    if (*d.rs == 0) *d.rs = cols;
+    const long long extent = (long long)(rows - 1) * *d.rs + cols;
+    if (*d.bs == 0) *d.bs = extent;
+    if (*d.rs < cols || *d.rs > (1ll << 40) || *d.bs < extent || *d.bs > (1ll << 45))
+      return fail(RA_ERR_INVALID_ARG, "%s strides (%lld, %lld) make rows or matrices overlap", d.name, *d.bs, *d.rs);
+  }
+  const NsWs l = ns_layout(s);
+  if ((rc = check_workspace(workspace, ws_bytes, l.total))) return rc;
+  int* st;
+  if ((rc = status_ptr(&st))) return rc;
+  if (!device_is_sm103()) return fail(RA_ERR_UNSUPPORTED, "tensor-core kernels are built for sm_103a only");
+  char* base = static_cast<char*>(workspace);
+  PairPlan plan{static_cast<cudaStream_t>(stream), st, device_sms()};
+  float* parts = reinterpret_cast<float*>(base + l.parts);
+  float* sums[2] = {reinterpret_cast<float*>(base + l.sums[0]), reinterpret_cast<float*>(base + l.sums[1])};
+  uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(base + l.hi[0]), reinterpret_cast<uint16_t*>(base + l.hi[1])};
+  uint16_t* lo = reinterpret_cast<uint16_t*>(base + l.lo);
+  void *A = base + l.a, *B = base + l.b;
+  const NsInput in{g, g_dtype, batch, rows, cols, g_rstride, g_bstride};
+  cudaError_t e = launch_ns_sumsq(in, parts, plan.st);
+  if (e == cudaSuccess) e = launch_ns_scale(in, parts, (float)s.sx, eps, hi[0], lo, s.ld, plan.st);
+  if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz scaling launch");
+  const bool tall = rows > cols;
+  const long long xb = (long long)rows * s.ld, gb = (long long)s.m * s.ldm;
+  int num_sums = 0;
+  const PairPlan::Operand Aop{A, s.m, s.m, s.ldm, gb}, Bop{B, s.m, s.m, s.ldm, gb};
+  for (int k = 0; k < steps; ++k) {
+    const uint16_t* x = hi[k & 1];
+    const PairPlan::Operand X{x, rows, cols, s.ld, xb};
+    PairArgs a;
+    memset(&a, 0, sizeof a);
+    a.batch = batch;
+    // alpha = |X|_F^2 / m, the mean of the Gram matrix's diagonal (1 / m at first)
+    a.sums = sums[k & 1];
+    a.num_sums = num_sums;
+    a.sums_mul = (float)(num_sums ? 1.0 / (s.sx * s.sx * s.m) : 1.0 / s.m);
+    a.ns_a = coeffs[0]; a.ns_b = coeffs[1]; a.ns_c = coeffs[2];
+    // A' = X X^T - alpha I, or X^T X - alpha I on the smaller side
+    a.epi = PAIR_GRAM;
+    a.M = a.N = s.m;
+    a.K = tall ? rows : cols;
+    a.a_mn = a.b_mn = tall ? 1 : 0;
+    a.ns_acc = (float)(s.sa / (s.sx * s.sx));
+    a.ns_out = (float)s.sa;
+    if ((rc = make_map_3d(&a.tm_c, A, RA_F16, s.m, s.m, batch, s.ldm, gb, 64, 32, true)) ||
+        (rc = make_map_3d(&a.tm_ct, A, RA_F16, s.m, s.m, batch, s.ldm, gb, 32, 64, false)) ||
+        (rc = plan.run(a, plan.tile_cols(a), X, X, RA_F16)))
+      return rc;
+    // B' = (b + 2 c alpha) A' + c A'^2
+    a.epi = PAIR_SQUARE;
+    a.K = s.m;
+    a.a_mn = a.b_mn = 0;
+    a.ns_acc = (float)(coeffs[2] * s.sb / (s.sa * s.sa));
+    a.ns_lin = (float)(s.sb / s.sa);
+    a.hi_in = static_cast<const uint16_t*>(A);
+    a.ld = s.ldm;
+    if ((rc = make_map_3d(&a.tm_c, B, RA_F16, s.m, s.m, batch, s.ldm, gb, 64, 32, true)) ||
+        (rc = make_map_3d(&a.tm_ct, B, RA_F16, s.m, s.m, batch, s.ldm, gb, 32, 64, false)) ||
+        (rc = plan.run(a, plan.tile_cols(a), Aop, Aop, RA_F16)))
+      return rc;
+    // X <- (a + b alpha + c alpha^2) X + B' X, or X B'
+    a.epi = PAIR_UPDATE;
+    a.M = rows; a.N = cols; a.K = s.m;
+    a.a_mn = 0;
+    a.b_mn = tall ? 0 : 1;
+    a.ns_acc = (float)(1.0 / s.sb);
+    a.ns_out = (float)(1.0 / s.sx);
+    a.hi_in = x;
+    a.lo = lo;
+    a.ld = s.ld;
+    a.c_dtype = out_dtype;
+    const int bn = plan.tile_cols(a);
+    if (k == steps - 1) {
+      a.out = out;
+      a.out_ld = out_rstride;
+      a.out_bstride = out_bstride;
+      const long long es = (long long)dtype_size(out_dtype);
+      a.out_vec = aligned16(out) && (out_rstride * es) % 16 == 0 && (out_bstride * es) % 16 == 0;
+    } else {
+      // the low terms are replaced where they are: each is read by the thread that
+      // then writes it
+      if ((rc = make_map_3d(&a.tm_c, hi[(k + 1) & 1], RA_F16, cols, rows, batch, s.ld, xb, 32, 32, false)) ||
+          (rc = make_map_3d(&a.tm_ct, lo, RA_F16, cols, rows, batch, s.ld, xb, 32, 32, false)))
+        return rc;
+    }
+    // partial sums of this step, read by the next step's three products
+    a.sums_out = sums[(k + 1) & 1];
+    num_sums = 16 * pair_tiles(a, bn);
+    if ((rc = tall ? plan.run(a, bn, X, Bop, RA_F16) : plan.run(a, bn, Bop, X, RA_F16))) return rc;
+  }
   return RA_OK;
 }
 

@@ -231,4 +231,87 @@ struct GemmArgs {
 };
 cudaError_t launch_tc_gemm(GemmArgs& a, int num_sms, cudaStream_t st);
 
+// ------------------------------------------------------- CTA-pair products
+// C[M, N] = epilogue(sum_k A(m, k) B(n, k)) for `batch` equal problems, on pairs
+// of CTAs (tiles of 256 x 256 or 256 x 128); operands K-major or MN-major, sizes
+// of any value.  The epilogues:
+enum PairEpi {
+  PAIR_STATS = 0,    // softmax statistics of each row's columns and the target's logit
+  PAIR_DLOGITS = 1,  // gradient of the logits, 16-bit
+  PAIR_STORE = 2,    // C, 16-bit or fp32, fp32 optionally added to what is there
+  PAIR_GRAM = 3,     // Newton-Schulz: A' = X X^T - alpha I (symmetric)
+  PAIR_SQUARE = 4,   // Newton-Schulz: B' = (b + 2 c alpha) A' + c A'^2 (symmetric)
+  PAIR_UPDATE = 5,   // Newton-Schulz: X <- (a + b alpha + c alpha^2) X + B' X
+};
+struct PairArgs {
+  // operands: K-major: boxes of 64 x 128 (A), 64 x BN/2 (B); MN-major: 64 x 64
+  CUtensorMap tm_a, tm_b;
+  // outputs: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle;
+  // tm_ct: the mirror image of a symmetric product (box 32 x 64, no swizzle).
+  // PAIR_UPDATE: tm_c, tm_ct the high and low terms (boxes 32 x 32, no swizzle)
+  CUtensorMap tm_c, tm_ct;
+  int M, N, K, batch;
+  int a_mn, b_mn;
+  int ab_bf16;
+  int epi;
+  int group_m;  // tile rows taken together (see tile_at)
+  int* status;
+  unsigned long long wait_limit_ns;
+  // cross entropy
+  const long long* targets;  // [M]
+  long long ignore;          // target of rows without loss
+  long long vocab;           // V
+  long long col_off;         // vocabulary entry of column 0
+  const float* lse;          // [M]
+  const float* grad;         // [M]: gradient of each row's loss
+  const float* scale;        // {2^k, 2^-k} on the device, or NULL: {1, 1}
+  float2* stats;             // [column parts][M]: (max, sum of exponentials) of BN / 2 columns
+  float* target_logit;       // [M]
+  // PAIR_STORE
+  int c_dtype;
+  int c_accumulate;          // fp32: add to C
+  const float* c_add;        // 16-bit: packed fp32 [M, N] added to the product
+  // Newton-Schulz; X, A', B' are held as fp16 times powers of two
+  const float* sums;         // [batch][num_sums]: partial sums of X's squares
+  int num_sums;              // 0: alpha = sums_mul
+  float sums_mul;            // alpha = sums_mul * sum
+  float* sums_out;           // PAIR_UPDATE: [batch][16 * tiles]
+  float ns_a, ns_b, ns_c;    // coefficients
+  float ns_acc;              // factor of the accumulator
+  float ns_lin;              // PAIR_SQUARE: factor of A'
+  float ns_out;              // PAIR_GRAM: factor of alpha; PAIR_UPDATE: factor of the final result
+  const uint16_t* hi_in;     // PAIR_SQUARE: A'; PAIR_UPDATE: high terms of X ([batch][M][ld])
+  const uint16_t* lo;        // PAIR_UPDATE: low terms of X
+  long long ld;
+  void* out;                 // PAIR_UPDATE, last step: result in c_dtype
+  long long out_ld, out_bstride;
+  int out_vec;               // result rows are 16-byte aligned
+};
+// Tiles per batch entry with tiles of 256 x bn; bn is 128 or 256.
+int pair_tiles(const PairArgs& a, int bn);
+cudaError_t launch_tc_pair(const PairArgs& a, int bn, int num_sms, cudaStream_t st);
+
+// --------------------------------------------- cross entropy, small kernels
+// loss and lse from the column parts' statistics; a target outside [0, V) that is
+// not `ignore` gives loss = NaN and RA_ERR_INVALID_ARG in *status.
+cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,
+                               long long ignore, long long V, long long T, float* loss, float* lse, int* status,
+                               cudaStream_t st);
+// scale = {2^k, 2^-k} with 2^k max |grad| in [2^13, 2^14) over the rows with a loss.
+cudaError_t launch_xent_scale(const float* grad, const long long* targets, long long ignore, long long V, long long T,
+                              float* scale, cudaStream_t st);
+
+// --------------------------------------------- Newton-Schulz, small kernels
+struct NsInput {
+  const void* g;
+  int dtype, batch, rows, cols;
+  long long ld, bstride;
+};
+constexpr int kNsParts = 256;  // partial sums per batch entry
+// parts[batch][kNsParts][3]: sums of squares in three ranges of magnitude.
+cudaError_t launch_ns_sumsq(const NsInput& in, float* parts, cudaStream_t st);
+// hi + lo = mul * G / (|G|_F + eps) as two fp16 terms, rows of ld elements.
+cudaError_t launch_ns_scale(const NsInput& in, const float* parts, float mul, float eps, uint16_t* hi, uint16_t* lo,
+                            long long ld, cudaStream_t st);
+
 }  // namespace ra

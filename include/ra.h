@@ -337,8 +337,81 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
                long long T, int d_model, int d_hidden, int block, void* dx, ra_dtype dx_dtype,
                float* dw1, float* dw2, void* workspace, size_t ws_bytes, void* stream);
 
+/* Softmax cross entropy of a large vocabulary, the loss at the head of a model:
+ *     z_tv = x_t . w_v,   lse_t = ln sum_v e^{z_tv},   loss_t = lse_t - z_{t, y_t}
+ * without the logits z ever being held: the forward keeps, per token, a (max,
+ * sum) pair for each tile of the vocabulary; the backward recomputes the logits
+ * of `block` vocabulary entries at a time, so that only one block's gradient
+ * [T, block] exists at once (the vocabulary's counterpart of the feed-forward
+ * layer's blocks of tokens).
+ *   x [T, D] hidden states (tokens of all batches), w [V, D] the vocabulary's
+ *   weights, both in `dtype` (RA_BF16 or RA_F16), rows at x_rstride / w_rstride
+ *   elements (0 = D; multiples of 8); targets [T] 64-bit integers.  D is a multiple
+ *   of 8; T, V and block are of any size >= 1 (blocks that are multiples of 256 fill
+ *   the tiles).
+ *   A token whose target equals ignore_index has loss 0 and no gradient (its lse is
+ *   still written, and its x, multiplied by exact zeros in dw, has to be finite).  Any other target outside [0, V) gives loss NaN, no gradient,
+ *   and RA_ERR_INVALID_ARG in the status word.
+ *   loss, lse [T] fp32.  Products accumulate in fp32; the softmax's maxima and sums
+ *   are fp32.  Infinities and NaN among the logits give NaN, as the formula does; a
+ *   row whose logits are all -inf has lse = -inf and loss NaN.
+ *   workspace: device memory, 256-byte aligned, of the size given (about T V / 8
+ *   bytes for the forward, 2 T block bytes, and 4 T D where dx is 16-bit and there
+ *   is more than one block, for the backward).  It must not be in use by work that
+ *   overlaps the call on the GPU. */
+size_t ra_xent_fwd_workspace_bytes(ra_dtype dtype, long long T, int D, int V);
+int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,
+                long long x_rstride, long long w_rstride, const long long* targets,
+                long long ignore_index, float* loss, float* lse, void* workspace, size_t ws_bytes,
+                void* stream);
+
+/* Backward of ra_xent_fwd: gradients of L = sum_t dloss_t loss_t,
+ *     d_tv = dloss_t (e^{z_tv - lse_t} - [v = y_t]),   dx = d W,   dW = d^T x.
+ *   lse from ra_xent_fwd of the same x, w, targets; dloss [T] fp32 (1 / T for a mean;
+ *   values at ignored tokens are not used).
+ *   dx [T, D] in dx_dtype and dw [V, D] in dw_dtype, packed, fully overwritten.  d is
+ *   rounded to `dtype` before the two products (it is a tensor-core operand: half a
+ *   unit of 2^-8 relative for bf16, of 2^-11 for fp16, whose values are brought into
+ *   range by a power of two from max |dloss|); their sums, over blocks too, are fp32.
+ *   The results do not vary from run to run. */
+size_t ra_xent_bwd_workspace_bytes(ra_dtype dtype, ra_dtype dx_dtype, long long T, int D, int V,
+                                   int block);
+int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,
+                long long x_rstride, long long w_rstride, const long long* targets,
+                long long ignore_index, const float* lse, const float* dloss, int block, void* dx,
+                ra_dtype dx_dtype, void* dw, ra_dtype dw_dtype, void* workspace, size_t ws_bytes,
+                void* stream);
+
+/* Orthogonalises a weight gradient by Newton-Schulz products, as the Muon
+ * optimiser does with the update of a hidden layer's matrix (the dW1 and dW2 of
+ * ra_ffn_bwd, for instance):
+ *     X = G / (|G|_F + eps);   `steps` times:  A = X X^T (X^T X where rows > cols),
+ *     X <- a X + (b A + c A^2) X
+ * with (a, b, c) = coeffs[0..2], read on the host; (3.4445, -4.7750, 2.0315) and five
+ * steps bring every singular value that is not tiny near 1.
+ *   g [batch, rows, cols] in any dtype, out [batch, rows, cols] in any dtype; rows and
+ *   matrices at the strides given (elements, 0 = packed).  out may be g itself where
+ *   dtype and strides agree.  Sizes of any value up to 65536; each matrix of the
+ *   batch is orthogonalised by itself.
+ *   The products run on the tensor cores with fp16 operands (held times powers of two
+ *   that follow from the size and the coefficients, so that nothing leaves fp16's
+ *   range) and fp32 sums; X is carried as two fp16 terms, and the Gram matrix without
+ *   the mean of its diagonal, which enters in fp32, so that its rounding is no common
+ *   factor of the result.  For gradients with a side of 32 or more the result is
+ *   within about 2e-3 (relative, 2-norm) of exact arithmetic.  G = 0 gives 0;
+ *   infinities and NaN in a matrix give NaN.  Coefficients that let the singular
+ *   values grow past 64 return RA_ERR_UNSUPPORTED.
+ *   workspace: device memory, 256-byte aligned, about 6 bytes per element of g and 4
+ *   per element of the two square matrices of the smaller side. */
+size_t ra_newton_schulz_workspace_bytes(int batch, int rows, int cols);
+int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int cols,
+                     long long g_bstride, long long g_rstride, const float* coeffs, int steps,
+                     float eps, void* out, ra_dtype out_dtype, long long out_bstride,
+                     long long out_rstride, void* workspace, size_t ws_bytes, void* stream);
+
 /* Synchronise `stream`, then return and clear the device status word
- * (RA_OK, RA_ERR_RANGE or RA_ERR_TIMEOUT), or RA_ERR_CUDA if the stream
+ * (RA_OK, RA_ERR_RANGE, RA_ERR_TIMEOUT, or RA_ERR_INVALID_ARG for a target outside
+ * the vocabulary), or RA_ERR_CUDA if the stream
  * itself reports an error. */
 int ra_sync_status(void* stream);
 
@@ -390,7 +463,8 @@ typedef enum {
   RA_KERNEL_GEMM_TC = 4,  /* tensor-core GEMM of the feed-forward layer (every launch) */
   RA_COPY_H2D = 5,        /* ra_ring_step_host uploads (two groups per call) */
   RA_COPY_D2H = 6,        /* ra_ring_step_host downloads (two groups per call) */
-  RA_KERNEL_COUNT = 7
+  RA_KERNEL_PAIR_TC = 7,  /* tensor-core CTA-pair products (cross entropy, Newton-Schulz) */
+  RA_KERNEL_COUNT = 8
 } ra_kernel_id;
 int ra_kernel_timing(int enable);
 int ra_kernel_timing_read(int kernel, double* total_ms, unsigned long long* launches);

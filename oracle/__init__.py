@@ -1,5 +1,6 @@
-"""fp64 CPU oracle for blockwise exact attention and the blockwise
-feed-forward layer (test infrastructure only).
+"""fp64 CPU oracle for blockwise exact attention, the blockwise feed-forward
+layer, the vocabulary cross entropy and the Newton-Schulz update (test
+infrastructure only).
 
 Only the test suite, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  The CUDA product path never imports,
@@ -28,4 +29,10 @@ from .ffn import (  # noqa: F401
     ffn_bwd,
     ffn_blocked,
     ffn_bwd_blocked,
+)
+from .train import (  # noqa: F401
+    xent_fwd,
+    xent_bwd,
+    newton_schulz,
+    singular_map,
 )
