@@ -412,40 +412,37 @@ def ffn_bwd(x, w1, w2, dy, block=None, dx_dtype=torch.float32, stream=None):
     return dx, dw1, dw2
 
 
-def _on_device(ref, **tensors):
+def _on_device(ref, *tensors):
     """Every tensor lies on ref's device, and that is the current one (the
     stream and the library's kernels belong to it)."""
-    if not ref.is_cuda or ref.device.index != torch.cuda.current_device():
-        raise RAError(1, f"tensors must be on the current CUDA device (got {ref.device})")
-    for name, t in tensors.items():
-        if t is not None and t.device != ref.device:
-            raise RAError(1, f"{name} is on {t.device}, not on {ref.device}")
-
-
-def _rows(t, name, shape=None, dtype=None):
-    """Row stride of a 2-D tensor with contiguous rows (0 where it has one row
-    or is packed)."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise RAError(1, f"{name} must be {list(shape) if shape else '2-D'} (got {list(t.shape)})")
-    if dtype is not None and t.dtype != dtype:
-        raise RAError(1, f"{name} must be {dtype} (got {t.dtype})")
-    if t.stride(1) != 1 and t.shape[1] > 1:
-        raise RAError(1, f"{name} must have contiguous rows (strides {t.stride()})")
-    return t.stride(0) if t.shape[0] > 1 else 0
+    dev = ref.device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise RAError(1, f"tensors must be on the current CUDA device (got {dev})")
+    for t in tensors:
+        if t.device != dev:
+            raise RAError(1, f"tensors must be on one device (got {t.device} and {dev})")
 
 
 def _vector(t, name, T, dtype):
-    if t.dim() != 1 or t.shape[0] != T or t.dtype != dtype or not t.is_contiguous():
+    if t.dtype != dtype or t.shape != (T,) or not t.is_contiguous():
         raise RAError(1, f"{name} must be a contiguous {dtype} tensor [{T}] (got {t.dtype} {list(t.shape)})")
 
 
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
 def _xent_check(x, w, targets):
+    """(T, D, V, row stride of x, row stride of w); a single row passes 0."""
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
         raise RAError(1, f"x [T, D] and w [V, D] must have one D and one dtype (got {list(x.shape)} {x.dtype}, "
                          f"{list(w.shape)} {w.dtype})")
-    T, D = x.shape
+    (T, D), V = x.shape, w.shape[0]
+    (xs, xc), (ws, wc) = x.stride(), w.stride()
+    if D > 1 and (xc != 1 or wc != 1):
+        raise RAError(1, f"x and w must have contiguous rows (strides {x.stride()}, {w.stride()})")
     _vector(targets, "targets", T, torch.int64)
-    return T, D, w.shape[0], _rows(x, "x"), _rows(w, "w")
+    return T, D, V, xs if T > 1 else 0, ws if V > 1 else 0
 
 
 def ra_xent_fwd_workspace_bytes(dtype, T, D, V):
@@ -456,40 +453,52 @@ def ra_xent_bwd_workspace_bytes(dtype, dx_dtype, T, D, V, block):
     return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), int(block)))
 
 
+def _xent_fwd(sizes, x, w, targets, loss, lse, workspace, ignore_index, stream):
+    T, D, V, xs, ws = sizes
+    _on_device(x, w, targets, loss, lse, workspace)
+    _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
+                              loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                              _stream(stream)))
+
+
+def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index, stream):
+    T, D, V, xs, ws = sizes
+    _vector(lse, "lse", T, torch.float32)
+    _vector(dloss, "dloss", T, torch.float32)
+    _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
+    _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
+                              lse.data_ptr(), dloss.data_ptr(), block, dx.data_ptr(), _dt(dx), dw.data_ptr(), _dt(dw),
+                              workspace.data_ptr(), _nbytes(workspace), _stream(stream)))
+
+
 def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
     """loss and lse [T] fp32 of the softmax cross entropy of x w^T [T, V] against
     targets [T] int64, without the logits.  See include/ra.h."""
-    T, D, V, xs, ws = _xent_check(x, w, targets)
-    for t, name in ((loss, "loss"), (lse, "lse")):
-        _vector(t, name, T, torch.float32)
-    _on_device(x, w=w, targets=targets, loss=loss, lse=lse, workspace=workspace)
-    _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
-                              int(ignore_index), loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream(stream)))
+    sizes = _xent_check(x, w, targets)
+    _vector(loss, "loss", sizes[0], torch.float32)
+    _vector(lse, "lse", sizes[0], torch.float32)
+    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, int(ignore_index), stream)
 
 
 def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index=-100, stream=None):
     """Gradients of sum(dloss * loss): dx [T, D] and dw [V, D] (packed,
     overwritten), `block` vocabulary entries at a time."""
-    T, D, V, xs, ws = _xent_check(x, w, targets)
-    for t, name in ((lse, "lse"), (dloss, "dloss")):
-        _vector(t, name, T, torch.float32)
-    for t, name, shape in ((dx, "dx", (T, D)), (dw, "dw", (V, D))):
-        if tuple(t.shape) != shape or not t.is_contiguous():
+    sizes = _xent_check(x, w, targets)
+    for t, name, shape in ((dx, "dx", sizes[:2]), (dw, "dw", (sizes[2], sizes[1]))):
+        if t.shape != shape or not t.is_contiguous():
             raise RAError(1, f"{name} must be a packed {list(shape)} tensor")
-    _on_device(x, w=w, targets=targets, lse=lse, dloss=dloss, dx=dx, dw=dw, workspace=workspace)
-    _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
-                              int(ignore_index), lse.data_ptr(), dloss.data_ptr(), int(block), dx.data_ptr(), _dt(dx),
-                              dw.data_ptr(), _dt(dw), workspace.data_ptr(),
-                              workspace.numel() * workspace.element_size(), _stream(stream)))
+    _xent_bwd(sizes, x, w, targets, lse, dloss, int(block), dx, dw, workspace, int(ignore_index), stream)
 
 
 def xent_fwd(x, w, targets, ignore_index=-100, stream=None):
     """Convenience wrapper: allocates loss, lse and the workspace."""
-    T, D, V, _, _ = _xent_check(x, w, targets)
-    loss, lse = torch.empty(2, T, dtype=torch.float32, device=x.device)
-    ws = _workspace(ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), x.device)
-    ra_xent_fwd(x, w, targets, loss, lse, ws, ignore_index, stream)
+    sizes = _xent_check(x, w, targets)
+    T, D, V = sizes[:3]
+    dev = x.device
+    loss = torch.empty(T, dtype=torch.float32, device=dev)
+    lse = torch.empty(T, dtype=torch.float32, device=dev)
+    ws = _workspace(_lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), dev)
+    _xent_fwd(sizes, x, w, targets, loss, lse, ws, int(ignore_index), stream)
     return loss, lse
 
 
@@ -497,12 +506,14 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
              ignore_index=-100, stream=None):
     """Convenience wrapper: allocates dx, dw and the workspace (block: the whole
     vocabulary by default)."""
-    T, D, V, _, _ = _xent_check(x, w, targets)
-    block = V if block is None else block
-    dx = torch.empty(T, D, dtype=dx_dtype, device=x.device)
-    dw = torch.empty(V, D, dtype=dw_dtype, device=x.device)
-    ws = _workspace(ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), x.device)
-    ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, ws, ignore_index, stream)
+    sizes = _xent_check(x, w, targets)
+    T, D, V = sizes[:3]
+    block = V if block is None else int(block)
+    dev = x.device
+    dx = torch.empty(T, D, dtype=dx_dtype, device=dev)
+    dw = torch.empty(V, D, dtype=dw_dtype, device=dev)
+    ws = _workspace(_lib().ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), dev)
+    _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, ws, int(ignore_index), stream)
     return dx, dw
 
 
@@ -513,35 +524,42 @@ def ra_newton_schulz_workspace_bytes(batch, rows, cols):
 def _ns_layout(t, name):
     """(batch, rows, cols, batch stride, row stride) of a [rows, cols] or
     [batch, rows, cols] tensor with contiguous rows."""
-    if t.dim() not in (2, 3):
+    n = t.dim()
+    if n not in (2, 3):
         raise RAError(1, f"{name} must be [rows, cols] or [batch, rows, cols] (got {list(t.shape)})")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise RAError(1, f"{name} must have contiguous rows (strides {t.stride()})")
-    rows, cols = t.shape[-2:]
-    batch = t.shape[0] if t.dim() == 3 else 1
-    return (batch, rows, cols, t.stride(0) if t.dim() == 3 and batch > 1 else 0,
-            t.stride(-2) if rows > 1 else 0)
+    batch, rows, cols = t.shape if n == 3 else (1, *t.shape)
+    strides = t.stride()
+    if strides[-1] != 1 and cols > 1:
+        raise RAError(1, f"{name} must have contiguous rows (strides {strides})")
+    return batch, rows, cols, strides[0] if n == 3 and batch > 1 else 0, strides[-2] if rows > 1 else 0
 
 
-def ra_newton_schulz(g, out, workspace, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, stream=None):
+_NS_COEFFS = (3.4445, -4.7750, 2.0315)
+_Float3 = ctypes.c_float * 3
+
+
+def _newton_schulz(layout, g, out, out_strides, workspace, steps, coeffs, eps, stream):
+    _on_device(g, out, workspace)
+    _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), *layout, _Float3(*coeffs), int(steps), float(eps),
+                                   out.data_ptr(), _dt(out), *out_strides, workspace.data_ptr(), _nbytes(workspace),
+                                   _stream(stream)))
+
+
+def ra_newton_schulz(g, out, workspace, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
     """out <- `steps` Newton-Schulz steps on g / (|g| + eps), each matrix of a
     batch by itself.  See include/ra.h."""
-    batch, rows, cols, gb, gr = _ns_layout(g, "g")
-    if tuple(out.shape) != tuple(g.shape):
+    layout = _ns_layout(g, "g")
+    if out.shape != g.shape:
         raise RAError(1, f"out must have the shape of g ({list(out.shape)} vs {list(g.shape)})")
-    _, _, _, ob, orr = _ns_layout(out, "out")
-    _on_device(g, out=out, workspace=workspace)
-    _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), batch, rows, cols, gb, gr, (ctypes.c_float * 3)(*coeffs),
-                                   int(steps), float(eps), out.data_ptr(), _dt(out), ob, orr, workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream(stream)))
+    _newton_schulz(layout, g, out, _ns_layout(out, "out")[3:], workspace, steps, coeffs, eps, stream)
 
 
-def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, out_dtype=None, stream=None):
+def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, stream=None):
     """Convenience wrapper: allocates out (g's dtype by default) and the workspace."""
-    batch, rows, cols, _, _ = _ns_layout(g, "g")
+    layout = _ns_layout(g, "g")
     out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
-    ws = _workspace(ra_newton_schulz_workspace_bytes(batch, rows, cols), g.device)
-    ra_newton_schulz(g, out, ws, steps, coeffs, eps, stream)
+    ws = _workspace(_lib().ra_newton_schulz_workspace_bytes(*layout[:3]), g.device)
+    _newton_schulz(layout, g, out, (0, 0), ws, steps, coeffs, eps, stream)
     return out
 
 

@@ -186,11 +186,11 @@ int make_map_2d(CUtensorMap* m, const void* base, int is_bf16, long long rows, l
 
 namespace {
 
-// Batch of row-major matrices [batch, rows, cols]: dims (cols, rows, batch), any
-// box; cols and rows may be of any size, ld and bstride (elements) multiples of
+// Batch of row-major matrices [batch, rows, cols]: dims (cols, rows, batch), boxes of
+// 128-byte rows with the 128-byte swizzle; cols and rows may be of any size, ld and bstride (elements) multiples of
 // 16 bytes.
 int make_map_3d(CUtensorMap* m, const void* base, int dtype, long long cols, long long rows, long long batch,
-                long long ld, long long bstride, int box_cols, int box_rows, bool swizzle) {
+                long long ld, long long bstride, int box_cols, int box_rows) {
   EncodeTiledFn fn;
   int rc = encoder(&fn);
   if (rc) return rc;
@@ -202,8 +202,7 @@ int make_map_3d(CUtensorMap* m, const void* base, int dtype, long long cols, lon
   CUresult r = fn(m, dtype == RA_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                      : dtype == RA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                   3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(RA_ERR_CUDA, "cuTensorMapEncodeTiled (3-D) failed (%d)", (int)r);
   return RA_OK;
 }
@@ -1247,43 +1246,56 @@ int ra_ring_step_host(const void* q, const void* k, const void* v, const void* d
 namespace ra {
 namespace {
 
-// One CTA-pair product: fills in the operands' maps and picks the tile width.
+// How one product is cut up.  A CTA pair works on a tile of 256 rows by 256 or 128
+// columns; GB300 has 76 pairs, and the cut is made for that number whatever the device,
+// so that workspaces and results do not depend on it.
+//   - Where the wide tiles fill less than half the pairs and K may be split (the result
+//     is a sum in fp32 planes), K is split over the idle pairs, 8 k-slabs (512) or more
+//     per split.
+//   - A narrow tile takes as long as a wide one (measured: 0.98 against 1.86 PFLOP/s on
+//     8192 x 131072 x 2048), only its epilogue is shorter: it is taken where even the
+//     narrow tiles find a pair each.
+constexpr int kPairs = 76;
+struct Cut {
+  int bn, splits;
+};
+Cut cut_product(long long M, long long N, long long K, bool may_split) {
+  const long long tm = (M + 255) / 256, wide = tm * ((N + 255) / 256), narrow = tm * ((N + 127) / 128);
+  if (may_split && wide * 2 <= kPairs) {
+    const long long by_k = (K + 511) / 512, by_pairs = kPairs / wide;
+    const int splits = (int)(by_k < by_pairs ? by_k : by_pairs);
+    if (splits > 1) return Cut{256, splits};
+  }
+  return Cut{narrow <= kPairs ? 128 : 256, 1};
+}
+
+// One CTA-pair product of the cross entropy: fills in the operands' maps.
 struct PairPlan {
   cudaStream_t st;
   int* status;
   int sms;
-
-  // Tiles are 256 rows by 256 or 128 columns.  The wide tile moves fewer operand
-  // bytes per product, the narrow one splits the work finer: the rule takes the one
-  // whose waves over the pairs cost less, a narrow tile counted as 0.56 of a wide
-  // one (half the products, 12% slower per product).
-  int tile_cols(const PairArgs& a) const {
-    const long long pairs = sms / 2;
-    const long long w256 = ((long long)pair_tiles(a, 256) * a.batch + pairs - 1) / pairs;
-    const long long w128 = ((long long)pair_tiles(a, 128) * a.batch + pairs - 1) / pairs;
-    return 0.56 * (double)w128 < (double)w256 ? 128 : 256;
-  }
-  // a: everything but the operands' maps and the fields set here.  Operands are
-  // matrices of `rows` x `cols` (as stored) with leading dimension ld.
-  struct Operand {
+  struct Operand {  // a matrix of rows x cols as stored
     const void* p;
-    long long rows, cols, ld, bstride;
+    long long rows, cols, ld;
   };
-  int run(PairArgs& a, int bn, const Operand& A, const Operand& B, int dtype) const {
+  // a: everything but the operands' maps and the fields set here
+  int run(PairArgs& a, Cut cut, const Operand& A, const Operand& B, int dtype) const {
     int rc;
-    if ((rc = make_map_3d(&a.tm_a, A.p, dtype, A.cols, A.rows, a.batch, A.ld, A.bstride, 64, a.a_mn ? 64 : 128, true)) ||
-        (rc = make_map_3d(&a.tm_b, B.p, dtype, B.cols, B.rows, a.batch, B.ld, B.bstride, 64, a.b_mn ? 64 : bn / 2, true)))
+    if ((rc = make_map_3d(&a.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, a.a_mn ? 64 : 128)) ||
+        (rc = make_map_3d(&a.tm_b, B.p, dtype, B.cols, B.rows, 1, B.ld, 0, 64, a.b_mn ? 64 : cut.bn / 2)))
       return rc;
     a.ab_bf16 = dtype == RA_BF16;
+    a.bn = cut.bn;
+    a.splits = cut.splits;
     a.status = status;
     a.wait_limit_ns = wait_limit_ns();
     // the pairs at work together cover all columns of a few tile rows, or 16 tile
     // rows where the columns are many
-    const int tn = (a.N + bn - 1) / bn, pairs = sms / 2 > 0 ? sms / 2 : 1;
-    a.group_m = tn < 5 ? (pairs + tn - 1) / tn : 16;
+    const int tn = (a.N + cut.bn - 1) / cut.bn;
+    a.group_m = tn < 5 ? (kPairs + tn - 1) / tn : 16;
     TimedLaunch tl(RA_KERNEL_PAIR_TC, st);
-    const cudaError_t e = launch_tc_pair(a, bn, sms, st);
-    return e == cudaSuccess ? RA_OK : cuda_fail(e, "CTA-pair product launch");
+    const cudaError_t e = launch_xent_pair(a, sms, st);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy product launch");
   }
 };
 
@@ -1323,17 +1335,25 @@ XentFwdWs xent_fwd_layout(const XentShape& s) {
 }
 
 // backward: scale (256 bytes) | gradient of one block's logits [T][ld] 16-bit | fp32
-// sum of dx [T, D] (16-bit dx and more than one block)
+// sum of dx: its splits' planes, or [T, D] where dx is 16-bit and there is more than
+// one block | planes of one block's dw where its product is split
 struct XentBwdWs {
-  size_t scale, d, acc, total;
+  size_t scale, d, acc, dw, total;
   long long ld;
+  Cut dx_cut, dw_cut;
 };
 XentBwdWs xent_bwd_layout(const XentShape& s, int dx_dtype) {
   XentBwdWs w{};
   w.ld = (s.block + 63) / 64 * 64;
+  w.dx_cut = cut_product(s.T, s.D, s.block, true);
+  w.dw_cut = cut_product(s.block, s.D, s.T, true);
   w.d = 256;
   w.acc = w.d + align256((size_t)s.T * w.ld * 2);
-  w.total = w.acc + (dx_dtype != RA_F32 && s.block < s.V ? align256((size_t)s.T * s.D * 4) : 0);
+  w.dw = w.acc;
+  if (w.dx_cut.splits > 1) w.dw += align256((size_t)w.dx_cut.splits * s.T * s.D * 4);
+  else if (dx_dtype != RA_F32 && s.block < s.V) w.dw += align256((size_t)s.T * s.D * 4);
+  w.total = w.dw;
+  if (w.dw_cut.splits > 1) w.total += align256((size_t)w.dw_cut.splits * s.block * s.D * 4);
   return w;
 }
 
@@ -1392,16 +1412,17 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
   PairArgs a;
   memset(&a, 0, sizeof a);
   a.epi = PAIR_STATS;
-  a.M = (int)s.T; a.N = s.V; a.K = s.D; a.batch = 1;
+  a.M = (int)s.T; a.N = s.V; a.K = s.D;
   a.targets = targets;
   a.ignore = ignore_index;
   a.vocab = s.V;
   a.stats = reinterpret_cast<float2*>(base + l.stats);
   a.target_logit = reinterpret_cast<float*>(base);
-  const int bn = plan.tile_cols(a);
-  if ((rc = plan.run(a, bn, {x, s.T, s.D, s.xs, 0}, {w, s.V, s.D, s.ws, 0}, dtype))) return rc;
-  const cudaError_t e = launch_xent_finish(a.stats, (s.V + bn / 2 - 1) / (bn / 2), a.target_logit, targets,
-                                           ignore_index, s.V, s.T, loss, lse, st, plan.st);
+  const Cut cut = cut_product(s.T, s.V, s.D, false);
+  if ((rc = plan.run(a, cut, {x, s.T, s.D, s.xs}, {w, s.V, s.D, s.ws}, dtype))) return rc;
+  const int part = cut.bn / 2;
+  const cudaError_t e = launch_xent_finish(a.stats, (s.V + part - 1) / part, a.target_logit, targets, ignore_index, s.V,
+                                           s.T, loss, lse, st, plan.st);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy reduction launch");
 }
 
@@ -1431,14 +1452,16 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     if (e != cudaSuccess) return cuda_fail(e, "gradient scale launch");
   }
   void* d = base + l.d;
-  void* acc = dx_dtype == RA_F32 ? dx : base + l.acc;
+  float* planes = reinterpret_cast<float*>(base + l.acc);
+  float* dw_planes = reinterpret_cast<float*>(base + l.dw);
+  const bool dx_split = l.dx_cut.splits > 1, dw_split = l.dw_cut.splits > 1;
   for (int v0 = 0; v0 < s.V; v0 += s.block) {
     const int C = s.V - v0 < s.block ? s.V - v0 : s.block;
     const bool first = v0 == 0, last = v0 + C == s.V;
     const char* wb = static_cast<const char*>(w) + (size_t)v0 * s.ws * 2;
+    const PairPlan::Operand W{wb, C, s.D, s.ws}, X{x, s.T, s.D, s.xs}, Dl{d, s.T, C, l.ld};
     PairArgs a;
     memset(&a, 0, sizeof a);
-    a.batch = 1;
     a.scale = scale;
     // d = gradient of this block's logits, recomputed from x and w
     a.epi = PAIR_DLOGITS;
@@ -1449,28 +1472,46 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     a.col_off = v0;
     a.lse = lse;
     a.grad = dloss;
-    if ((rc = make_map_3d(&a.tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32, true))) return rc;
-    if ((rc = plan.run(a, plan.tile_cols(a), {x, s.T, s.D, s.xs, 0}, {wb, C, s.D, s.ws, 0}, dtype))) return rc;
+    if ((rc = make_map_3d(&a.tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
+        (rc = plan.run(a, cut_product(s.T, C, s.D, false), X, W, dtype)))
+      return rc;
     // dx += d W  (W's rows as [K, N]: MN-major); summed over blocks in fp32
-    const int cdt = last && dx_dtype != RA_F32 ? dx_dtype : RA_F32;
-    void* c = cdt == RA_F32 ? acc : dx;
     a.epi = PAIR_STORE;
     a.M = (int)s.T; a.N = s.D; a.K = C;
     a.b_mn = 1;
-    a.c_dtype = cdt;
-    a.c_accumulate = cdt == RA_F32 && !first;
-    a.c_add = cdt != RA_F32 && !first ? static_cast<const float*>(acc) : nullptr;
-    if ((rc = make_map_3d(&a.tm_c, c, cdt, s.D, s.T, 1, s.D, 0, cdt == RA_F32 ? 32 : 64, 32, true))) return rc;
-    if ((rc = plan.run(a, plan.tile_cols(a), {d, s.T, C, l.ld, 0}, {wb, C, s.D, s.ws, 0}, dtype))) return rc;
+    a.c_dtype = dx_split || dx_dtype == RA_F32 || !last ? RA_F32 : dx_dtype;
+    void* c = dx_split || (a.c_dtype == RA_F32 && dx_dtype != RA_F32) ? (void*)planes : dx;
+    a.c_accumulate = a.c_dtype == RA_F32 && !first;
+    a.c_add = a.c_dtype != RA_F32 && !first ? planes : nullptr;
+    const bool c32 = a.c_dtype == RA_F32;
+    // the last block may be too short for as many splits: its planes are fewer, the
+    // others keep what they hold
+    const int k_slabs = (C + 63) / 64;
+    Cut cut = l.dx_cut;
+    if (cut.splits > k_slabs) cut.splits = k_slabs;
+    if ((rc = make_map_3d(&a.tm_c, c, a.c_dtype, s.D, s.T, dx_split ? l.dx_cut.splits : 1, s.D, s.T * s.D, c32 ? 32 : 64,
+                          32)) ||
+        (rc = plan.run(a, cut, Dl, W, dtype)))
+      return rc;
     // dw of this block = d^T x  (both MN-major)
     a.M = C; a.N = s.D; a.K = (int)s.T;
     a.a_mn = 1;
-    a.c_dtype = dw_dtype;
+    a.c_dtype = dw_split ? RA_F32 : dw_dtype;
     a.c_accumulate = 0;
     a.c_add = nullptr;
     void* dwb = static_cast<char*>(dw) + (size_t)v0 * s.D * dtype_size(dw_dtype);
-    if ((rc = make_map_3d(&a.tm_c, dwb, dw_dtype, s.D, C, 1, s.D, 0, dw_dtype == RA_F32 ? 32 : 64, 32, true))) return rc;
-    if ((rc = plan.run(a, plan.tile_cols(a), {d, s.T, C, l.ld, 0}, {x, s.T, s.D, s.xs, 0}, dtype))) return rc;
+    if ((rc = make_map_3d(&a.tm_c, dw_split ? dw_planes : dwb, a.c_dtype, s.D, C, l.dw_cut.splits, s.D,
+                          (long long)C * s.D, a.c_dtype == RA_F32 ? 32 : 64, 32)) ||
+        (rc = plan.run(a, l.dw_cut, Dl, X, dtype)))
+      return rc;
+    if (dw_split) {
+      const cudaError_t e = launch_sum_planes(dw_planes, l.dw_cut.splits, (long long)C * s.D, dwb, dw_dtype, plan.st);
+      if (e != cudaSuccess) return cuda_fail(e, "dw sum launch");
+    }
+  }
+  if (dx_split) {
+    const cudaError_t e = launch_sum_planes(planes, l.dx_cut.splits, s.T * s.D, dx, dx_dtype, plan.st);
+    if (e != cudaSuccess) return cuda_fail(e, "dx sum launch");
   }
   return RA_OK;
 }
@@ -1545,14 +1586,36 @@ int check_ns(int batch, int rows, int cols, const float* coeffs, int steps, floa
   return RA_OK;
 }
 
-// norm parts | sums of X's squares (two buffers) | X high terms (two buffers) | X low terms | A' | B'
-struct NsWs {
-  size_t parts, sums[2], hi[2], lo, a, b, total;
-};
-int ns_sums(const NsShape& s) {
-  // 16 partial sums per tile; narrow tiles bound the count
-  return 16 * ((s.rows + 255) / 256) * ((s.cols + 127) / 128);
+// The cut of one phase: the tile's width as for the cross entropy's products; K may be
+// split for every phase, over at most as many pairs as run at once.  A k-slab of a wide
+// tile takes about 0.33 us; handing one split's sum over takes 6 us, 2 us more for each
+// further split (measured on 8192 x 2048).  Wide tiles only.
+Cut ns_cut(const NsArgs& a, int kind, int pairs) {
+  const long long K = kind == NS_GRAM && !a.tall ? a.cols : kind == NS_GRAM ? a.rows : a.m;
+  const long long wide = (long long)a.batch * ns_phase_tiles(a, kind, 256);
+  const long long narrow = (long long)a.batch * ns_phase_tiles(a, kind, 128);
+  const long long by_pairs = pairs / wide;
+  const double whole = 0.33 * (double)((K + 63) / 64);
+  int best = 1;
+  double best_us = whole;
+  for (int s = 2; s <= by_pairs && s <= K / 256; ++s) {
+    const double us = whole / s + 4.0 + 2.0 * (s - 1);
+    if (us < best_us) {
+      best_us = us;
+      best = s;
+    }
+  }
+  if (best > 1) return Cut{256, best};
+  return Cut{narrow <= pairs ? 128 : 256, 1};
 }
+
+// barrier words and flags | norm parts | sums of X's squares (two buffers) | X high terms
+// (two buffers) | X low terms | A' | B' | sums of splits
+struct NsWs {
+  size_t words, parts, sums[2], hi[2], lo, a, b, partials, total;
+};
+// 16 partial sums per tile of X; narrow tiles bound their number
+size_t ns_sums(const NsShape& s) { return (size_t)16 * ((s.rows + 255) / 256) * ((s.cols + 127) / 128); }
 NsWs ns_layout(const NsShape& s) {
   NsWs w{};
   size_t off = 0;
@@ -1562,6 +1625,7 @@ NsWs ns_layout(const NsShape& s) {
     return at;
   };
   const size_t x = (size_t)s.batch * s.rows * s.ld * 2, g = (size_t)s.batch * s.m * s.ldm * 2;
+  w.words = take(((size_t)kNsWords + s.batch) * 4);
   w.parts = take((size_t)s.batch * kNsParts * 3 * 4);
   for (size_t& at : w.sums) at = take((size_t)s.batch * ns_sums(s) * 4);
   w.hi[0] = take(x);
@@ -1569,6 +1633,14 @@ NsWs ns_layout(const NsShape& s) {
   w.lo = take(x);
   w.a = take(g);
   w.b = take(g);
+  NsArgs a;
+  memset(&a, 0, sizeof a);
+  a.batch = s.batch; a.rows = s.rows; a.cols = s.cols; a.m = s.m; a.tall = s.rows > s.cols;
+  size_t units = 0;
+  for (int k = NS_GRAM; k <= NS_UPDATE; ++k) {
+    units += (size_t)(ns_cut(a, k, kPairs).splits - 1) * s.batch * ns_phase_tiles(a, k, 256);
+  }
+  w.partials = take(units * 2 * 8 * 128 * 32 * 4);
   w.total = off;
   return w;
 }
@@ -1614,85 +1686,78 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
   if ((rc = status_ptr(&st))) return rc;
   if (!device_is_sm103()) return fail(RA_ERR_UNSUPPORTED, "tensor-core kernels are built for sm_103a only");
   char* base = static_cast<char*>(workspace);
-  PairPlan plan{static_cast<cudaStream_t>(stream), st, device_sms()};
-  float* parts = reinterpret_cast<float*>(base + l.parts);
-  float* sums[2] = {reinterpret_cast<float*>(base + l.sums[0]), reinterpret_cast<float*>(base + l.sums[1])};
+  NsArgs a;
+  memset(&a, 0, sizeof a);
+  a.batch = batch; a.rows = rows; a.cols = cols; a.m = s.m; a.tall = rows > cols;
+  a.steps = steps;
+  a.in = NsInput{g, g_dtype, batch, rows, cols, g_rstride, g_bstride, 0};
+  const long long gs = (long long)dtype_size(g_dtype), os = (long long)dtype_size(out_dtype);
+  a.in.vec = aligned16(g) && (g_rstride * gs) % 16 == 0 && (g_bstride * gs) % 16 == 0;
+  a.ca = coeffs[0]; a.cb = coeffs[1]; a.cc = coeffs[2];
+  a.sx = (float)s.sx; a.sa = (float)s.sa; a.eps = eps;
+  a.alpha_mul = (float)(1.0 / (s.sx * s.sx * s.m));
+  a.gram_acc = (float)(s.sa / (s.sx * s.sx));
+  a.square_acc = (float)(coeffs[2] * s.sb / (s.sa * s.sa));
+  a.square_lin = (float)(s.sb / s.sa);
+  a.update_acc = (float)(1.0 / s.sb);
+  a.out_mul = (float)(1.0 / s.sx);
+  a.words = reinterpret_cast<unsigned int*>(base + l.words);
+  a.flags = a.words + 64;
+  a.partials = reinterpret_cast<float*>(base + l.partials);
+  a.parts = reinterpret_cast<float*>(base + l.parts);
+  for (int i = 0; i < 2; ++i) a.sums[i] = reinterpret_cast<float*>(base + l.sums[i]);
+  a.sums_ld = (long long)ns_sums(s);
+  a.counts = a.words + kNsWords;
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(base + l.hi[0]), reinterpret_cast<uint16_t*>(base + l.hi[1])};
-  uint16_t* lo = reinterpret_cast<uint16_t*>(base + l.lo);
-  void *A = base + l.a, *B = base + l.b;
-  const NsInput in{g, g_dtype, batch, rows, cols, g_rstride, g_bstride};
-  cudaError_t e = launch_ns_sumsq(in, parts, plan.st);
-  if (e == cudaSuccess) e = launch_ns_scale(in, parts, (float)s.sx, eps, hi[0], lo, s.ld, plan.st);
-  if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz scaling launch");
-  const bool tall = rows > cols;
-  const long long xb = (long long)rows * s.ld, gb = (long long)s.m * s.ldm;
-  int num_sums = 0;
-  const PairPlan::Operand Aop{A, s.m, s.m, s.ldm, gb}, Bop{B, s.m, s.m, s.ldm, gb};
-  for (int k = 0; k < steps; ++k) {
-    const uint16_t* x = hi[k & 1];
-    const PairPlan::Operand X{x, rows, cols, s.ld, xb};
-    PairArgs a;
-    memset(&a, 0, sizeof a);
-    a.batch = batch;
-    // alpha = |X|_F^2 / m, the mean of the Gram matrix's diagonal (1 / m at first)
-    a.sums = sums[k & 1];
-    a.num_sums = num_sums;
-    a.sums_mul = (float)(num_sums ? 1.0 / (s.sx * s.sx * s.m) : 1.0 / s.m);
-    a.ns_a = coeffs[0]; a.ns_b = coeffs[1]; a.ns_c = coeffs[2];
-    // A' = X X^T - alpha I, or X^T X - alpha I on the smaller side
-    a.epi = PAIR_GRAM;
-    a.M = a.N = s.m;
-    a.K = tall ? rows : cols;
-    a.a_mn = a.b_mn = tall ? 1 : 0;
-    a.ns_acc = (float)(s.sa / (s.sx * s.sx));
-    a.ns_out = (float)s.sa;
-    if ((rc = make_map_3d(&a.tm_c, A, RA_F16, s.m, s.m, batch, s.ldm, gb, 64, 32, true)) ||
-        (rc = make_map_3d(&a.tm_ct, A, RA_F16, s.m, s.m, batch, s.ldm, gb, 32, 64, false)) ||
-        (rc = plan.run(a, plan.tile_cols(a), X, X, RA_F16)))
-      return rc;
-    // B' = (b + 2 c alpha) A' + c A'^2
-    a.epi = PAIR_SQUARE;
-    a.K = s.m;
-    a.a_mn = a.b_mn = 0;
-    a.ns_acc = (float)(coeffs[2] * s.sb / (s.sa * s.sa));
-    a.ns_lin = (float)(s.sb / s.sa);
-    a.hi_in = static_cast<const uint16_t*>(A);
-    a.ld = s.ldm;
-    if ((rc = make_map_3d(&a.tm_c, B, RA_F16, s.m, s.m, batch, s.ldm, gb, 64, 32, true)) ||
-        (rc = make_map_3d(&a.tm_ct, B, RA_F16, s.m, s.m, batch, s.ldm, gb, 32, 64, false)) ||
-        (rc = plan.run(a, plan.tile_cols(a), Aop, Aop, RA_F16)))
-      return rc;
-    // X <- (a + b alpha + c alpha^2) X + B' X, or X B'
-    a.epi = PAIR_UPDATE;
-    a.M = rows; a.N = cols; a.K = s.m;
-    a.a_mn = 0;
-    a.b_mn = tall ? 0 : 1;
-    a.ns_acc = (float)(1.0 / s.sb);
-    a.ns_out = (float)(1.0 / s.sx);
-    a.hi_in = x;
-    a.lo = lo;
-    a.ld = s.ld;
-    a.c_dtype = out_dtype;
-    const int bn = plan.tile_cols(a);
-    if (k == steps - 1) {
-      a.out = out;
-      a.out_ld = out_rstride;
-      a.out_bstride = out_bstride;
-      const long long es = (long long)dtype_size(out_dtype);
-      a.out_vec = aligned16(out) && (out_rstride * es) % 16 == 0 && (out_bstride * es) % 16 == 0;
-    } else {
-      // the low terms are replaced where they are: each is read by the thread that
-      // then writes it
-      if ((rc = make_map_3d(&a.tm_c, hi[(k + 1) & 1], RA_F16, cols, rows, batch, s.ld, xb, 32, 32, false)) ||
-          (rc = make_map_3d(&a.tm_ct, lo, RA_F16, cols, rows, batch, s.ld, xb, 32, 32, false)))
-        return rc;
-    }
-    // partial sums of this step, read by the next step's three products
-    a.sums_out = sums[(k + 1) & 1];
-    num_sums = 16 * pair_tiles(a, bn);
-    if ((rc = tall ? plan.run(a, bn, X, Bop, RA_F16) : plan.run(a, bn, Bop, X, RA_F16))) return rc;
+  a.hi0 = hi[0];
+  a.lo = reinterpret_cast<uint16_t*>(base + l.lo);
+  a.ld = s.ld;
+  a.out = out; a.out_dtype = out_dtype; a.out_ld = out_rstride; a.out_bstride = out_bstride;
+  a.out_vec = aligned16(out) && (out_rstride * os) % 16 == 0 && (out_bstride * os) % 16 == 0;
+  a.status = st;
+  a.wait_limit_ns = wait_limit_ns();
+  int pairs = 0;
+  cudaError_t e = ns_max_pairs(&pairs);
+  if (e != cudaSuccess) return cuda_fail(e, "Newton-Schulz occupancy");
+  if (pairs > kPairs) pairs = kPairs;
+  static_assert(3 * kPairs * 16 <= kNsFlags, "16 flags per pair and phase");
+  // as many pairs as the widest phase has units, and enough to read G at 32 KB or so
+  // per CTA
+  long long most = ((long long)batch * rows * cols + 16383) / 16384;
+  for (int k = NS_GRAM; k <= NS_UPDATE; ++k) {
+    const Cut cut = ns_cut(a, k, pairs);
+    a.bn[k] = cut.bn;
+    a.splits[k] = cut.splits;
+    a.per[k] = ns_phase_tiles(a, k, cut.bn);
+    if (k < NS_UPDATE) a.split_base[k + 1] = a.split_base[k] + (cut.splits - 1) * batch * a.per[k];
+    const long long units = (long long)batch * a.per[k] * cut.splits;
+    if (units > 0x3fffffff) return fail(RA_ERR_INVALID_ARG, "Newton-Schulz batch too large");
+    if (units > most) most = units;
   }
-  return RA_OK;
+  if (most < pairs) pairs = (int)most;
+  const int tn = (cols + a.bn[NS_UPDATE] - 1) / a.bn[NS_UPDATE];
+  a.group_m = tn < 5 ? (kPairs + tn - 1) / tn : 16;
+  const long long xb = (long long)rows * s.ld, gb = (long long)s.m * s.ldm;
+  void *A = base + l.a, *B = base + l.b;
+  auto xmap = [&](CUtensorMap* m, const void* p, int box_cols, int box_rows) {
+    return make_map_3d(m, p, RA_F16, cols, rows, batch, s.ld, xb, box_cols, box_rows);
+  };
+  auto gmap = [&](CUtensorMap* m, const void* p, int box_cols, int box_rows) {
+    return make_map_3d(m, p, RA_F16, s.m, s.m, batch, s.ldm, gb, box_cols, box_rows);
+  };
+  for (int i = 0; i < 2; ++i)
+    if ((rc = xmap(&a.x_k[i], hi[i], 64, 128)) || (rc = xmap(&a.x_kb[i], hi[i], 64, a.bn[NS_GRAM] / 2)) ||
+        (rc = xmap(&a.x_mn[i], hi[i], 64, 64)) || (rc = xmap(&a.hi_io[i], hi[i], 64, 32)))
+      return rc;
+  if ((rc = xmap(&a.lo_io, a.lo, 64, 32)) || (rc = gmap(&a.a_row, A, 64, 128)) ||
+      (rc = gmap(&a.a_col, A, 64, a.bn[NS_SQUARE] / 2)) || (rc = gmap(&a.a_mn, A, 64, 64)) ||
+      (rc = gmap(&a.a_io, A, 64, 32)) || (rc = gmap(&a.b_row, B, 64, 128)) ||
+      (rc = gmap(&a.b_col, B, 64, a.bn[NS_UPDATE] / 2)) || (rc = gmap(&a.b_mn, B, 64, 64)) ||
+      (rc = gmap(&a.b_io, B, 64, 32)))
+    return rc;
+  TimedLaunch tl(RA_KERNEL_PAIR_TC, static_cast<cudaStream_t>(stream));
+  e = launch_ns(a, pairs, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "Newton-Schulz launch");
 }
 
 #pragma GCC visibility pop

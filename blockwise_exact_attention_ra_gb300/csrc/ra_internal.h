@@ -231,33 +231,27 @@ struct GemmArgs {
 };
 cudaError_t launch_tc_gemm(GemmArgs& a, int num_sms, cudaStream_t st);
 
-// ------------------------------------------------------- CTA-pair products
-// C[M, N] = epilogue(sum_k A(m, k) B(n, k)) for `batch` equal problems, on pairs
-// of CTAs (tiles of 256 x 256 or 256 x 128); operands K-major or MN-major, sizes
-// of any value.  The epilogues:
+// -------------------------------------------- vocabulary cross entropy
+// C[M, N] = epilogue(sum_k A(m, k) B(n, k)) on pairs of CTAs; operands K-major or
+// MN-major, sizes of any value.  The epilogues:
 enum PairEpi {
   PAIR_STATS = 0,    // softmax statistics of each row's columns and the target's logit
   PAIR_DLOGITS = 1,  // gradient of the logits, 16-bit
   PAIR_STORE = 2,    // C, 16-bit or fp32, fp32 optionally added to what is there
-  PAIR_GRAM = 3,     // Newton-Schulz: A' = X X^T - alpha I (symmetric)
-  PAIR_SQUARE = 4,   // Newton-Schulz: B' = (b + 2 c alpha) A' + c A'^2 (symmetric)
-  PAIR_UPDATE = 5,   // Newton-Schulz: X <- (a + b alpha + c alpha^2) X + B' X
 };
 struct PairArgs {
-  // operands: K-major: boxes of 64 x 128 (A), 64 x BN/2 (B); MN-major: 64 x 64
+  // operands: K-major: boxes of 64 x 128 (A), 64 x bn/2 (B); MN-major: 64 x 64
   CUtensorMap tm_a, tm_b;
-  // outputs: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle;
-  // tm_ct: the mirror image of a symmetric product (box 32 x 64, no swizzle).
-  // PAIR_UPDATE: tm_c, tm_ct the high and low terms (boxes 32 x 32, no swizzle)
-  CUtensorMap tm_c, tm_ct;
-  int M, N, K, batch;
+  CUtensorMap tm_c;   // output: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle
+  int M, N, K;
   int a_mn, b_mn;
   int ab_bf16;
   int epi;
-  int group_m;  // tile rows taken together (see tile_at)
+  int bn;             // tile columns: 128 or 256
+  int splits;         // PAIR_STORE, fp32: K is split, split s writes plane s of C
+  int group_m;        // tile rows taken together
   int* status;
   unsigned long long wait_limit_ns;
-  // cross entropy
   const long long* targets;  // [M]
   long long ignore;          // target of rows without loss
   long long vocab;           // V
@@ -265,33 +259,13 @@ struct PairArgs {
   const float* lse;          // [M]
   const float* grad;         // [M]: gradient of each row's loss
   const float* scale;        // {2^k, 2^-k} on the device, or NULL: {1, 1}
-  float2* stats;             // [column parts][M]: (max, sum of exponentials) of BN / 2 columns
+  float2* stats;             // [column parts][M]: (max, sum of exponentials) of bn / 2 columns
   float* target_logit;       // [M]
-  // PAIR_STORE
   int c_dtype;
   int c_accumulate;          // fp32: add to C
   const float* c_add;        // 16-bit: packed fp32 [M, N] added to the product
-  // Newton-Schulz; X, A', B' are held as fp16 times powers of two
-  const float* sums;         // [batch][num_sums]: partial sums of X's squares
-  int num_sums;              // 0: alpha = sums_mul
-  float sums_mul;            // alpha = sums_mul * sum
-  float* sums_out;           // PAIR_UPDATE: [batch][16 * tiles]
-  float ns_a, ns_b, ns_c;    // coefficients
-  float ns_acc;              // factor of the accumulator
-  float ns_lin;              // PAIR_SQUARE: factor of A'
-  float ns_out;              // PAIR_GRAM: factor of alpha; PAIR_UPDATE: factor of the final result
-  const uint16_t* hi_in;     // PAIR_SQUARE: A'; PAIR_UPDATE: high terms of X ([batch][M][ld])
-  const uint16_t* lo;        // PAIR_UPDATE: low terms of X
-  long long ld;
-  void* out;                 // PAIR_UPDATE, last step: result in c_dtype
-  long long out_ld, out_bstride;
-  int out_vec;               // result rows are 16-byte aligned
 };
-// Tiles per batch entry with tiles of 256 x bn; bn is 128 or 256.
-int pair_tiles(const PairArgs& a, int bn);
-cudaError_t launch_tc_pair(const PairArgs& a, int bn, int num_sms, cudaStream_t st);
-
-// --------------------------------------------- cross entropy, small kernels
+cudaError_t launch_xent_pair(const PairArgs& a, int num_sms, cudaStream_t st);
 // loss and lse from the column parts' statistics; a target outside [0, V) that is
 // not `ignore` gives loss = NaN and RA_ERR_INVALID_ARG in *status.
 cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,
@@ -300,18 +274,57 @@ cudaError_t launch_xent_finish(const float2* stats, int parts, const float* targ
 // scale = {2^k, 2^-k} with 2^k max |grad| in [2^13, 2^14) over the rows with a loss.
 cudaError_t launch_xent_scale(const float* grad, const long long* targets, long long ignore, long long V, long long T,
                               float* scale, cudaStream_t st);
+// out (dtype) <- the sum of `planes` fp32 planes of n elements each (n a multiple of 8)
+cudaError_t launch_sum_planes(const float* planes, int count, long long n, void* out, int dtype, cudaStream_t st);
 
-// --------------------------------------------- Newton-Schulz, small kernels
+// -------------------------------------------- Newton-Schulz
 struct NsInput {
   const void* g;
   int dtype, batch, rows, cols;
   long long ld, bstride;
+  int vec;  // rows start on 16-byte boundaries
 };
-constexpr int kNsParts = 256;  // partial sums per batch entry
-// parts[batch][kNsParts][3]: sums of squares in three ranges of magnitude.
-cudaError_t launch_ns_sumsq(const NsInput& in, float* parts, cudaStream_t st);
-// hi + lo = mul * G / (|G|_F + eps) as two fp16 terms, rows of ld elements.
-cudaError_t launch_ns_scale(const NsInput& in, const float* parts, float mul, float eps, uint16_t* hi, uint16_t* lo,
-                            long long ld, cudaStream_t st);
+constexpr int kNsParts = 304;     // partial sums of G's squares per batch entry
+constexpr int kNsFlags = 3 * 16 * 128;  // 16 per unit that holds a split, three phases
+constexpr int kNsWords = 64 + kNsFlags;  // mark of a launch that gave up, flags; counts per matrix follow
+enum NsPhase { NS_GRAM = 0, NS_SQUARE = 1, NS_UPDATE = 2 };
+struct NsArgs {
+  // operands of X's two buffers: K-major boxes for A and for B, MN-major boxes
+  CUtensorMap x_k[2], x_kb[2], x_mn[2];
+  // A' and B' as A (boxes of 64 x 128), as B (64 x bn/2) and MN-major (64 x 64)
+  CUtensorMap a_row, a_col, a_mn, b_row, b_col, b_mn;
+  // what the epilogues read and write: boxes of 64 x 32, 128-byte swizzle
+  CUtensorMap hi_io[2], lo_io, a_io, b_io;
+  NsInput in;
+  int batch, rows, cols, m, tall;  // m: the smaller side; tall: rows > cols
+  int steps;
+  int bn[3];      // tile columns of each phase
+  int per[3];     // tiles per matrix of each phase
+  int splits[3];  // parts of K of each phase; above 1 only with a pair for every part
+  int split_base[3];  // units that hold a split in the phases before
+  int group_m;    // NS_UPDATE: tile rows taken together
+  float ca, cb, cc;                                            // coefficients
+  float sx, sa, eps, alpha_mul;                                // scales of X and A'; alpha = alpha_mul sum x^2
+  float gram_acc, square_acc, square_lin, update_acc, out_mul;  // factors of accumulators, of A', of the result
+  float* parts;
+  int num_parts;
+  float* sums[2];  // [batch][16 per tile], read by a step and written for the next one
+  long long sums_ld;
+  uint16_t *hi0, *lo;
+  long long ld;    // X's padded rows
+  void* out;
+  int out_dtype, out_vec;
+  long long out_ld, out_bstride;
+  unsigned int* words;  // zeroed at first: the mark of a launch that gave up, the flags, the counts
+  unsigned int* counts; // per matrix: warps that have scaled it and halves of tiles written
+  unsigned int* flags;  // per warp of a split: the last phase whose partial sums it has written
+  float* partials;      // sums of the splits but the first, [unit][CTA][warp][128 columns][32 rows]
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+// Pairs of CTAs that can run at the same time on the current device.
+cudaError_t ns_max_pairs(int* pairs);
+int ns_phase_tiles(const NsArgs& a, int kind, int bn);  // per batch entry
+cudaError_t launch_ns(NsArgs& a, int pairs, cudaStream_t st);
 
 }  // namespace ra

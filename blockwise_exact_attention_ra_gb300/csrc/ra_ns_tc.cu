@@ -1,0 +1,700 @@
+// Newton-Schulz orthogonalisation of a batch of matrices: one launch for the norm and
+// one persistent launch for everything else, on CTA pairs (ra_pair.cuh).
+//
+// The iteration is a chain of products, 3 per step, each of which needs all of the one
+// before:
+//   GRAM     A' = X X^T - alpha I      (X^T X where rows > cols), alpha = |X|_F^2 / m
+//   SQUARE   B' = (b + 2 c alpha) A' + c A'^2
+//   UPDATE   X <- (a + b alpha + c alpha^2) X + B' X   (X B')
+// which is a X + (b A + c A^2) X with A = A' + alpha I.  The products' operands are fp16
+// (times powers of two); taking alpha I out keeps the rounding of the Gram matrix's
+// large common diagonal out of the result, and X is carried as two fp16 terms (hi the
+// operand, hi + lo the state).  A' and B' are symmetric: blocks left of the diagonal are
+// neither computed nor held, the products read their mirror images (ra_pair.cuh).
+//
+// One launch because the chain of a small matrix is all latency: as launches of their
+// own the products of a 128 x 512 matrix took 7 us each.  All tiles of the chain, step by
+// step and phase by phase, form one sequence that the pairs take in turn.  A tile waits
+// until all tiles of its matrix's phase before are written (a count per matrix), so that
+// with several matrices one's phase ends while another's runs and no pair idles at the
+// phases' ends.  Tiles wait only for earlier ones in the sequence, and the launch is
+// cooperative, so all pairs are there.  Every wait is bounded: a CTA that gives up marks
+// the launch's word, records RA_ERR_TIMEOUT, and the others leave when they see the mark.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math.h>
+
+#include <mutex>
+
+#include "ra_pair.cuh"
+
+namespace ra {
+namespace {
+
+// 5 stages of 32 KB; 8 KB of staging per epilogue warp (two tiles of 32 rows x 64
+// columns).  Extra barriers: staging filled [8].
+using S = PairSmem<5, 8192, 8>;
+
+__device__ __forceinline__ float load_as_f32(const void* p, int dtype, long long i) {
+  if (dtype == RA_F32) return static_cast<const float*>(p)[i];
+  if (dtype == RA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+  return __half2float(static_cast<const __half*>(p)[i]);
+}
+
+// Eight consecutive elements of a row (fewer at its end; the rest read as zero).
+constexpr int kNsBatch = 4;  // groups of eight in flight per thread
+__device__ __forceinline__ void load8(const NsInput& in, long long off, int left, float* v) {
+  if (in.vec && left >= 8) {
+    if (in.dtype == RA_F32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(in.g) + off);
+      const float4 x = p[0], y = p[1];
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    } else {
+      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.g) + off);
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float2 f;
+        if (in.dtype == RA_BF16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
+        else f = unpack_half2(w[j]);
+        v[2 * j] = f.x;
+        v[2 * j + 1] = f.y;
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = j < left ? load_as_f32(in.g, in.dtype, off + j) : 0.f;
+}
+
+// Squares are summed in three accumulators by magnitude, the large values scaled
+// down and the small ones up, so that none of them overflows or vanishes (J. L.
+// Blue, "A Portable Fortran Program to Find the Euclidean Norm of a Vector", 1978).
+constexpr float kBig = 1099511627776.f, kSmall = 1.f / 1099511627776.f;         // 2^40, 2^-40
+constexpr float kDown = 8.271806125530277e-25f, kUp = 1.2089258196146292e24f;  // 2^-80, 2^80
+
+// Bound by reading G once.  Also readies the chain's words.
+__global__ void __launch_bounds__(512) ns_sumsq_kernel(const __grid_constant__ NsInput in, float* parts,
+                                                       unsigned int* words, int num_words) {
+  __shared__ float part[3][16];
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < num_words; i += 512) words[i] = 0u;
+  const unsigned chunks = (in.cols + 7) / 8;
+  const unsigned total = in.rows * chunks;  // at most 2^29: sides are at most 2^16
+  float s[3] = {0.f, 0.f, 0.f};
+  for (unsigned i = blockIdx.x * 512 + threadIdx.x; i < total; i += gridDim.x * 512 * kNsBatch) {
+    float v[kNsBatch][8];
+#pragma unroll
+    for (int k = 0; k < kNsBatch; ++k) {
+      const unsigned j = i + k * gridDim.x * 512, r = j / chunks, c = (j - r * chunks) * 8;
+      load8(in, blockIdx.y * in.bstride + r * in.ld + c, j < total ? in.cols - (int)c : 0, v[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kNsBatch; ++k) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float x = fabsf(v[k][j]);
+        const float up = x > kBig ? x * kDown : 0.f, down = x < kSmall ? x * kUp : 0.f;
+        const float mid = (x > kBig || x < kSmall) ? 0.f : x;  // NaN stays here
+        s[0] = fmaf(mid, mid, s[0]);
+        s[1] = fmaf(up, up, s[1]);
+        s[2] = fmaf(down, down, s[2]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    s[k] = warp_sum(s[k]);
+    if ((threadIdx.x & 31) == 0) part[k][threadIdx.x >> 5] = s[k];
+  }
+  __syncthreads();
+  if (threadIdx.x < 3) {
+    float x = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) x += part[threadIdx.x][j];
+    parts[((long long)blockIdx.y * kNsParts + blockIdx.x) * 3 + threadIdx.x] = x;
+  }
+}
+
+// mul / (|G|_F + eps) as f 2^e0 2^e1 (in range for every norm), by one warp; the parts
+// are added in a fixed order, in 64 bits.
+__device__ __forceinline__ void ns_factor(const float* parts, int num_parts, float mul, float eps, float* f) {
+  double s = 0.0;
+  for (int i = lane_id(); i < num_parts; i += 32) {
+    const float* p = parts + 3 * i;
+    s += (double)p[0] + (double)p[1] * 1.4615016373309029e48 + (double)p[2] * 6.8422776578360209e-49;  // 2^160, 2^-160
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  const double norm = sqrt(s) + (double)eps;
+  const double inv = norm > 0.0 ? (double)mul / norm : 0.0;
+  int e = 0;
+  f[2] = (float)frexp(inv, &e);
+  f[0] = ldexpf(1.f, e / 2);
+  f[1] = ldexpf(1.f, e - e / 2);
+}
+
+// sum of n floats by one warp, in an order that depends on n alone
+__device__ __forceinline__ float warp_total(const float* p, int n) {
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int i = lane_id(); i < n; i += 256) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] += i + 32 * j < n ? __ldcg(p + i + 32 * j) : 0.f;
+  }
+  return warp_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
+}
+
+// Tiles of a symmetric product: only those that reach the diagonal or lie right of it.
+__device__ __forceinline__ Tile tile_sym(int t, int tn, int bn) {
+  int m = 0;
+  for (int left = tn; t >= left; ++m) {
+    t -= left;
+    left -= 256 / bn;
+  }
+  return Tile{m, m * (256 / bn) + t};
+}
+
+// One phase as every role sees it.  Unit u of a phase is split u / tiles of tile
+// u % tiles, which takes an even share of the k-slabs; only with at least as many pairs
+// as units is K split.
+struct Phase {
+  int M, N, bn, tm, tn, per, tiles, sym, k_slabs, splits, units;
+  Operand A, B;
+  __device__ __forceinline__ int k_at(int split) const { return k_slabs * split / splits; }
+};
+__device__ __forceinline__ Phase phase_at(const NsArgs& a, int step, int kind) {
+  Phase f;
+  f.bn = a.bn[kind];
+  f.splits = a.splits[kind];
+  f.sym = kind != NS_UPDATE;
+  const int x = step & 1;
+  int K = a.m;
+  if (kind == NS_UPDATE) {
+    f.M = a.rows; f.N = a.cols;
+    if (a.tall) {
+      f.A = Operand{&a.x_k[x], nullptr, 0};
+      f.B = Operand{&a.b_col, &a.b_mn, 2};
+    } else {
+      f.A = Operand{&a.b_row, &a.b_mn, 2};
+      f.B = Operand{nullptr, &a.x_mn[x], 1};
+    }
+  } else {
+    f.M = f.N = a.m;
+    if (kind == NS_SQUARE) {
+      f.A = Operand{&a.a_row, &a.a_mn, 2};
+      f.B = Operand{&a.a_col, &a.a_mn, 2};
+    } else if (a.tall) {
+      K = a.rows;
+      f.A = f.B = Operand{nullptr, &a.x_mn[x], 1};
+    } else {
+      K = a.cols;
+      f.A = Operand{&a.x_k[x], nullptr, 0};
+      f.B = Operand{&a.x_kb[x], nullptr, 0};
+    }
+  }
+  f.k_slabs = (K + 63) / 64;
+  f.tm = (f.M + 255) / 256;
+  f.tn = (f.N + f.bn - 1) / f.bn;
+  f.per = a.per[kind];
+  f.tiles = f.per * a.batch;
+  f.units = f.tiles * f.splits;
+  return f;
+}
+// The first of a phase's units that a pair takes, `base` units of the sequence before it.
+__device__ __forceinline__ int first_unit(int base, int cluster, int clusters) {
+  const int u = cluster - base;
+  return u < 0 ? u + clusters : u;
+}
+// Tiles of one matrix that are written before a phase begins.
+__device__ __forceinline__ unsigned ready_tiles(const NsArgs& a, int step, int kind) {
+  const unsigned g = a.per[NS_GRAM], q = a.per[NS_SQUARE], u = a.per[NS_UPDATE];
+  return step * (g + q + u) + (kind > NS_GRAM ? g : 0) + (kind > NS_SQUARE ? q : 0);
+}
+__device__ __forceinline__ Tile phase_tile(const NsArgs& a, const Phase& f, int t) {
+  return f.sym ? tile_sym(t, f.tn, f.bn) : tile_grouped(t, f.tm, f.tn, a.group_m);
+}
+
+// The result's 64 columns from cc on of one row.
+__device__ __forceinline__ void write_out(const NsArgs& a, int b, int row, int cc, int N, float* v) {
+  if (cc >= N) return;
+  const long long o = b * a.out_bstride + (long long)row * a.out_ld + cc;
+#pragma unroll
+  for (int j = 0; j < 64; ++j) v[j] *= a.out_mul;
+  if (a.out_vec && cc + 64 <= N) {
+    if (a.out_dtype == RA_F32) {
+      float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    } else {
+      uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o);
+      const int bf = a.out_dtype == RA_BF16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        q[j] = make_uint4(pack_pair(v[8 * j], v[8 * j + 1], bf), pack_pair(v[8 * j + 2], v[8 * j + 3], bf),
+                          pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 64; ++j) {
+    if (cc + j < N) {
+      if (a.out_dtype == RA_F32) static_cast<float*>(a.out)[o + j] = v[j];
+      else if (a.out_dtype == RA_BF16) static_cast<__nv_bfloat16*>(a.out)[o + j] = __float2bfloat16_rn(v[j]);
+      else static_cast<__half*>(a.out)[o + j] = __float2half_rn(v[j]);
+    }
+  }
+}
+
+// CTAs that scale batch entry b: the entries are shared out in teams, entry b to the CTAs
+// c = b mod teams.
+__device__ __forceinline__ unsigned ns_teams(const NsArgs& a) { return min((unsigned)a.batch, gridDim.x); }
+__device__ __forceinline__ unsigned ns_team_size(const NsArgs& a, unsigned b) {
+  const unsigned teams = ns_teams(a), team = b % teams;
+  return (gridDim.x - team + teams - 1) / teams;
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+    ns_chain_kernel(const __grid_constant__ NsArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ unsigned int s_passed;    // this CTA's units whose matrix is ready for them
+  // epilogue warps that have finished a unit, for four units in flight: a warp is never
+  // three units ahead of another, since a unit's accumulator is the one two units before
+  __shared__ unsigned int s_finished[4];
+  if (threadIdx.x == 0) s_passed = s_finished[0] = s_finished[1] = s_finished[2] = s_finished[3] = 0u;
+  Pair<S> p;
+  p.begin(smem_raw, a.status, a.wait_limit_ns, [&] {
+    for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(p.extra(w), 1);
+  });
+  const uint32_t warp = warp_id(), lane = lane_id();
+  const int clusters = gridDim.x / 2, cluster = blockIdx.x / 2;
+  // a wait on another CTA's word goes on: false once the limit is past or some CTA has
+  // given up
+  auto still = [&](uint64_t t0, uint32_t it) {
+    const bool gone = *reinterpret_cast<volatile unsigned*>(a.words) != 0u;
+    if (!gone && !*p.abort && globaltimer_ns() - t0 <= p.lim && it <= 0x7fffffffu) return true;
+    *p.abort = 1;
+    report(p.status, RA_ERR_TIMEOUT);
+    return false;
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        tma_prefetch_desc(&a.x_k[i]);
+        tma_prefetch_desc(&a.x_kb[i]);
+        tma_prefetch_desc(&a.x_mn[i]);
+        tma_prefetch_desc(&a.hi_io[i]);
+      }
+      for (const CUtensorMap* m : {&a.a_row, &a.a_col, &a.a_mn, &a.b_row, &a.b_col, &a.b_mn, &a.lo_io, &a.a_io, &a.b_io})
+        tma_prefetch_desc(m);
+    }
+    // ------------------------------------------------------------ producer
+    // also waits for the units' matrices and tells the epilogue warps
+    if (lane == 0) {
+      uint32_t cnt = 0, passed = 0;
+      unsigned seen = 0;
+      int seen_b = -1, base = 0;
+      bool ok = true;
+      for (int step = 0; step < a.steps && ok; ++step) {
+        for (int kind = NS_GRAM; kind <= NS_UPDATE && ok; ++kind) {
+          const Phase f = phase_at(a, step, kind);
+          for (int u = first_unit(base, cluster, clusters); u < f.units && ok; u += clusters) {
+            const int s = u / f.tiles, t = u - s * f.tiles, b = t / f.per;
+            const unsigned need = kPairEpiWarps * ns_team_size(a, b) + 2u * ready_tiles(a, step, kind);
+            if (b != seen_b || seen < need) {  // counts only grow: often the last look still holds
+              const unsigned* count = a.counts + b;
+              const uint64_t t0 = globaltimer_ns();
+              for (uint32_t it = 1;; ++it) {
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(seen) : "l"(count) : "memory");
+                if (seen >= need) break;
+                if ((it & 63u) == 0 && !still(t0, it)) { ok = false; break; }
+              }
+              if (!ok) break;
+              seen_b = b;
+              asm volatile("fence.proxy.async;" ::: "memory");
+            }
+            ++passed;
+            asm volatile("st.release.cta.shared.u32 [%0], %1;" ::"r"(smem_u32(&s_passed)), "r"(passed) : "memory");
+            const Tile tile = phase_tile(a, f, t - b * f.per);
+            ok = p.produce(cnt, f.A, f.B, f.bn, tile.m * 256, tile.n * f.bn, b, f.k_at(s), f.k_at(s + 1));
+          }
+          base = (base + f.units) % clusters;
+        }
+      }
+      if (!ok) atomicExch(a.words, 1u);
+      if (*p.abort) p.producer_drain(cnt);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    uint32_t cnt = 0, lt = 0;
+    int base = 0;
+    bool ok = true;
+    for (int step = 0; step < a.steps && ok; ++step) {
+      for (int kind = NS_GRAM; kind <= NS_UPDATE && ok; ++kind) {
+        const Phase f = phase_at(a, step, kind);
+        for (int u = first_unit(base, cluster, clusters); u < f.units && ok; u += clusters) {
+          const int s = u / f.tiles, t = u - s * f.tiles;
+          const Tile tile = phase_tile(a, f, t % f.per);
+          ok = p.rank == 0 ? p.multiply(cnt, lt, 0, f.A, f.B, f.bn, tile.m * 256, tile.n * f.bn, f.k_at(s), f.k_at(s + 1))
+                           : p.forward(lt);
+        }
+        base = (base + f.units) % clusters;
+      }
+    }
+    if (p.rank == 0) p.multiply_drain();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int w = (int)warp - 2;
+    const uint32_t quarter = warp & 3;  // TMEM lanes 32 * quarter .. + 31
+    const int half = w >> 2;            // columns [half * bn / 2, + bn / 2)
+    const uint32_t stage = p.sbase + S::kOut + w * 8192;
+    uint8_t* const stage_p = p.smem + S::kOut + w * 8192;
+    const uint32_t FILLED = p.extra(w);
+    uint32_t loads = 0, fills = 0, lt = 0;  // staging loads issued and received
+    // a 16-byte piece of the staging rows of 128 bytes, 128-byte swizzle; buf 0 or 1
+    auto piece = [&](int buf, int j) {
+      return reinterpret_cast<uint4*>(stage_p + buf * 4096 + lane * 128 + ((j ^ (lane & 7)) << 4));
+    };
+    auto count = [&](int b) {
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(a.counts + b) : "memory");
+    };
+    // What lane 0 wrote for the CTA's unit-th unit, one of matrix b, is done (copies and
+    // partial sums); the last of the CTA's epilogue warps counts the unit.
+    auto finish = [&](uint32_t unit, int b) {
+      if (lane == 0) {
+        bulk_wait_all();
+        asm volatile("fence.proxy.async;" ::: "memory");
+        const uint32_t slot = smem_u32(&s_finished[unit & 3]);
+        unsigned before;
+        asm volatile("atom.acq_rel.cta.shared.add.u32 %0, [%1], 1;" : "=r"(before) : "r"(slot) : "memory");
+        if (before == kPairEpiWarps - 1) {
+          asm volatile("st.relaxed.cta.shared.u32 [%0], 0;" ::"r"(slot) : "memory");
+          count(b);
+        }
+      }
+      __syncwarp();
+    };
+    // ---- phase 0: X = sx G / (|G|_F + eps) as two fp16 terms
+    {
+      const unsigned chunks = (a.in.cols + 7) / 8, per = a.in.rows * chunks;
+      const unsigned teams = ns_teams(a), team = blockIdx.x % teams;
+      const unsigned id = (blockIdx.x / teams) * 256 + (threadIdx.x - 64), all = ns_team_size(a, team) * 256;
+      for (int b = team; b < a.batch; b += teams) {
+        float f[3];
+        ns_factor(a.parts + (long long)b * kNsParts * 3, a.num_parts, a.sx, a.eps, f);
+        for (unsigned i = id; i < per; i += all * kNsBatch) {
+          float v[kNsBatch][8];
+#pragma unroll
+          for (int k = 0; k < kNsBatch; ++k) {
+            const unsigned q = i + k * all, r = q / chunks, c = (q - r * chunks) * 8;
+            load8(a.in, b * a.in.bstride + r * a.in.ld + c, q < per ? a.in.cols - (int)c : 0, v[k]);
+          }
+#pragma unroll
+          for (int k = 0; k < kNsBatch; ++k) {
+            const unsigned q = i + k * all, r = q / chunks, c = (q - r * chunks) * 8;
+            if (q >= per) break;
+            uint32_t h[4], l[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float x = ((v[k][2 * j] * f[0]) * f[1]) * f[2], y = ((v[k][2 * j + 1] * f[0]) * f[1]) * f[2];
+              h[j] = pack_half2(x, y);
+              const float2 g = unpack_half2(h[j]);
+              l[j] = pack_half2(x - g.x, y - g.y);
+            }
+            // rows are padded to a multiple of 64 elements: whole 16-byte pieces
+            const long long o = ((long long)b * a.rows + r) * a.ld + c;
+            *reinterpret_cast<uint4*>(a.hi0 + o) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(a.lo + o) = make_uint4(l[0], l[1], l[2], l[3]);
+          }
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) count(b);
+      }
+    }
+    bool ok = true;
+    uint32_t units = 0;  // units this CTA has begun
+    int base = 0;
+    for (int step = 0; step < a.steps && ok; ++step) {
+      const float* sums = a.sums[step & 1];
+      float* sums_out = a.sums[(step + 1) & 1];
+      const bool last = step == a.steps - 1;
+      for (int kind = NS_GRAM; kind <= NS_UPDATE && ok; ++kind) {
+        const Phase f = phase_at(a, step, kind);
+        const int cols = f.bn / 2;
+        for (int u = first_unit(base, cluster, clusters); u < f.units; u += clusters, ++lt) {
+          const uint32_t acc = lt & 1;
+          const int split = u / f.tiles, t = u - split * f.tiles, b = t / f.per;
+          // the matrix is ready once the producer says so
+          ++units;
+          if (lane == 0) {
+            const uint64_t t0 = globaltimer_ns();
+            for (uint32_t it = 1;; ++it) {
+              unsigned x;
+              asm volatile("ld.acquire.cta.shared.u32 %0, [%1];" : "=r"(x) : "r"(smem_u32(&s_passed)) : "memory");
+              if (x >= units) break;
+              if ((it & 255u) == 0 && !still(t0, it)) { ok = false; break; }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          if (!ok) break;
+          const uint32_t src = p.tmem + acc * 256 + half * cols + ((quarter * 32) << 16);
+          // the sums of splits 1, 2, ... wait in memory for the CTA that has split 0: a
+          // column of 32 rows is one line
+          const long long mine = ((a.split_base[kind] + (long long)t * (f.splits - 1)) * 2 + p.rank) * kPairEpiWarps + w;
+          auto partial = [&](int s) { return a.partials + (mine + (s - 1) * 2 * kPairEpiWarps) * (128 * 32) + lane; };
+          auto flag = [&](int s) { return a.flags + mine + (s - 1) * 2 * kPairEpiWarps; };
+          const unsigned now = step * 3 + kind + 1;
+          if (split) {
+            if (!p.wait(p.acc_full(acc), (lt >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            float* q = partial(split);
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+              float v[32];
+              tmem_load32(src + c, v);
+              if (c == cols - 32) p.release(acc);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) __stcg(q + (c + j) * 32, v[j]);
+            }
+            __syncwarp();
+            if (lane == 0)
+              asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flag(split)), "r"(now) : "memory");
+            continue;  // the tile is counted by the CTA that has split 0
+          }
+          const Tile tile = phase_tile(a, f, t - b * f.per);
+          const int row0 = tile.m * 256 + (int)p.rank * 128 + (int)quarter * 32;
+          const int row = row0 + (int)lane;
+          const int col0 = tile.n * f.bn + half * cols;
+          // GRAM writes through staging buffer 0; SQUARE reads A' and UPDATE the two
+          // terms of X into the staging buffers, change them in place and write back
+          auto prefetch = [&](int c) {
+            if (lane == 0) {
+              bulk_wait_read();
+              if (kind != NS_GRAM) {
+                mbar_arrive_expect_tx(FILLED, kind == NS_UPDATE ? 8192 : 4096);
+                if (kind == NS_UPDATE) {
+                  tma_load_3d(stage, &a.hi_io[step & 1], FILLED, col0 + c, row0, b);
+                  tma_load_3d(stage + 4096, &a.lo_io, FILLED, col0 + c, row0, b);
+                } else {
+                  tma_load_3d(stage, &a.a_io, FILLED, col0 + c, row0, b);
+                }
+              }
+            }
+            __syncwarp();
+            if (kind != NS_GRAM) ++loads;
+          };
+          prefetch(0);
+          // alpha: the mean of the Gram matrix's diagonal, 1 / m at first
+          const float alpha =
+              step ? warp_total(sums + (long long)b * a.sums_ld, 16 * a.per[NS_UPDATE]) * a.alpha_mul : 1.f / (float)a.m;
+          float sq = 0.f;  // UPDATE: squares of this warp's part of the new X
+          const float lin = (a.cb + 2.f * a.cc * alpha) * a.square_lin;
+          const float own = a.ca + alpha * (a.cb + a.cc * alpha);
+          const float shift = alpha * a.sa;
+          if (!p.wait(p.acc_full(acc), (lt >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          for (int s = 1; s < f.splits && ok; ++s) {
+            if (lane == 0) {
+              const uint64_t t0 = globaltimer_ns();
+              for (uint32_t it = 1;; ++it) {
+                unsigned x;
+                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(flag(s)) : "memory");
+                if (x >= now) break;
+                if ((it & 63u) == 0 && !still(t0, it)) { ok = false; break; }
+              }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          }
+          if (!ok) break;
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 64) {
+            if (c) prefetch(c);
+            float v[64];
+            {
+              uint32_t r0[32], r1[32];
+              RA_TMEM_LD32(src + c, r0);
+              RA_TMEM_LD32(src + c + 32, r1);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                v[j] = __uint_as_float(r0[j]);
+                v[32 + j] = __uint_as_float(r1[j]);
+              }
+            }
+            if (c == cols - 64) p.release(acc);
+            for (int s = 1; s < f.splits; ++s) {
+              const float* q = partial(s) + c * 32;
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] += __ldcg(q + j * 32);
+            }
+            if (kind != NS_GRAM) {
+              if (!p.wait(FILLED, fills & 1)) { ok = false; break; }
+              ++fills;
+            }
+            const bool inside = row0 < f.M && col0 + c < f.N;
+            if (kind == NS_GRAM) {
+              const int diag = row - col0 - c;  // this row's column of the diagonal
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] = fmaf(v[j], a.gram_acc, j == diag ? -shift : 0.f);
+            } else if (kind == NS_SQUARE) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint4 q = *piece(0, j);
+                const uint32_t qq[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 g = unpack_half2(qq[i]);
+                  v[8 * j + 2 * i] = fmaf(v[8 * j + 2 * i], a.square_acc, lin * g.x);
+                  v[8 * j + 2 * i + 1] = fmaf(v[8 * j + 2 * i + 1], a.square_acc, lin * g.y);
+                }
+              }
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const uint4 q = *piece(0, j), r = *piece(1, j);
+                const uint32_t qq[4] = {q.x, q.y, q.z, q.w}, rr[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 g = unpack_half2(qq[i]), e = unpack_half2(rr[i]);
+                  v[8 * j + 2 * i] = fmaf(v[8 * j + 2 * i], a.update_acc, own * (g.x + e.x));
+                  v[8 * j + 2 * i + 1] = fmaf(v[8 * j + 2 * i + 1], a.update_acc, own * (g.y + e.y));
+                }
+              }
+            }
+            if (kind == NS_UPDATE && last) {
+              if (row < f.M) write_out(a, b, row, col0 + c, f.N, v);
+              fence_proxy_async_smem();
+              __syncwarp();
+              continue;
+            }
+            // what lies past the edges came in as zeros on both sides
+            if (kind == NS_UPDATE) {
+              float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int j = 0; j < 64; ++j) s4[j & 3] = fmaf(v[j], v[j], s4[j & 3]);
+              sq += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint32_t hi[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) hi[i] = pack_half2(v[8 * j + 2 * i], v[8 * j + 2 * i + 1]);
+              *piece(0, j) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+              if (kind == NS_UPDATE) {
+                uint32_t lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 g = unpack_half2(hi[i]);
+                  lo[i] = pack_half2(v[8 * j + 2 * i] - g.x, v[8 * j + 2 * i + 1] - g.y);
+                }
+                *piece(1, j) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && inside) {
+              if (kind == NS_UPDATE) {
+                tma_store_3d(&a.hi_io[(step + 1) & 1], stage, col0 + c, row0, b);
+                tma_store_3d(&a.lo_io, stage + 4096, col0 + c, row0, b);
+              } else {
+                tma_store_3d(kind == NS_GRAM ? &a.a_io : &a.b_io, stage, col0 + c, row0, b);
+              }
+              bulk_commit();
+            }
+          }
+          if (!ok) break;
+          if (kind == NS_UPDATE && !last) {
+            sq = warp_sum(sq);
+            if (lane == 0)
+              sums_out[(long long)b * a.sums_ld + ((t - b * f.per) * 2 + (int)p.rank) * kPairEpiWarps + w] = sq;
+          }
+          finish(units, b);
+        }
+        base = (base + f.units) % clusters;
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    // after a wait gave up: a staging load in flight lands before the CTA exits
+    if (loads != fills) (void)mbar_wait(FILLED, fills & 1, p.abort, nullptr, 100000000ull);
+  }
+  p.end();
+}
+
+int ns_sumsq_blocks(const NsInput& in) {
+  const long long chunks = (long long)in.rows * ((in.cols + 7) / 8);
+  const long long n = (chunks + 1023) / 1024;
+  return (int)(n < 1 ? 1 : n < kNsParts ? n : kNsParts);
+}
+
+// Pairs of CTAs that run at the same time on the current device (0: unknown yet).
+constexpr int kMaxDevices = 64;
+std::mutex g_mu;
+int g_pairs[kMaxDevices] = {};
+
+}  // namespace
+
+cudaError_t ns_max_pairs(int* pairs) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_pairs[dev]) {
+    e = cudaFuncSetAttribute(ns_chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
+    if (e != cudaSuccess) return e;
+    int sms = 0;
+    if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(sms / 2 * 2);
+    cfg.blockDim = dim3(kPairThreads);
+    cfg.dynamicSmemBytes = S::kAlloc;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&n, ns_chain_kernel, &cfg)) != cudaSuccess) return e;
+    if (n < 1) return cudaErrorLaunchOutOfResources;
+    g_pairs[dev] = n < sms / 2 ? n : sms / 2;
+  }
+  *pairs = g_pairs[dev];
+  return cudaSuccess;
+}
+
+int ns_phase_tiles(const NsArgs& a, int kind, int bn) {
+  const int M = kind == NS_UPDATE ? a.rows : a.m, N = kind == NS_UPDATE ? a.cols : a.m;
+  const int tm = (M + 255) / 256, tn = (N + bn - 1) / bn;
+  if (kind == NS_UPDATE) return tm * tn;
+  int n = 0;
+  for (int m = 0; m < tm; ++m) n += tn - m * (256 / bn) > 0 ? tn - m * (256 / bn) : 0;
+  return n;
+}
+
+cudaError_t launch_ns(NsArgs& a, int pairs, cudaStream_t st) {
+  a.num_parts = ns_sumsq_blocks(a.in);
+  ns_sumsq_kernel<<<dim3(a.num_parts, a.batch), 512, 0, st>>>(a.in, a.parts, a.words, kNsWords + a.batch);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  count_launch();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * pairs);
+  cfg.blockDim = dim3(kPairThreads);
+  cfg.dynamicSmemBytes = S::kAlloc;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, ns_chain_kernel, (const NsArgs&)a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return cudaSuccess;
+}
+
+}  // namespace ra
