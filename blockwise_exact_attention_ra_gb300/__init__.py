@@ -151,6 +151,17 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+# The current stream's handle without the Stream object around it (3 us a call), where
+# this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _handle(stream, device):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
+
+
 def _dt(t):
     try:
         return _DTYPES[t.dtype]
@@ -458,7 +469,7 @@ def _xent_fwd(sizes, x, w, targets, loss, lse, workspace, ignore_index, stream):
     _on_device(x, w, targets, loss, lse, workspace)
     _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
                               loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-                              _stream(stream)))
+                              _handle(stream, x.device)))
 
 
 def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index, stream):
@@ -468,7 +479,7 @@ def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, ignore
     _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
     _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
                               lse.data_ptr(), dloss.data_ptr(), block, dx.data_ptr(), _dt(dx), dw.data_ptr(), _dt(dw),
-                              workspace.data_ptr(), _nbytes(workspace), _stream(stream)))
+                              workspace.data_ptr(), _nbytes(workspace), _handle(stream, x.device)))
 
 
 def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
@@ -542,7 +553,7 @@ def _newton_schulz(layout, g, out, out_strides, workspace, steps, coeffs, eps, s
     _on_device(g, out, workspace)
     _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), *layout, _Float3(*coeffs), int(steps), float(eps),
                                    out.data_ptr(), _dt(out), *out_strides, workspace.data_ptr(), _nbytes(workspace),
-                                   _stream(stream)))
+                                   _handle(stream, g.device)))
 
 
 def ra_newton_schulz(g, out, workspace, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):

@@ -1249,9 +1249,9 @@ namespace {
 // How one product is cut up.  A CTA pair works on a tile of 256 rows by 256 or 128
 // columns; GB300 has 76 pairs, and the cut is made for that number whatever the device,
 // so that workspaces and results do not depend on it.
-//   - Where the wide tiles fill less than half the pairs and K may be split (the result
-//     is a sum in fp32 planes), K is split over the idle pairs, 8 k-slabs (512) or more
-//     per split.
+//   - Where the result may be a sum of fp32 planes and wide tiles fill less than half the
+//     pairs, K is split over the idle ones.  A k-slab (64) of a wide tile takes about
+//     0.33 us; planes cost another launch that adds them up, 5 us in all.
 //   - A narrow tile takes as long as a wide one (measured: 0.98 against 1.86 PFLOP/s on
 //     8192 x 131072 x 2048), only its epilogue is shorter: it is taken where even the
 //     narrow tiles find a pair each.
@@ -1262,14 +1262,15 @@ struct Cut {
 Cut cut_product(long long M, long long N, long long K, bool may_split) {
   const long long tm = (M + 255) / 256, wide = tm * ((N + 255) / 256), narrow = tm * ((N + 127) / 128);
   if (may_split && wide * 2 <= kPairs) {
-    const long long by_k = (K + 511) / 512, by_pairs = kPairs / wide;
+    const long long by_k = (K + 255) / 256, by_pairs = kPairs / wide;
     const int splits = (int)(by_k < by_pairs ? by_k : by_pairs);
-    if (splits > 1) return Cut{256, splits};
+    const double whole = 0.33 * (double)((K + 63) / 64);
+    if (splits > 1 && whole / splits + 5.0 < whole) return Cut{256, splits};
   }
   return Cut{narrow <= kPairs ? 128 : 256, 1};
 }
 
-// One CTA-pair product of the cross entropy: fills in the operands' maps.
+// CTA-pair products of the cross entropy, one or two in a launch.
 struct PairPlan {
   cudaStream_t st;
   int* status;
@@ -1278,21 +1279,24 @@ struct PairPlan {
     const void* p;
     long long rows, cols, ld;
   };
-  // a: everything but the operands' maps and the fields set here
-  int run(PairArgs& a, Cut cut, const Operand& A, const Operand& B, int dtype) const {
+  // q: M, N, K, the majornesses and the output; sets the operands' maps and the cut
+  int problem(PairProblem& q, Cut cut, const Operand& A, const Operand& B, int dtype) const {
     int rc;
-    if ((rc = make_map_3d(&a.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, a.a_mn ? 64 : 128)) ||
-        (rc = make_map_3d(&a.tm_b, B.p, dtype, B.cols, B.rows, 1, B.ld, 0, 64, a.b_mn ? 64 : cut.bn / 2)))
+    if ((rc = make_map_3d(&q.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, q.a_mn ? 64 : 128)) ||
+        (rc = make_map_3d(&q.tm_b, B.p, dtype, B.cols, B.rows, 1, B.ld, 0, 64, q.b_mn ? 64 : cut.bn / 2)))
       return rc;
-    a.ab_bf16 = dtype == RA_BF16;
-    a.bn = cut.bn;
-    a.splits = cut.splits;
-    a.status = status;
-    a.wait_limit_ns = wait_limit_ns();
+    q.bn = cut.bn;
+    q.splits = cut.splits;
     // the pairs at work together cover all columns of a few tile rows, or 16 tile
     // rows where the columns are many
-    const int tn = (a.N + cut.bn - 1) / cut.bn;
-    a.group_m = tn < 5 ? (kPairs + tn - 1) / tn : 16;
+    const int tn = (q.N + cut.bn - 1) / cut.bn;
+    q.group_m = tn < 5 ? (kPairs + tn - 1) / tn : 16;
+    return RA_OK;
+  }
+  int launch(PairArgs& a, int dtype) const {
+    a.ab_bf16 = dtype == RA_BF16;
+    a.status = status;
+    a.wait_limit_ns = wait_limit_ns();
     TimedLaunch tl(RA_KERNEL_PAIR_TC, st);
     const cudaError_t e = launch_xent_pair(a, sms, st);
     return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy product launch");
@@ -1322,15 +1326,23 @@ int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, l
   return RA_OK;
 }
 
+// Blocks, and so parts, of the forward for a single token: 32 entries a block and turn,
+// four blocks per SM at most.
+int xent_token_parts(int V) {
+  const int n = (V + 31) / 32;
+  return n < 8 * kPairs ? n : 8 * kPairs;
+}
+
 // forward: target logits [T] fp32 | statistics [column parts][T] (max, sum); the
-// parts are at most ceil(V / 64)
+// tensor-core tiles' parts are at most ceil(V / 64)
 struct XentFwdWs {
   size_t target, stats, total;
 };
 XentFwdWs xent_fwd_layout(const XentShape& s) {
   XentFwdWs w{};
   w.stats = align256((size_t)s.T * 4);
-  w.total = w.stats + align256((size_t)((s.V + 63) / 64) * s.T * 8);
+  const int tiles = (s.V + 63) / 64, token = s.T == 1 ? xent_token_parts(s.V) : 0;
+  w.total = w.stats + align256((size_t)(tiles > token ? tiles : token) * s.T * 8);
   return w;
 }
 
@@ -1412,17 +1424,28 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
   PairArgs a;
   memset(&a, 0, sizeof a);
   a.epi = PAIR_STATS;
-  a.M = (int)s.T; a.N = s.V; a.K = s.D;
+  a.problems = 1;
+  a.q[0].M = (int)s.T; a.q[0].N = s.V; a.q[0].K = s.D;
   a.targets = targets;
   a.ignore = ignore_index;
   a.vocab = s.V;
   a.stats = reinterpret_cast<float2*>(base + l.stats);
   a.target_logit = reinterpret_cast<float*>(base);
-  const Cut cut = cut_product(s.T, s.V, s.D, false);
-  if ((rc = plan.run(a, cut, {x, s.T, s.D, s.xs}, {w, s.V, s.D, s.ws}, dtype))) return rc;
-  const int part = cut.bn / 2;
-  const cudaError_t e = launch_xent_finish(a.stats, (s.V + part - 1) / part, a.target_logit, targets, ignore_index, s.V,
-                                           s.T, loss, lse, st, plan.st);
+  int parts = 0;
+  cudaError_t e;
+  if (s.T == 1 && s.D * 4 <= kXentTokenSmem) {
+    parts = xent_token_parts(s.V);
+    TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
+    e = launch_xent_token(x, w, dtype == RA_BF16, s.D, s.V, s.ws, targets, a.stats, a.target_logit, parts, plan.st);
+    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy token launch");
+  } else {
+    const Cut cut = cut_product(s.T, s.V, s.D, false);
+    if ((rc = plan.problem(a.q[0], cut, {x, s.T, s.D, s.xs}, {w, s.V, s.D, s.ws}, dtype)) ||
+        (rc = plan.launch(a, dtype)))
+      return rc;
+    parts = (s.V + cut.bn / 2 - 1) / (cut.bn / 2);
+  }
+  e = launch_xent_finish(a.stats, parts, a.target_logit, targets, ignore_index, s.V, s.T, loss, lse, st, plan.st);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy reduction launch");
 }
 
@@ -1465,44 +1488,47 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     a.scale = scale;
     // d = gradient of this block's logits, recomputed from x and w
     a.epi = PAIR_DLOGITS;
-    a.M = (int)s.T; a.N = C; a.K = s.D;
+    a.problems = 1;
+    a.q[0].M = (int)s.T; a.q[0].N = C; a.q[0].K = s.D;
     a.targets = targets;
     a.ignore = ignore_index;
     a.vocab = s.V;
     a.col_off = v0;
     a.lse = lse;
     a.grad = dloss;
-    if ((rc = make_map_3d(&a.tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
-        (rc = plan.run(a, cut_product(s.T, C, s.D, false), X, W, dtype)))
+    if ((rc = make_map_3d(&a.q[0].tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
+        (rc = plan.problem(a.q[0], cut_product(s.T, C, s.D, false), X, W, dtype)) || (rc = plan.launch(a, dtype)))
       return rc;
-    // dx += d W  (W's rows as [K, N]: MN-major); summed over blocks in fp32
+    // dx += d W  (W's rows as [K, N]: MN-major), summed over blocks in fp32, and in the
+    // same launch this block's dw = d^T x  (both MN-major); the longer units first
     a.epi = PAIR_STORE;
-    a.M = (int)s.T; a.N = s.D; a.K = C;
-    a.b_mn = 1;
-    a.c_dtype = dx_split || dx_dtype == RA_F32 || !last ? RA_F32 : dx_dtype;
-    void* c = dx_split || (a.c_dtype == RA_F32 && dx_dtype != RA_F32) ? (void*)planes : dx;
-    a.c_accumulate = a.c_dtype == RA_F32 && !first;
-    a.c_add = a.c_dtype != RA_F32 && !first ? planes : nullptr;
-    const bool c32 = a.c_dtype == RA_F32;
+    a.problems = 2;
+    const bool dx_first = C / l.dx_cut.splits >= s.T / l.dw_cut.splits;
+    PairProblem &qx = a.q[dx_first ? 0 : 1], &qw = a.q[dx_first ? 1 : 0];
+    qx.M = (int)s.T; qx.N = s.D; qx.K = C;
+    qx.a_mn = 0;
+    qx.b_mn = 1;
+    qx.c_dtype = dx_split || dx_dtype == RA_F32 || !last ? RA_F32 : dx_dtype;
+    void* c = dx_split || (qx.c_dtype == RA_F32 && dx_dtype != RA_F32) ? (void*)planes : dx;
+    qx.c_accumulate = qx.c_dtype == RA_F32 && !first;
+    qx.c_add = qx.c_dtype != RA_F32 && !first ? planes : nullptr;
     // the last block may be too short for as many splits: its planes are fewer, the
     // others keep what they hold
     const int k_slabs = (C + 63) / 64;
     Cut cut = l.dx_cut;
     if (cut.splits > k_slabs) cut.splits = k_slabs;
-    if ((rc = make_map_3d(&a.tm_c, c, a.c_dtype, s.D, s.T, dx_split ? l.dx_cut.splits : 1, s.D, s.T * s.D, c32 ? 32 : 64,
-                          32)) ||
-        (rc = plan.run(a, cut, Dl, W, dtype)))
-      return rc;
-    // dw of this block = d^T x  (both MN-major)
-    a.M = C; a.N = s.D; a.K = (int)s.T;
-    a.a_mn = 1;
-    a.c_dtype = dw_split ? RA_F32 : dw_dtype;
-    a.c_accumulate = 0;
-    a.c_add = nullptr;
+    qw.M = C; qw.N = s.D; qw.K = (int)s.T;
+    qw.a_mn = qw.b_mn = 1;
+    qw.c_dtype = dw_split ? RA_F32 : dw_dtype;
+    qw.c_accumulate = 0;
+    qw.c_add = nullptr;
     void* dwb = static_cast<char*>(dw) + (size_t)v0 * s.D * dtype_size(dw_dtype);
-    if ((rc = make_map_3d(&a.tm_c, dw_split ? dw_planes : dwb, a.c_dtype, s.D, C, l.dw_cut.splits, s.D,
-                          (long long)C * s.D, a.c_dtype == RA_F32 ? 32 : 64, 32)) ||
-        (rc = plan.run(a, l.dw_cut, Dl, X, dtype)))
+    if ((rc = make_map_3d(&qx.tm_c, c, qx.c_dtype, s.D, s.T, dx_split ? l.dx_cut.splits : 1, s.D, s.T * s.D,
+                          qx.c_dtype == RA_F32 ? 32 : 64, 32)) ||
+        (rc = plan.problem(qx, cut, Dl, W, dtype)) ||
+        (rc = make_map_3d(&qw.tm_c, dw_split ? dw_planes : dwb, qw.c_dtype, s.D, C, l.dw_cut.splits, s.D,
+                          (long long)C * s.D, qw.c_dtype == RA_F32 ? 32 : 64, 32)) ||
+        (rc = plan.problem(qw, l.dw_cut, Dl, X, dtype)) || (rc = plan.launch(a, dtype)))
       return rc;
     if (dw_split) {
       const cudaError_t e = launch_sum_planes(dw_planes, l.dw_cut.splits, (long long)C * s.D, dwb, dw_dtype, plan.st);

@@ -239,17 +239,25 @@ enum PairEpi {
   PAIR_DLOGITS = 1,  // gradient of the logits, 16-bit
   PAIR_STORE = 2,    // C, 16-bit or fp32, fp32 optionally added to what is there
 };
-struct PairArgs {
+struct PairProblem {
   // operands: K-major: boxes of 64 x 128 (A), 64 x bn/2 (B); MN-major: 64 x 64
   CUtensorMap tm_a, tm_b;
   CUtensorMap tm_c;   // output: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle
   int M, N, K;
   int a_mn, b_mn;
-  int ab_bf16;
-  int epi;
   int bn;             // tile columns: 128 or 256
   int splits;         // PAIR_STORE, fp32: K is split, split s writes plane s of C
   int group_m;        // tile rows taken together
+  // PAIR_STORE
+  int c_dtype;
+  int c_accumulate;   // fp32: add to C
+  const float* c_add; // 16-bit: packed fp32 [M, N] added to the product
+};
+struct PairArgs {
+  PairProblem q[2];   // one launch works on one problem, PAIR_STORE on one or two
+  int problems;
+  int ab_bf16;
+  int epi;
   int* status;
   unsigned long long wait_limit_ns;
   const long long* targets;  // [M]
@@ -261,11 +269,14 @@ struct PairArgs {
   const float* scale;        // {2^k, 2^-k} on the device, or NULL: {1, 1}
   float2* stats;             // [column parts][M]: (max, sum of exponentials) of bn / 2 columns
   float* target_logit;       // [M]
-  int c_dtype;
-  int c_accumulate;          // fp32: add to C
-  const float* c_add;        // 16-bit: packed fp32 [M, N] added to the product
 };
 cudaError_t launch_xent_pair(const PairArgs& a, int num_sms, cudaStream_t st);
+// The statistics of a single token (D kXentTokenSmem / 4 or less) on the CUDA cores,
+// `blocks` parts.
+constexpr int kXentTokenSmem = 32768;
+cudaError_t launch_xent_token(const void* x, const void* w, int bf16, int D, int V, long long ws,
+                              const long long* targets, float2* stats, float* target_logit, int blocks,
+                              cudaStream_t st);
 // loss and lse from the column parts' statistics; a target outside [0, V) that is
 // not `ignore` gives loss = NaN and RA_ERR_INVALID_ARG in *status.
 cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,

@@ -5,6 +5,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "ra_device.cuh"
 #include "ra_internal.h"
 
@@ -15,42 +17,50 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------- cross entropy
 // lse_t = m + ln sum_p l_p e^{m_p - m} over the column parts p, m = max_p m_p;
-// loss_t = lse_t - z_{t, y_t}.  A block takes 32 rows; its 32 warps share the parts
-// (lane = row, so every read is a full line) and meet in shared memory.
-__global__ void __launch_bounds__(1024) xent_finish_kernel(const float2* stats, int parts, const float* target_logit,
-                                                          const long long* targets, long long ignore, long long V,
-                                                          long long T, float* loss, float* lse, int* status) {
-  __shared__ float2 part[32][33];
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  const long long t = (long long)blockIdx.x * 32 + lane;
+// loss_t = lse_t - z_{t, y_t}.  A block takes Rows rows: with 32, lane = row while reading,
+// so that every read is a full line, and the warps share the parts; with 1 all threads
+// share the parts of that row.  Then a warp folds one row's shares.
+__device__ __forceinline__ void fold_stats(float& m, float& l, float2 s) {
+  const float mx = fmaxf(m, s.x);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  l = l * ex2_approx((m - ref) * kLog2e) + s.y * ex2_approx((s.x - ref) * kLog2e);
+  m = mx;
+}
+template <int Rows>
+__global__ void __launch_bounds__(Rows == 1 ? 256 : 1024)
+    xent_finish_kernel(const float2* stats, int parts, const float* target_logit, const long long* targets,
+                       long long ignore, long long V, long long T, float* loss, float* lse, int* status) {
+  constexpr int kThreads = Rows == 1 ? 256 : 1024;
+  constexpr int kShares = kThreads / Rows;  // threads per row
+  __shared__ float2 part[Rows][kShares + 1];
+  pdl_trigger();
+  pdl_wait();
+  const int r = threadIdx.x % Rows, first = threadIdx.x / Rows;
+  const long long t = (long long)blockIdx.x * Rows + r;
   float m = -INFINITY, l = 0.f;
-  auto fold = [&](float2 s) {
-    const float mx = fmaxf(m, s.x);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    l = l * ex2_approx((m - ref) * kLog2e) + s.y * ex2_approx((s.x - ref) * kLog2e);
-    m = mx;
-  };
   if (t < T) {
-    int p = w;
-    for (; p + 96 < parts; p += 128) {
+    int p = first;
+    for (; p + 3 * kShares < parts; p += 4 * kShares) {
       float2 s[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[j] = stats[(long long)(p + 32 * j) * T + t];
+      for (int j = 0; j < 4; ++j) s[j] = stats[(long long)(p + j * kShares) * T + t];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) fold(s[j]);
+      for (int j = 0; j < 4; ++j) fold_stats(m, l, s[j]);
     }
-    for (; p < parts; p += 32) fold(stats[(long long)p * T + t]);
+    for (; p < parts; p += kShares) fold_stats(m, l, stats[(long long)p * T + t]);
   }
-  part[w][lane] = make_float2(m, l);
+  part[r][first] = make_float2(m, l);
   __syncthreads();
-  // warp w folds row w's 32 values, one per lane
-  const long long row = (long long)blockIdx.x * 32 + w;
-  if (row >= T) return;
-  const float2 q = part[lane][w];
-  m = warp_max(q.x);
-  l = warp_sum(q.y * ex2_approx((q.x - (m == -INFINITY ? 0.f : m)) * kLog2e));
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const long long row = (long long)blockIdx.x * Rows + w;
+  if (w >= Rows || row >= T) return;
+  m = -INFINITY, l = 0.f;
+#pragma unroll
+  for (int j = 0; j < kShares; j += 32) fold_stats(m, l, part[w][j + lane]);
+  const float top = warp_max(m);
+  l = warp_sum(l * ex2_approx((m - (top == -INFINITY ? 0.f : top)) * kLog2e));
   if (lane) return;
-  const float z = m + logf(l);
+  const float z = top + logf(l);
   lse[row] = z;
   const long long y = targets[row];
   float out = 0.f;
@@ -65,9 +75,83 @@ __global__ void __launch_bounds__(1024) xent_finish_kernel(const float2* stats, 
   loss[row] = out;
 }
 
+// The logits' statistics of a single token on the CUDA cores, bound by reading w once.  A
+// warp takes kEntries vocabulary entries at a time: each lane holds eight columns of
+// every one and multiplies them with x from shared memory (fp32), then the lanes' sums
+// are added up.  The tensor-core kernel would multiply tiles of 256 rows of which one is
+// filled, in rounds of 76 tiles: 37 us against 32768 x 2048 weights.  (With two tokens
+// this kernel is no faster than that one any more.)  Sums are plain fp32, which also keeps
+// the loss of a single token exact.
+constexpr int kEntries = 4;
+template <typename T>
+__global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w, int D, int V, long long ws,
+                                                         const long long* targets, float2* stats,
+                                                         float* target_logit) {
+  extern __shared__ float xf[];  // [D]
+  __shared__ float2 part[8];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < D; i += 256) xf[i] = to_f32(x[i]);
+  __syncthreads();
+  const long long y = targets[0];
+  float m = -INFINITY, l = 0.f;
+  const int chunks = D / 8;
+  for (int v0 = (blockIdx.x * 8 + warp) * kEntries; v0 < V; v0 += gridDim.x * 8 * kEntries) {
+    float acc[kEntries][2];
+#pragma unroll
+    for (int r = 0; r < kEntries; ++r) acc[r][0] = acc[r][1] = 0.f;
+#pragma unroll 4
+    for (int c = lane; c < chunks; c += 32) {
+      uint4 q[kEntries];
+#pragma unroll
+      for (int r = 0; r < kEntries; ++r)
+        q[r] = __ldg(reinterpret_cast<const uint4*>(w + (long long)min(v0 + r, V - 1) * ws) + c);
+      const float4* xp = reinterpret_cast<const float4*>(xf + 8 * c);
+      const float4 x0 = xp[0], x1 = xp[1];
+#pragma unroll
+      for (int r = 0; r < kEntries; ++r) {
+        const T* e = reinterpret_cast<const T*>(&q[r]);
+        acc[r][0] = fmaf(x0.x, to_f32(e[0]), acc[r][0]);
+        acc[r][1] = fmaf(x0.y, to_f32(e[1]), acc[r][1]);
+        acc[r][0] = fmaf(x0.z, to_f32(e[2]), acc[r][0]);
+        acc[r][1] = fmaf(x0.w, to_f32(e[3]), acc[r][1]);
+        acc[r][0] = fmaf(x1.x, to_f32(e[4]), acc[r][0]);
+        acc[r][1] = fmaf(x1.y, to_f32(e[5]), acc[r][1]);
+        acc[r][0] = fmaf(x1.z, to_f32(e[6]), acc[r][0]);
+        acc[r][1] = fmaf(x1.w, to_f32(e[7]), acc[r][1]);
+      }
+    }
+    float z[kEntries], mx = m;
+#pragma unroll
+    for (int r = 0; r < kEntries; ++r) {
+      z[r] = warp_sum(acc[r][0] + acc[r][1]);
+      if (lane == 0 && y == v0 + r && v0 + r < V) target_logit[0] = z[r];
+      if (v0 + r >= V) z[r] = -INFINITY;
+      mx = fmaxf(mx, z[r]);
+    }
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    l *= ex2_approx((m - ref) * kLog2e);
+#pragma unroll
+    for (int r = 0; r < kEntries; ++r) l += ex2_approx((z[r] - ref) * kLog2e);
+    m = mx;
+  }
+  if (lane == 0) part[warp] = make_float2(m, l);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float top = -INFINITY, sum = 0.f;
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, part[j].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int j = 0; j < 8; ++j) sum += part[j].y * ex2_approx((part[j].x - ref) * kLog2e);
+    stats[blockIdx.x] = make_float2(top, sum);
+  }
+}
+
 __global__ void __launch_bounds__(1024) xent_scale_kernel(const float* grad, const long long* targets,
                                                           long long ignore, long long V, long long T, float* scale) {
   __shared__ float part[32];
+  pdl_trigger();
+  pdl_wait();
   float m = 0.f;
   for (long long t = threadIdx.x; t < T; t += 1024) {
     const long long y = targets[t];
@@ -92,6 +176,8 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const float* grad, con
 // Sum of fp32 planes in order, converted.  Bound by reading the planes.
 template <typename T>
 __global__ void __launch_bounds__(256) sum_planes_kernel(const float* planes, int count, long long n, T* out) {
+  pdl_trigger();
+  pdl_wait();
   for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n / 4; i += (long long)gridDim.x * 256) {
     float4 s = reinterpret_cast<const float4*>(planes)[i];
 #pragma unroll 4
@@ -111,30 +197,48 @@ __global__ void __launch_bounds__(256) sum_planes_kernel(const float* planes, in
 
 }  // namespace
 
+cudaError_t launch_xent_token(const void* x, const void* w, int bf16, int D, int V, long long ws,
+                              const long long* targets, float2* stats, float* target_logit, int blocks,
+                              cudaStream_t st) {
+  if (D * 4 > kXentTokenSmem || blocks < 1) return cudaErrorInvalidValue;
+  const cudaError_t e =
+      bf16 ? launch_pdl(xent_token_kernel<__nv_bfloat16>, blocks, 256, D * 4, st, static_cast<const __nv_bfloat16*>(x),
+                        static_cast<const __nv_bfloat16*>(w), D, V, ws, targets, stats, target_logit)
+           : launch_pdl(xent_token_kernel<__half>, blocks, 256, D * 4, st, static_cast<const __half*>(x),
+                        static_cast<const __half*>(w), D, V, ws, targets, stats, target_logit);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
 cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,
                                long long ignore, long long V, long long T, float* loss, float* lse, int* status,
                                cudaStream_t st) {
-  xent_finish_kernel<<<(unsigned)((T + 31) / 32), 1024, 0, st>>>(stats, parts, target_logit, targets, ignore, V, T, loss,
-                                                                lse, status);
-  count_launch();
-  return cudaGetLastError();
+  // up to 304 rows a block each keeps the reads of all of them in flight at once
+  const cudaError_t e = T <= 304 ? launch_pdl(xent_finish_kernel<1>, (int)T, 256, 0, st, stats, parts, target_logit,
+                                              targets, ignore, V, T, loss, lse, status)
+                                 : launch_pdl(xent_finish_kernel<32>, (int)((T + 31) / 32), 1024, 0, st, stats, parts,
+                                              target_logit, targets, ignore, V, T, loss, lse, status);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 cudaError_t launch_xent_scale(const float* grad, const long long* targets, long long ignore, long long V, long long T,
                               float* scale, cudaStream_t st) {
-  xent_scale_kernel<<<1, 1024, 0, st>>>(grad, targets, ignore, V, T, scale);
-  count_launch();
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(xent_scale_kernel, 1, 1024, 0, st, grad, targets, ignore, V, T, scale);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 cudaError_t launch_sum_planes(const float* planes, int count, long long n, void* out, int dtype, cudaStream_t st) {
   const long long blocks = (n / 4 + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < 1216 ? blocks : 1216);
-  if (dtype == RA_F32) sum_planes_kernel<<<grid, 256, 0, st>>>(planes, count, n, static_cast<float*>(out));
-  else if (dtype == RA_BF16) sum_planes_kernel<<<grid, 256, 0, st>>>(planes, count, n, static_cast<__nv_bfloat16*>(out));
-  else sum_planes_kernel<<<grid, 256, 0, st>>>(planes, count, n, static_cast<__half*>(out));
-  count_launch();
-  return cudaGetLastError();
+  const int grid = (int)(blocks < 1216 ? blocks : 1216);
+  const cudaError_t e =
+      dtype == RA_F32 ? launch_pdl(sum_planes_kernel<float>, grid, 256, 0, st, planes, count, n, static_cast<float*>(out))
+      : dtype == RA_BF16
+          ? launch_pdl(sum_planes_kernel<__nv_bfloat16>, grid, 256, 0, st, planes, count, n, static_cast<__nv_bfloat16*>(out))
+          : launch_pdl(sum_planes_kernel<__half>, grid, 256, 0, st, planes, count, n, static_cast<__half*>(out));
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace ra

@@ -2,12 +2,13 @@
 // (ra_pair.cuh):
 //   PAIR_STATS    logits' softmax statistics and the target's logit (forward)
 //   PAIR_DLOGITS  gradient of one block's logits, recomputed from x and w
-//   PAIR_STORE    dx = d W and dw = d^T x, whole or split along K
+//   PAIR_STORE    dx = d W and dw = d^T x, whole or split along K, in one launch
 // The logits themselves stay in TMEM.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "ra_pair.cuh"
@@ -18,45 +19,88 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 using S = PairSmem<6, 4096, 0>;  // 6 stages of 32 KB, 4 KB of staging per epilogue warp
 
+// The units of one or two problems shared out over the pairs.  A unit is a tile, or one
+// split of its K.  The first problem's units go round the pairs; where the last round
+// leaves pairs idle, those take as many of the second's as fit into one unit of the first
+// (by k-slabs); the rest goes round again, beginning with them.  With dx (128 tiles of 128
+// slabs) and dw (256 of 64) on 76 pairs the longest share is 448 slabs; in launches of
+// their own they take 2 x 128 + 4 x 64 = 512.
+struct Share {
+  int units0, units1, pairs, pair, over, fill;
+  __device__ __forceinline__ Share(const PairArgs& a, int pair_, int pairs_) : pairs(pairs_), pair(pair_) {
+    const int slabs0 = slabs(a.q[0]), slabs1 = a.problems > 1 ? slabs(a.q[1]) : 1;
+    units0 = tiles(a.q[0]) * a.q[0].splits;
+    units1 = a.problems > 1 ? tiles(a.q[1]) * a.q[1].splits : 0;
+    over = units0 % pairs;                                        // pairs of the last round
+    fill = over ? (slabs0 + slabs1 / 2) / (slabs1 > 0 ? slabs1 : 1) : 0;  // units of the second that fill it up
+  }
+  static __device__ __forceinline__ int tiles(const PairProblem& q) {
+    return ((q.M + 255) / 256) * ((q.N + q.bn - 1) / q.bn);
+  }
+  static __device__ __forceinline__ int slabs(const PairProblem& q) { return ((q.K + 63) / 64 + q.splits - 1) / q.splits; }
+  // The n-th unit of this pair: index within its problem, the problem in *which; -1: none.
+  __device__ __forceinline__ int unit(int n, int* which) const {
+    const int mine0 = units0 / pairs + (pair < over ? 1 : 0);
+    *which = 0;
+    if (n < mine0) return pair + n * pairs;
+    *which = 1;
+    n -= mine0;
+    const int idle = pairs - over;
+    int place = pair - over;  // the idle pairs come first
+    if (place >= 0) {
+      if (n < fill) {
+        const int j = place + n * idle;
+        return j < units1 ? j : -1;
+      }
+      n -= fill;
+    } else {
+      place += pairs;
+    }
+    const int j = (over ? fill * idle : 0) + place + n * pairs;
+    return j < units1 ? j : -1;
+  }
+};
+
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
     xent_pair_kernel(const __grid_constant__ PairArgs a) {
   extern __shared__ uint8_t smem_raw[];
   Pair<S> p;
   p.begin(smem_raw, a.status, a.wait_limit_ns, [] {});
+  pdl_trigger();
+  pdl_wait();
   const uint32_t warp = warp_id(), lane = lane_id();
-  const int clusters = gridDim.x / 2, cluster = blockIdx.x / 2;
-  const int bn = a.bn;
-  const int tm = (a.M + 255) / 256, tn = (a.N + bn - 1) / bn;
-  const int tiles = tm * tn, units = tiles * a.splits;
-  const int k_steps = (a.K + 63) / 64;
-  // unit u: tile u % tiles of split u / tiles, which takes an even share of the k-slabs
-  auto k_at = [&](int s) { return (int)((long long)k_steps * s / a.splits); };
-  const Operand A{&a.tm_a, &a.tm_a, a.a_mn}, B{&a.tm_b, &a.tm_b, a.b_mn};
+  const Share share(a, blockIdx.x / 2, gridDim.x / 2);
+  // split s of a problem takes an even share of the k-slabs
+  auto k_at = [&](const PairProblem& q, int s) { return (int)((long long)((q.K + 63) / 64) * s / q.splits); };
+  int which = 0, u = 0;
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t cnt = 0;
       bool ok = true;
-      for (int u = cluster; u < units && ok; u += clusters) {
-        const int s = u / tiles;
-        const Tile t = tile_grouped(u - s * tiles, tm, tn, a.group_m);
-        ok = p.produce(cnt, A, B, bn, t.m * 256, t.n * bn, 0, k_at(s), k_at(s + 1));
+      for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
+        const PairProblem& q = a.q[which];
+        const int tm = (q.M + 255) / 256, tn = (q.N + q.bn - 1) / q.bn, s = u / (tm * tn);
+        const Tile t = tile_grouped(u - s * tm * tn, tm, tn, q.group_m);
+        const Operand A{&q.tm_a, &q.tm_a, q.a_mn}, B{&q.tm_b, &q.tm_b, q.b_mn};
+        ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1));
       }
       if (*p.abort) p.producer_drain(cnt);
     }
   } else if (warp == 1) {
     uint32_t cnt = 0, lt = 0;
     bool ok = true;
-    for (int u = cluster; u < units && ok; u += clusters) {
-      const int s = u / tiles;
-      ok = p.rank == 0 ? p.multiply(cnt, lt, a.ab_bf16, A, B, bn, 0, 0, k_at(s), k_at(s + 1)) : p.forward(lt);
+    for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
+      const PairProblem& q = a.q[which];
+      const int s = u / Share::tiles(q);
+      const Operand A{nullptr, nullptr, q.a_mn}, B{nullptr, nullptr, q.b_mn};
+      ok = p.rank == 0 ? p.multiply(cnt, lt, a.ab_bf16, A, B, q.bn, 0, 0, k_at(q, s), k_at(q, s + 1)) : p.forward(lt);
     }
     if (p.rank == 0) p.multiply_drain();
   } else {
     const uint32_t quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
     const int half = (int)(warp - 2) >> 2;  // columns [half * bn / 2, + bn / 2)
-    const int cols = bn / 2;
     const uint32_t stage = p.sbase + S::kOut + (warp - 2) * 4096;
     uint8_t* const stage_p = p.smem + S::kOut + (warp - 2) * 4096;
     // one 16-byte piece of the warp's staging rows of 128 bytes, 128-byte swizzle
@@ -77,10 +121,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     };
     uint32_t lt = 0;
-    for (int u = cluster; u < units; u += clusters, ++lt) {
+    for (int n = 0; (u = share.unit(n, &which)) >= 0; ++n, ++lt) {
+      const PairProblem& q = a.q[which];
       const uint32_t b = lt & 1;
-      const int split = u / tiles;
-      const Tile t = tile_grouped(u - split * tiles, tm, tn, a.group_m);
+      const int bn = q.bn, cols = bn / 2;
+      const int tm = (q.M + 255) / 256, tn = (q.N + bn - 1) / bn, split = u / (tm * tn);
+      const Tile t = tile_grouped(u - split * tm * tn, tm, tn, q.group_m);
       const int row0 = t.m * 256 + (int)p.rank * 128 + (int)quarter * 32;
       const int row = row0 + (int)lane;
       const int col0 = t.n * bn + half * cols;
@@ -92,7 +138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // Online softmax statistics of the tile's columns for this row, and the
         // target's logit where it lies among them.  Bound by the matrix product;
         // the exponentials (bn / 2 per thread and tile) hide behind it for K > 256.
-        const long long y = row < a.M ? a.targets[row] : -1;
+        const long long y = row < q.M ? a.targets[row] : -1;
         const int ycol = (y >= col0 && y < col0 + cols) ? (int)(y - col0) : -1;
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
@@ -100,10 +146,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
           float v[32];
           tmem_load32(src + c, v);
           if (c == cols - 32) p.release(b);
-          if (col0 + c + 32 > a.N) {
+          if (col0 + c + 32 > q.N) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (col0 + c + j >= a.N) v[j] = -INFINITY;
+              if (col0 + c + j >= q.N) v[j] = -INFINITY;
           }
           float mk[4];
 #pragma unroll
@@ -134,13 +180,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               if (ycol == c + j) a.target_logit[row] = v[j];
           }
         }
-        if (row < a.M && col0 < a.N) a.stats[(long long)(t.n * 2 + half) * a.M + row] = make_float2(m, l);
+        if (row < q.M && col0 < q.N) a.stats[(long long)(t.n * 2 + half) * q.M + row] = make_float2(m, l);
       } else if (EPI == PAIR_DLOGITS) {
         // d = g (e^{z - lse} - [column = target]), rounded to the operand type of
         // the two products that follow (bf16: any range; fp16: g is brought near
         // 2^13 by a power of two that those products take out again)
-        const long long y = row < a.M ? a.targets[row] : a.ignore;
-        const bool live = row < a.M && y != a.ignore && y >= 0 && y < a.vocab;
+        const long long y = row < q.M ? a.targets[row] : a.ignore;
+        const bool live = row < q.M && y != a.ignore && y >= 0 && y < a.vocab;
         const float g = live ? a.grad[row] * (a.scale ? a.scale[0] : 1.f) : 0.f;
         const float lse2 = live ? a.lse[row] * kLog2e : 0.f;
         const long long yc = y - a.col_off - col0;
@@ -171,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                             pack_pair(v[8 * j + 6], v[8 * j + 7], a.ab_bf16)));
           }
           stage_out([&]() {
-            if (row0 < a.M && col0 + c < a.N) tma_store_3d(&a.tm_c, stage, col0 + c, row0, 0);
+            if (row0 < q.M && col0 + c < q.N) tma_store_3d(&q.tm_c, stage, col0 + c, row0, 0);
           });
         }
       } else {
@@ -179,7 +225,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
         // there (each element once per launch, so the sum's order is fixed).  Split
         // along K, each split has a plane of its own.
         const float mul = a.scale ? a.scale[1] : 1.f;
-        if (a.c_dtype == RA_F32) {
+        if (q.c_dtype == RA_F32) {
 #pragma unroll 1
           for (int c = 0; c < cols; c += 32) {
             stage_free();
@@ -191,14 +237,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               stage16(j, make_uint4(__float_as_uint(v[4 * j] * mul), __float_as_uint(v[4 * j + 1] * mul),
                                     __float_as_uint(v[4 * j + 2] * mul), __float_as_uint(v[4 * j + 3] * mul)));
             stage_out([&]() {
-              if (row0 < a.M && col0 + c < a.N) {
-                if (a.c_accumulate) tma_add_3d(&a.tm_c, stage, col0 + c, row0, split);
-                else tma_store_3d(&a.tm_c, stage, col0 + c, row0, split);
+              if (row0 < q.M && col0 + c < q.N) {
+                if (q.c_accumulate) tma_add_3d(&q.tm_c, stage, col0 + c, row0, split);
+                else tma_store_3d(&q.tm_c, stage, col0 + c, row0, split);
               }
             });
           }
         } else {
-          const int bf = a.c_dtype == RA_BF16;
+          const int bf = q.c_dtype == RA_BF16;
 #pragma unroll 1
           for (int c = 0; c < cols; c += 64) {
             stage_free();
@@ -210,12 +256,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               if (cc == cols - 32) p.release(b);
 #pragma unroll
               for (int j = 0; j < 32; ++j) v[j] *= mul;
-              if (a.c_add && row < a.M) {  // N is a multiple of 8 where c_add is used
-                const float4* q = reinterpret_cast<const float4*>(a.c_add + (long long)row * a.N + col0 + cc);
+              if (q.c_add && row < q.M) {  // N is a multiple of 8 where c_add is used
+                const float4* add = reinterpret_cast<const float4*>(q.c_add + (long long)row * q.N + col0 + cc);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                  if (col0 + cc + 4 * j < a.N) {
-                    const float4 f = q[j];
+                  if (col0 + cc + 4 * j < q.N) {
+                    const float4 f = add[j];
                     v[4 * j] += f.x;
                     v[4 * j + 1] += f.y;
                     v[4 * j + 2] += f.z;
@@ -230,7 +276,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
                                    pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf)));
             }
             stage_out([&]() {
-              if (row0 < a.M && col0 + c < a.N) tma_store_3d(&a.tm_c, stage, col0 + c, row0, 0);
+              if (row0 < q.M && col0 + c < q.N) tma_store_3d(&q.tm_c, stage, col0 + c, row0, 0);
             });
           }
         }
@@ -244,21 +290,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
 }  // namespace
 
 cudaError_t launch_xent_pair(const PairArgs& a, int num_sms, cudaStream_t st) {
-  if (a.M <= 0 || a.N <= 0 || a.K <= 0 || a.group_m <= 0 || num_sms < 2 || (a.bn != 128 && a.bn != 256) ||
-      a.splits < 1 || a.splits > (a.K + 63) / 64)
+  if (a.problems < 1 || a.problems > 2 || (a.problems > 1 && a.epi != PAIR_STORE) || num_sms < 2)
     return cudaErrorInvalidValue;
-  const long long units = (long long)((a.M + 255) / 256) * ((a.N + a.bn - 1) / a.bn) * a.splits;
+  long long units = 0;
+  for (int i = 0; i < a.problems; ++i) {
+    const PairProblem& q = a.q[i];
+    if (q.M <= 0 || q.N <= 0 || q.K <= 0 || q.group_m <= 0 || (q.bn != 128 && q.bn != 256) || q.splits < 1 ||
+        q.splits > (q.K + 63) / 64)
+      return cudaErrorInvalidValue;
+    units += (long long)((q.M + 255) / 256) * ((q.N + q.bn - 1) / q.bn) * q.splits;
+  }
   if (units > 0x3fffffff) return cudaErrorInvalidValue;
   const int pairs = num_sms / 2;
   const int grid = 2 * (int)(units < pairs ? units : pairs);
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
   auto run = [&](auto epi) {
     auto kernel = xent_pair_kernel<decltype(epi)::value>;
-    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
-    if (err != cudaSuccess) return err;
-    kernel<<<grid, kPairThreads, S::kAlloc, st>>>(a);
-    return cudaGetLastError();
+    // the attribute is set once per device (setting it twice does no harm)
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (dev > 63 || !(ready.load(std::memory_order_acquire) & bit)) {
+      const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kAlloc);
+      if (err != cudaSuccess) return err;
+      if (dev <= 63) ready.fetch_or(bit, std::memory_order_release);
+    }
+    return launch_pdl(kernel, grid, kPairThreads, S::kAlloc, st, a);
   };
-  cudaError_t e;
   switch (a.epi) {
     case PAIR_STATS: e = run(std::integral_constant<int, PAIR_STATS>{}); break;
     case PAIR_DLOGITS: e = run(std::integral_constant<int, PAIR_DLOGITS>{}); break;

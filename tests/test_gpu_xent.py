@@ -89,7 +89,8 @@ def check(ra, x, w, y, g, loss, lse, dx=None, dw=None):
 
 SIZES = [
     # T, D, V, block
-    (1, 8, 1, 1), (1, 64, 1000, 256), (3, 72, 5, 2), (127, 64, 255, 255), (128, 128, 256, 128), (129, 136, 257, 100),
+    (1, 8, 1, 1), (1, 64, 1000, 256), (2, 2048, 3000, 1024), (3, 72, 5, 2), (4, 264, 20011, 8192), (7, 2048, 333, 333),
+    (8, 2040, 700, 256), (8, 2056, 700, 256), (9, 64, 2001, 500), (127, 64, 255, 255), (128, 128, 256, 128), (129, 136, 257, 100),
     (256, 200, 1025, 512), (333, 256, 2000, 768), (600, 520, 1111, 1111), (1025, 64, 3001, 1024), (40, 1048, 777, 256),
 ]
 
