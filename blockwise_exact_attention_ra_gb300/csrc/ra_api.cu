@@ -1326,11 +1326,11 @@ int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, l
   return RA_OK;
 }
 
-// Blocks, and so parts, of the forward for a single token: 32 entries a block and turn,
-// four blocks per SM at most.
+// Blocks, and so parts, of the forward for a single token: 16 entries a block and turn,
+// eight blocks per SM at most.
 int xent_token_parts(int V) {
-  const int n = (V + 31) / 32;
-  return n < 8 * kPairs ? n : 8 * kPairs;
+  const int n = (V + 15) / 16;
+  return n < 16 * kPairs ? n : 16 * kPairs;
 }
 
 // forward: target logits [T] fp32 | statistics [column parts][T] (max, sum); the
@@ -1612,6 +1612,24 @@ int check_ns(int batch, int rows, int cols, const float* coeffs, int steps, floa
   return RA_OK;
 }
 
+// Matrices with a side of at most 128 and the other at most 4096 go to clusters of CTAs
+// that hold them whole: slices of 64 columns on up to 8 CTAs where the SMs suffice for the
+// batch, wider ones and 16 CTAs (the largest cluster) beyond.
+bool ns_small_cut(const NsShape& s, int* slice, int* cluster) {
+  const int n = s.rows > s.cols ? s.rows : s.cols;
+  if (s.m > 128 || n > 4096) return false;
+  auto ctas = [&](int c) {
+    int g = 1;
+    while (g * c < n) g *= 2;
+    return g;
+  };
+  int c = 64;
+  while (c < 256 && (ctas(c) > 8 || (long long)s.batch * ctas(c) > 2 * kPairs)) c *= 2;
+  *slice = c;
+  *cluster = ctas(c);
+  return true;
+}
+
 // The cut of one phase: the tile's width as for the cross entropy's products; K may be
 // split for every phase, over at most as many pairs as run at once.  A k-slab of a wide
 // tile takes about 0.33 us; handing one split's sum over takes 6 us, 2 us more for each
@@ -1711,14 +1729,39 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
   int* st;
   if ((rc = status_ptr(&st))) return rc;
   if (!device_is_sm103()) return fail(RA_ERR_UNSUPPORTED, "tensor-core kernels are built for sm_103a only");
+  const long long gs = (long long)dtype_size(g_dtype), os = (long long)dtype_size(out_dtype);
+  const NsInput in{g, g_dtype, batch, rows, cols, g_rstride, g_bstride,
+                   aligned16(g) && (g_rstride * gs) % 16 == 0 && (g_bstride * gs) % 16 == 0};
+  const bool out_vec = aligned16(out) && (out_rstride * os) % 16 == 0 && (out_bstride * os) % 16 == 0;
+  int slice = 0, cluster = 0;
+  if (ns_small_cut(s, &slice, &cluster)) {
+    NsSmallArgs a;
+    memset(&a, 0, sizeof a);
+    a.in = in;
+    a.m = s.m;
+    a.n = rows > cols ? rows : cols;
+    a.tall = rows > cols;
+    a.steps = steps;
+    a.ca = coeffs[0]; a.cb = coeffs[1]; a.cc = coeffs[2];
+    a.sx = (float)s.sx; a.sa = (float)s.sa; a.sb = (float)s.sb; a.inv_sb = (float)(1.0 / s.sb); a.eps = eps;
+    a.alpha_mul = (float)(1.0 / (s.sx * s.sx * s.m));
+    a.gram_acc = (float)(s.sa / (s.sx * s.sx));
+    a.square_acc = (float)(coeffs[2] * s.sb / (s.sa * s.sa));
+    a.square_lin = (float)(s.sb / s.sa);
+    a.out_mul = (float)(1.0 / s.sx);
+    a.out = out; a.out_dtype = out_dtype; a.out_vec = out_vec; a.out_ld = out_rstride; a.out_bstride = out_bstride;
+    a.status = st;
+    a.wait_limit_ns = wait_limit_ns();
+    TimedLaunch tl(RA_KERNEL_PAIR_TC, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_ns_small(a, slice, cluster, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "Newton-Schulz launch");
+  }
   char* base = static_cast<char*>(workspace);
   NsArgs a;
   memset(&a, 0, sizeof a);
   a.batch = batch; a.rows = rows; a.cols = cols; a.m = s.m; a.tall = rows > cols;
   a.steps = steps;
-  a.in = NsInput{g, g_dtype, batch, rows, cols, g_rstride, g_bstride, 0};
-  const long long gs = (long long)dtype_size(g_dtype), os = (long long)dtype_size(out_dtype);
-  a.in.vec = aligned16(g) && (g_rstride * gs) % 16 == 0 && (g_bstride * gs) % 16 == 0;
+  a.in = in;
   a.ca = coeffs[0]; a.cb = coeffs[1]; a.cc = coeffs[2];
   a.sx = (float)s.sx; a.sa = (float)s.sa; a.eps = eps;
   a.alpha_mul = (float)(1.0 / (s.sx * s.sx * s.m));
@@ -1739,7 +1782,7 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
   a.lo = reinterpret_cast<uint16_t*>(base + l.lo);
   a.ld = s.ld;
   a.out = out; a.out_dtype = out_dtype; a.out_ld = out_rstride; a.out_bstride = out_bstride;
-  a.out_vec = aligned16(out) && (out_rstride * os) % 16 == 0 && (out_bstride * os) % 16 == 0;
+  a.out_vec = out_vec;
   a.status = st;
   a.wait_limit_ns = wait_limit_ns();
   int pairs = 0;

@@ -36,6 +36,13 @@ __device__ __forceinline__ uint32_t warp_id() {
   return __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_lane() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Appends {kind, head, query tile, key tile} to a debug visit log (one
 // thread; its entries keep their order because its atomics on one address
 // are ordered).

@@ -333,6 +333,22 @@ struct NsArgs {
   int* status;
   unsigned long long wait_limit_ns;
 };
+// Matrices whose smaller side m is at most 128: a cluster of CTAs per matrix (a power of
+// two, at most 16), each with a slice of 64, 128 or 256 of the n columns of X (rows of a
+// tall gradient).
+struct NsSmallArgs {
+  NsInput in;
+  int m, n, tall, steps;
+  float ca, cb, cc;
+  float sx, sa, sb, inv_sb, eps, alpha_mul;
+  float gram_acc, square_acc, square_lin, out_mul;
+  void* out;
+  int out_dtype, out_vec;
+  long long out_ld, out_bstride;
+  int* status;
+  unsigned long long wait_limit_ns;
+};
+cudaError_t launch_ns_small(const NsSmallArgs& a, int slice, int cluster, cudaStream_t st);
 // Pairs of CTAs that can run at the same time on the current device.
 cudaError_t ns_max_pairs(int* pairs);
 int ns_phase_tiles(const NsArgs& a, int kind, int bn);  // per batch entry

@@ -26,6 +26,7 @@
 
 #include <mutex>
 
+#include "ra_ns.cuh"
 #include "ra_pair.cuh"
 
 namespace ra {
@@ -34,45 +35,6 @@ namespace {
 // 5 stages of 32 KB; 8 KB of staging per epilogue warp (two tiles of 32 rows x 64
 // columns).  Extra barriers: staging filled [8].
 using S = PairSmem<5, 8192, 8>;
-
-__device__ __forceinline__ float load_as_f32(const void* p, int dtype, long long i) {
-  if (dtype == RA_F32) return static_cast<const float*>(p)[i];
-  if (dtype == RA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
-}
-
-// Eight consecutive elements of a row (fewer at its end; the rest read as zero).
-constexpr int kNsBatch = 4;  // groups of eight in flight per thread
-__device__ __forceinline__ void load8(const NsInput& in, long long off, int left, float* v) {
-  if (in.vec && left >= 8) {
-    if (in.dtype == RA_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(in.g) + off);
-      const float4 x = p[0], y = p[1];
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.g) + off);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 f;
-        if (in.dtype == RA_BF16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
-        else f = unpack_half2(w[j]);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < left ? load_as_f32(in.g, in.dtype, off + j) : 0.f;
-}
-
-// Squares are summed in three accumulators by magnitude, the large values scaled
-// down and the small ones up, so that none of them overflows or vanishes (J. L.
-// Blue, "A Portable Fortran Program to Find the Euclidean Norm of a Vector", 1978).
-constexpr float kBig = 1099511627776.f, kSmall = 1.f / 1099511627776.f;         // 2^40, 2^-40
-constexpr float kDown = 8.271806125530277e-25f, kUp = 1.2089258196146292e24f;  // 2^-80, 2^80
 
 // Bound by reading G once.  Also readies the chain's words.
 __global__ void __launch_bounds__(512) ns_sumsq_kernel(const __grid_constant__ NsInput in, float* parts,
@@ -93,14 +55,7 @@ __global__ void __launch_bounds__(512) ns_sumsq_kernel(const __grid_constant__ N
 #pragma unroll
     for (int k = 0; k < kNsBatch; ++k) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float x = fabsf(v[k][j]);
-        const float up = x > kBig ? x * kDown : 0.f, down = x < kSmall ? x * kUp : 0.f;
-        const float mid = (x > kBig || x < kSmall) ? 0.f : x;  // NaN stays here
-        s[0] = fmaf(mid, mid, s[0]);
-        s[1] = fmaf(up, up, s[1]);
-        s[2] = fmaf(down, down, s[2]);
-      }
+      for (int j = 0; j < 8; ++j) ns_add_square(v[k][j], s);
     }
   }
 #pragma unroll
@@ -115,24 +70,6 @@ __global__ void __launch_bounds__(512) ns_sumsq_kernel(const __grid_constant__ N
     for (int j = 0; j < 16; ++j) x += part[threadIdx.x][j];
     parts[((long long)blockIdx.y * kNsParts + blockIdx.x) * 3 + threadIdx.x] = x;
   }
-}
-
-// mul / (|G|_F + eps) as f 2^e0 2^e1 (in range for every norm), by one warp; the parts
-// are added in a fixed order, in 64 bits.
-__device__ __forceinline__ void ns_factor(const float* parts, int num_parts, float mul, float eps, float* f) {
-  double s = 0.0;
-  for (int i = lane_id(); i < num_parts; i += 32) {
-    const float* p = parts + 3 * i;
-    s += (double)p[0] + (double)p[1] * 1.4615016373309029e48 + (double)p[2] * 6.8422776578360209e-49;  // 2^160, 2^-160
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const double norm = sqrt(s) + (double)eps;
-  const double inv = norm > 0.0 ? (double)mul / norm : 0.0;
-  int e = 0;
-  f[2] = (float)frexp(inv, &e);
-  f[0] = ldexpf(1.f, e / 2);
-  f[1] = ldexpf(1.f, e - e / 2);
 }
 
 // sum of n floats by one warp, in an order that depends on n alone
@@ -213,37 +150,6 @@ __device__ __forceinline__ unsigned ready_tiles(const NsArgs& a, int step, int k
 }
 __device__ __forceinline__ Tile phase_tile(const NsArgs& a, const Phase& f, int t) {
   return f.sym ? tile_sym(t, f.tn, f.bn) : tile_grouped(t, f.tm, f.tn, a.group_m);
-}
-
-// The result's 64 columns from cc on of one row.
-__device__ __forceinline__ void write_out(const NsArgs& a, int b, int row, int cc, int N, float* v) {
-  if (cc >= N) return;
-  const long long o = b * a.out_bstride + (long long)row * a.out_ld + cc;
-#pragma unroll
-  for (int j = 0; j < 64; ++j) v[j] *= a.out_mul;
-  if (a.out_vec && cc + 64 <= N) {
-    if (a.out_dtype == RA_F32) {
-      float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.out) + o);
-#pragma unroll
-      for (int j = 0; j < 16; ++j) q[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    } else {
-      uint4* q = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + o);
-      const int bf = a.out_dtype == RA_BF16;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        q[j] = make_uint4(pack_pair(v[8 * j], v[8 * j + 1], bf), pack_pair(v[8 * j + 2], v[8 * j + 3], bf),
-                          pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf));
-    }
-    return;
-  }
-#pragma unroll
-  for (int j = 0; j < 64; ++j) {
-    if (cc + j < N) {
-      if (a.out_dtype == RA_F32) static_cast<float*>(a.out)[o + j] = v[j];
-      else if (a.out_dtype == RA_BF16) static_cast<__nv_bfloat16*>(a.out)[o + j] = __float2bfloat16_rn(v[j]);
-      else static_cast<__half*>(a.out)[o + j] = __float2half_rn(v[j]);
-    }
-  }
 }
 
 // CTAs that scale batch entry b: the entries are shared out in teams, entry b to the CTAs
@@ -565,7 +471,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
               }
             }
             if (kind == NS_UPDATE && last) {
-              if (row < f.M) write_out(a, b, row, col0 + c, f.N, v);
+#pragma unroll
+              for (int j = 0; j < 64; ++j) v[j] *= a.out_mul;
+              if (row < f.M)
+                ns_write_row<64>(a.out, a.out_dtype, a.out_vec, b * a.out_bstride + (long long)row * a.out_ld + col0 + c,
+                                 col0 + c, f.N, v);
               fence_proxy_async_smem();
               __syncwarp();
               continue;

@@ -62,11 +62,6 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-  return p != 0;
-}
 __device__ __forceinline__ void pair_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(
@@ -252,7 +247,7 @@ struct Pair {
   __device__ __forceinline__ bool multiply(uint32_t& cnt, uint32_t& lt, int ab_bf16, const Operand& A,
                                            const Operand& B, int bn, int m0, int n0, int k_from, int k_to) const {
     const uint32_t b = lt & 1;
-    const bool issuer = elect_one();
+    const bool issuer = elect_lane();
     if (!__all_sync(0xffffffffu, wait(acc_empty(b), ((lt >> 1) & 1) ^ 1))) return false;
     tc_fence_after();
     const uint32_t acc = tmem + b * 256;
@@ -288,7 +283,7 @@ struct Pair {
   }
   // Every MMA issued has completed before TMEM is released.
   __device__ __forceinline__ void multiply_drain() const {
-    if (elect_one()) pair_commit(drain());
+    if (elect_lane()) pair_commit(drain());
     __syncwarp();
     (void)mbar_wait(drain(), 0, abort, nullptr, 100000000ull);
   }

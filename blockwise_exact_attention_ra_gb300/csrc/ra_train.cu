@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(Rows == 1 ? 256 : 1024)
 // filled, in rounds of 76 tiles: 37 us against 32768 x 2048 weights.  (With two tokens
 // this kernel is no faster than that one any more.)  Sums are plain fp32, which also keeps
 // the loss of a single token exact.
-constexpr int kEntries = 4;
+constexpr int kEntries = 2;
 template <typename T>
 __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w, int D, int V, long long ws,
                                                          const long long* targets, float2* stats,
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w,
     float acc[kEntries][2];
 #pragma unroll
     for (int r = 0; r < kEntries; ++r) acc[r][0] = acc[r][1] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int c = lane; c < chunks; c += 32) {
       uint4 q[kEntries];
 #pragma unroll

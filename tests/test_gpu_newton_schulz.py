@@ -120,7 +120,10 @@ def check(ra, g, out, steps=5, eps=1e-7, coeffs=COEFFS):
 
 
 SIZES = [(32, 32), (33, 100), (100, 33), (64, 512), (256, 256), (257, 255), (200, 1000), (1000, 333), (130, 3001),
-         (768, 520), (1030, 1030)]
+         (768, 520), (1030, 1030),
+         # at and around the sizes where the path changes: a side of 128, the other of 64 ... 4096
+         (128, 128), (128, 129), (129, 128), (129, 129), (64, 65), (512, 127), (40, 513), (100, 1025), (2049, 128),
+         (128, 4096), (128, 4097), (4096, 33), (129, 4096)]
 
 
 @pytest.mark.parametrize("rows,cols", SIZES)
@@ -175,7 +178,7 @@ def test_other_coefficients(ra):
         assert rel(f64(o), want) <= 2e-3
 
 
-@pytest.mark.parametrize("rows,cols", [(40, 96), (300, 130)])
+@pytest.mark.parametrize("rows,cols", [(40, 96), (300, 130), (96, 1500)])
 def test_batch_equals_single_matrices(ra, rows, cols):
     g = gradient(rows, cols, 25, batch=5)
     g[2] *= 1e4
@@ -187,25 +190,27 @@ def test_batch_equals_single_matrices(ra, rows, cols):
         assert torch.equal(o[i], ra.newton_schulz(g[i])), i
 
 
-def test_strides_and_in_place(ra):
-    g = gradient(100, 77, 26, batch=3)
+@pytest.mark.parametrize("rows,cols", [(100, 77), (150, 177), (77, 300)])
+def test_strides_and_in_place(ra, rows, cols):
+    g = gradient(rows, cols, 26, batch=3)
     want = ra.newton_schulz(g)
-    wide = torch.full((3, 110, 90), float("nan"), device="cuda")
-    wide[:, 5:105, 3:80] = g
-    view = wide[:, 5:105, 3:80]
+    wide = torch.full((3, rows + 10, cols + 13), float("nan"), device="cuda")
+    wide[:, 5:5 + rows, 3:3 + cols] = g
+    view = wide[:, 5:5 + rows, 3:3 + cols]
     assert torch.equal(ra.newton_schulz(view), want)
-    ws = torch.empty(ra.ra_newton_schulz_workspace_bytes(3, 100, 77), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ra.ra_newton_schulz_workspace_bytes(3, rows, cols), dtype=torch.uint8, device="cuda")
     ra.ra_newton_schulz(view, view, ws)        # in place, in a larger tensor
     ra.ra_sync_status()
     assert torch.equal(view, want)
-    wide[:, 5:105, 3:80] = float("nan")
+    wide[:, 5:5 + rows, 3:3 + cols] = float("nan")
     assert torch.isnan(wide).all()             # nothing written beside it
 
 
-def test_scale_of_the_gradient(ra):
+@pytest.mark.parametrize("rows,cols", [(64, 96), (140, 200)])
+def test_scale_of_the_gradient(ra, rows, cols):
     # powers of two change nothing but the norm's last bit (its squares are summed by
     # magnitude), from norms whose squares overflow or vanish in fp32 to ordinary ones
-    g = gradient(64, 96, 27)
+    g = gradient(rows, cols, 27)
     want = f64(ra.newton_schulz(g, steps=1, eps=0.0))
     for k in (-100, -70, -30, 30, 62, 100):
         o = ra.newton_schulz(g * 2.0 ** k, steps=1, eps=0.0)
@@ -214,11 +219,12 @@ def test_scale_of_the_gradient(ra):
     ra.ra_sync_status()
 
 
-def test_zero_and_unusable_gradients(ra):
-    z = torch.zeros(2, 40, 50, device="cuda")
+@pytest.mark.parametrize("rows,cols", [(40, 50), (150, 140)])
+def test_zero_and_unusable_gradients(ra, rows, cols):
+    z = torch.zeros(2, rows, cols, device="cuda")
     for eps in (1e-7, 0.0):
         assert not ra.newton_schulz(z, eps=eps).any()
-    g = gradient(40, 50, 28, batch=3)
+    g = gradient(rows, cols, 28, batch=3)
     good = ra.newton_schulz(g)
     g[1, 3, 4] = float("nan")
     o = ra.newton_schulz(g)
@@ -229,8 +235,9 @@ def test_zero_and_unusable_gradients(ra):
     assert torch.isnan(o[1]).any() and torch.equal(o[0], good[0]) and torch.equal(o[2], good[2])
 
 
-def test_repeats_and_other_streams(ra):
-    g = gradient(300, 700, 29, batch=2)
+@pytest.mark.parametrize("rows,cols", [(300, 700), (100, 2000)])
+def test_repeats_and_other_streams(ra, rows, cols):
+    g = gradient(rows, cols, 29, batch=2)
     want = ra.newton_schulz(g)
     torch.cuda.synchronize()
     outs = []
@@ -242,10 +249,11 @@ def test_repeats_and_other_streams(ra):
     assert all(torch.equal(o, want) for o in outs)
 
 
-def test_replays_from_a_cuda_graph(ra):
-    g = gradient(200, 520, 30)
+@pytest.mark.parametrize("rows,cols", [(200, 520), (120, 520)])
+def test_replays_from_a_cuda_graph(ra, rows, cols):
+    g = gradient(rows, cols, 30)
     out = torch.empty_like(g)
-    ws = torch.empty(ra.ra_newton_schulz_workspace_bytes(1, 200, 520), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(ra.ra_newton_schulz_workspace_bytes(1, rows, cols), dtype=torch.uint8, device="cuda")
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
     ra.ra_newton_schulz(g, out, ws, stream=stream)
@@ -253,7 +261,7 @@ def test_replays_from_a_cuda_graph(ra):
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph, stream=stream):
         ra.ra_newton_schulz(g, out, ws, stream=stream)
-    g.copy_(gradient(200, 520, 31))
+    g.copy_(gradient(rows, cols, 31))
     out.fill_(float("nan"))
     ws.fill_(255)
     graph.replay()
@@ -262,8 +270,9 @@ def test_replays_from_a_cuda_graph(ra):
     assert torch.equal(out, ra.newton_schulz(g))
 
 
-def test_nothing_is_written_past_the_buffers(ra):
-    rows, cols, guard = 131, 77, 4096
+@pytest.mark.parametrize("rows,cols", [(131, 77), (131, 177), (77, 131)])
+def test_nothing_is_written_past_the_buffers(ra, rows, cols):
+    guard = 4096
     g = gradient(rows, cols, 32)
     buf = torch.full((rows * cols + 2 * guard,), 7.0, device="cuda")
     n = ra.ra_newton_schulz_workspace_bytes(1, rows, cols)
