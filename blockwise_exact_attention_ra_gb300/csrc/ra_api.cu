@@ -1322,7 +1322,11 @@ int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, l
     return fail(RA_ERR_INVALID_ARG, "row strides (%lld, %lld) must be 0 or at least D=%d", x_rstride, w_rstride, D);
   if (x_rstride % 8 || w_rstride % 8)
     return fail(RA_ERR_INVALID_ARG, "row strides must be multiples of 8 elements (got %lld, %lld)", x_rstride, w_rstride);
-  *out = XentShape{T, x_rstride, w_rstride, D, V, block < V ? block : V};
+  // a block whose gradient takes less than 64 MB (half of L2) is widened to that: narrower
+  // ones leave SMs idle and are bound by launches
+  const long long least = ((64ll << 20) / (2 * T)) / 256 * 256;
+  const long long wide = block > least ? block : least;
+  *out = XentShape{T, x_rstride, w_rstride, D, V, (int)(wide < V ? wide : V)};
   return RA_OK;
 }
 

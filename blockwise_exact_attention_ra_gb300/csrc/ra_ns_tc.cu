@@ -32,6 +32,7 @@
 namespace ra {
 namespace {
 
+constexpr int kThreads = 320;  // producer, MMA issuer, 8 epilogue warps
 // 5 stages of 32 KB; 8 KB of staging per epilogue warp (two tiles of 32 rows x 64
 // columns).  Extra barriers: staging filled [8].
 using S = PairSmem<5, 8192, 8>;
@@ -160,7 +161,7 @@ __device__ __forceinline__ unsigned ns_team_size(const NsArgs& a, unsigned b) {
   return (gridDim.x - team + teams - 1) / teams;
 }
 
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ns_chain_kernel(const __grid_constant__ NsArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ unsigned int s_passed;    // this CTA's units whose matrix is ready for them
@@ -168,7 +169,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   // three units ahead of another, since a unit's accumulator is the one two units before
   __shared__ unsigned int s_finished[4];
   if (threadIdx.x == 0) s_passed = s_finished[0] = s_finished[1] = s_finished[2] = s_finished[3] = 0u;
-  Pair<S> p;
+  Pair<S> p{};
   p.begin(smem_raw, a.status, a.wait_limit_ns, [&] {
     for (int w = 0; w < kPairEpiWarps; ++w) mbar_init(p.extra(w), 1);
   });
@@ -559,7 +560,7 @@ cudaError_t ns_max_pairs(int* pairs) {
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sms / 2 * 2);
-    cfg.blockDim = dim3(kPairThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = S::kAlloc;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeClusterDimension;
@@ -593,7 +594,7 @@ cudaError_t launch_ns(NsArgs& a, int pairs, cudaStream_t st) {
   count_launch();
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * pairs);
-  cfg.blockDim = dim3(kPairThreads);
+  cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = S::kAlloc;
   cfg.stream = st;
   cudaLaunchAttribute at[1];

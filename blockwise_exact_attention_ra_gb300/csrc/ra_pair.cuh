@@ -13,7 +13,7 @@
 //   warp 1      allocates TMEM (both); the leader's lane 0 issues tcgen05.mma
 //               (M 256, N bn, K 16) into one of two accumulators and commits to
 //               both CTAs' barriers
-//   warps 2-9   epilogue (both CTAs): 32 rows x bn / 2 columns each, while the
+//   8 warps     epilogue (both CTAs): 32 rows x bn / 2 columns each, while the
 //               other accumulator fills
 // The narrow tile takes 0.75 of the wide one's time, not 0.5: per product it reads
 // shared memory 1.5 times as often, which is then the limit (0.97 against 1.54 PFLOP/s
@@ -28,7 +28,7 @@
 
 namespace ra {
 
-constexpr int kPairThreads = 320, kPairEpiWarps = 8;
+constexpr int kPairEpiWarps = 8;
 
 // Shared memory: a ring of `Stages` k-slabs, `WarpBytes` of staging per epilogue warp,
 // the barriers (full, empty [Stages]; acc_full, acc_empty [2]; drain; `Extra` more).
@@ -314,6 +314,19 @@ __device__ __forceinline__ void tmem_load32(uint32_t src, float* v) {
   tmem_ld_wait();
 #pragma unroll
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
+}
+
+// 16 columns of the accumulator, added to v (or, at first, in its place).
+__device__ __forceinline__ void tmem_add16(uint32_t src, float* v, bool first) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(src));
+  tmem_ld_wait();
+#pragma unroll
+  for (int j = 0; j < 16; ++j) v[j] = first ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
 }
 
 // ---------------------------------------------------------------- tile order

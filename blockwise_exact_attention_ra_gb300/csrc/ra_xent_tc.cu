@@ -18,6 +18,19 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 using S = PairSmem<6, 4096, 0>;  // 6 stages of 32 KB, 4 KB of staging per epilogue warp
+// Three warpgroups: producer, MMA issuer and two idle warps; then the 8 epilogue warps.
+// PAIR_STATS gives the first one's registers to the others: 40 + 2 x 232 = 3 x 168.
+constexpr int kThreads = 384;
+// PAIR_STATS adds the tensor core's sums of at most 12 k-slabs (768 products) up in
+// registers: its accumulator rounds towards zero, which over 2048 products left logits of
+// 16 off by 1e-5 and the loss of a sure token by as much.  Errors of loss and lse on 8192 x
+// 131072 x 2048 (2-norm, relative), and the time: whole 1.5e-6, 2.37 ms; 16 slabs 7e-7,
+// 2.46 ms; 12 slabs 5e-7, 2.49 ms; 4 slabs 2e-7, 2.80 ms; a sum in fp32 has 4e-7.
+constexpr int kChunk = 12;
+__device__ __forceinline__ int chunk_slabs(int slabs) {
+  const int chunks = (slabs + kChunk - 1) / kChunk;
+  return (slabs + chunks - 1) / chunks;
+}
 
 // The units of one or two problems shared out over the pairs.  A unit is a tile, or one
 // split of its K.  The first problem's units go round the pairs; where the last round
@@ -62,10 +75,10 @@ struct Share {
 };
 
 template <int EPI>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     xent_pair_kernel(const __grid_constant__ PairArgs a) {
   extern __shared__ uint8_t smem_raw[];
-  Pair<S> p;
+  Pair<S> p{};
   p.begin(smem_raw, a.status, a.wait_limit_ns, [] {});
   pdl_trigger();
   pdl_wait();
@@ -75,34 +88,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
   auto k_at = [&](const PairProblem& q, int s) { return (int)((long long)((q.K + 63) / 64) * s / q.splits); };
   int which = 0, u = 0;
 
-  if (warp == 0) {
-    if (lane == 0) {
-      uint32_t cnt = 0;
-      bool ok = true;
-      for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
-        const PairProblem& q = a.q[which];
-        const int tm = (q.M + 255) / 256, tn = (q.N + q.bn - 1) / q.bn, s = u / (tm * tn);
-        const Tile t = tile_grouped(u - s * tm * tn, tm, tn, q.group_m);
-        const Operand A{&q.tm_a, &q.tm_a, q.a_mn}, B{&q.tm_b, &q.tm_b, q.b_mn};
-        ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1));
-      }
-      if (*p.abort) p.producer_drain(cnt);
-    }
-  } else if (warp == 1) {
-    uint32_t cnt = 0, lt = 0;
-    bool ok = true;
-    for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
-      const PairProblem& q = a.q[which];
-      const int s = u / Share::tiles(q);
-      const Operand A{nullptr, nullptr, q.a_mn}, B{nullptr, nullptr, q.b_mn};
-      ok = p.rank == 0 ? p.multiply(cnt, lt, a.ab_bf16, A, B, q.bn, 0, 0, k_at(q, s), k_at(q, s + 1)) : p.forward(lt);
-    }
-    if (p.rank == 0) p.multiply_drain();
-  } else {
+  if (warp >= 4) {
+    if (EPI == PAIR_STATS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
-    const int half = (int)(warp - 2) >> 2;  // columns [half * bn / 2, + bn / 2)
-    const uint32_t stage = p.sbase + S::kOut + (warp - 2) * 4096;
-    uint8_t* const stage_p = p.smem + S::kOut + (warp - 2) * 4096;
+    const int half = (int)(warp - 4) >> 2;  // columns [half * bn / 2, + bn / 2)
+    const uint32_t stage = p.sbase + S::kOut + (warp - 4) * 4096;
+    uint8_t* const stage_p = p.smem + S::kOut + (warp - 4) * 4096;
     // one 16-byte piece of the warp's staging rows of 128 bytes, 128-byte swizzle
     auto stage16 = [&](int piece, uint4 v) {
       *reinterpret_cast<uint4*>(stage_p + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
@@ -130,58 +121,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       const int row0 = t.m * 256 + (int)p.rank * 128 + (int)quarter * 32;
       const int row = row0 + (int)lane;
       const int col0 = t.n * bn + half * cols;
-      if (!p.wait(p.acc_full(b), (lt >> 1) & 1)) break;
-      tc_fence_after();
-      const uint32_t src = p.tmem + b * 256 + half * cols + ((quarter * 32) << 16);
+      const uint32_t from = p.tmem + half * cols + ((quarter * 32) << 16);
 
       if (EPI == PAIR_STATS) {
-        // Online softmax statistics of the tile's columns for this row, and the
-        // target's logit where it lies among them.  Bound by the matrix product;
-        // the exponentials (bn / 2 per thread and tile) hide behind it for K > 256.
+        // Softmax statistics of the tile's columns for this row, and the target's logit
+        // where it lies among them.  Bound by the matrix product.
         const long long y = row < q.M ? a.targets[row] : -1;
         const int ycol = (y >= col0 && y < col0 + cols) ? (int)(y - col0) : -1;
-        float m = -INFINITY, l = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          float v[32];
-          tmem_load32(src + c, v);
-          if (c == cols - 32) p.release(b);
-          if (col0 + c + 32 > q.N) {
+        float z[128];
+        const int slabs = (q.K + 63) / 64, chunk = chunk_slabs(slabs);
+        bool ok = true;
+        for (int k0 = 0; k0 < slabs; k0 += chunk, ++lt) {
+          const uint32_t acc = lt & 1;
+          ok = p.wait(p.acc_full(acc), (lt >> 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (col0 + c + j >= q.N) v[j] = -INFINITY;
-          }
-          float mk[4];
+          for (int c = 0; c < 128; c += 16)
+            if (c < cols) tmem_add16(from + acc * 256 + c, z + c, k0 == 0);
+          p.release(acc);
+        }
+        if (!ok) break;
+        --lt;  // counted once more at the end of the loop
+        float m = -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mk[k] = fmax3(v[k], v[k + 4], v[k + 8]);
+        for (int c = 0; c < 128; c += 32) {
+          if (c < cols) {
+            if (col0 + c + 32 > q.N) {
 #pragma unroll
-          for (int j = 12; j < 28; j += 8) {
+              for (int j = 0; j < 32; ++j)
+                if (col0 + c + j >= q.N) z[c + j] = -INFINITY;
+            }
+            float mk[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mk[k] = fmax3(mk[k], v[j + k], v[j + 4 + k]);
-          }
+            for (int k = 0; k < 4; ++k) mk[k] = fmax3(z[c + k], z[c + k + 4], z[c + k + 8]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mk[k] = fmaxf(mk[k], v[28 + k]);
-          const float mx = fmax3(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]), m);
-          // a row without a finite logit so far keeps l = 0 (-inf - (-inf) is not formed)
-          const float ref = mx == -INFINITY ? 0.f : mx * kLog2e;
-          float s0 = l * ex2_approx(m * kLog2e - ref), s1 = 0.f, s2 = 0.f, s3 = 0.f;
+            for (int j = 12; j < 28; j += 8) {
 #pragma unroll
-          for (int j = 0; j < 32; j += 4) {
-            s0 += ex2_approx(fmaf(v[j], kLog2e, -ref));
-            s1 += ex2_approx(fmaf(v[j + 1], kLog2e, -ref));
-            s2 += ex2_approx(fmaf(v[j + 2], kLog2e, -ref));
-            s3 += ex2_approx(fmaf(v[j + 3], kLog2e, -ref));
-          }
-          l = (s0 + s1) + (s2 + s3);
-          m = mx;
-          if (__any_sync(0xffffffffu, ycol >= c && ycol < c + 32)) {
+              for (int k = 0; k < 4; ++k) mk[k] = fmax3(mk[k], z[c + j + k], z[c + j + 4 + k]);
+            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (ycol == c + j) a.target_logit[row] = v[j];
+            for (int k = 0; k < 4; ++k) mk[k] = fmaxf(mk[k], z[c + 28 + k]);
+            m = fmax3(fmaxf(mk[0], mk[1]), fmaxf(mk[2], mk[3]), m);
           }
         }
-        if (row < q.M && col0 < q.N) a.stats[(long long)(t.n * 2 + half) * q.M + row] = make_float2(m, l);
-      } else if (EPI == PAIR_DLOGITS) {
+        // with no finite logit the sum is 0 (-inf - (-inf) is not formed)
+        const float ref = m == -INFINITY ? 0.f : m * kLog2e;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          if (c < cols) {
+            if (__any_sync(0xffffffffu, ycol >= c && ycol < c + 32)) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (ycol == c + j) a.target_logit[row] = z[c + j];
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s4[j & 3] += ex2_approx(fmaf(z[c + j], kLog2e, -ref));
+          }
+        }
+        if (row < q.M && col0 < q.N)
+          a.stats[(long long)(t.n * 2 + half) * q.M + row] = make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        continue;
+      }
+      if (!p.wait(p.acc_full(b), (lt >> 1) & 1)) break;
+      tc_fence_after();
+      const uint32_t src = from + b * 256;
+      if (EPI == PAIR_DLOGITS) {
         // d = g (e^{z - lse} - [column = target]), rounded to the operand type of
         // the two products that follow (bf16: any range; fp16: g is brought near
         // 2^13 by a power of two that those products take out again)
@@ -283,6 +289,37 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kPairThreads, 1)
       }
     }
     if (lane == 0) bulk_wait_all();
+  } else {
+    if (EPI == PAIR_STATS) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      if (lane == 0) {
+        uint32_t cnt = 0;
+        bool ok = true;
+        for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
+          const PairProblem& q = a.q[which];
+          const int tm = (q.M + 255) / 256, tn = (q.N + q.bn - 1) / q.bn, s = u / (tm * tn);
+          const Tile t = tile_grouped(u - s * tm * tn, tm, tn, q.group_m);
+          const Operand A{&q.tm_a, &q.tm_a, q.a_mn}, B{&q.tm_b, &q.tm_b, q.b_mn};
+          ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1));
+        }
+        if (*p.abort) p.producer_drain(cnt);
+      }
+    } else if (warp == 1) {
+      uint32_t cnt = 0, lt = 0;
+      bool ok = true;
+      for (int n = 0; ok && (u = share.unit(n, &which)) >= 0; ++n) {
+        const PairProblem& q = a.q[which];
+        const int s = u / Share::tiles(q);
+        const Operand A{nullptr, nullptr, q.a_mn}, B{nullptr, nullptr, q.b_mn};
+        const int k1 = k_at(q, s + 1);
+        for (int k0 = k_at(q, s); ok && k0 < k1;) {
+          const int k = EPI == PAIR_STATS ? min(k0 + chunk_slabs(k1), k1) : k1;  // one split: k1 slabs
+          ok = p.rank == 0 ? p.multiply(cnt, lt, a.ab_bf16, A, B, q.bn, 0, 0, k0, k) : p.forward(lt);
+          k0 = k;
+        }
+      }
+      if (p.rank == 0) p.multiply_drain();
+    }
   }
   p.end();
 }
@@ -316,7 +353,7 @@ cudaError_t launch_xent_pair(const PairArgs& a, int num_sms, cudaStream_t st) {
       if (err != cudaSuccess) return err;
       if (dev <= 63) ready.fetch_or(bit, std::memory_order_release);
     }
-    return launch_pdl(kernel, grid, kPairThreads, S::kAlloc, st, a);
+    return launch_pdl(kernel, grid, kThreads, S::kAlloc, st, a);
   };
   switch (a.epi) {
     case PAIR_STATS: e = run(std::integral_constant<int, PAIR_STATS>{}); break;

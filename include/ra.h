@@ -348,7 +348,7 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   weights, both in `dtype` (RA_BF16 or RA_F16), rows at x_rstride / w_rstride
  *   elements (0 = D; multiples of 8); targets [T] 64-bit integers.  D is a multiple
  *   of 8; T, V and block are of any size >= 1 (blocks that are multiples of 256 fill
- *   the tiles).
+ *   the tiles; a block whose gradient takes less than 64 MB is widened to that).
  *   A token whose target equals ignore_index has loss 0 and no gradient (its lse is
  *   still written, and its x, multiplied by exact zeros in dw, has to be finite).  Any other target outside [0, V) gives loss NaN, no gradient,
  *   and RA_ERR_INVALID_ARG in the status word.
@@ -356,8 +356,9 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   are fp32.  Infinities and NaN among the logits give NaN, as the formula does; a
  *   row whose logits are all -inf has lse = -inf and loss NaN.
  *   workspace: device memory, 256-byte aligned, of the size given (about T V / 8
- *   bytes for the forward, 2 T block bytes, and 4 T D where dx is 16-bit and there
- *   is more than one block, for the backward).  It must not be in use by work that
+ *   bytes for the forward; 2 T block bytes, 4 T D where dx is 16-bit and there is more
+ *   than one block, and up to 20 MB each for dx and dw where their products are split,
+ *   for the backward).  It must not be in use by work that
  *   overlaps the call on the GPU. */
 size_t ra_xent_fwd_workspace_bytes(ra_dtype dtype, long long T, int D, int V);
 int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,

@@ -116,6 +116,31 @@ def test_many_tiles(ra):
     check(ra, x, w, y, g, loss, lse, dx, dw)
 
 
+@pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32)])
+def test_several_blocks(ra, dtype, out):
+    # blocks of more than 64 MB of gradient (2 x 2000 entries, the last of 200): dx summed
+    # over them in fp32, in the workspace or in dx itself
+    T, D, V, block = 16800, 72, 4200, 2000
+    assert 2 * T * block > 64 << 20
+    x, w, y, g = make(T, D, V, dtype, 6)
+    loss, lse = ra.xent_fwd(x, w, y)
+    dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block, dx_dtype=out, dw_dtype=out)
+    ra.ra_sync_status()
+    check(ra, x, w, y, g, loss, lse, dx, dw)
+
+
+def test_several_blocks_with_split_products(ra):
+    # few tiles of dx and long blocks: K of dx = d W is split, its planes summed over blocks
+    T, D, V, block = 4200, 8, 24500, 12000
+    assert 2 * T * block > 64 << 20
+    x, w, y, g = make(T, D, V, torch.bfloat16, 17)
+    loss, lse = ra.xent_fwd(x, w, y)
+    for out in (torch.bfloat16, torch.float32):
+        dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block, dx_dtype=out, dw_dtype=out)
+        ra.ra_sync_status()
+        check(ra, x, w, y, g, loss, lse, dx, dw)
+
+
 def test_row_strides(ra):
     x, w, y, g = make(200, 128, 700, torch.bfloat16, 11)
     wide_x = torch.full((200, 3, 128), float("nan"), dtype=torch.bfloat16, device="cuda")

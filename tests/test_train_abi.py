@@ -22,13 +22,16 @@ def test_xent_workspaces(ra):
     fwd, bwd = ra.ra_xent_fwd_workspace_bytes, ra.ra_xent_bwd_workspace_bytes
     assert fwd(ra.RA_BF16, 1000, 64, 3001) >= 1000 * 4 + 1000 * 8 * ((3001 + 127) // 128)
     assert fwd(ra.RA_F32, 1000, 64, 3001) == 0 and fwd(ra.RA_BF16, 0, 64, 10) == 0
-    one = bwd(ra.RA_BF16, ra.RA_BF16, 1000, 64, 3001, 3001)
-    assert one >= 1000 * 3001 * 2
-    assert bwd(ra.RA_BF16, ra.RA_BF16, 1000, 64, 3001, 1 << 30) == one      # a block past V is V
-    some = bwd(ra.RA_BF16, ra.RA_BF16, 1000, 64, 3001, 512)
-    assert 1000 * (512 * 2 + 64 * 4) <= some < one
-    assert bwd(ra.RA_BF16, ra.RA_F32, 1000, 64, 3001, 512) <= some - 1000 * 64 * 4
-    assert bwd(ra.RA_BF16, 9, 1000, 64, 3001, 512) == 0
+    T, V = 100000, 3001
+    one = bwd(ra.RA_BF16, ra.RA_BF16, T, 64, V, V)
+    assert one >= T * V * 2
+    assert bwd(ra.RA_BF16, ra.RA_BF16, T, 64, V, 1 << 30) == one      # a block past V is V
+    some = bwd(ra.RA_BF16, ra.RA_BF16, T, 64, V, 512)
+    assert T * (512 * 2 + 64 * 4) <= some < one
+    assert bwd(ra.RA_BF16, ra.RA_F32, T, 64, V, 512) <= some - T * 64 * 4
+    assert bwd(ra.RA_BF16, 9, T, 64, V, 512) == 0
+    # a narrow block is widened until its gradient takes 64 MB
+    assert bwd(ra.RA_BF16, ra.RA_F32, 1000, 64, V, 1) == bwd(ra.RA_BF16, ra.RA_F32, 1000, 64, V, V)
 
 
 def test_xent_refusals(ra):
