@@ -1282,7 +1282,10 @@ struct PairPlan {
   // q: M, N, K, the majornesses and the output; sets the operands' maps and the cut
   int problem(PairProblem& q, Cut cut, const Operand& A, const Operand& B, int dtype) const {
     int rc;
-    if ((rc = make_map_3d(&q.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, q.a_mn ? 64 : 128)) ||
+    // few rows: only those are loaded (whole boxes would fill in zeros, which costs as much
+    // as data)
+    q.a_rows = !q.a_mn && q.M < 128 ? (q.M + 7) / 8 * 8 : 128;
+    if ((rc = make_map_3d(&q.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, q.a_mn ? 64 : q.a_rows)) ||
         (rc = make_map_3d(&q.tm_b, B.p, dtype, B.cols, B.rows, 1, B.ld, 0, 64, q.b_mn ? 64 : cut.bn / 2)))
       return rc;
     q.bn = cut.bn;
@@ -1322,9 +1325,10 @@ int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, l
     return fail(RA_ERR_INVALID_ARG, "row strides (%lld, %lld) must be 0 or at least D=%d", x_rstride, w_rstride, D);
   if (x_rstride % 8 || w_rstride % 8)
     return fail(RA_ERR_INVALID_ARG, "row strides must be multiples of 8 elements (got %lld, %lld)", x_rstride, w_rstride);
-  // a block whose gradient takes less than 64 MB (half of L2) is widened to that: narrower
-  // ones leave SMs idle and are bound by launches
-  const long long least = ((64ll << 20) / (2 * T)) / 256 * 256;
+  // a block whose gradient takes less than 256 MB is widened to that: narrower ones are
+  // bound by launches and leave SMs idle at their ends (4096 tokens, D 2048, V 32768: 1193
+  // us in blocks of 64 MB, 1021 us in one of 256 MB)
+  const long long least = ((256ll << 20) / (2 * T)) / 256 * 256;
   const long long wide = block > least ? block : least;
   *out = XentShape{T, x_rstride, w_rstride, D, V, (int)(wide < V ? wide : V)};
   return RA_OK;

@@ -240,11 +240,12 @@ enum PairEpi {
   PAIR_STORE = 2,    // C, 16-bit or fp32, fp32 optionally added to what is there
 };
 struct PairProblem {
-  // operands: K-major: boxes of 64 x 128 (A), 64 x bn/2 (B); MN-major: 64 x 64
+  // operands: K-major: boxes of 64 x a_rows (A), 64 x bn/2 (B); MN-major: 64 x 64
   CUtensorMap tm_a, tm_b;
   CUtensorMap tm_c;   // output: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle
   int M, N, K;
   int a_mn, b_mn;
+  int a_rows;         // rows of a K-major A a CTA loads: 128, or all of them (M < 128, multiple of 8)
   int bn;             // tile columns: 128 or 256
   int splits;         // PAIR_STORE, fp32: K is split, split s writes plane s of C
   int group_m;        // tile rows taken together

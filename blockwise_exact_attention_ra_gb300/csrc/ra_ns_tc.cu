@@ -420,17 +420,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int c = 0; c < cols; c += 64) {
             if (c) prefetch(c);
             float v[64];
-            {
-              uint32_t r0[32], r1[32];
-              RA_TMEM_LD32(src + c, r0);
-              RA_TMEM_LD32(src + c + 32, r1);
-              tmem_ld_wait();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                v[j] = __uint_as_float(r0[j]);
-                v[32 + j] = __uint_as_float(r1[j]);
-              }
-            }
+            tmem_load64(src + c, v);
             if (c == cols - 64) p.release(acc);
             for (int s = 1; s < f.splits; ++s) {
               const float* q = partial(s) + c * 32;

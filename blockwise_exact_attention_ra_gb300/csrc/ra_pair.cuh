@@ -106,6 +106,7 @@ __device__ __forceinline__ void tma_add_3d(const CUtensorMap* map, uint32_t src,
                : "memory");
 }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read_but_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
@@ -200,13 +201,15 @@ struct Pair {
   }
 
   // Producer (one lane of warp 0 in both CTAs): k-slabs [k_from, k_to) of the tile
-  // whose first row and column are m0 and n0.
+  // whose first row and column are m0 and n0.  a_rows < 128: all of A's rows, K-major, lie
+  // in the leader and are that few: the peer loads none, and what the rest of the A slab
+  // holds makes only rows of C that nobody reads.
   __device__ __forceinline__ bool produce(uint32_t& cnt, const Operand& A, const Operand& B, int bn, int m0, int n0,
-                                          int batch, int k_from, int k_to) const {
+                                          int batch, int k_from, int k_to, int a_rows = 128) const {
     const int a_block = m0 / 256, b_block = n0 / 256;
     m0 += (int)rank * 128;
     n0 += (int)rank * (bn / 2);
-    const uint32_t bytes = 2 * (S::kA + bn * 64);
+    const uint32_t bytes = (a_rows < 128 ? a_rows * 128 : 2 * S::kA) + bn * 128;
     for (int kb = k_from; kb < k_to; ++kb, ++cnt) {
       const int s = cnt % S::kStages;
       if (!wait(empty(s), ((cnt / S::kStages) & 1) ^ 1)) return false;
@@ -217,7 +220,7 @@ struct Pair {
       if (A.mn_at(a_block, kb)) {
         pair_tma_load(dA, A.by_mn, bar, m0, k0, batch);
         pair_tma_load(dA + 8192, A.by_mn, bar, m0 + 64, k0, batch);
-      } else {
+      } else if (a_rows == 128 || rank == 0) {
         pair_tma_load(dA, A.by_k, bar, k0, m0, batch);
       }
       if (B.mn_at(b_block, kb)) {
@@ -316,17 +319,17 @@ __device__ __forceinline__ void tmem_load32(uint32_t src, float* v) {
   for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]);
 }
 
-// 16 columns of the accumulator, added to v (or, at first, in its place).
-__device__ __forceinline__ void tmem_add16(uint32_t src, float* v, bool first) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(src));
+// 64 columns, with one wait.
+__device__ __forceinline__ void tmem_load64(uint32_t src, float* v) {
+  uint32_t r0[32], r1[32];
+  RA_TMEM_LD32(src, r0);
+  RA_TMEM_LD32(src + 32, r1);
   tmem_ld_wait();
 #pragma unroll
-  for (int j = 0; j < 16; ++j) v[j] = first ? __uint_as_float(r[j]) : v[j] + __uint_as_float(r[j]);
+  for (int j = 0; j < 32; ++j) {
+    v[j] = __uint_as_float(r0[j]);
+    v[32 + j] = __uint_as_float(r1[j]);
+  }
 }
 
 // ---------------------------------------------------------------- tile order

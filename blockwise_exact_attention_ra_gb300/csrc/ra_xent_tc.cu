@@ -17,7 +17,8 @@ namespace ra {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-using S = PairSmem<6, 4096, 0>;  // 6 stages of 32 KB, 4 KB of staging per epilogue warp
+// 5 stages of 32 KB (4, 5 and 6 run alike); two staging buffers of 4 KB per epilogue warp.
+using S = PairSmem<5, 8192, 0>;
 // Three warpgroups: producer, MMA issuer and two idle warps; then the 8 epilogue warps.
 // PAIR_STATS gives the first one's registers to the others: 40 + 2 x 232 = 3 x 168.
 constexpr int kThreads = 384;
@@ -35,17 +36,19 @@ __device__ __forceinline__ int chunk_slabs(int slabs) {
 // The units of one or two problems shared out over the pairs.  A unit is a tile, or one
 // split of its K.  The first problem's units go round the pairs; where the last round
 // leaves pairs idle, those take as many of the second's as fit into one unit of the first
-// (by k-slabs); the rest goes round again, beginning with them.  With dx (128 tiles of 128
+// (by k-slabs; a unit takes 6 slabs' time at least, its epilogue); the rest goes round
+// again, beginning with them.  With dx (128 tiles of 128
 // slabs) and dw (256 of 64) on 76 pairs the longest share is 448 slabs; in launches of
 // their own they take 2 x 128 + 4 x 64 = 512.
 struct Share {
-  int units0, units1, pairs, pair, over, fill;
+  int units0, units1, pairs, pair, over, fill, mine0;
   __device__ __forceinline__ Share(const PairArgs& a, int pair_, int pairs_) : pairs(pairs_), pair(pair_) {
-    const int slabs0 = slabs(a.q[0]), slabs1 = a.problems > 1 ? slabs(a.q[1]) : 1;
+    const int cost0 = max(slabs(a.q[0]), 6), cost1 = a.problems > 1 ? max(slabs(a.q[1]), 6) : 1;
     units0 = tiles(a.q[0]) * a.q[0].splits;
     units1 = a.problems > 1 ? tiles(a.q[1]) * a.q[1].splits : 0;
     over = units0 % pairs;                                        // pairs of the last round
-    fill = over ? (slabs0 + slabs1 / 2) / (slabs1 > 0 ? slabs1 : 1) : 0;  // units of the second that fill it up
+    mine0 = units0 / pairs + (pair < over ? 1 : 0);
+    fill = over ? (cost0 + cost1 / 2) / cost1 : 0;                // units of the second that fill it up
   }
   static __device__ __forceinline__ int tiles(const PairProblem& q) {
     return ((q.M + 255) / 256) * ((q.N + q.bn - 1) / q.bn);
@@ -53,7 +56,6 @@ struct Share {
   static __device__ __forceinline__ int slabs(const PairProblem& q) { return ((q.K + 63) / 64 + q.splits - 1) / q.splits; }
   // The n-th unit of this pair: index within its problem, the problem in *which; -1: none.
   __device__ __forceinline__ int unit(int n, int* which) const {
-    const int mine0 = units0 / pairs + (pair < over ? 1 : 0);
     *which = 0;
     if (n < mine0) return pair + n * pairs;
     *which = 1;
@@ -85,32 +87,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t warp = warp_id(), lane = lane_id();
   const Share share(a, blockIdx.x / 2, gridDim.x / 2);
   // split s of a problem takes an even share of the k-slabs
-  auto k_at = [&](const PairProblem& q, int s) { return (int)((long long)((q.K + 63) / 64) * s / q.splits); };
+  // (k-slabs times splits stay below 2^24 * 76)
+  auto k_at = [&](const PairProblem& q, int s) {
+    const unsigned slabs = (q.K + 63) / 64;
+    return (int)(q.splits == 1 ? (s ? slabs : 0u) : slabs * s / q.splits);
+  };
   int which = 0, u = 0;
 
   if (warp >= 4) {
     if (EPI == PAIR_STATS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
     const int half = (int)(warp - 4) >> 2;  // columns [half * bn / 2, + bn / 2)
-    const uint32_t stage = p.sbase + S::kOut + (warp - 4) * 4096;
-    uint8_t* const stage_p = p.smem + S::kOut + (warp - 4) * 4096;
-    // one 16-byte piece of the warp's staging rows of 128 bytes, 128-byte swizzle
-    auto stage16 = [&](int piece, uint4 v) {
-      *reinterpret_cast<uint4*>(stage_p + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
-    };
-    // the staging buffer is free again once the last copy out of it has read it
-    auto stage_free = [&]() {
-      if (lane == 0) bulk_wait_read();
-      __syncwarp();
+    const uint32_t stage = p.sbase + S::kOut + (warp - 4) * 8192;
+    uint8_t* const stage_p = p.smem + S::kOut + (warp - 4) * 8192;
+    // one 16-byte piece of staging rows of 128 bytes, 128-byte swizzle; buffer 0 or 1
+    auto stage16 = [&](int buf, int piece, uint4 v) {
+      *reinterpret_cast<uint4*>(stage_p + buf * 4096 + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
     };
     auto stage_out = [&](auto issue) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         issue();
-        bulk_commit();
+        bulk_commit();  // a group per buffer filled, also where there is nothing to copy
       }
     };
+    // 64 columns as 16-bit values into buffer buf
+    auto stage64 = [&](int buf, const float* v, int bf) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        stage16(buf, j, make_uint4(pack_pair(v[8 * j], v[8 * j + 1], bf), pack_pair(v[8 * j + 2], v[8 * j + 3], bf),
+                                   pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf)));
+    };
+    int buf = 0;  // 16-bit outputs: the buffers in turn
     uint32_t lt = 0;
     for (int n = 0; (u = share.unit(n, &which)) >= 0; ++n, ++lt) {
       const PairProblem& q = a.q[which];
@@ -136,13 +145,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = p.wait(p.acc_full(acc), (lt >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
+          if (row0 < q.M) {
+            const uint32_t src = from + acc * 256;
+            if (k0 == 0) {
+              tmem_load64(src, z);
+              if (cols > 64) tmem_load64(src + 64, z + 64);
+            } else {
 #pragma unroll
-          for (int c = 0; c < 128; c += 16)
-            if (c < cols) tmem_add16(from + acc * 256 + c, z + c, k0 == 0);
+              for (int c = 0; c < 128; c += 32) {
+                if (c < cols) {
+                  float v[32];
+                  tmem_load32(src + c, v);
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) z[c + j] += v[j];
+                }
+              }
+            }
+          }
           p.release(acc);
         }
         if (!ok) break;
         --lt;  // counted once more at the end of the loop
+        if (row0 >= q.M || col0 >= q.N) continue;
         float m = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -167,7 +191,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         // with no finite logit the sum is 0 (-inf - (-inf) is not formed)
         const float ref = m == -INFINITY ? 0.f : m * kLog2e;
-        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 log2e = make_float2(kLog2e, kLog2e), off = make_float2(-ref, -ref);
+        float2 s2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           if (c < cols) {
@@ -177,16 +202,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 if (ycol == c + j) a.target_logit[row] = z[c + j];
             }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) s4[j & 3] += ex2_approx(fmaf(z[c + j], kLog2e, -ref));
+            for (int j = 0; j < 32; j += 2) {
+              const float2 e = __ffma2_rn(make_float2(z[c + j], z[c + j + 1]), log2e, off);
+              s2[(j / 2) & 1] = __fadd2_rn(s2[(j / 2) & 1], make_float2(ex2_approx(e.x), ex2_approx(e.y)));
+            }
           }
         }
-        if (row < q.M && col0 < q.N)
-          a.stats[(long long)(t.n * 2 + half) * q.M + row] = make_float2(m, (s4[0] + s4[1]) + (s4[2] + s4[3]));
+        if (row < q.M)
+          a.stats[(long long)(t.n * 2 + half) * q.M + row] =
+              make_float2(m, (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y));
         continue;
       }
       if (!p.wait(p.acc_full(b), (lt >> 1) & 1)) break;
       tc_fence_after();
       const uint32_t src = from + b * 256;
+      if (row0 >= q.M || col0 >= q.N) {  // nothing of this warp's part is inside
+        p.release(b);
+        continue;
+      }
       if (EPI == PAIR_DLOGITS) {
         // d = g (e^{z - lse} - [column = target]), rounded to the operand type of
         // the two products that follow (bf16: any range; fp16: g is brought near
@@ -197,33 +230,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float lse2 = live ? a.lse[row] * kLog2e : 0.f;
         const long long yc = y - a.col_off - col0;
         const int ycol = (live && yc >= 0 && yc < cols) ? (int)yc : -1;
+        const float2 log2e = make_float2(kLog2e, kLog2e), off = make_float2(-lse2, -lse2), gg = make_float2(g, g);
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 64) {
-          stage_free();
+        for (int c = 0; c < cols; c += 64, buf ^= 1) {
+          if (lane == 0) bulk_wait_read_but_one();
+          float v[64];
+          tmem_load64(src + c, v);
+          if (c == cols - 64) p.release(b);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int cc = c + 32 * h;
-            float v[32];
-            tmem_load32(src + cc, v);
-            if (cc == cols - 32) p.release(b);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = ex2_approx(fmaf(v[j], kLog2e, -lse2));
-            if (__any_sync(0xffffffffu, ycol >= cc && ycol < cc + 32)) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (ycol == cc + j) v[j] -= 1.f;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = live ? v[j] * g : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              stage16(4 * h + j, make_uint4(pack_pair(v[8 * j], v[8 * j + 1], a.ab_bf16),
-                                            pack_pair(v[8 * j + 2], v[8 * j + 3], a.ab_bf16),
-                                            pack_pair(v[8 * j + 4], v[8 * j + 5], a.ab_bf16),
-                                            pack_pair(v[8 * j + 6], v[8 * j + 7], a.ab_bf16)));
+          for (int j = 0; j < 64; j += 2) {
+            const float2 e = __ffma2_rn(make_float2(v[j], v[j + 1]), log2e, off);
+            v[j] = ex2_approx(e.x);
+            v[j + 1] = ex2_approx(e.y);
           }
+          if (__any_sync(0xffffffffu, ycol >= c && ycol < c + 64)) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (ycol == c + j) v[j] -= 1.f;
+          }
+#pragma unroll
+          for (int j = 0; j < 64; j += 2) {
+            const float2 e = __fmul2_rn(make_float2(v[j], v[j + 1]), gg);
+            v[j] = live ? e.x : 0.f;  // a row without loss may hold anything
+            v[j + 1] = live ? e.y : 0.f;
+          }
+          __syncwarp();
+          stage64(buf, v, a.ab_bf16);
           stage_out([&]() {
-            if (row0 < q.M && col0 + c < q.N) tma_store_3d(&q.tm_c, stage, col0 + c, row0, 0);
+            if (col0 + c < q.N) tma_store_3d(&q.tm_c, stage + buf * 4096, col0 + c, row0, 0);
           });
         }
       } else {
@@ -231,59 +265,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // there (each element once per launch, so the sum's order is fixed).  Split
         // along K, each split has a plane of its own.
         const float mul = a.scale ? a.scale[1] : 1.f;
-        if (q.c_dtype == RA_F32) {
+        const bool f32 = q.c_dtype == RA_F32;
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            stage_free();
-            float v[32];
-            tmem_load32(src + c, v);
-            if (c == cols - 32) p.release(b);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-              stage16(j, make_uint4(__float_as_uint(v[4 * j] * mul), __float_as_uint(v[4 * j + 1] * mul),
-                                    __float_as_uint(v[4 * j + 2] * mul), __float_as_uint(v[4 * j + 3] * mul)));
-            stage_out([&]() {
-              if (row0 < q.M && col0 + c < q.N) {
-                if (q.c_accumulate) tma_add_3d(&q.tm_c, stage, col0 + c, row0, split);
-                else tma_store_3d(&q.tm_c, stage, col0 + c, row0, split);
-              }
-            });
+        for (int c = 0; c < cols; c += 64) {
+          // fp32 takes both buffers at once, 16-bit values one at a time
+          if (lane == 0) {
+            if (f32) bulk_wait_read();
+            else bulk_wait_read_but_one();
           }
-        } else {
-          const int bf = q.c_dtype == RA_BF16;
-#pragma unroll 1
-          for (int c = 0; c < cols; c += 64) {
-            stage_free();
+          float v[64];
+          tmem_load64(src + c, v);
+          if (c == cols - 64) p.release(b);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int cc = c + 32 * h;
-              float v[32];
-              tmem_load32(src + cc, v);
-              if (cc == cols - 32) p.release(b);
+          for (int j = 0; j < 64; ++j) v[j] *= mul;
+          __syncwarp();
+          if (f32) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] *= mul;
-              if (q.c_add && row < q.M) {  // N is a multiple of 8 where c_add is used
-                const float4* add = reinterpret_cast<const float4*>(q.c_add + (long long)row * q.N + col0 + cc);
+            for (int j = 0; j < 16; ++j)
+              stage16(j >> 3, j & 7, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
+                                                __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            stage_out([&]() {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                  if (col0 + cc + 4 * j < q.N) {
-                    const float4 f = add[j];
-                    v[4 * j] += f.x;
-                    v[4 * j + 1] += f.y;
-                    v[4 * j + 2] += f.z;
-                    v[4 * j + 3] += f.w;
-                  }
+              for (int h = 0; h < 2; ++h) {
+                const int cc = col0 + c + 32 * h;
+                if (cc < q.N) {
+                  if (q.c_accumulate) tma_add_3d(&q.tm_c, stage + h * 4096, cc, row0, split);
+                  else tma_store_3d(&q.tm_c, stage + h * 4096, cc, row0, split);
                 }
               }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                stage16(4 * h + j,
-                        make_uint4(pack_pair(v[8 * j], v[8 * j + 1], bf), pack_pair(v[8 * j + 2], v[8 * j + 3], bf),
-                                   pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf)));
-            }
-            stage_out([&]() {
-              if (row0 < q.M && col0 + c < q.N) tma_store_3d(&q.tm_c, stage, col0 + c, row0, 0);
             });
+          } else {
+            if (q.c_add && row < q.M) {  // N is a multiple of 8 where c_add is used
+              const float4* add = reinterpret_cast<const float4*>(q.c_add + (long long)row * q.N + col0 + c);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                if (col0 + c + 4 * j < q.N) {
+                  const float4 f = add[j];
+                  v[4 * j] += f.x;
+                  v[4 * j + 1] += f.y;
+                  v[4 * j + 2] += f.z;
+                  v[4 * j + 3] += f.w;
+                }
+              }
+            }
+            stage64(buf, v, q.c_dtype == RA_BF16);
+            stage_out([&]() {
+              if (col0 + c < q.N) tma_store_3d(&q.tm_c, stage + buf * 4096, col0 + c, row0, 0);
+            });
+            buf ^= 1;
           }
         }
       }
@@ -300,7 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int tm = (q.M + 255) / 256, tn = (q.N + q.bn - 1) / q.bn, s = u / (tm * tn);
           const Tile t = tile_grouped(u - s * tm * tn, tm, tn, q.group_m);
           const Operand A{&q.tm_a, &q.tm_a, q.a_mn}, B{&q.tm_b, &q.tm_b, q.b_mn};
-          ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1));
+          ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1), q.a_rows);
         }
         if (*p.abort) p.producer_drain(cnt);
       }

@@ -348,7 +348,7 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   weights, both in `dtype` (RA_BF16 or RA_F16), rows at x_rstride / w_rstride
  *   elements (0 = D; multiples of 8); targets [T] 64-bit integers.  D is a multiple
  *   of 8; T, V and block are of any size >= 1 (blocks that are multiples of 256 fill
- *   the tiles; a block whose gradient takes less than 64 MB is widened to that).
+ *   the tiles; a block whose gradient takes less than 256 MB is widened to that).
  *   A token whose target equals ignore_index has loss 0 and no gradient (its lse is
  *   still written, and its x, multiplied by exact zeros in dw, has to be finite).  Any other target outside [0, V) gives loss NaN, no gradient,
  *   and RA_ERR_INVALID_ARG in the status word.

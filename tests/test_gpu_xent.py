@@ -116,29 +116,80 @@ def test_many_tiles(ra):
     check(ra, x, w, y, g, loss, lse, dx, dw)
 
 
+def check_on_gpu(x, w, y, g, loss, lse, dx, dw):
+    """`check` for sizes at which the CPU's fp64 takes too long: the same formulas and
+    bounds in fp64 torch operations on the GPU."""
+    X, W, G = x.double(), w.double(), g.double()
+    (T, D), V = X.shape, W.shape[0]
+    z = X @ W.T
+    r_lse = torch.logsumexp(z, dim=1)
+    kept = y != -100
+    at = torch.where(kept, y, torch.zeros_like(y))[:, None]
+    s = (X.abs() @ W.abs().T).amax(dim=1)
+    e_z = D * 2.0 ** -23 * s
+    e_lse = e_z + 2.0 ** -21 * z.abs().amax(dim=1) + 2.0 ** -18 + 2.0 ** -23 * r_lse.abs()
+    zero = torch.zeros_like(r_lse)
+
+    def inside(name, got, want, bound):
+        worst = float(((got.double() - want).abs() - bound).max())
+        assert worst <= 0.0, f"{name}: past its bound by {worst:.3e}"
+    inside("lse", lse, r_lse, e_lse)
+    inside("loss", loss, torch.where(kept, r_lse - z.gather(1, at)[:, 0], zero), torch.where(kept, e_lse + e_z, zero))
+    live = torch.where(kept, G, zero)
+    p = torch.exp(z - r_lse[:, None])
+    d = p.clone()
+    d.scatter_add_(1, at, torch.full_like(r_lse, -1.0)[:, None])
+    d *= live[:, None]
+    e_d = live.abs()[:, None] * p * (e_z + e_lse)[:, None] * 1.01 + 1.01 * U[x.dtype] * d.abs()
+    e_d += (1.0 + live.abs()[:, None]) * 2.0 ** -126
+    if x.dtype == torch.float16:
+        e_d += live.abs().max() * 2.0 ** -38
+    e_d *= kept[:, None]
+    for name, got, want, bound in (
+            ("dx", dx, d @ W, e_d @ W.abs() + V * 2.0 ** -23 * (d.abs() @ W.abs())),
+            ("dw", dw, d.T @ X, e_d.T @ X.abs() + T * 2.0 ** -23 * (d.abs().T @ X.abs()))):
+        tiny = 2.0 ** -25 if got.dtype == torch.float16 else 0.0
+        inside(name, got, want, bound + U[got.dtype] * (want.abs() + bound) + tiny)
+
+
 @pytest.mark.parametrize("dtype,out", [(torch.bfloat16, torch.bfloat16), (torch.float16, torch.float32)])
 def test_several_blocks(ra, dtype, out):
-    # blocks of more than 64 MB of gradient (2 x 2000 entries, the last of 200): dx summed
+    # blocks of more than 256 MB of gradient (2 x 4100 entries, the last of 200): dx summed
     # over them in fp32, in the workspace or in dx itself
-    T, D, V, block = 16800, 72, 4200, 2000
-    assert 2 * T * block > 64 << 20
+    T, D, V, block = 33000, 72, 8400, 4100
+    assert 2 * T * block > 256 << 20
     x, w, y, g = make(T, D, V, dtype, 6)
     loss, lse = ra.xent_fwd(x, w, y)
     dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block, dx_dtype=out, dw_dtype=out)
     ra.ra_sync_status()
-    check(ra, x, w, y, g, loss, lse, dx, dw)
+    check_on_gpu(x, w, y, g, loss, lse, dx, dw)
 
 
 def test_several_blocks_with_split_products(ra):
-    # few tiles of dx and long blocks: K of dx = d W is split, its planes summed over blocks
-    T, D, V, block = 4200, 8, 24500, 12000
-    assert 2 * T * block > 64 << 20
+    # few tiles of dx and long blocks: K of dx = d W is split, its planes summed over blocks;
+    # the last block (100) is too short for as many splits
+    T, D, V, block = 4200, 8, 64300, 32100
+    assert 2 * T * block > 256 << 20
     x, w, y, g = make(T, D, V, torch.bfloat16, 17)
     loss, lse = ra.xent_fwd(x, w, y)
     for out in (torch.bfloat16, torch.float32):
         dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block, dx_dtype=out, dw_dtype=out)
         ra.ra_sync_status()
-        check(ra, x, w, y, g, loss, lse, dx, dw)
+        check_on_gpu(x, w, y, g, loss, lse, dx, dw)
+
+
+def test_checks_on_cpu_and_gpu_agree(ra):
+    x, w, y, g = make(90, 64, 300, torch.float16, 18)
+    loss, lse = ra.xent_fwd(x, w, y)
+    dx, dw = ra.xent_bwd(x, w, y, lse, g)
+    check(ra, x, w, y, g, loss, lse, dx, dw)
+    check_on_gpu(x, w, y, g, loss, lse, dx, dw)
+    # a mistake planted in what the oracle is told is past the bounds of both
+    g2 = g.clone()
+    g2[int(torch.nonzero(y != -100)[0])] *= 1.1
+    for f in (lambda: check(ra, x, w, y, g2, loss, lse, dx, dw), lambda: check_on_gpu(x, w, y, g2, loss, lse, dx, dw)):
+        with pytest.raises(AssertionError):
+            f()
 
 
 def test_row_strides(ra):

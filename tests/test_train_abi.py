@@ -30,7 +30,7 @@ def test_xent_workspaces(ra):
     assert T * (512 * 2 + 64 * 4) <= some < one
     assert bwd(ra.RA_BF16, ra.RA_F32, T, 64, V, 512) <= some - T * 64 * 4
     assert bwd(ra.RA_BF16, 9, T, 64, V, 512) == 0
-    # a narrow block is widened until its gradient takes 64 MB
+    # a narrow block is widened until its gradient takes 256 MB
     assert bwd(ra.RA_BF16, ra.RA_F32, 1000, 64, V, 1) == bwd(ra.RA_BF16, ra.RA_F32, 1000, 64, V, V)
 
 
