@@ -8,38 +8,67 @@
 
 namespace ra {
 
-__device__ __forceinline__ float load_as_f32(const void* p, int dtype, long long i) {
-  if (dtype == RA_F32) return static_cast<const float*>(p)[i];
-  if (dtype == RA_BF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
-  return __half2float(static_cast<const __half*>(p)[i]);
+constexpr int kNsBatch = 4;  // groups of eight in flight per thread; eight run no faster
+
+// One element as its bits, and as a number.  Loading and converting are apart so that a
+// thread's loads are all in flight before the first is used.
+__device__ __forceinline__ uint32_t load_bits(const NsInput& in, long long i) {
+  return in.dtype == RA_F32 ? static_cast<const uint32_t*>(in.g)[i] : static_cast<const uint16_t*>(in.g)[i];
+}
+__device__ __forceinline__ float bits_value(const NsInput& in, uint32_t u) {
+  if (in.dtype == RA_F32) return __uint_as_float(u);
+  if (in.dtype == RA_BF16) return __uint_as_float(u << 16);
+  return __half2float(__ushort_as_half((unsigned short)u));
 }
 
-constexpr int kNsBatch = 4;  // groups of eight in flight per thread
-
-// Eight consecutive elements of a row (fewer at its end; the rest read as zero).
-__device__ __forceinline__ void load8(const NsInput& in, long long off, int left, float* v) {
+// Eight consecutive elements of a row (fewer at its end; the rest read as zero), as
+// loaded: fp32, or 16-bit in x.
+struct NsRaw {
+  uint4 x, y;
+};
+__device__ __forceinline__ NsRaw load8(const NsInput& in, long long off, int left) {
+  NsRaw r{{0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
   if (in.vec && left >= 8) {
     if (in.dtype == RA_F32) {
-      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(in.g) + off);
-      const float4 x = p[0], y = p[1];
-      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(in.g) + off);
+      r.x = p[0];
+      r.y = p[1];
     } else {
-      const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.g) + off);
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float2 f;
-        if (in.dtype == RA_BF16) f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[j]));
-        else f = unpack_half2(w[j]);
-        v[2 * j] = f.x;
-        v[2 * j + 1] = f.y;
-      }
+      r.x = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(in.g) + off);
     }
-    return;
-  }
+  } else if (left > 0) {
+    uint32_t w[8];
+    if (in.dtype == RA_F32) {
+      const uint32_t* p = static_cast<const uint32_t*>(in.g) + off;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = j < left ? load_as_f32(in.g, in.dtype, off + j) : 0.f;
+      for (int j = 0; j < 8; ++j) w[j] = j < left ? p[j] : 0u;
+      r.y = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(in.g) + off;
+      uint32_t h[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = j < left ? p[j] : 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = h[2 * j] | h[2 * j + 1] << 16;
+    }
+    r.x = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  return r;
+}
+__device__ __forceinline__ void unpack8(const NsInput& in, const NsRaw& r, float* v) {
+  const uint32_t w[8] = {r.x.x, r.x.y, r.x.z, r.x.w, r.y.x, r.y.y, r.y.z, r.y.w};
+  if (in.dtype == RA_F32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = in.dtype == RA_BF16 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u))
+                                           : unpack_half2(w[j]);
+      v[2 * j] = f.x;
+      v[2 * j + 1] = f.y;
+    }
+  }
 }
 
 // Squares are summed in three accumulators by magnitude, the large values scaled

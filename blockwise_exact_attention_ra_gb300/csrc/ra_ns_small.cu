@@ -154,13 +154,19 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
     const int first = (int)rank * C + (int)half * kCols;    // column of X
     const long long at = entry * a.in.bstride;
     if (a.tall) {  // X's columns are G's rows: the lanes read consecutive elements
+      uint32_t u[kCols];
 #pragma unroll
       for (int j = 0; j < kCols; ++j)
-        x[j] = (row < a.m && first + j < a.n) ? load_as_f32(a.in.g, a.in.dtype, at + (first + j) * a.in.ld + row) : 0.f;
+        u[j] = (row < a.m && first + j < a.n) ? load_bits(a.in, at + (first + j) * a.in.ld + row) : 0u;
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) x[j] = bits_value(a.in, u[j]);
     } else {
+      NsRaw g[kCols / 8];
 #pragma unroll
       for (int j = 0; j < kCols; j += 8)
-        load8(a.in, at + row * a.in.ld + first + j, row < a.m ? a.n - first - j : 0, x + j);
+        g[j / 8] = load8(a.in, at + row * a.in.ld + first + j, row < a.m ? a.n - first - j : 0);
+#pragma unroll
+      for (int j = 0; j < kCols; j += 8) unpack8(a.in, g[j / 8], x + j);
     }
     float s[3] = {0.f, 0.f, 0.f};
 #pragma unroll

@@ -47,16 +47,18 @@ __global__ void __launch_bounds__(512) ns_sumsq_kernel(const __grid_constant__ N
   const unsigned total = in.rows * chunks;  // at most 2^29: sides are at most 2^16
   float s[3] = {0.f, 0.f, 0.f};
   for (unsigned i = blockIdx.x * 512 + threadIdx.x; i < total; i += gridDim.x * 512 * kNsBatch) {
-    float v[kNsBatch][8];
+    NsRaw g[kNsBatch];
 #pragma unroll
     for (int k = 0; k < kNsBatch; ++k) {
       const unsigned j = i + k * gridDim.x * 512, r = j / chunks, c = (j - r * chunks) * 8;
-      load8(in, blockIdx.y * in.bstride + r * in.ld + c, j < total ? in.cols - (int)c : 0, v[k]);
+      g[k] = load8(in, blockIdx.y * in.bstride + r * in.ld + c, j < total ? in.cols - (int)c : 0);
     }
 #pragma unroll
     for (int k = 0; k < kNsBatch; ++k) {
+      float v[8];
+      unpack8(in, g[k], v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ns_add_square(v[k][j], s);
+      for (int j = 0; j < 8; ++j) ns_add_square(v[j], s);
     }
   }
 #pragma unroll
@@ -291,23 +293,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float f[3];
         ns_factor(a.parts + (long long)b * kNsParts * 3, a.num_parts, a.sx, a.eps, f);
         for (unsigned i = id; i < per; i += all * kNsBatch) {
-          float v[kNsBatch][8];
+          NsRaw g[kNsBatch];
 #pragma unroll
           for (int k = 0; k < kNsBatch; ++k) {
             const unsigned q = i + k * all, r = q / chunks, c = (q - r * chunks) * 8;
-            load8(a.in, b * a.in.bstride + r * a.in.ld + c, q < per ? a.in.cols - (int)c : 0, v[k]);
+            g[k] = load8(a.in, b * a.in.bstride + r * a.in.ld + c, q < per ? a.in.cols - (int)c : 0);
           }
 #pragma unroll
           for (int k = 0; k < kNsBatch; ++k) {
             const unsigned q = i + k * all, r = q / chunks, c = (q - r * chunks) * 8;
             if (q >= per) break;
+            float v[8];
+            unpack8(a.in, g[k], v);
             uint32_t h[4], l[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float x = ((v[k][2 * j] * f[0]) * f[1]) * f[2], y = ((v[k][2 * j + 1] * f[0]) * f[1]) * f[2];
+              const float x = ((v[2 * j] * f[0]) * f[1]) * f[2], y = ((v[2 * j + 1] * f[0]) * f[1]) * f[2];
               h[j] = pack_half2(x, y);
-              const float2 g = unpack_half2(h[j]);
-              l[j] = pack_half2(x - g.x, y - g.y);
+              const float2 high = unpack_half2(h[j]);
+              l[j] = pack_half2(x - high.x, y - high.y);
             }
             // rows are padded to a multiple of 64 elements: whole 16-byte pieces
             const long long o = ((long long)b * a.rows + r) * a.ld + c;
