@@ -13,6 +13,7 @@ Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 ``RAError`` on a non-OK status.  ``ring_attention_fwd`` / ``ring_attention_bwd``
 additionally allocate outputs and workspace with torch.
 """
+import contextlib
 import ctypes
 import os
 import threading
@@ -443,6 +444,21 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
+def _stride(stride, count, name):
+    """A stride for the library, where 0 means packed: 0 for a single row (its
+    stride is arbitrary), no expanded dimension."""
+    if count <= 1:
+        return 0
+    if stride == 0:
+        raise RAError(1, f"{name} must not be expanded (stride 0)")
+    return stride
+
+
+def _on_stream(stream):
+    """What is allocated inside belongs to `stream`, where it is used."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _xent_check(x, w, targets):
     """(T, D, V, row stride of x, row stride of w); a single row passes 0."""
     if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
@@ -453,7 +469,7 @@ def _xent_check(x, w, targets):
     if D > 1 and (xc != 1 or wc != 1):
         raise RAError(1, f"x and w must have contiguous rows (strides {x.stride()}, {w.stride()})")
     _vector(targets, "targets", T, torch.int64)
-    return T, D, V, xs if T > 1 else 0, ws if V > 1 else 0
+    return T, D, V, _stride(xs, T, "x"), _stride(ws, V, "w")
 
 
 def ra_xent_fwd_workspace_bytes(dtype, T, D, V):
@@ -506,9 +522,10 @@ def xent_fwd(x, w, targets, ignore_index=-100, stream=None):
     sizes = _xent_check(x, w, targets)
     T, D, V = sizes[:3]
     dev = x.device
-    loss = torch.empty(T, dtype=torch.float32, device=dev)
-    lse = torch.empty(T, dtype=torch.float32, device=dev)
-    ws = _workspace(_lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), dev)
+    with _on_stream(stream):
+        loss = torch.empty(T, dtype=torch.float32, device=dev)
+        lse = torch.empty(T, dtype=torch.float32, device=dev)
+        ws = _workspace(_lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), dev)
     _xent_fwd(sizes, x, w, targets, loss, lse, ws, int(ignore_index), stream)
     return loss, lse
 
@@ -521,9 +538,10 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
     T, D, V = sizes[:3]
     block = V if block is None else int(block)
     dev = x.device
-    dx = torch.empty(T, D, dtype=dx_dtype, device=dev)
-    dw = torch.empty(V, D, dtype=dw_dtype, device=dev)
-    ws = _workspace(_lib().ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), dev)
+    with _on_stream(stream):
+        dx = torch.empty(T, D, dtype=dx_dtype, device=dev)
+        dw = torch.empty(V, D, dtype=dw_dtype, device=dev)
+        ws = _workspace(_lib().ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), dev)
     _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, ws, int(ignore_index), stream)
     return dx, dw
 
@@ -542,7 +560,7 @@ def _ns_layout(t, name):
     strides = t.stride()
     if strides[-1] != 1 and cols > 1:
         raise RAError(1, f"{name} must have contiguous rows (strides {strides})")
-    return batch, rows, cols, strides[0] if n == 3 and batch > 1 else 0, strides[-2] if rows > 1 else 0
+    return (batch, rows, cols, _stride(strides[0], batch, name) if n == 3 else 0, _stride(strides[-2], rows, name))
 
 
 _NS_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -568,8 +586,9 @@ def ra_newton_schulz(g, out, workspace, steps=5, coeffs=_NS_COEFFS, eps=1e-7, st
 def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, stream=None):
     """Convenience wrapper: allocates out (g's dtype by default) and the workspace."""
     layout = _ns_layout(g, "g")
-    out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
-    ws = _workspace(_lib().ra_newton_schulz_workspace_bytes(*layout[:3]), g.device)
+    with _on_stream(stream):
+        out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
+        ws = _workspace(_lib().ra_newton_schulz_workspace_bytes(*layout[:3]), g.device)
     _newton_schulz(layout, g, out, (0, 0), ws, steps, coeffs, eps, stream)
     return out
 

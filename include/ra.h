@@ -350,16 +350,17 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   of 8; T, V and block are of any size >= 1 (blocks that are multiples of 256 fill
  *   the tiles; a block whose gradient takes less than 256 MB is widened to that).
  *   A token whose target equals ignore_index has loss 0 and no gradient (its lse is
- *   still written, and its x, multiplied by exact zeros in dw, has to be finite).  Any other target outside [0, V) gives loss NaN, no gradient,
- *   and RA_ERR_INVALID_ARG in the status word.
+ *   still written, and its x, multiplied by exact zeros in dw, has to be finite).  Any
+ *   other target outside [0, V) gives loss NaN, no gradient, and RA_ERR_INVALID_ARG in
+ *   the status word.
  *   loss, lse [T] fp32.  Products accumulate in fp32; the softmax's maxima and sums
  *   are fp32.  Infinities and NaN among the logits give NaN, as the formula does; a
  *   row whose logits are all -inf has lse = -inf and loss NaN.
  *   workspace: device memory, 256-byte aligned, of the size given (about T V / 8
  *   bytes for the forward; 2 T block bytes, 4 T D where dx is 16-bit and there is more
  *   than one block, and up to 20 MB each for dx and dw where their products are split,
- *   for the backward).  It must not be in use by work that
- *   overlaps the call on the GPU. */
+ *   for the backward).  It must not be in use by work that overlaps the call on the
+ *   GPU.  Outputs overlap neither each other nor the inputs or the workspace. */
 size_t ra_xent_fwd_workspace_bytes(ra_dtype dtype, long long T, int D, int V);
 int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,
                 long long x_rstride, long long w_rstride, const long long* targets,
@@ -402,8 +403,11 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *   within about 2e-3 (relative, 2-norm) of exact arithmetic.  G = 0 gives 0;
  *   infinities and NaN in a matrix give NaN.  Coefficients that let the singular
  *   values grow past 64 return RA_ERR_UNSUPPORTED.
- *   workspace: device memory, 256-byte aligned, about 6 bytes per element of g and 4
- *   per element of the two square matrices of the smaller side. */
+ *   workspace: device memory, 256-byte aligned, about 6 bytes per element of g, 4 per
+ *   element of a square matrix of the smaller side, and up to 20 MB for each of the
+ *   three products that is split.  It must not be in use by work that overlaps the call
+ *   on the GPU.  (A matrix with a side of at most 128 and the other of at most 4096 needs
+ *   none of it; the size asked for is the same.) */
 size_t ra_newton_schulz_workspace_bytes(int batch, int rows, int cols);
 int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int cols,
                      long long g_bstride, long long g_rstride, const float* coeffs, int steps,

@@ -116,3 +116,19 @@ def test_step_replays_from_a_cuda_graph_beside_an_eager_one(ra):
             assert torch.equal(a, b)
         for a, b in zip(eager, want[1]):
             assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_what_a_call_on_another_stream_allocates_belongs_to_that_stream(ra):
+    """Or the allocator could hand a workspace, freed when the call returns, to work of the
+    current stream while the kernels still use it."""
+    x, w1, w2, wv, y, g = inputs(torch.bfloat16, 44)
+    stream = torch.cuda.Stream()
+    stream.wait_stream(torch.cuda.current_stream())
+    loss, lse = ra.xent_fwd(x, wv, y, stream=stream)
+    dx, dw = ra.xent_bwd(x, wv, y, lse, g, stream=stream)
+    u = ra.newton_schulz(w1, stream=stream)
+    stream.synchronize()
+    owner = {b["address"]: s["stream"] for s in torch.cuda.memory_snapshot() for b in s["blocks"] if "address" in b}
+    for t in (loss, lse, dx, dw, u):
+        assert owner[t.data_ptr()] == stream.cuda_stream

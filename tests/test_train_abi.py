@@ -105,3 +105,15 @@ def test_binding_refuses_before_the_library(ra):
                 lambda: ra.ra_xent_fwd(x, w, y, f, f, f), lambda: ra.ra_newton_schulz(x, x, f)):
         with pytest.raises(ra.RAError):
             bad()
+
+
+def test_binding_refuses_expanded_tensors(ra):
+    """A stride of 0 means packed to the library: an expanded tensor would be read past its end."""
+    x, w, y = torch.zeros(4, 16).bfloat16(), torch.zeros(9, 16).bfloat16(), torch.zeros(4, dtype=torch.int64)
+    f, g = torch.zeros(4), torch.zeros(2, 4, 6)
+    for bad in (lambda: ra.xent_fwd(x[:1].expand(4, 16), w, y), lambda: ra.xent_fwd(x, w[:1].expand(9, 16), y),
+                lambda: ra.xent_bwd(x[:1].expand(4, 16), w, y, f, f), lambda: ra.newton_schulz(g[:1].expand(2, 4, 6)),
+                lambda: ra.newton_schulz(g[:, :1].expand(2, 4, 6)), lambda: ra.newton_schulz(g[0, :1].expand(4, 6)),
+                lambda: ra.ra_newton_schulz(g, g[:1].expand(2, 4, 6), f)):
+        with pytest.raises(ra.RAError, match="expanded"):
+            bad()
