@@ -13,7 +13,6 @@ Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 ``RAError`` on a non-OK status.  ``ring_attention_fwd`` / ``ring_attention_bwd``
 additionally allocate outputs and workspace with torch.
 """
-import contextlib
 import ctypes
 import os
 import threading
@@ -163,11 +162,15 @@ def _handle(stream, device):
     return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream().cuda_stream
 
 
-def _dt(t):
+def _code(dtype):
     try:
-        return _DTYPES[t.dtype]
+        return _DTYPES[dtype]
     except KeyError:
-        raise RAError(1, f"unsupported dtype {t.dtype}") from None
+        raise RAError(1, f"unsupported dtype {dtype}") from None
+
+
+def _dt(t):
+    return _code(t.dtype)
 
 
 def _bstride(t):
@@ -425,7 +428,7 @@ def ffn_bwd(x, w1, w2, dy, block=None, dx_dtype=torch.float32, stream=None):
 
 
 def _on_device(ref, *tensors):
-    """Every tensor lies on ref's device, and that is the current one (the
+    """ref's device, on which every tensor lies, and which is the current one (the
     stream and the library's kernels belong to it)."""
     dev = ref.device
     if dev.type != "cuda" or dev.index != torch.cuda.current_device():
@@ -433,6 +436,7 @@ def _on_device(ref, *tensors):
     for t in tensors:
         if t.device != dev:
             raise RAError(1, f"tensors must be on one device (got {t.device} and {dev})")
+    return dev
 
 
 def _vector(t, name, T, dtype):
@@ -454,17 +458,22 @@ def _stride(stride, count, name):
     return stride
 
 
-def _on_stream(stream):
-    """What is allocated inside belongs to `stream`, where it is used."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _allocate(stream, dev, *tensors):
+    """torch.empty for each (shape, dtype); they belong to `stream`, where they are
+    used (so that the allocator hands none of them on while its kernels run)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _allocate(None, dev, *tensors)
+    return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in tensors]
 
 
 def _xent_check(x, w, targets):
     """(T, D, V, row stride of x, row stride of w); a single row passes 0."""
-    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1] or x.dtype != w.dtype:
-        raise RAError(1, f"x [T, D] and w [V, D] must have one D and one dtype (got {list(x.shape)} {x.dtype}, "
-                         f"{list(w.shape)} {w.dtype})")
-    (T, D), V = x.shape, w.shape[0]
+    shape, wshape = x.shape, w.shape
+    if len(shape) != 2 or len(wshape) != 2 or shape[1] != wshape[1] or x.dtype != w.dtype:
+        raise RAError(1, f"x [T, D] and w [V, D] must have one D and one dtype (got {list(shape)} {x.dtype}, "
+                         f"{list(wshape)} {w.dtype})")
+    (T, D), V = shape, wshape[0]
     (xs, xc), (ws, wc) = x.stride(), w.stride()
     if D > 1 and (xc != 1 or wc != 1):
         raise RAError(1, f"x and w must have contiguous rows (strides {x.stride()}, {w.stride()})")
@@ -480,22 +489,17 @@ def ra_xent_bwd_workspace_bytes(dtype, dx_dtype, T, D, V, block):
     return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), int(block)))
 
 
-def _xent_fwd(sizes, x, w, targets, loss, lse, workspace, ignore_index, stream):
+def _xent_fwd(sizes, x, w, targets, loss, lse, workspace, nbytes, ignore_index, stream, dev):
     T, D, V, xs, ws = sizes
-    _on_device(x, w, targets, loss, lse, workspace)
     _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
-                              loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-                              _handle(stream, x.device)))
+                              loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, _handle(stream, dev)))
 
 
-def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index, stream):
+def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, nbytes, ignore_index, stream, dev):
     T, D, V, xs, ws = sizes
-    _vector(lse, "lse", T, torch.float32)
-    _vector(dloss, "dloss", T, torch.float32)
-    _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
     _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
                               lse.data_ptr(), dloss.data_ptr(), block, dx.data_ptr(), _dt(dx), dw.data_ptr(), _dt(dw),
-                              workspace.data_ptr(), _nbytes(workspace), _handle(stream, x.device)))
+                              workspace.data_ptr(), nbytes, _handle(stream, dev)))
 
 
 def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
@@ -504,29 +508,32 @@ def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=N
     sizes = _xent_check(x, w, targets)
     _vector(loss, "loss", sizes[0], torch.float32)
     _vector(lse, "lse", sizes[0], torch.float32)
-    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, int(ignore_index), stream)
+    dev = _on_device(x, w, targets, loss, lse, workspace)
+    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, _nbytes(workspace), int(ignore_index), stream, dev)
 
 
 def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index=-100, stream=None):
     """Gradients of sum(dloss * loss): dx [T, D] and dw [V, D] (packed,
     overwritten), `block` vocabulary entries at a time."""
     sizes = _xent_check(x, w, targets)
+    _vector(lse, "lse", sizes[0], torch.float32)
+    _vector(dloss, "dloss", sizes[0], torch.float32)
     for t, name, shape in ((dx, "dx", sizes[:2]), (dw, "dw", (sizes[2], sizes[1]))):
         if t.shape != shape or not t.is_contiguous():
             raise RAError(1, f"{name} must be a packed {list(shape)} tensor")
-    _xent_bwd(sizes, x, w, targets, lse, dloss, int(block), dx, dw, workspace, int(ignore_index), stream)
+    dev = _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
+    _xent_bwd(sizes, x, w, targets, lse, dloss, int(block), dx, dw, workspace, _nbytes(workspace), int(ignore_index),
+              stream, dev)
 
 
 def xent_fwd(x, w, targets, ignore_index=-100, stream=None):
     """Convenience wrapper: allocates loss, lse and the workspace."""
     sizes = _xent_check(x, w, targets)
     T, D, V = sizes[:3]
-    dev = x.device
-    with _on_stream(stream):
-        loss = torch.empty(T, dtype=torch.float32, device=dev)
-        lse = torch.empty(T, dtype=torch.float32, device=dev)
-        ws = _workspace(_lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V), dev)
-    _xent_fwd(sizes, x, w, targets, loss, lse, ws, int(ignore_index), stream)
+    dev = _on_device(x, w, targets)
+    nbytes = _lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V)
+    loss, lse, workspace = _allocate(stream, dev, (T, torch.float32), (T, torch.float32), (nbytes, torch.uint8))
+    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, nbytes, int(ignore_index), stream, dev)
     return loss, lse
 
 
@@ -536,13 +543,13 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
     vocabulary by default)."""
     sizes = _xent_check(x, w, targets)
     T, D, V = sizes[:3]
+    _vector(lse, "lse", T, torch.float32)
+    _vector(dloss, "dloss", T, torch.float32)
+    dev = _on_device(x, w, targets, lse, dloss)
     block = V if block is None else int(block)
-    dev = x.device
-    with _on_stream(stream):
-        dx = torch.empty(T, D, dtype=dx_dtype, device=dev)
-        dw = torch.empty(V, D, dtype=dw_dtype, device=dev)
-        ws = _workspace(_lib().ra_xent_bwd_workspace_bytes(_dt(x), _dt(dx), T, D, V, block), dev)
-    _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, ws, int(ignore_index), stream)
+    nbytes = _lib().ra_xent_bwd_workspace_bytes(_dt(x), _code(dx_dtype), T, D, V, block)
+    dx, dw, workspace = _allocate(stream, dev, ((T, D), dx_dtype), ((V, D), dw_dtype), (nbytes, torch.uint8))
+    _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, nbytes, int(ignore_index), stream, dev)
     return dx, dw
 
 
@@ -567,11 +574,12 @@ _NS_COEFFS = (3.4445, -4.7750, 2.0315)
 _Float3 = ctypes.c_float * 3
 
 
-def _newton_schulz(layout, g, out, out_strides, workspace, steps, coeffs, eps, stream):
-    _on_device(g, out, workspace)
+def _newton_schulz(layout, g, out, out_strides, workspace, nbytes, steps, coeffs, eps, stream, dev):
+    if len(coeffs) != 3:
+        raise RAError(1, f"coeffs must be three numbers (got {len(coeffs)})")
     _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), *layout, _Float3(*coeffs), int(steps), float(eps),
-                                   out.data_ptr(), _dt(out), *out_strides, workspace.data_ptr(), _nbytes(workspace),
-                                   _handle(stream, g.device)))
+                                   out.data_ptr(), _dt(out), *out_strides, workspace.data_ptr(), nbytes,
+                                   _handle(stream, dev)))
 
 
 def ra_newton_schulz(g, out, workspace, steps=5, coeffs=_NS_COEFFS, eps=1e-7, stream=None):
@@ -580,16 +588,18 @@ def ra_newton_schulz(g, out, workspace, steps=5, coeffs=_NS_COEFFS, eps=1e-7, st
     layout = _ns_layout(g, "g")
     if out.shape != g.shape:
         raise RAError(1, f"out must have the shape of g ({list(out.shape)} vs {list(g.shape)})")
-    _newton_schulz(layout, g, out, _ns_layout(out, "out")[3:], workspace, steps, coeffs, eps, stream)
+    strides = _ns_layout(out, "out")[3:]
+    dev = _on_device(g, out, workspace)
+    _newton_schulz(layout, g, out, strides, workspace, _nbytes(workspace), steps, coeffs, eps, stream, dev)
 
 
 def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, stream=None):
     """Convenience wrapper: allocates out (g's dtype by default) and the workspace."""
     layout = _ns_layout(g, "g")
-    with _on_stream(stream):
-        out = torch.empty(g.shape, dtype=out_dtype or g.dtype, device=g.device)
-        ws = _workspace(_lib().ra_newton_schulz_workspace_bytes(*layout[:3]), g.device)
-    _newton_schulz(layout, g, out, (0, 0), ws, steps, coeffs, eps, stream)
+    dev = _on_device(g)
+    nbytes = _lib().ra_newton_schulz_workspace_bytes(*layout[:3])
+    out, workspace = _allocate(stream, dev, (g.shape, out_dtype or g.dtype), (nbytes, torch.uint8))
+    _newton_schulz(layout, g, out, (0, 0), workspace, nbytes, steps, coeffs, eps, stream, dev)
     return out
 
 
