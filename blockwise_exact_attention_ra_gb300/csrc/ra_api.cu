@@ -187,8 +187,8 @@ int make_map_2d(CUtensorMap* m, const void* base, int is_bf16, long long rows, l
 namespace {
 
 // Batch of row-major matrices [batch, rows, cols]: dims (cols, rows, batch), boxes of
-// 128-byte rows with the 128-byte swizzle; cols and rows may be of any size, ld and bstride (elements) multiples of
-// 16 bytes.
+// 128-byte rows with the 128-byte swizzle; cols and rows may be of any size, ld and
+// bstride (elements) are multiples of 16 bytes.
 int make_map_3d(CUtensorMap* m, const void* base, int dtype, long long cols, long long rows, long long batch,
                 long long ld, long long bstride, int box_cols, int box_rows) {
   EncodeTiledFn fn;

@@ -6,7 +6,8 @@
 // rows (bn / 2) r .. of B, so each SM loads half of the shared operand: against the
 // 128 x 256 tiles of a single CTA that cuts the operand bytes an SM takes from L2 by a
 // third, which is what bounds those (the feed-forward products reach 1470-1505
-// TFLOP/s that way; these reach 1610-1670 on 8192 x 131072 x 2048 logits).
+// TFLOP/s that way; these 1760 on 4096 x 32768 x 2048 logits alone and 1670 on 8192 x
+// 131072 x 2048, 2.6 ms at the power limit).
 //   warp 0      TMA producer (both CTAs): the CTA's halves of the A and B k-slabs,
 //               64 deep, into a ring of stages; all bytes are counted on the
 //               leader's (CTA 0's) barrier
@@ -15,9 +16,9 @@
 //               both CTAs' barriers
 //   8 warps     epilogue (both CTAs): 32 rows x bn / 2 columns each, while the
 //               other accumulator fills
-// The narrow tile takes 0.75 of the wide one's time, not 0.5: per product it reads
-// shared memory 1.5 times as often, which is then the limit (0.97 against 1.54 PFLOP/s
-// on 32768 x 2048 x 4096 products).
+// A k-slab takes 0.33 us, of a narrow tile as of a wide one (0.98 against 1.86 PFLOP/s on
+// 8192 x 131072 x 2048 products), so the narrow one pays only where more tiles find an
+// idle pair, by its shorter epilogue.  Rings of 4, 5 and 6 stages run alike.
 // Operands are K-major (row-major [rows, K]) or MN-major (row-major [K, rows]), of
 // any size: the tensor maps end at the real extents, so what lies past an edge reads
 // as zeros.
