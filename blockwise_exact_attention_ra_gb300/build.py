@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libra.so")
 SOURCES = ["ra_api.cu", "ra_simt.cu", "ra_fwd_tc.cu", "ra_bwd_tc.cu", "ra_gemm_tc.cu", "ra_noalloc.cu",
-           "ra_xent_tc.cu", "ra_ns_tc.cu", "ra_ns_small.cu", "ra_train.cu"]
+           "ra_xent_tc.cu", "ra_xent_few.cu", "ra_ns_tc.cu", "ra_ns_small.cu", "ra_train.cu"]
 HEADERS = ["ra_device.cuh", "ra_internal.h", "ra_pair.cuh", "ra_ns.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

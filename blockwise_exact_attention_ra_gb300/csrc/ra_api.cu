@@ -1341,8 +1341,14 @@ int xent_token_parts(int V) {
   return n < 16 * kPairs ? n : 16 * kPairs;
 }
 
+// CTAs, and so parts, of the kernel for few tokens: units of 16 entries, four at a time.
+int xent_few_blocks(int V) {
+  const int n = ((V + 15) / 16 + 3) / 4;
+  return n < 2 * kPairs ? n : 2 * kPairs;
+}
+
 // forward: target logits [T] fp32 | statistics [column parts][T] (max, sum); the
-// tensor-core tiles' parts are at most ceil(V / 64)
+// tensor-core tiles' parts and those of few tokens are at most ceil(V / 64)
 struct XentFwdWs {
   size_t target, stats, total;
 };
@@ -1446,6 +1452,16 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
     e = launch_xent_token(x, w, dtype == RA_BF16, s.D, s.V, s.ws, targets, a.stats, a.target_logit, parts, plan.st);
     if (e != cudaSuccess) return cuda_fail(e, "cross-entropy token launch");
+  } else if (xent_few(s.T, s.D)) {
+    XentFewArgs f;
+    memset(&f, 0, sizeof f);
+    f.x = x; f.w = w; f.bf16 = dtype == RA_BF16; f.T = (int)s.T; f.D = s.D; f.V = s.V;
+    f.blocks = parts = xent_few_blocks(s.V);
+    f.xs = s.xs; f.ws = s.ws; f.targets = targets; f.ignore = ignore_index; f.vocab = s.V;
+    f.stats = a.stats; f.target_logit = a.target_logit;
+    TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
+    e = launch_xent_few(f, plan.st);
+    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch for few tokens");
   } else {
     const Cut cut = cut_product(s.T, s.V, s.D, false);
     if ((rc = plan.problem(a.q[0], cut, {x, s.T, s.D, s.xs}, {w, s.V, s.D, s.ws}, dtype)) ||
@@ -1495,18 +1511,31 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     memset(&a, 0, sizeof a);
     a.scale = scale;
     // d = gradient of this block's logits, recomputed from x and w
-    a.epi = PAIR_DLOGITS;
-    a.problems = 1;
-    a.q[0].M = (int)s.T; a.q[0].N = C; a.q[0].K = s.D;
-    a.targets = targets;
-    a.ignore = ignore_index;
-    a.vocab = s.V;
-    a.col_off = v0;
-    a.lse = lse;
-    a.grad = dloss;
-    if ((rc = make_map_3d(&a.q[0].tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
-        (rc = plan.problem(a.q[0], cut_product(s.T, C, s.D, false), X, W, dtype)) || (rc = plan.launch(a, dtype)))
-      return rc;
+    if (xent_few(s.T, s.D)) {
+      XentFewArgs f;
+      memset(&f, 0, sizeof f);
+      f.x = x; f.w = wb; f.bf16 = dtype == RA_BF16; f.T = (int)s.T; f.D = s.D; f.V = C;
+      f.blocks = xent_few_blocks(C);
+      f.xs = s.xs; f.ws = s.ws; f.targets = targets; f.ignore = ignore_index; f.vocab = s.V; f.col_off = v0;
+      f.lse = lse; f.grad = dloss; f.scale = scale;
+      f.d = d; f.ld = l.ld;
+      TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
+      const cudaError_t e = launch_xent_few(f, plan.st);
+      if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch for few tokens");
+    } else {
+      a.epi = PAIR_DLOGITS;
+      a.problems = 1;
+      a.q[0].M = (int)s.T; a.q[0].N = C; a.q[0].K = s.D;
+      a.targets = targets;
+      a.ignore = ignore_index;
+      a.vocab = s.V;
+      a.col_off = v0;
+      a.lse = lse;
+      a.grad = dloss;
+      if ((rc = make_map_3d(&a.q[0].tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
+          (rc = plan.problem(a.q[0], cut_product(s.T, C, s.D, false), X, W, dtype)) || (rc = plan.launch(a, dtype)))
+        return rc;
+    }
     // dx += d W  (W's rows as [K, N]: MN-major), summed over blocks in fp32, and in the
     // same launch this block's dw = d^T x  (both MN-major); the longer units first
     a.epi = PAIR_STORE;

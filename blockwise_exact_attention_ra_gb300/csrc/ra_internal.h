@@ -278,6 +278,22 @@ constexpr int kXentTokenSmem = 32768;
 cudaError_t launch_xent_token(const void* x, const void* w, int bf16, int D, int V, long long ws,
                               const long long* targets, float2* stats, float* target_logit, int blocks,
                               cudaStream_t st);
+// The logits of few tokens: statistics (d NULL; a part per block), or the gradient of V
+// entries from col_off on.
+struct XentFewArgs {
+  const void *x, *w;
+  int bf16, T, D, V, blocks;
+  long long xs, ws;
+  const long long* targets;
+  long long ignore, vocab, col_off;
+  float2* stats;
+  float* target_logit;
+  const float *lse, *grad, *scale;  // as in PairArgs
+  void* d;                          // [T] rows at ld elements
+  long long ld;
+};
+bool xent_few(long long T, int D);  // whether that kernel takes such a call
+cudaError_t launch_xent_few(const XentFewArgs& a, cudaStream_t st);
 // loss and lse from the column parts' statistics; a target outside [0, V) that is
 // not `ignore` gives loss = NaN and RA_ERR_INVALID_ARG in *status.
 cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,

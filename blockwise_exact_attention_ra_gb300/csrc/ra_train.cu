@@ -79,8 +79,8 @@ __global__ void __launch_bounds__(Rows == 1 ? 256 : 1024)
 // warp takes kEntries vocabulary entries at a time: each lane holds eight columns of
 // every one and multiplies them with x from shared memory (fp32), then the lanes' sums
 // are added up.  The tensor-core kernel would multiply tiles of 256 rows of which one is
-// filled, in rounds of 76 tiles: 37 us against 32768 x 2048 weights.  (With two tokens
-// this kernel is no faster than that one any more.)  Sums are plain fp32, which also keeps
+// filled, in rounds of 76 tiles: 37 us against 32768 x 2048 weights.  For two tokens and
+// more: ra_xent_few.cu.  Sums are plain fp32, which also keeps
 // the loss of a single token exact.
 constexpr int kEntries = 2;
 template <typename T>

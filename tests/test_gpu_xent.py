@@ -381,3 +381,50 @@ def test_nothing_is_written_past_the_outputs(ra):
         assert (b[:guard] == 7).all() and (b[guard + n:] == 7).all()
     assert (wf[nf:] == 9).all() and (wb[nb:] == 9).all()
     check(ra, x, w, y, g, loss, lse, dx.view(T, D), dw.view(V, D))
+
+
+FEW = [
+    # T, D, V: ends of units of 16 entries and of rounds of them (152 blocks, four at a time), sums in
+    # several pieces, the longest rows that x's share of shared memory holds and the first past it
+    (2, 40, 15), (5, 72, 16), (9, 32, 17), (16, 8, 9729), (10, 264, 64), (3, 4104, 200), (8, 13408, 40), (8, 13448, 40),
+    (16, 5664, 65), (16, 5672, 65), (17, 64, 700),
+]
+
+
+@pytest.mark.parametrize("T,D,V", FEW)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_few_tokens(ra, T, D, V, dtype):
+    x, w, y, g = make(T, D, V, dtype, T + D + V)
+    loss, lse = ra.xent_fwd(x, w, y)
+    dx, dw = ra.xent_bwd(x, w, y, lse, g)
+    ra.ra_sync_status()
+    check(ra, x, w, y, g, loss, lse, dx, dw)
+
+
+def test_few_tokens_with_strides_and_unusable_values(ra):
+    x, w, y, g = make(12, 72, 500, torch.bfloat16, 31, ignored=0.0)
+    wide_x = torch.full((12, 3, 72), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide_w = torch.full((500, 88), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide_x[:, 1], wide_w[:, :72] = x, w
+    y[3], y[7] = -100, 500                     # no loss; outside the vocabulary
+    g[3] = g[7] = float("nan")
+    loss, lse = ra.xent_fwd(wide_x[:, 1], wide_w[:, :72], y)
+    with pytest.raises(ra.RAError):
+        ra.ra_sync_status()
+    dx, dw = ra.xent_bwd(wide_x[:, 1], wide_w[:, :72], y, lse, g)
+    ra.ra_sync_status()
+    assert torch.isnan(loss[7]) and not dx[3].any() and not dx[7].any()
+    y[7], g[3], g[7] = -100, 0.0, 0.0
+    loss[7] = 0.0
+    check(ra, x, w, y, g, loss, lse, dx, dw)
+
+
+def test_few_tokens_in_several_blocks(ra):
+    T, D, V, block = 16, 8, 9000000, 8500000
+    assert 2 * T * block > 256 << 20
+    x, w, y, g = make(T, D, V, torch.float16, 32)
+    y[0], y[1] = block - 2, block + 1          # targets beside the blocks' edge
+    loss, lse = ra.xent_fwd(x, w, y)
+    dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block)
+    ra.ra_sync_status()
+    check_on_gpu(x, w, y, g, loss, lse, dx, dw)
