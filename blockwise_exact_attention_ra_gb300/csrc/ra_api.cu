@@ -1275,9 +1275,10 @@ struct PairPlan {
   cudaStream_t st;
   int* status;
   int sms;
-  struct Operand {  // a matrix of rows x cols as stored
+  struct Operand {  // a matrix of rows x cols as stored, or several, one after the other
     const void* p;
     long long rows, cols, ld;
+    int count = 1;
   };
   // q: M, N, K, the majornesses and the output; sets the operands' maps and the cut
   int problem(PairProblem& q, Cut cut, const Operand& A, const Operand& B, int dtype) const {
@@ -1285,7 +1286,8 @@ struct PairPlan {
     // few rows: only those are loaded (whole boxes would fill in zeros, which costs as much
     // as data)
     q.a_rows = !q.a_mn && q.M < 128 ? (q.M + 7) / 8 * 8 : 128;
-    if ((rc = make_map_3d(&q.tm_a, A.p, dtype, A.cols, A.rows, 1, A.ld, 0, 64, q.a_mn ? 64 : q.a_rows)) ||
+    if ((rc = make_map_3d(&q.tm_a, A.p, dtype, A.cols, A.rows, A.count, A.ld, A.rows * A.ld, 64,
+                          q.a_mn ? 64 : q.a_rows)) ||
         (rc = make_map_3d(&q.tm_b, B.p, dtype, B.cols, B.rows, 1, B.ld, 0, 64, q.b_mn ? 64 : cut.bn / 2)))
       return rc;
     q.bn = cut.bn;
@@ -1303,6 +1305,12 @@ struct PairPlan {
     TimedLaunch tl(RA_KERNEL_PAIR_TC, st);
     const cudaError_t e = launch_xent_pair(a, sms, st);
     return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy product launch");
+  }
+  int launch_few(const XentFewArgs& f) const {
+    TimedLaunch tl(RA_KERNEL_PAIR_TC, st);
+    const cudaError_t e =
+        f.T == 1 && f.D * 4 <= kXentTokenSmem ? launch_xent_token(f, st) : launch_xent_few(f, st);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "cross-entropy launch for few tokens");
   }
 };
 
@@ -1334,17 +1342,26 @@ int check_xent(ra_dtype dtype, long long T, int D, int V, long long x_rstride, l
   return RA_OK;
 }
 
-// Blocks, and so parts, of the forward for a single token: 16 entries a block and turn,
-// eight blocks per SM at most.
-int xent_token_parts(int V) {
-  const int n = (V + 15) / 16;
-  return n < 16 * kPairs ? n : 16 * kPairs;
+// Whether the kernels for few tokens take a call, and their blocks (and so parts) for V
+// entries: a single token 16 entries a block and turn, eight blocks per SM at most;
+// several tokens units of 16 entries, four at a time.
+bool single_token(const XentShape& s) { return s.T == 1 && s.D * 4 <= kXentTokenSmem; }
+bool few_tokens(const XentShape& s) { return single_token(s) || xent_few(s.T, s.D); }
+int few_blocks(const XentShape& s, int V) {
+  const int n = (V + 15) / 16, turns = (n + 3) / 4;
+  if (single_token(s)) return n < 16 * kPairs ? n : 16 * kPairs;
+  return turns < 2 * kPairs ? turns : 2 * kPairs;
 }
-
-// CTAs, and so parts, of the kernel for few tokens: units of 16 entries, four at a time.
-int xent_few_blocks(int V) {
-  const int n = ((V + 15) / 16 + 3) / 4;
-  return n < 2 * kPairs ? n : 2 * kPairs;
+XentFewArgs few_args(const XentShape& s, const void* x, const void* w, int dtype, const long long* targets,
+                     long long ignore, int V) {
+  XentFewArgs f;
+  memset(&f, 0, sizeof f);
+  f.x = x; f.w = w; f.bf16 = dtype == RA_BF16;
+  f.T = (int)s.T; f.D = s.D; f.V = V;
+  f.blocks = few_blocks(s, V);
+  f.xs = s.xs; f.ws = s.ws;
+  f.targets = targets; f.ignore = ignore; f.vocab = s.V;
+  return f;
 }
 
 // forward: target logits [T] fp32 | statistics [column parts][T] (max, sum); the
@@ -1355,28 +1372,35 @@ struct XentFwdWs {
 XentFwdWs xent_fwd_layout(const XentShape& s) {
   XentFwdWs w{};
   w.stats = align256((size_t)s.T * 4);
-  const int tiles = (s.V + 63) / 64, token = s.T == 1 ? xent_token_parts(s.V) : 0;
+  const int tiles = (s.V + 63) / 64, token = single_token(s) ? few_blocks(s, s.V) : 0;
   w.total = w.stats + align256((size_t)(tiles > token ? tiles : token) * s.T * 8);
   return w;
 }
 
-// backward: scale (256 bytes) | gradient of one block's logits [T][ld] 16-bit | fp32
-// sum of dx: its splits' planes, or [T, D] where dx is 16-bit and there is more than
-// one block | planes of one block's dw where its product is split
+// Up to so many tokens the logits' gradient is kept as two 16-bit terms, a matrix each: both
+// fit the tiles that one would take.
+constexpr int kTwoTerms = 64;  // one k-slab of dw = d^T x
+
+// backward: scale (256 bytes) | gradient of one block's logits [terms][T][ld] 16-bit | fp32
+// sum of dx: its splits' planes (of both terms' products, one below the other), or [T, D]
+// where dx is 16-bit and there is more than one block | planes of one block's dw where its
+// product is split
 struct XentBwdWs {
   size_t scale, d, acc, dw, total;
   long long ld;
+  int terms;
   Cut dx_cut, dw_cut;
 };
 XentBwdWs xent_bwd_layout(const XentShape& s, int dx_dtype) {
   XentBwdWs w{};
   w.ld = (s.block + 63) / 64 * 64;
-  w.dx_cut = cut_product(s.T, s.D, s.block, true);
+  w.terms = s.T <= kTwoTerms ? 2 : 1;
+  w.dx_cut = cut_product(s.T * w.terms, s.D, s.block, true);
   w.dw_cut = cut_product(s.block, s.D, s.T, true);
   w.d = 256;
-  w.acc = w.d + align256((size_t)s.T * w.ld * 2);
+  w.acc = w.d + align256((size_t)s.T * w.terms * w.ld * 2);
   w.dw = w.acc;
-  if (w.dx_cut.splits > 1) w.dw += align256((size_t)w.dx_cut.splits * s.T * s.D * 4);
+  if (w.dx_cut.splits > 1) w.dw += align256((size_t)w.dx_cut.splits * w.terms * s.T * s.D * 4);
   else if (dx_dtype != RA_F32 && s.block < s.V) w.dw += align256((size_t)s.T * s.D * 4);
   w.total = w.dw;
   if (w.dw_cut.splits > 1) w.total += align256((size_t)w.dw_cut.splits * s.block * s.D * 4);
@@ -1447,21 +1471,12 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
   a.target_logit = reinterpret_cast<float*>(base);
   int parts = 0;
   cudaError_t e;
-  if (s.T == 1 && s.D * 4 <= kXentTokenSmem) {
-    parts = xent_token_parts(s.V);
-    TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
-    e = launch_xent_token(x, w, dtype == RA_BF16, s.D, s.V, s.ws, targets, a.stats, a.target_logit, parts, plan.st);
-    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy token launch");
-  } else if (xent_few(s.T, s.D)) {
-    XentFewArgs f;
-    memset(&f, 0, sizeof f);
-    f.x = x; f.w = w; f.bf16 = dtype == RA_BF16; f.T = (int)s.T; f.D = s.D; f.V = s.V;
-    f.blocks = parts = xent_few_blocks(s.V);
-    f.xs = s.xs; f.ws = s.ws; f.targets = targets; f.ignore = ignore_index; f.vocab = s.V;
-    f.stats = a.stats; f.target_logit = a.target_logit;
-    TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
-    e = launch_xent_few(f, plan.st);
-    if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch for few tokens");
+  if (few_tokens(s)) {
+    XentFewArgs f = few_args(s, x, w, dtype, targets, ignore_index, s.V);
+    parts = f.blocks;
+    f.stats = a.stats;
+    f.target_logit = a.target_logit;
+    if ((rc = plan.launch_few(f))) return rc;
   } else {
     const Cut cut = cut_product(s.T, s.V, s.D, false);
     if ((rc = plan.problem(a.q[0], cut, {x, s.T, s.D, s.xs}, {w, s.V, s.D, s.ws}, dtype)) ||
@@ -1506,22 +1521,21 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     const int C = s.V - v0 < s.block ? s.V - v0 : s.block;
     const bool first = v0 == 0, last = v0 + C == s.V;
     const char* wb = static_cast<const char*>(w) + (size_t)v0 * s.ws * 2;
-    const PairPlan::Operand W{wb, C, s.D, s.ws}, X{x, s.T, s.D, s.xs}, Dl{d, s.T, C, l.ld};
+    const PairPlan::Operand W{wb, C, s.D, s.ws}, X{x, s.T, s.D, s.xs}, Dl{d, s.T, C, l.ld, l.terms};
+    const int k_slabs = (C + 63) / 64;
     PairArgs a;
     memset(&a, 0, sizeof a);
     a.scale = scale;
     // d = gradient of this block's logits, recomputed from x and w
-    if (xent_few(s.T, s.D)) {
-      XentFewArgs f;
-      memset(&f, 0, sizeof f);
-      f.x = x; f.w = wb; f.bf16 = dtype == RA_BF16; f.T = (int)s.T; f.D = s.D; f.V = C;
-      f.blocks = xent_few_blocks(C);
-      f.xs = s.xs; f.ws = s.ws; f.targets = targets; f.ignore = ignore_index; f.vocab = s.V; f.col_off = v0;
-      f.lse = lse; f.grad = dloss; f.scale = scale;
-      f.d = d; f.ld = l.ld;
-      TimedLaunch tl(RA_KERNEL_PAIR_TC, plan.st);
-      const cudaError_t e = launch_xent_few(f, plan.st);
-      if (e != cudaSuccess) return cuda_fail(e, "cross-entropy launch for few tokens");
+    if (few_tokens(s)) {
+      XentFewArgs f = few_args(s, x, wb, dtype, targets, ignore_index, C);
+      f.col_off = v0;
+      f.lse = lse;
+      f.grad = dloss;
+      f.scale = scale;
+      f.d = d;
+      f.ld = l.ld;
+      if ((rc = plan.launch_few(f))) return rc;
     } else {
       a.epi = PAIR_DLOGITS;
       a.problems = 1;
@@ -1532,17 +1546,25 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
       a.col_off = v0;
       a.lse = lse;
       a.grad = dloss;
-      if ((rc = make_map_3d(&a.q[0].tm_c, d, dtype, C, s.T, 1, l.ld, 0, 64, 32)) ||
+      a.two_terms = l.terms == 2;
+      if ((rc = make_map_3d(&a.q[0].tm_c, d, dtype, C, s.T, l.terms, l.ld, s.T * l.ld, 64, 32)) ||
           (rc = plan.problem(a.q[0], cut_product(s.T, C, s.D, false), X, W, dtype)) || (rc = plan.launch(a, dtype)))
         return rc;
     }
     // dx += d W  (W's rows as [K, N]: MN-major), summed over blocks in fp32, and in the
-    // same launch this block's dw = d^T x  (both MN-major); the longer units first
+    // same launch this block's dw = d^T x  (both MN-major); the longer units first.  Two
+    // terms of d are further rows of a split dx, whose planes are added up anyway; otherwise
+    // they follow each other along K, x or W being read again.
     a.epi = PAIR_STORE;
     a.problems = 2;
     const bool dx_first = C / l.dx_cut.splits >= s.T / l.dw_cut.splits;
     PairProblem &qx = a.q[dx_first ? 0 : 1], &qw = a.q[dx_first ? 1 : 0];
-    qx.M = (int)s.T; qx.N = s.D; qx.K = C;
+    const long long dx_rows = dx_split ? s.T * l.terms : s.T;
+    qx.M = (int)dx_rows; qx.N = s.D; qx.K = C;
+    if (l.terms == 2 && !dx_split) {
+      qx.fold = k_slabs;
+      qx.K = 2 * k_slabs * 64;
+    }
     qx.a_mn = 0;
     qx.b_mn = 1;
     qx.c_dtype = dx_split || dx_dtype == RA_F32 || !last ? RA_F32 : dx_dtype;
@@ -1551,18 +1573,22 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     qx.c_add = qx.c_dtype != RA_F32 && !first ? planes : nullptr;
     // the last block may be too short for as many splits: its planes are fewer, the
     // others keep what they hold
-    const int k_slabs = (C + 63) / 64;
     Cut cut = l.dx_cut;
     if (cut.splits > k_slabs) cut.splits = k_slabs;
     qw.M = C; qw.N = s.D; qw.K = (int)s.T;
+    if (l.terms == 2) {
+      qw.fold = 1;
+      qw.K = 2 * 64;
+    }
     qw.a_mn = qw.b_mn = 1;
     qw.c_dtype = dw_split ? RA_F32 : dw_dtype;
     qw.c_accumulate = 0;
     qw.c_add = nullptr;
     void* dwb = static_cast<char*>(dw) + (size_t)v0 * s.D * dtype_size(dw_dtype);
-    if ((rc = make_map_3d(&qx.tm_c, c, qx.c_dtype, s.D, s.T, dx_split ? l.dx_cut.splits : 1, s.D, s.T * s.D,
+    const PairPlan::Operand rows{d, dx_rows, C, l.ld};
+    if ((rc = make_map_3d(&qx.tm_c, c, qx.c_dtype, s.D, dx_rows, dx_split ? l.dx_cut.splits : 1, s.D, dx_rows * s.D,
                           qx.c_dtype == RA_F32 ? 32 : 64, 32)) ||
-        (rc = plan.problem(qx, cut, Dl, W, dtype)) ||
+        (rc = plan.problem(qx, cut, dx_split ? rows : Dl, W, dtype)) ||
         (rc = make_map_3d(&qw.tm_c, dw_split ? dw_planes : dwb, qw.c_dtype, s.D, C, l.dw_cut.splits, s.D,
                           (long long)C * s.D, qw.c_dtype == RA_F32 ? 32 : 64, 32)) ||
         (rc = plan.problem(qw, l.dw_cut, Dl, X, dtype)) || (rc = plan.launch(a, dtype)))
@@ -1573,7 +1599,7 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
     }
   }
   if (dx_split) {
-    const cudaError_t e = launch_sum_planes(planes, l.dx_cut.splits, s.T * s.D, dx, dx_dtype, plan.st);
+    const cudaError_t e = launch_sum_planes(planes, l.dx_cut.splits * l.terms, s.T * s.D, dx, dx_dtype, plan.st);
     if (e != cudaSuccess) return cuda_fail(e, "dx sum launch");
   }
   return RA_OK;

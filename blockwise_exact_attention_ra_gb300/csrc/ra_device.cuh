@@ -313,6 +313,11 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// e^t - [target] from t = z - lse, z's own sum: the target's, which is small where the
+// model is sure, without cancellation.
+__device__ __forceinline__ float logit_gradient(float t, bool target) {
+  return target ? expm1f(t) : ex2_approx(t * 1.4426950408889634f);
+}
 
 // max(a, b, c) in one instruction (three-input form, sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {

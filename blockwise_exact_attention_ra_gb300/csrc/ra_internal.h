@@ -236,7 +236,7 @@ cudaError_t launch_tc_gemm(GemmArgs& a, int num_sms, cudaStream_t st);
 // MN-major, sizes of any value.  The epilogues:
 enum PairEpi {
   PAIR_STATS = 0,    // softmax statistics of each row's columns and the target's logit
-  PAIR_DLOGITS = 1,  // gradient of the logits, 16-bit
+  PAIR_DLOGITS = 1,  // gradient of the logits, 16-bit, rounded or as two terms
   PAIR_STORE = 2,    // C, 16-bit or fp32, fp32 optionally added to what is there
 };
 struct PairProblem {
@@ -245,6 +245,7 @@ struct PairProblem {
   CUtensorMap tm_c;   // output: boxes of 64 x 32 (16-bit) or 32 x 32 (fp32), 128-byte swizzle
   int M, N, K;
   int a_mn, b_mn;
+  int fold;           // > 0: A is matrices of `fold` k-slabs each, all multiplied with one B
   int a_rows;         // rows of a K-major A a CTA loads: 128, or all of them (M < 128, multiple of 8)
   int bn;             // tile columns: 128 or 256
   int splits;         // PAIR_STORE, fp32: K is split, split s writes plane s of C
@@ -259,6 +260,7 @@ struct PairArgs {
   int problems;
   int ab_bf16;
   int epi;
+  int two_terms;             // PAIR_DLOGITS: matrix 1 of tm_c gets what rounding takes from matrix 0
   int* status;
   unsigned long long wait_limit_ns;
   const long long* targets;  // [M]
@@ -272,12 +274,6 @@ struct PairArgs {
   float* target_logit;       // [M]
 };
 cudaError_t launch_xent_pair(const PairArgs& a, int num_sms, cudaStream_t st);
-// The statistics of a single token (D kXentTokenSmem / 4 or less) on the CUDA cores,
-// `blocks` parts.
-constexpr int kXentTokenSmem = 32768;
-cudaError_t launch_xent_token(const void* x, const void* w, int bf16, int D, int V, long long ws,
-                              const long long* targets, float2* stats, float* target_logit, int blocks,
-                              cudaStream_t st);
 // The logits of few tokens: statistics (d NULL; a part per block), or the gradient of V
 // entries from col_off on.
 struct XentFewArgs {
@@ -289,10 +285,13 @@ struct XentFewArgs {
   float2* stats;
   float* target_logit;
   const float *lse, *grad, *scale;  // as in PairArgs
-  void* d;                          // [T] rows at ld elements
+  void* d;                          // [2 T] rows at ld elements: rounded, and the rest
   long long ld;
 };
-bool xent_few(long long T, int D);  // whether that kernel takes such a call
+// A single token (D kXentTokenSmem / 4 or less), on the CUDA cores.
+constexpr int kXentTokenSmem = 32768;
+cudaError_t launch_xent_token(const XentFewArgs& a, cudaStream_t st);
+bool xent_few(long long T, int D);  // whether the next kernel takes such a call
 cudaError_t launch_xent_few(const XentFewArgs& a, cudaStream_t st);
 // loss and lse from the column parts' statistics; a target outside [0, V) that is
 // not `ignore` gives loss = NaN and RA_ERR_INVALID_ARG in *status.

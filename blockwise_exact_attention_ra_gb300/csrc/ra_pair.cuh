@@ -204,9 +204,10 @@ struct Pair {
   // Producer (one lane of warp 0 in both CTAs): k-slabs [k_from, k_to) of the tile
   // whose first row and column are m0 and n0.  a_rows < 128: all of A's rows, K-major, lie
   // in the leader and are that few: the peer loads none, and what the rest of the A slab
-  // holds makes only rows of C that nobody reads.
+  // holds makes only rows of C that nobody reads.  fold > 0: A's slabs are those of matrices
+  // batch, batch + 1, ... of `fold` slabs each, B's those of the one matrix again and again.
   __device__ __forceinline__ bool produce(uint32_t& cnt, const Operand& A, const Operand& B, int bn, int m0, int n0,
-                                          int batch, int k_from, int k_to, int a_rows = 128) const {
+                                          int batch, int k_from, int k_to, int a_rows = 128, int fold = 0) const {
     const int a_block = m0 / 256, b_block = n0 / 256;
     m0 += (int)rank * 128;
     n0 += (int)rank * (bn / 2);
@@ -217,12 +218,12 @@ struct Pair {
       if (rank == 0) mbar_arrive_expect_tx(full(s), bytes);
       const uint32_t bar = map_rank(full(s), 0);
       const uint32_t dA = sbase + s * S::kStage, dB = dA + S::kA;
-      const int k0 = kb * 64;
+      const int z = fold ? kb / fold : 0, k0 = (kb - z * fold) * 64;
       if (A.mn_at(a_block, kb)) {
-        pair_tma_load(dA, A.by_mn, bar, m0, k0, batch);
-        pair_tma_load(dA + 8192, A.by_mn, bar, m0 + 64, k0, batch);
+        pair_tma_load(dA, A.by_mn, bar, m0, k0, batch + z);
+        pair_tma_load(dA + 8192, A.by_mn, bar, m0 + 64, k0, batch + z);
       } else if (a_rows == 128 || rank == 0) {
-        pair_tma_load(dA, A.by_k, bar, k0, m0, batch);
+        pair_tma_load(dA, A.by_k, bar, k0, m0, batch + z);
       }
       if (B.mn_at(b_block, kb)) {
         pair_tma_load(dB, B.by_mn, bar, n0, k0, batch);

@@ -75,28 +75,37 @@ __global__ void __launch_bounds__(Rows == 1 ? 256 : 1024)
   loss[row] = out;
 }
 
-// The logits' statistics of a single token on the CUDA cores, bound by reading w once.  A
-// warp takes kEntries vocabulary entries at a time: each lane holds eight columns of
-// every one and multiplies them with x from shared memory (fp32), then the lanes' sums
-// are added up.  The tensor-core kernel would multiply tiles of 256 rows of which one is
-// filled, in rounds of 76 tiles: 37 us against 32768 x 2048 weights.  For two tokens and
-// more: ra_xent_few.cu.  Sums are plain fp32, which also keeps
-// the loss of a single token exact.
+// The logits of a single token on the CUDA cores, bound by reading w once: their statistics,
+// or one block's gradient of them (two terms, as in ra_xent_few.cu).  A warp takes kEntries
+// vocabulary entries at a time: each lane holds eight columns of every one and multiplies
+// them with x from shared memory (fp32), then the lanes' sums are added up.  The
+// tensor-core kernel would multiply tiles of 256 rows of which one is filled, in rounds of
+// 76 tiles: 37 us against 32768 x 2048 weights.  (For two tokens and more: ra_xent_few.cu.)
+// Sums are plain fp32, which keeps the loss of a single sure token exact, and both
+// directions form the same ones, so that z - lse in the gradient is.
 constexpr int kEntries = 2;
-template <typename T>
-__global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w, int D, int V, long long ws,
-                                                         const long long* targets, float2* stats,
-                                                         float* target_logit) {
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(256) xent_token_kernel(const __grid_constant__ XentFewArgs a) {
   extern __shared__ float xf[];  // [D]
   __shared__ float2 part[8];
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < D; i += 256) xf[i] = to_f32(x[i]);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, V = a.V;
+  const T* const x = static_cast<const T*>(a.x);
+  const T* const w = static_cast<const T*>(a.w);
+  for (int i = threadIdx.x; i < a.D; i += 256) xf[i] = to_f32(x[i]);
   __syncthreads();
-  const long long y = targets[0];
-  float m = -INFINITY, l = 0.f;
-  const int chunks = D / 8;
+  long long y = a.targets[0];
+  float m = -INFINITY, l = 0.f, mul = 0.f, lse = 0.f;
+  const bool live = y != a.ignore && y >= 0 && y < a.vocab;
+  if (GRAD) {
+    y -= a.col_off;
+    if (live) {
+      mul = a.grad[0] * (a.scale ? a.scale[0] : 1.f);
+      lse = a.lse[0];
+    }
+  }
+  const int chunks = a.D / 8;
   for (int v0 = (blockIdx.x * 8 + warp) * kEntries; v0 < V; v0 += gridDim.x * 8 * kEntries) {
     float acc[kEntries][2];
 #pragma unroll
@@ -106,7 +115,7 @@ __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w,
       uint4 q[kEntries];
 #pragma unroll
       for (int r = 0; r < kEntries; ++r)
-        q[r] = __ldg(reinterpret_cast<const uint4*>(w + (long long)min(v0 + r, V - 1) * ws) + c);
+        q[r] = __ldg(reinterpret_cast<const uint4*>(w + (long long)min(v0 + r, V - 1) * a.ws) + c);
       const float4* xp = reinterpret_cast<const float4*>(xf + 8 * c);
       const float4 x0 = xp[0], x1 = xp[1];
 #pragma unroll
@@ -122,11 +131,27 @@ __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w,
         acc[r][1] = fmaf(x1.w, to_f32(e[7]), acc[r][1]);
       }
     }
+    if (GRAD) {
+      float z = 0.f;
+#pragma unroll
+      for (int r = 0; r < kEntries; ++r) {
+        const float t = warp_sum(acc[r][0] + acc[r][1]);
+        if (lane == r) z = t;
+      }
+      const int v = v0 + lane;
+      if (lane < kEntries && v < V) {
+        const float d = live ? mul * logit_gradient(z - lse, y == v) : 0.f;
+        const T high = from_f32<T>(d);
+        static_cast<T*>(a.d)[v] = high;
+        static_cast<T*>(a.d)[a.ld + v] = from_f32<T>(d - to_f32(high));
+      }
+      continue;
+    }
     float z[kEntries], mx = m;
 #pragma unroll
     for (int r = 0; r < kEntries; ++r) {
       z[r] = warp_sum(acc[r][0] + acc[r][1]);
-      if (lane == 0 && y == v0 + r && v0 + r < V) target_logit[0] = z[r];
+      if (lane == 0 && y == v0 + r && v0 + r < V) a.target_logit[0] = z[r];
       if (v0 + r >= V) z[r] = -INFINITY;
       mx = fmaxf(mx, z[r]);
     }
@@ -136,6 +161,7 @@ __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w,
     for (int r = 0; r < kEntries; ++r) l += ex2_approx((z[r] - ref) * kLog2e);
     m = mx;
   }
+  if (GRAD) return;
   if (lane == 0) part[warp] = make_float2(m, l);
   __syncthreads();
   if (threadIdx.x == 0) {
@@ -143,7 +169,7 @@ __global__ void __launch_bounds__(256) xent_token_kernel(const T* x, const T* w,
     for (int j = 0; j < 8; ++j) top = fmaxf(top, part[j].x);
     const float ref = top == -INFINITY ? 0.f : top;
     for (int j = 0; j < 8; ++j) sum += part[j].y * ex2_approx((part[j].x - ref) * kLog2e);
-    stats[blockIdx.x] = make_float2(top, sum);
+    a.stats[blockIdx.x] = make_float2(top, sum);
   }
 }
 
@@ -197,15 +223,11 @@ __global__ void __launch_bounds__(256) sum_planes_kernel(const float* planes, in
 
 }  // namespace
 
-cudaError_t launch_xent_token(const void* x, const void* w, int bf16, int D, int V, long long ws,
-                              const long long* targets, float2* stats, float* target_logit, int blocks,
-                              cudaStream_t st) {
-  if (D * 4 > kXentTokenSmem || blocks < 1) return cudaErrorInvalidValue;
-  const cudaError_t e =
-      bf16 ? launch_pdl(xent_token_kernel<__nv_bfloat16>, blocks, 256, D * 4, st, static_cast<const __nv_bfloat16*>(x),
-                        static_cast<const __nv_bfloat16*>(w), D, V, ws, targets, stats, target_logit)
-           : launch_pdl(xent_token_kernel<__half>, blocks, 256, D * 4, st, static_cast<const __half*>(x),
-                        static_cast<const __half*>(w), D, V, ws, targets, stats, target_logit);
+cudaError_t launch_xent_token(const XentFewArgs& a, cudaStream_t st) {
+  if (a.T != 1 || a.D * 4 > kXentTokenSmem || a.blocks < 1) return cudaErrorInvalidValue;
+  auto run = [&](auto kernel) { return launch_pdl(kernel, a.blocks, 256, a.D * 4, st, a); };
+  const cudaError_t e = a.bf16 ? (a.d ? run(xent_token_kernel<__nv_bfloat16, true>) : run(xent_token_kernel<__nv_bfloat16, false>))
+                               : (a.d ? run(xent_token_kernel<__half, true>) : run(xent_token_kernel<__half, false>));
   if (e == cudaSuccess) count_launch();
   return e;
 }

@@ -4,18 +4,17 @@
 // The pair kernels multiply tiles of 256 rows whatever their number, 0.33 us per 64 x 256
 // slab of w and pair, in rounds of 76 tiles; here w goes from memory straight into
 // registers as the left operand of warp-level products (m16n8k16, 16 entries of the
-// vocabulary by 8 tokens), each element once, and x waits in shared memory.  Forward and
-// backward in us, against the pair kernel's: 8 tokens, 4096 x 2000 (D x V) 18.5 and 31.7
-// (32.8, 42.0), 512 x 32768 16.4 and 42.0 (20.5, 44.1), 2048 x 65536 63.5 and 163 (73.7,
-// 171); 16 tokens, 512 x 32768 18.4 and 46.1 (22.5, 49.8).  With 32 tokens it would read x
-// from shared memory twice as often as w from memory and lose: 2048 x 65536 82 and 185
-// (76, 173).
+// vocabulary by 8 tokens), each element once, and x waits in shared memory.  The forward in
+// us, against the pair kernel's: 8 tokens, 4096 x 2000 (D x V) 18.4 (32.8), 512 x 32768 16.4
+// (20.5), 2048 x 65536 63.5 (73.7); 16 tokens, 512 x 32768 18.4 (22.5).  With 32 tokens it
+// would read x from shared memory twice as often as w from memory and lose: 2048 x 65536 82
+// (76).
 //   - A unit is 16 entries.  Four warps share its columns, 32 at a time; a lane loads 16
 //     bytes of two entries and takes them as the operands of two products: which columns of
 //     a product are which is the same for w and x, so any order does.
 //   - The warps' sums meet in shared memory and are added up there in fp32.  So are a
-//     warp's own after every 24 groups (768 products), since the tensor core's sums are not
-//     rounded to nearest.
+//     warp's own after every four groups (128 products), since the tensor core's sums are
+//     not rounded to nearest.
 //   - Each lane then holds one logit of each eighth token: statistics go on in registers
 //     over the units, gradients are written.
 // Units go round the CTAs first, so that the last round is spread over all SMs.
@@ -34,7 +33,6 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWarps = 16, kShare = 4, kGroups = kWarps / kShare;
 constexpr int kUnroll = 4;       // groups of 32 columns in flight per warp
-constexpr int kChunk = 24;       // groups of 32 columns summed by the tensor core
 constexpr long long kNoLoss = -(1ll << 62);
 
 template <int NT>
@@ -91,18 +89,18 @@ __global__ void __launch_bounds__(kWarps * 32, 1) xent_few_kernel(const __grid_c
   // this lane's tokens: lane % 8 + 8 j; its entry of a unit: 4 part + lane / 8
   const int token = lane & 7, entry = 4 * part + (lane >> 3);
   long long y[NT];
-  float m[NT], l[NT], mul[NT], lse2[NT];
+  float m[NT], l[NT], mul[NT], lse[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int n = token + 8 * j;
     y[j] = n < a.T ? a.targets[n] : -1;
     m[j] = -INFINITY;
-    l[j] = mul[j] = lse2[j] = 0.f;
+    l[j] = mul[j] = lse[j] = 0.f;
     if (GRAD) {
       const bool live = n < a.T && y[j] != a.ignore && y[j] >= 0 && y[j] < a.vocab;
       if (live) {
         mul[j] = a.grad[n] * (a.scale ? a.scale[0] : 1.f);
-        lse2[j] = a.lse[n] * kLog2e;
+        lse[j] = a.lse[n];
       }
       y[j] = live ? y[j] - a.col_off : kNoLoss;
     }
@@ -120,7 +118,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) xent_few_kernel(const __grid_c
     for (int j = 0; j < NT; ++j)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[j][k] = tot[j][k] = 0.f;
-    int held = 0;
     for (int c = part; c < groups; c += kShare * kUnroll) {
       uint4 p[kUnroll], q[kUnroll];
 #pragma unroll
@@ -142,26 +139,22 @@ __global__ void __launch_bounds__(kWarps * 32, 1) xent_few_kernel(const __grid_c
           mma(acc[j], p[k].z, q[k].z, p[k].w, q[k].w, b.z, b.w, T());
         }
       }
-      held += kUnroll;
-      if (held == kChunk) {
-        held = 0;
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            tot[j][k] += acc[j][k];
-            acc[j][k] = 0.f;
-          }
-      }
+        for (int k = 0; k < 4; ++k) {
+          tot[j][k] += acc[j][k];
+          acc[j][k] = 0.f;
+        }
     }
     // the last unit's sums are read by then: each warp has passed the barrier since
     float* const mine = sums + ((group * 2 + flip) * kShare + part) * F::kSums;
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
       *reinterpret_cast<float2*>(mine + g * F::kLine + 8 * j + 2 * t) =
-          make_float2(tot[j][0] + acc[j][0], tot[j][1] + acc[j][1]);
+          make_float2(tot[j][0], tot[j][1]);
       *reinterpret_cast<float2*>(mine + (g + 8) * F::kLine + 8 * j + 2 * t) =
-          make_float2(tot[j][2] + acc[j][2], tot[j][3] + acc[j][3]);
+          make_float2(tot[j][2], tot[j][3]);
     }
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kShare * 32) : "memory");
     const float* const all = sums + (group * 2 + flip) * kShare * F::kSums + entry * F::kLine + token;
@@ -173,9 +166,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) xent_few_kernel(const __grid_c
       const float z = (s[0] + s[F::kSums]) + (s[2 * F::kSums] + s[3 * F::kSums]);
       if (GRAD) {
         if (n < a.T) {
-          float d = ex2_approx(fmaf(z, kLog2e, -lse2[j])) - (y[j] == v ? 1.f : 0.f);
-          d = y[j] == kNoLoss ? 0.f : d * mul[j];  // a row without loss may hold anything
-          static_cast<T*>(a.d)[n * a.ld + v] = from_f32<T>(d);
+          // two terms: see PAIR_DLOGITS; a row without loss may hold anything
+          const float d = y[j] == kNoLoss ? 0.f : mul[j] * logit_gradient(z - lse[j], y[j] == v);
+          const T high = from_f32<T>(d);
+          static_cast<T*>(a.d)[n * a.ld + v] = high;
+          static_cast<T*>(a.d)[(a.T + n) * a.ld + v] = from_f32<T>(d - to_f32(high));
         }
       } else {
         if (y[j] == v) a.target_logit[n] = z;

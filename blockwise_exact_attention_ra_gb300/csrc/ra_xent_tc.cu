@@ -223,30 +223,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (EPI == PAIR_DLOGITS) {
         // d = g (e^{z - lse} - [column = target]), rounded to the operand type of
         // the two products that follow (bf16: any range; fp16: g is brought near
-        // 2^13 by a power of two that those products take out again)
+        // 2^13 by a power of two that those products take out again).  With few rows a
+        // gradient is little more than one element of d times a row of w or x, whose
+        // rounding nothing averages out: there what it takes away is kept as a second term.
         const long long y = row < q.M ? a.targets[row] : a.ignore;
         const bool live = row < q.M && y != a.ignore && y >= 0 && y < a.vocab;
         const float g = live ? a.grad[row] * (a.scale ? a.scale[0] : 1.f) : 0.f;
-        const float lse2 = live ? a.lse[row] * kLog2e : 0.f;
+        const float lse = live ? a.lse[row] : 0.f;
         const long long yc = y - a.col_off - col0;
         const int ycol = (live && yc >= 0 && yc < cols) ? (int)yc : -1;
-        const float2 log2e = make_float2(kLog2e, kLog2e), off = make_float2(-lse2, -lse2), gg = make_float2(g, g);
+        const float2 log2e = make_float2(kLog2e, kLog2e), off = make_float2(-lse, -lse), gg = make_float2(g, g);
 #pragma unroll 1
         for (int c = 0; c < cols; c += 64, buf ^= 1) {
-          if (lane == 0) bulk_wait_read_but_one();
+          if (lane == 0) {
+            if (a.two_terms) bulk_wait_read();
+            else bulk_wait_read_but_one();
+          }
           float v[64];
           tmem_load64(src + c, v);
           if (c == cols - 64) p.release(b);
+          const bool target = __any_sync(0xffffffffu, ycol >= c && ycol < c + 64);
+          float own = 0.f;
+          if (target) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              if (ycol == c + j) own = v[j];
+            own = logit_gradient(own - lse, true);
+          }
 #pragma unroll
           for (int j = 0; j < 64; j += 2) {
-            const float2 e = __ffma2_rn(make_float2(v[j], v[j + 1]), log2e, off);
+            const float2 e = __fmul2_rn(__fadd2_rn(make_float2(v[j], v[j + 1]), off), log2e);
             v[j] = ex2_approx(e.x);
             v[j + 1] = ex2_approx(e.y);
           }
-          if (__any_sync(0xffffffffu, ycol >= c && ycol < c + 64)) {
+          if (target) {
 #pragma unroll
             for (int j = 0; j < 64; ++j)
-              if (ycol == c + j) v[j] -= 1.f;
+              if (ycol == c + j) v[j] = own;
           }
 #pragma unroll
           for (int j = 0; j < 64; j += 2) {
@@ -259,6 +272,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           stage_out([&]() {
             if (col0 + c < q.N) tma_store_3d(&q.tm_c, stage + buf * 4096, col0 + c, row0, 0);
           });
+          if (a.two_terms) {
+#pragma unroll
+            for (int j = 0; j < 64; ++j)
+              v[j] -= a.ab_bf16 ? to_f32(__float2bfloat16_rn(v[j])) : to_f32(__float2half_rn(v[j]));
+            stage64(buf ^ 1, v, a.ab_bf16);
+            stage_out([&]() {
+              if (col0 + c < q.N) tma_store_3d(&q.tm_c, stage + (buf ^ 1) * 4096, col0 + c, row0, 1);
+            });
+          }
         }
       } else {
         // c = mul * acc (+ c_add): 16-bit or fp32 out; fp32 may be added to what is
@@ -329,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int tm = (q.M + 255) / 256, tn = (q.N + q.bn - 1) / q.bn, s = u / (tm * tn);
           const Tile t = tile_grouped(u - s * tm * tn, tm, tn, q.group_m);
           const Operand A{&q.tm_a, &q.tm_a, q.a_mn}, B{&q.tm_b, &q.tm_b, q.b_mn};
-          ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1), q.a_rows);
+          ok = p.produce(cnt, A, B, q.bn, t.m * 256, t.n * q.bn, 0, k_at(q, s), k_at(q, s + 1), q.a_rows, q.fold);
         }
         if (*p.abort) p.producer_drain(cnt);
       }

@@ -357,7 +357,7 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   are fp32.  Infinities and NaN among the logits give NaN, as the formula does; a
  *   row whose logits are all -inf has lse = -inf and loss NaN.
  *   workspace: device memory, 256-byte aligned, of the size given (about T V / 8
- *   bytes for the forward; 2 T block bytes, 4 T D where dx is 16-bit and there is more
+ *   bytes for the forward; 2 T block bytes (4 for up to 64 tokens), 4 T D where dx is 16-bit and there is more
  *   than one block, and up to 20 MB each for dx and dw where their products are split,
  *   for the backward).  It must not be in use by work that overlaps the call on the
  *   GPU.  Outputs overlap neither each other nor the inputs or the workspace. */
@@ -374,7 +374,8 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *   dx [T, D] in dx_dtype and dw [V, D] in dw_dtype, packed, fully overwritten.  d is
  *   rounded to `dtype` before the two products (it is a tensor-core operand: half a
  *   unit of 2^-8 relative for bf16, of 2^-11 for fp16, whose values are brought into
- *   range by a power of two from max |dloss|); their sums, over blocks too, are fp32.
+ *   range by a power of two from max |dloss|), and kept as two such terms for up to 64
+ *   tokens, where no sum averages its roundings out; the sums, over blocks too, are fp32.
  *   The results do not vary from run to run. */
 size_t ra_xent_bwd_workspace_bytes(ra_dtype dtype, ra_dtype dx_dtype, long long T, int D, int V,
                                    int block);

@@ -428,3 +428,32 @@ def test_few_tokens_in_several_blocks(ra):
     dx, dw = ra.xent_bwd(x, w, y, lse, g, block=block)
     ra.ra_sync_status()
     check_on_gpu(x, w, y, g, loss, lse, dx, dw)
+
+
+@pytest.mark.parametrize("T,D,V", [(1, 64, 700), (2, 2048, 20011), (16, 264, 1000), (17, 72, 300), (40, 1048, 9000),
+                                   (64, 136, 5001), (64, 9800, 130)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_few_tokens_lose_nothing_to_the_rounding_of_the_logit_gradients(ra, T, D, V, dtype):
+    """Up to 64 tokens d is kept as two terms: its error is u^2 instead of the u that `check`
+    allows (dx whole and split, its tiles' rows full and not)."""
+    x, w, y, g = make(T, D, V, dtype, 3 * T + V, ignored=0.0)
+    _, lse = ra.xent_fwd(x, w, y)
+    dx, dw = ra.xent_bwd(x, w, y, lse, g)
+    ra.ra_sync_status()
+    X, W, G = x.double(), w.double(), g.double()
+    z = X @ W.T
+    e_z = D * 2.0 ** -23 * (X.abs() @ W.abs().T).amax(dim=1)
+    e_lse = e_z + 2.0 ** -21 * z.abs().amax(dim=1) + 2.0 ** -18 + 2.0 ** -23 * torch.logsumexp(z, 1).abs()
+    p = torch.softmax(z, dim=1)
+    d = p.clone()
+    d[torch.arange(T), y] -= 1.0
+    d *= G[:, None]
+    u = U[dtype]
+    # as in `check`; d itself is an fp32 number (2^-22: the difference and the product)
+    e_d = G.abs()[:, None] * p * (e_z + e_lse)[:, None] * 1.01 + (1.01 * u * u + 2.0 ** -22) * d.abs()
+    e_d += (1.0 + G.abs()[:, None]) * 2.0 ** -126 + (G.abs().max() * 2.0 ** -38 if dtype == torch.float16 else 0.0)
+    for name, got, want, bound in (
+            ("dx", dx, d @ W, e_d @ W.abs() + 2 * V * 2.0 ** -23 * (d.abs() @ W.abs())),
+            ("dw", dw, d.T @ X, e_d.T @ X.abs() + 2 * T * 2.0 ** -23 * (d.abs().T @ X.abs()))):
+        worst = float(((got.double() - want).abs() - bound - U[torch.float32] * want.abs()).max())
+        assert worst <= 0.0, f"{name}: past its bound by {worst:.3e}"
