@@ -329,15 +329,15 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
   }
 
   // ---- the result
-  if (row < a.m) {
+  {
     const int first = (int)rank * C + (int)half * kCols;
     const long long at = entry * a.out_bstride;
 #pragma unroll
     for (int j = 0; j < kCols; ++j) x[j] *= a.out_mul;
-    if (a.tall) {
+    if (a.tall) {  // X's columns are the result's rows: the lanes write consecutive elements
 #pragma unroll
       for (int j = 0; j < kCols; ++j) {
-        if (first + j < a.n) {
+        if (row < a.m && first + j < a.n) {
           const long long o = at + (first + j) * a.out_ld + row;
           if (a.out_dtype == RA_F32) static_cast<float*>(a.out)[o] = x[j];
           else if (a.out_dtype == RA_BF16) static_cast<__nv_bfloat16*>(a.out)[o] = __float2bfloat16_rn(x[j]);
@@ -345,9 +345,14 @@ __global__ void __launch_bounds__(kThreads, 1) ns_small_kernel(const __grid_cons
         }
       }
     } else {
+      constexpr int kPart = kCols < 64 ? kCols : 64;
+      const int row0 = row - (int)lane;
+      // the partial Gram matrices' place: their last readers have passed a cluster barrier
+      float* const stage = reinterpret_cast<float*>(smem + S::kP + warp * 8192);
 #pragma unroll
-      for (int j = 0; j < kCols; j += 8)
-        ns_write_row<8>(a.out, a.out_dtype, a.out_vec, at + row * a.out_ld + first + j, first + j, a.n, x + j);
+      for (int j = 0; j < kCols; j += kPart)
+        ns_write_rows<kPart>(a.out, a.out_dtype, a.out_vec, at + row0 * a.out_ld + first + j, a.out_ld, a.m - row0,
+                             a.n - first - j, x + j, stage);
     }
   }
   tc_fence_before();

@@ -468,9 +468,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (kind == NS_UPDATE && last) {
 #pragma unroll
               for (int j = 0; j < 64; ++j) v[j] *= a.out_mul;
-              if (row < f.M)
-                ns_write_row<64>(a.out, a.out_dtype, a.out_vec, b * a.out_bstride + (long long)row * a.out_ld + col0 + c,
-                                 col0 + c, f.N, v);
+              ns_write_rows<64>(a.out, a.out_dtype, a.out_vec, b * a.out_bstride + (long long)row0 * a.out_ld + col0 + c,
+                                a.out_ld, f.M - row0, f.N - col0 - c, v, reinterpret_cast<float*>(stage_p));
               fence_proxy_async_smem();
               __syncwarp();
               continue;
