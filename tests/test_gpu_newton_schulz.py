@@ -280,3 +280,12 @@ def test_nothing_is_written_past_the_buffers(ra, rows, cols):
     ra.ra_newton_schulz(g, buf[guard:guard + rows * cols].view(rows, cols), ws[:n])
     ra.ra_sync_status()
     assert (buf[:guard] == 7).all() and (buf[guard + rows * cols:] == 7).all() and (ws[n:] == 9).all()
+
+
+@pytest.mark.parametrize("batch,rows,cols", [(1, 100, 1757), (2, 2048, 128), (12, 128, 2000), (40, 65, 513), (3, 1, 2049)])
+def test_slices_of_small_matrices(ra, batch, rows, cols):
+    # slices of 64, 128 and 256 columns, as size and batch ask for
+    g = torch.stack([gradient(rows, cols, 50 + i, "gauss") for i in range(batch)])
+    o = ra.newton_schulz(g)
+    ra.ra_sync_status()
+    check(ra, g, o)
