@@ -1698,8 +1698,9 @@ bool ns_small_cut(const NsShape& s, int* slice, int* cluster) {
 
 // The cut of one phase: the tile's width as for the cross entropy's products; K may be
 // split for every phase, over at most as many pairs as run at once.  A k-slab of a wide
-// tile takes about 0.33 us; handing one split's sum over takes 6 us, 2 us more for each
-// further split (measured on 8192 x 2048).  Wide tiles only.
+// tile takes about 0.33 us; exchanging the splits' sums takes 5 us and 1.5 us more for each
+// split past the second.  (2600 x 400: 180 us in all, 191 with splits taken for 4 us and 0.3
+// us each; 16 of 256 x 1024: 158 without splits, 178 with them.)  Wide tiles only.
 Cut ns_cut(const NsArgs& a, int kind, int pairs) {
   const long long K = kind == NS_GRAM && !a.tall ? a.cols : kind == NS_GRAM ? a.rows : a.m;
   const long long wide = (long long)a.batch * ns_phase_tiles(a, kind, 256);
@@ -1709,7 +1710,7 @@ Cut ns_cut(const NsArgs& a, int kind, int pairs) {
   int best = 1;
   double best_us = whole;
   for (int s = 2; s <= by_pairs && s <= K / 256; ++s) {
-    const double us = whole / s + 4.0 + 2.0 * (s - 1);
+    const double us = whole / s + 5.0 + 1.5 * (s - 2);
     if (us < best_us) {
       best_us = us;
       best = s;
@@ -1724,8 +1725,12 @@ Cut ns_cut(const NsArgs& a, int kind, int pairs) {
 struct NsWs {
   size_t words, parts, sums[2], hi[2], lo, a, b, partials, total;
 };
-// 16 partial sums per tile of X; narrow tiles bound their number
-size_t ns_sums(const NsShape& s) { return (size_t)16 * ((s.rows + 255) / 256) * ((s.cols + 127) / 128); }
+// 16 partial sums per unit of the update; narrow tiles bound their number, or pairs where
+// tiles are split
+size_t ns_sums(const NsShape& s) {
+  const size_t tiles = (size_t)((s.rows + 255) / 256) * ((s.cols + 127) / 128);
+  return 16 * (tiles > kPairs ? tiles : kPairs);
+}
 NsWs ns_layout(const NsShape& s) {
   NsWs w{};
   size_t off = 0;
@@ -1748,7 +1753,8 @@ NsWs ns_layout(const NsShape& s) {
   a.batch = s.batch; a.rows = s.rows; a.cols = s.cols; a.m = s.m; a.tall = s.rows > s.cols;
   size_t units = 0;
   for (int k = NS_GRAM; k <= NS_UPDATE; ++k) {
-    units += (size_t)(ns_cut(a, k, kPairs).splits - 1) * s.batch * ns_phase_tiles(a, k, 256);
+    const int splits = ns_cut(a, k, kPairs).splits;
+    if (splits > 1) units += (size_t)splits * s.batch * ns_phase_tiles(a, k, 256);
   }
   w.partials = take(units * 2 * 8 * 128 * 32 * 4);
   w.total = off;
@@ -1864,7 +1870,7 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
     a.bn[k] = cut.bn;
     a.splits[k] = cut.splits;
     a.per[k] = ns_phase_tiles(a, k, cut.bn);
-    if (k < NS_UPDATE) a.split_base[k + 1] = a.split_base[k] + (cut.splits - 1) * batch * a.per[k];
+    if (k < NS_UPDATE) a.split_base[k + 1] = a.split_base[k] + (cut.splits > 1 ? cut.splits * batch * a.per[k] : 0);
     const long long units = (long long)batch * a.per[k] * cut.splits;
     if (units > 0x3fffffff) return fail(RA_ERR_INVALID_ARG, "Newton-Schulz batch too large");
     if (units > most) most = units;

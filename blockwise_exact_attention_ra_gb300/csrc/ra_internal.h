@@ -312,7 +312,7 @@ struct NsInput {
   int vec;  // rows start on 16-byte boundaries
 };
 constexpr int kNsParts = 304;     // partial sums of G's squares per batch entry
-constexpr int kNsFlags = 3 * 16 * 128;  // 16 per unit that holds a split, three phases
+constexpr int kNsFlags = 3 * 16 * 128;  // 16 per unit of split tiles, three phases
 constexpr int kNsWords = 64 + kNsFlags;  // mark of a launch that gave up, flags; counts per matrix follow
 enum NsPhase { NS_GRAM = 0, NS_SQUARE = 1, NS_UPDATE = 2 };
 struct NsArgs {
@@ -328,14 +328,14 @@ struct NsArgs {
   int bn[3];      // tile columns of each phase
   int per[3];     // tiles per matrix of each phase
   int splits[3];  // parts of K of each phase; above 1 only with a pair for every part
-  int split_base[3];  // units that hold a split in the phases before
+  int split_base[3];  // units of split tiles in the phases before
   int group_m;    // NS_UPDATE: tile rows taken together
   float ca, cb, cc;                                            // coefficients
   float sx, sa, eps, alpha_mul;                                // scales of X and A'; alpha = alpha_mul sum x^2
   float gram_acc, square_acc, square_lin, update_acc, out_mul;  // factors of accumulators, of A', of the result
   float* parts;
   int num_parts;
-  float* sums[2];  // [batch][16 per tile], read by a step and written for the next one
+  float* sums[2];  // [batch][16 per unit], read by a step and written for the next one
   long long sums_ld;
   uint16_t *hi0, *lo;
   long long ld;    // X's padded rows
@@ -344,8 +344,8 @@ struct NsArgs {
   long long out_ld, out_bstride;
   unsigned int* words;  // zeroed at first: the mark of a launch that gave up, the flags, the counts
   unsigned int* counts; // per matrix: warps that have scaled it and halves of tiles written
-  unsigned int* flags;  // per warp of a split: the last phase whose partial sums it has written
-  float* partials;      // sums of the splits but the first, [unit][CTA][warp][128 columns][32 rows]
+  unsigned int* flags;  // per warp of a split: the last phase whose sums for the others it has written
+  float* partials;      // sums that splits leave each other, [unit][CTA][warp][128 columns][32 rows]
   int* status;
   unsigned long long wait_limit_ns;
 };

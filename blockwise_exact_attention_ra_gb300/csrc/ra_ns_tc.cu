@@ -97,7 +97,8 @@ __device__ __forceinline__ Tile tile_sym(int t, int tn, int bn) {
 
 // One phase as every role sees it.  Unit u of a phase is split u / tiles of tile
 // u % tiles, which takes an even share of the k-slabs; only with at least as many pairs
-// as units is K split.
+// as units is K split, so that the splits of a tile, which wait for each other's sums, are
+// all under way.
 struct Phase {
   int M, N, bn, tm, tn, per, tiles, sym, k_slabs, splits, units;
   Operand A, B;
@@ -146,9 +147,10 @@ __device__ __forceinline__ int first_unit(int base, int cluster, int clusters) {
   const int u = cluster - base;
   return u < 0 ? u + clusters : u;
 }
-// Tiles of one matrix that are written before a phase begins.
-__device__ __forceinline__ unsigned ready_tiles(const NsArgs& a, int step, int kind) {
-  const unsigned g = a.per[NS_GRAM], q = a.per[NS_SQUARE], u = a.per[NS_UPDATE];
+// Units of one matrix that are done before a phase begins.
+__device__ __forceinline__ unsigned ready_units(const NsArgs& a, int step, int kind) {
+  const unsigned g = a.per[NS_GRAM] * a.splits[NS_GRAM], q = a.per[NS_SQUARE] * a.splits[NS_SQUARE],
+                 u = a.per[NS_UPDATE] * a.splits[NS_UPDATE];
   return step * (g + q + u) + (kind > NS_GRAM ? g : 0) + (kind > NS_SQUARE ? q : 0);
 }
 __device__ __forceinline__ Tile phase_tile(const NsArgs& a, const Phase& f, int t) {
@@ -210,7 +212,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const Phase f = phase_at(a, step, kind);
           for (int u = first_unit(base, cluster, clusters); u < f.units && ok; u += clusters) {
             const int s = u / f.tiles, t = u - s * f.tiles, b = t / f.per;
-            const unsigned need = kPairEpiWarps * ns_team_size(a, b) + 2u * ready_tiles(a, step, kind);
+            const unsigned need = kPairEpiWarps * ns_team_size(a, b) + 2u * ready_units(a, step, kind);
             if (b != seen_b || seen < need) {  // counts only grow: often the last look still holds
               const unsigned* count = a.counts + b;
               const uint64_t t0 = globaltimer_ns();
@@ -352,29 +354,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
           if (!ok) break;
           const uint32_t src = p.tmem + acc * 256 + half * cols + ((quarter * 32) << 16);
-          // the sums of splits 1, 2, ... wait in memory for the CTA that has split 0: a
-          // column of 32 rows is one line
-          const long long mine = ((a.split_base[kind] + (long long)t * (f.splits - 1)) * 2 + p.rank) * kPairEpiWarps + w;
-          auto partial = [&](int s) { return a.partials + (mine + (s - 1) * 2 * kPairEpiWarps) * (128 * 32) + lane; };
-          auto flag = [&](int s) { return a.flags + mine + (s - 1) * 2 * kPairEpiWarps; };
+          // Splits share the finishing of their tile: of the 16 pieces of 32 rows x 64
+          // columns that a CTA's warps hold (two each), split s finishes pieces s, s +
+          // splits, ...; it leaves its sums of the others in memory, for the CTAs that
+          // finish them, and takes theirs.  A column of 32 rows is one line.
+          const long long mine =
+              ((a.split_base[kind] + (long long)t * f.splits + split) * 2 + p.rank) * kPairEpiWarps + w;
+          auto other = [&](int s) { return mine + (s - split) * 2 * kPairEpiWarps; };
+          auto finishes = [&](int c) { return f.splits == 1 || (2 * w + (c >> 6)) % f.splits == split; };
           const unsigned now = step * 3 + kind + 1;
-          if (split) {
-            if (!p.wait(p.acc_full(acc), (lt >> 1) & 1)) { ok = false; break; }
-            tc_fence_after();
-            float* q = partial(split);
-#pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-              float v[32];
-              tmem_load32(src + c, v);
-              if (c == cols - 32) p.release(acc);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) __stcg(q + (c + j) * 32, v[j]);
-            }
-            __syncwarp();
-            if (lane == 0)
-              asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flag(split)), "r"(now) : "memory");
-            continue;  // the tile is counted by the CTA that has split 0
-          }
           const Tile tile = phase_tile(a, f, t - b * f.per);
           const int row0 = tile.m * 256 + (int)p.rank * 128 + (int)quarter * 32;
           const int row = row0 + (int)lane;
@@ -397,37 +385,62 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (kind != NS_GRAM) ++loads;
           };
-          prefetch(0);
+          int next = 0;  // the next piece to finish
+          while (next < cols && !finishes(next)) next += 64;
+          if (next < cols) prefetch(next);
           // alpha: the mean of the Gram matrix's diagonal, 1 / m at first
           const float alpha =
-              step ? warp_total(sums + (long long)b * a.sums_ld, 16 * a.per[NS_UPDATE]) * a.alpha_mul : 1.f / (float)a.m;
+              step ? warp_total(sums + (long long)b * a.sums_ld, 16 * a.per[NS_UPDATE] * a.splits[NS_UPDATE]) * a.alpha_mul
+                   : 1.f / (float)a.m;
           float sq = 0.f;  // UPDATE: squares of this warp's part of the new X
           const float lin = (a.cb + 2.f * a.cc * alpha) * a.square_lin;
           const float own = a.ca + alpha * (a.cb + a.cc * alpha);
           const float shift = alpha * a.sa;
           if (!p.wait(p.acc_full(acc), (lt >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          for (int s = 1; s < f.splits && ok; ++s) {
-            if (lane == 0) {
-              const uint64_t t0 = globaltimer_ns();
-              for (uint32_t it = 1;; ++it) {
-                unsigned x;
-                asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(flag(s)) : "memory");
-                if (x >= now) break;
-                if ((it & 63u) == 0 && !still(t0, it)) { ok = false; break; }
+          if (f.splits > 1) {
+            float* q = a.partials + mine * (128 * 32) + lane;
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 64) {
+              if (finishes(c)) continue;
+              float v[64];
+              tmem_load64(src + c, v);
+#pragma unroll
+              for (int j = 0; j < 64; ++j) __stcg(q + (c + j) * 32, v[j]);
+            }
+            __syncwarp();
+            if (lane == 0)
+              asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(a.flags + mine), "r"(now) : "memory");
+            if (next >= cols) {
+              p.release(acc);  // nothing to finish here
+            } else {
+              for (int s0 = 0; s0 < f.splits && ok; s0 += 32) {  // a flag per lane
+                const int s = s0 + (int)lane;
+                if (s < f.splits && s != split) {
+                  const uint64_t t0 = globaltimer_ns();
+                  for (uint32_t it = 1;; ++it) {
+                    unsigned x;
+                    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(x) : "l"(a.flags + other(s)) : "memory");
+                    if (x >= now) break;
+                    if ((it & 63u) == 0 && !still(t0, it)) { ok = false; break; }
+                  }
+                }
+                ok = __all_sync(0xffffffffu, ok);
               }
             }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
           }
           if (!ok) break;
+          bool first = true;
 #pragma unroll 1
-          for (int c = 0; c < cols; c += 64) {
-            if (c) prefetch(c);
+          for (int c = next; c < cols; c = next, first = false) {
+            for (next = c + 64; next < cols && !finishes(next);) next += 64;
+            if (!first) prefetch(c);
             float v[64];
             tmem_load64(src + c, v);
-            if (c == cols - 64) p.release(acc);
-            for (int s = 1; s < f.splits; ++s) {
-              const float* q = partial(s) + c * 32;
+            if (next >= cols) p.release(acc);
+            for (int s = 0; s < f.splits; ++s) {
+              if (s == split) continue;
+              const float* q = a.partials + other(s) * (128 * 32) + lane + c * 32;
 #pragma unroll
               for (int j = 0; j < 64; ++j) v[j] += __ldcg(q + j * 32);
             }
@@ -513,7 +526,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (kind == NS_UPDATE && !last) {
             sq = warp_sum(sq);
             if (lane == 0)
-              sums_out[(long long)b * a.sums_ld + ((t - b * f.per) * 2 + (int)p.rank) * kPairEpiWarps + w] = sq;
+              sums_out[(long long)b * a.sums_ld +
+                       (((t - b * f.per) * f.splits + split) * 2 + (int)p.rank) * kPairEpiWarps + w] = sq;
           }
           finish(units, b);
         }
