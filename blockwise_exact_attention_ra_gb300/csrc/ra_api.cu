@@ -1677,7 +1677,8 @@ int check_ns(int batch, int rows, int cols, const float* coeffs, int steps, floa
 
 // Matrices with a side of at most 128 and the other at most 4096 go to clusters of CTAs
 // that hold them whole: slices of 64 columns on up to 8 CTAs or of 128 on up to 16 (the
-// largest cluster) where the SMs suffice for the batch, of 256 otherwise.  Measured: 97 x
+// largest cluster) where the SMs suffice for the batch, of 256 otherwise.  Measured with
+// cold caches, code among what is cold: 97 x
 // 1757 63 us with 16 slices of 128, 100 with 8 of 256; 120 x 1000 49 with 8 of 128, 51
 // with 16 of 64; 12 of 128 x 2000 92 with slices of 256, 115 with 128 in two rounds; 120 x
 // 4000 105 with 256, 182 in the general chain.
