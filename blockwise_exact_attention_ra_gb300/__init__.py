@@ -489,27 +489,17 @@ def ra_xent_bwd_workspace_bytes(dtype, dx_dtype, T, D, V, block):
     return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), int(block)))
 
 
-def _xent_fwd(sizes, x, w, targets, loss, lse, workspace, nbytes, ignore_index, stream, dev):
-    T, D, V, xs, ws = sizes
-    _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
-                              loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, _handle(stream, dev)))
-
-
-def _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, nbytes, ignore_index, stream, dev):
-    T, D, V, xs, ws = sizes
-    _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(), ignore_index,
-                              lse.data_ptr(), dloss.data_ptr(), block, dx.data_ptr(), _dt(dx), dw.data_ptr(), _dt(dw),
-                              workspace.data_ptr(), nbytes, _handle(stream, dev)))
-
-
 def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
     """loss and lse [T] fp32 of the softmax cross entropy of x w^T [T, V] against
     targets [T] int64, without the logits.  See include/ra.h."""
     sizes = _xent_check(x, w, targets)
     _vector(loss, "loss", sizes[0], torch.float32)
     _vector(lse, "lse", sizes[0], torch.float32)
+    T, D, V, xs, ws = sizes
     dev = _on_device(x, w, targets, loss, lse, workspace)
-    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, _nbytes(workspace), int(ignore_index), stream, dev)
+    _check(_lib().ra_xent_fwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
+                              int(ignore_index), loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                              _nbytes(workspace), _handle(stream, dev)))
 
 
 def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_index=-100, stream=None):
@@ -521,19 +511,25 @@ def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_inde
     for t, name, shape in ((dx, "dx", sizes[:2]), (dw, "dw", (sizes[2], sizes[1]))):
         if t.shape != shape or not t.is_contiguous():
             raise RAError(1, f"{name} must be a packed {list(shape)} tensor")
+    T, D, V, xs, ws = sizes
     dev = _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
-    _xent_bwd(sizes, x, w, targets, lse, dloss, int(block), dx, dw, workspace, _nbytes(workspace), int(ignore_index),
-              stream, dev)
+    _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
+                              int(ignore_index), lse.data_ptr(), dloss.data_ptr(), int(block), dx.data_ptr(), _dt(dx),
+                              dw.data_ptr(), _dt(dw), workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
 
 
+# The two wrappers call the library themselves: host time bounds small losses, and each
+# further function on the way costs some of it.
 def xent_fwd(x, w, targets, ignore_index=-100, stream=None):
     """Convenience wrapper: allocates loss, lse and the workspace."""
-    sizes = _xent_check(x, w, targets)
-    T, D, V = sizes[:3]
-    dev = _on_device(x, w, targets)
-    nbytes = _lib().ra_xent_fwd_workspace_bytes(_dt(x), T, D, V)
+    T, D, V, xs, ws = _xent_check(x, w, targets)
+    dev, lib, dtype = _on_device(x, w, targets), _lib(), _dt(x)
+    nbytes = lib.ra_xent_fwd_workspace_bytes(dtype, T, D, V)
     loss, lse, workspace = _allocate(stream, dev, (T, torch.float32), (T, torch.float32), (nbytes, torch.uint8))
-    _xent_fwd(sizes, x, w, targets, loss, lse, workspace, nbytes, int(ignore_index), stream, dev)
+    code = lib.ra_xent_fwd(x.data_ptr(), w.data_ptr(), dtype, T, D, V, xs, ws, targets.data_ptr(), int(ignore_index),
+                           loss.data_ptr(), lse.data_ptr(), workspace.data_ptr(), nbytes, _handle(stream, dev))
+    if code:
+        _check(code)
     return loss, lse
 
 
@@ -541,15 +537,19 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
              ignore_index=-100, stream=None):
     """Convenience wrapper: allocates dx, dw and the workspace (block: the whole
     vocabulary by default)."""
-    sizes = _xent_check(x, w, targets)
-    T, D, V = sizes[:3]
+    T, D, V, xs, ws = _xent_check(x, w, targets)
     _vector(lse, "lse", T, torch.float32)
     _vector(dloss, "dloss", T, torch.float32)
-    dev = _on_device(x, w, targets, lse, dloss)
+    dev, lib, dtype = _on_device(x, w, targets, lse, dloss), _lib(), _dt(x)
+    dx_code, dw_code = _code(dx_dtype), _code(dw_dtype)
     block = V if block is None else int(block)
-    nbytes = _lib().ra_xent_bwd_workspace_bytes(_dt(x), _code(dx_dtype), T, D, V, block)
+    nbytes = lib.ra_xent_bwd_workspace_bytes(dtype, dx_code, T, D, V, block)
     dx, dw, workspace = _allocate(stream, dev, ((T, D), dx_dtype), ((V, D), dw_dtype), (nbytes, torch.uint8))
-    _xent_bwd(sizes, x, w, targets, lse, dloss, block, dx, dw, workspace, nbytes, int(ignore_index), stream, dev)
+    code = lib.ra_xent_bwd(x.data_ptr(), w.data_ptr(), dtype, T, D, V, xs, ws, targets.data_ptr(), int(ignore_index),
+                           lse.data_ptr(), dloss.data_ptr(), block, dx.data_ptr(), dx_code, dw.data_ptr(), dw_code,
+                           workspace.data_ptr(), nbytes, _handle(stream, dev))
+    if code:
+        _check(code)
     return dx, dw
 
 

@@ -385,8 +385,8 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
                 ra_dtype dx_dtype, void* dw, ra_dtype dw_dtype, void* workspace, size_t ws_bytes,
                 void* stream);
 
-/* Orthogonalises a weight gradient by Newton-Schulz products, as the Muon
- * optimiser does with the update of a hidden layer's matrix (the dW1 and dW2 of
+/* Orthogonalises a weight gradient by Newton-Schulz products, as optimisers do that
+ * make the update of a hidden layer's matrix orthogonal (the dW1 and dW2 of
  * ra_ffn_bwd, for instance):
  *     X = G / (|G|_F + eps);   `steps` times:  A = X X^T (X^T X where rows > cols),
  *     X <- a X + (b A + c A^2) X
