@@ -400,8 +400,9 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *   that follow from the size and the coefficients, so that nothing leaves fp16's
  *   range) and fp32 sums; X is carried as two fp16 terms, and the Gram matrix without
  *   the mean of its diagonal, which enters in fp32, so that its rounding is no common
- *   factor of the result.  For gradients with a side of 32 or more the result is
- *   within about 2e-3 (relative, 2-norm) of exact arithmetic.  G = 0 gives 0;
+ *   factor of the result.  For gradients with sides of 32 or more the result is within
+ *   about 2e-3 (relative, 2-norm) of exact arithmetic; with a side of 8 or less and
+ *   singular values a thousand apart it is within 5e-2.  G = 0 gives 0;
  *   infinities and NaN in a matrix give NaN.  Coefficients that let the singular
  *   values grow past 64 return RA_ERR_UNSUPPORTED.
  *   workspace: device memory, 256-byte aligned, about 6 bytes per element of g, 4 per
