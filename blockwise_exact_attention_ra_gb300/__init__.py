@@ -11,7 +11,11 @@ to.
 Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 ``ra_ring_bwd``, ...) take torch tensors in the [B, N, H, d] layout and raise
 ``RAError`` on a non-OK status.  ``ring_attention_fwd`` / ``ring_attention_bwd``
-additionally allocate outputs and workspace with torch.
+additionally allocate outputs and workspace with torch; so do ``ffn_fwd`` /
+``ffn_bwd`` (a feed-forward layer), ``xent_fwd`` / ``xent_bwd`` (the cross
+entropy of its output against a vocabulary) and ``newton_schulz`` (the
+orthogonalised update of a weight's gradient), the last three on the stream they
+are given.
 """
 import ctypes
 import os
