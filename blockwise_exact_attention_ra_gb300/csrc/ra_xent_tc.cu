@@ -104,12 +104,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     auto stage16 = [&](int buf, int piece, uint4 v) {
       *reinterpret_cast<uint4*>(stage_p + buf * 4096 + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
     };
+    // A bulk group per buffer filled, also where there is nothing to copy.  With the buffers
+    // taken in turn, waiting for all groups but the latest frees the one that is next.
     auto stage_out = [&](auto issue) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         issue();
-        bulk_commit();  // a group per buffer filled, also where there is nothing to copy
+        bulk_commit();
       }
     };
     // 64 columns as 16-bit values into buffer buf
@@ -119,7 +121,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         stage16(buf, j, make_uint4(pack_pair(v[8 * j], v[8 * j + 1], bf), pack_pair(v[8 * j + 2], v[8 * j + 3], bf),
                                    pack_pair(v[8 * j + 4], v[8 * j + 5], bf), pack_pair(v[8 * j + 6], v[8 * j + 7], bf)));
     };
-    int buf = 0;  // 16-bit outputs: the buffers in turn
+    int buf = 0;  // the next buffer
     uint32_t lt = 0;
     for (int n = 0; (u = share.unit(n, &which)) >= 0; ++n, ++lt) {
       const PairProblem& q = a.q[which];
@@ -306,6 +308,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 16; ++j)
               stage16(j >> 3, j & 7, make_uint4(__float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]),
                                                 __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3])));
+            // a group for each buffer; buffer 1's is the latest, so a 16-bit piece that follows
+            // takes buffer 0
             stage_out([&]() {
 #pragma unroll
               for (int h = 0; h < 2; ++h) {
@@ -314,8 +318,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                   if (q.c_accumulate) tma_add_3d(&q.tm_c, stage + h * 4096, cc, row0, split);
                   else tma_store_3d(&q.tm_c, stage + h * 4096, cc, row0, split);
                 }
+                if (h == 0) bulk_commit();
               }
             });
+            buf = 0;
           } else {
             if (q.c_add && row < q.M) {  // N is a multiple of 8 where c_add is used
               const float4* add = reinterpret_cast<const float4*>(q.c_add + (long long)row * q.N + col0 + c);
