@@ -352,6 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
           ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+          __syncwarp();  // what lane 0 has acquired holds for every lane (the shuffle orders no memory)
           if (!ok) break;
           const uint32_t src = p.tmem + acc * 256 + half * cols + ((quarter * 32) << 16);
           // Splits share the finishing of their tile: of the 16 pieces of 32 rows x 64
@@ -427,6 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                 }
                 ok = __all_sync(0xffffffffu, ok);
               }
+              __syncwarp();  // a lane reads the sums of all splits, whose flags other lanes acquired
             }
           }
           if (!ok) break;
