@@ -354,13 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         }
       }
       if (*abort_flag) {
-        const uint64_t drain = 100000000ull;
-        (void)mbar_wait(BAR_KV_FULL, (k - 1) & 1, abort_flag, nullptr, drain);
+        mbar_drain(BAR_KV_FULL, (k - 1) & 1);
         for (int s = 0; s < 2; ++s) {
           // phase of the last load issued on stage s (loads alternate stages)
           const uint32_t last = qd_cnt > (uint32_t)s ? ((qd_cnt - 1 - s) & ~1u) + s : 0;
-          if (q_issued[s]) (void)mbar_wait(bar_q_full(s), (last >> 1) & 1, abort_flag, nullptr, drain);
-          if (do_issued[s]) (void)mbar_wait(bar_do_full(s), (last >> 1) & 1, abort_flag, nullptr, drain);
+          if (q_issued[s]) mbar_drain(bar_q_full(s), (last >> 1) & 1);
+          if (do_issued[s]) mbar_drain(bar_do_full(s), (last >> 1) & 1);
         }
       }
     }
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         ++k;
       }
       mma_commit(BAR_DRAIN);
-      (void)mbar_wait(BAR_DRAIN, 0, abort_flag, nullptr, 100000000ull);
+      mbar_drain(BAR_DRAIN, 0);
     }
   } else if (warp < 10) {
     // ------------------------------------------------------------ compute

@@ -129,6 +129,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
   }
 }
 
+// Wait for work that the CTA has in flight (copies, products), also after a wait gave up:
+// for 100 ms at most, whatever the abort flag says.
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return;
+  const uint64_t t0 = globaltimer_ns();
+  while (!mbar_try_wait(bar, parity) && globaltimer_ns() - t0 <= 100000000ull) {
+  }
+}
+
 // ---------------------------------------------------------------------------
 // Tensor-map (TMA) copies
 // ---------------------------------------------------------------------------

@@ -402,10 +402,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       }
       if (*abort_flag) {
         // let copies already in flight land before the CTA exits
-        const uint64_t drain = 100000000ull;
         for (int s = 0; s < kStages; ++s)
-          if (issued[s]) (void)mbar_wait(bar_kv_full(s), last_phase[s], abort_flag, nullptr, drain);
-        if (q_issued) (void)mbar_wait(BAR_Q_FULL, (k - 1) & 1, abort_flag, nullptr, drain);
+          if (issued[s]) mbar_drain(bar_kv_full(s), last_phase[s]);
+        if (q_issued) mbar_drain(BAR_Q_FULL, (k - 1) & 1);
       }
     }
   } else if (warp == 1) {
@@ -510,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       }
       // wait for every MMA issued to finish before TMEM is released
       mma_commit(BAR_DRAIN);
-      (void)mbar_wait(BAR_DRAIN, 0, abort_flag, nullptr, 100000000ull);
+      mbar_drain(BAR_DRAIN, 0);
     }
   } else {
     // ------------------------------------------------------------ softmax

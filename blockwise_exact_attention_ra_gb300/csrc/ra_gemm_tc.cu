@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
       if (*abort_flag) {
         // let copies already in flight land before the CTA exits
         for (int s = 0; s < kStages; ++s)
-          if (issued[s]) (void)mbar_wait(bar_full(s), last_phase[s], abort_flag, nullptr, 100000000ull);
+          if (issued[s]) mbar_drain(bar_full(s), last_phase[s]);
       }
     }
   } else if (warp == 1) {
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_gemm_kernel(const __grid_const
       }
       // every MMA issued has completed before TMEM is released
       mma_commit(BAR_DRAIN);
-      (void)mbar_wait(BAR_DRAIN, 0, abort_flag, nullptr, 100000000ull);
+      mbar_drain(BAR_DRAIN, 0);
     }
   } else {
     // ------------------------------------------------------------ epilogue

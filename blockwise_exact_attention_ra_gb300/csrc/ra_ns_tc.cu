@@ -538,7 +538,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
     // after a wait gave up: a staging load in flight lands before the CTA exits
-    if (loads != fills) (void)mbar_wait(FILLED, fills & 1, p.abort, nullptr, 100000000ull);
+    if (loads != fills) mbar_drain(FILLED, fills & 1);
   }
   p.end();
 }

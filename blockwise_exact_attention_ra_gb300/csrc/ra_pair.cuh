@@ -234,12 +234,19 @@ struct Pair {
     }
     return true;
   }
-  // After a wait gave up: let the pair's copies in flight land before the CTAs exit.
+  // After a wait gave up: let the pair's copies in flight land before the CTAs exit.  Their bytes
+  // are counted in the leader, which has not expected those of stages that only the peer had
+  // reached: the peer stays for a millisecond, a copy takes microseconds.
   __device__ __forceinline__ void producer_drain(uint32_t cnt) const {
-    if (rank != 0) return;
+    if (rank != 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (globaltimer_ns() - t0 < 1000000ull) {
+      }
+      return;
+    }
     const uint32_t first = cnt > (uint32_t)S::kStages ? cnt - S::kStages : 0;
     for (uint32_t c = first; c < cnt; ++c)
-      (void)mbar_wait(full(c % S::kStages), (c / S::kStages) & 1, abort, nullptr, 100000000ull);
+      mbar_drain(full(c % S::kStages), (c / S::kStages) & 1);
   }
 
   // MMA issuer (warp 1 of the leader, whole warp): k-slabs [k_from, k_to) of one tile.
@@ -290,7 +297,7 @@ struct Pair {
   __device__ __forceinline__ void multiply_drain() const {
     if (elect_lane()) pair_commit(drain());
     __syncwarp();
-    (void)mbar_wait(drain(), 0, abort, nullptr, 100000000ull);
+    mbar_drain(drain(), 0);
   }
 
   // Epilogue: the accumulator goes back to the leader's MMA thread (whole warp).  The
