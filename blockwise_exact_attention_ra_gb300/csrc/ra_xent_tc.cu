@@ -20,10 +20,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // 5 stages of 32 KB (4, 5 and 6 run alike); two staging buffers of 4 KB per epilogue warp.
 using S = PairSmem<5, 8192, 0>;
 // Three warpgroups: producer, MMA issuer and two idle warps; then the 8 epilogue warps.
-// PAIR_STATS gives the first one's registers to the others: 40 + 2 x 232 = 3 x 168.
+// The logits' kernels give the first one's registers to the others: 40 + 2 x 232 = 3 x 168.
 constexpr int kThreads = 384;
-// PAIR_STATS adds the tensor core's sums of at most 12 k-slabs (768 products) up in
-// registers: its accumulator rounds towards zero, which over 2048 products left logits of
+// The logits' kernels add the tensor core's sums of at most 12 k-slabs (768 products) up in
+// registers: the accumulator rounds towards zero, which over 2048 products left logits of
 // 16 off by 1e-5 and the loss of a sure token by as much.  Errors of loss and lse on 8192 x
 // 131072 x 2048 (2-norm, relative), and the time: whole 1.5e-6, 2.37 ms; 16 slabs 7e-7,
 // 2.46 ms; 12 slabs 5e-7, 2.49 ms; 4 slabs 2e-7, 2.80 ms; a sum in fp32 has 4e-7.
@@ -95,7 +95,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int which = 0, u = 0;
 
   if (warp >= 4) {
-    if (EPI == PAIR_STATS) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    if (EPI != PAIR_STORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     const uint32_t quarter = warp & 3;      // TMEM lanes 32 * quarter .. + 31
     const int half = (int)(warp - 4) >> 2;  // columns [half * bn / 2, + bn / 2)
     const uint32_t stage = p.sbase + S::kOut + (warp - 4) * 8192;
@@ -134,12 +134,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int col0 = t.n * bn + half * cols;
       const uint32_t from = p.tmem + half * cols + ((quarter * 32) << 16);
 
-      if (EPI == PAIR_STATS) {
-        // Softmax statistics of the tile's columns for this row, and the target's logit
-        // where it lies among them.  Bound by the matrix product.
-        const long long y = row < q.M ? a.targets[row] : -1;
-        const int ycol = (y >= col0 && y < col0 + cols) ? (int)(y - col0) : -1;
-        float z[128];
+      float z[EPI == PAIR_STORE ? 1 : 128];
+      if (EPI != PAIR_STORE) {
+        // The logits of the tile's columns for this row, the same bits in both passes: the
+        // gradient of a sure token is what is left of z - lse.
         const int slabs = (q.K + 63) / 64, chunk = chunk_slabs(slabs);
         bool ok = true;
         for (int k0 = 0; k0 < slabs; k0 += chunk, ++lt) {
@@ -147,7 +145,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ok = p.wait(p.acc_full(acc), (lt >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          if (row0 < q.M) {
+          if (row0 < q.M && col0 < q.N) {
             const uint32_t src = from + acc * 256;
             if (k0 == 0) {
               tmem_load64(src, z);
@@ -169,6 +167,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         if (!ok) break;
         --lt;  // counted once more at the end of the loop
         if (row0 >= q.M || col0 >= q.N) continue;
+      }
+      if (EPI == PAIR_STATS) {
+        // Softmax statistics of these columns, and the target's logit where it lies among
+        // them.  Bound by the matrix product.
+        const long long y = row < q.M ? a.targets[row] : -1;
+        const int ycol = (y >= col0 && y < col0 + cols) ? (int)(y - col0) : -1;
         float m = -INFINITY;
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
@@ -215,13 +219,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               make_float2(m, (s2[0].x + s2[1].x) + (s2[0].y + s2[1].y));
         continue;
       }
-      if (!p.wait(p.acc_full(b), (lt >> 1) & 1)) break;
-      tc_fence_after();
-      const uint32_t src = from + b * 256;
-      if (row0 >= q.M || col0 >= q.N) {  // nothing of this warp's part is inside
-        p.release(b);
-        continue;
-      }
       if (EPI == PAIR_DLOGITS) {
         // d = g (e^{z - lse} - [column = target]), rounded to the operand type of
         // the two products that follow (bf16: any range; fp16: g is brought near
@@ -235,15 +232,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const long long yc = y - a.col_off - col0;
         const int ycol = (live && yc >= 0 && yc < cols) ? (int)yc : -1;
         const float2 log2e = make_float2(kLog2e, kLog2e), off = make_float2(-lse, -lse), gg = make_float2(g, g);
-#pragma unroll 1
-        for (int c = 0; c < cols; c += 64, buf ^= 1) {
+#pragma unroll
+        for (int c = 0; c < 128; c += 64) {
+          if (c >= cols) break;
           if (lane == 0) {
             if (a.two_terms) bulk_wait_read();
             else bulk_wait_read_but_one();
           }
-          float v[64];
-          tmem_load64(src + c, v);
-          if (c == cols - 64) p.release(b);
+          float* const v = z + c;
           const bool target = __any_sync(0xffffffffu, ycol >= c && ycol < c + 64);
           float own = 0.f;
           if (target) {
@@ -283,8 +279,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               if (col0 + c < q.N) tma_store_3d(&q.tm_c, stage + (buf ^ 1) * 4096, col0 + c, row0, 1);
             });
           }
+          buf ^= 1;
         }
       } else {
+        if (!p.wait(p.acc_full(b), (lt >> 1) & 1)) break;
+        tc_fence_after();
+        const uint32_t src = from + b * 256;
+        if (row0 >= q.M || col0 >= q.N) {  // nothing of this warp's part is inside
+          p.release(b);
+          continue;
+        }
         // c = mul * acc (+ c_add): 16-bit or fp32 out; fp32 may be added to what is
         // there (each element once per launch, so the sum's order is fixed).  Split
         // along K, each split has a plane of its own.
@@ -347,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     }
     if (lane == 0) bulk_wait_all();
   } else {
-    if (EPI == PAIR_STATS) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (EPI != PAIR_STORE) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0) {
       if (lane == 0) {
         uint32_t cnt = 0;
@@ -370,7 +374,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const Operand A{nullptr, nullptr, q.a_mn}, B{nullptr, nullptr, q.b_mn};
         const int k1 = k_at(q, s + 1);
         for (int k0 = k_at(q, s); ok && k0 < k1;) {
-          const int k = EPI == PAIR_STATS ? min(k0 + chunk_slabs(k1), k1) : k1;  // one split: k1 slabs
+          const int k = EPI != PAIR_STORE ? min(k0 + chunk_slabs(k1), k1) : k1;  // one split: k1 slabs
           ok = p.rank == 0 ? p.multiply(cnt, lt, a.ab_bf16, A, B, q.bn, 0, 0, k0, k) : p.forward(lt);
           k0 = k;
         }
