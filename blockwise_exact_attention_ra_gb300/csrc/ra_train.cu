@@ -191,8 +191,8 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const float* grad, con
   if (threadIdx.x == 0) {
     int k = 0;
     if (m > 0.f && m < INFINITY) {
-      k = 13 - ilogbf(m);
-      k = k > 100 ? 100 : (k < -100 ? -100 : k);
+      k = 13 - ilogbf(m);  // -114 at least
+      k = k > 126 ? 126 : k;  // 2^-126 is the smallest normal number
     }
     scale[0] = ldexpf(1.f, k);
     scale[1] = ldexpf(1.f, -k);
