@@ -298,8 +298,8 @@ cudaError_t launch_xent_few(const XentFewArgs& a, cudaStream_t st);
 cudaError_t launch_xent_finish(const float2* stats, int parts, const float* target_logit, const long long* targets,
                                long long ignore, long long V, long long T, float* loss, float* lse, int* status,
                                cudaStream_t st);
-// scale = {2^k, 2^-k} with 2^k max |grad| in [2^13, 2^14) over the rows with a loss, k at most
-// 126 (max |grad| from 2^-113 on).
+// scale = {2^k, 2^-k} with 2^k max |grad| in [2^13, 2^14) over the rows with a loss, infinities
+// left out; k at most 126 (max |grad| from 2^-113 on).
 cudaError_t launch_xent_scale(const float* grad, const long long* targets, long long ignore, long long V, long long T,
                               float* scale, cudaStream_t st);
 // out (dtype) <- the sum of `planes` fp32 planes of n elements each (n a multiple of 8)

@@ -181,7 +181,9 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const float* grad, con
   float m = 0.f;
   for (long long t = threadIdx.x; t < T; t += 1024) {
     const long long y = targets[t];
-    if (y != ignore && y >= 0 && y < V) m = fmaxf(m, fabsf(grad[t]));
+    const float g = fabsf(grad[t]);
+    // an infinity or NaN concerns its own token alone
+    if (y != ignore && y >= 0 && y < V && g < INFINITY) m = fmaxf(m, g);
   }
   m = warp_max(m);
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(1024) xent_scale_kernel(const float* grad, con
   m = warp_max(part[threadIdx.x]);
   if (threadIdx.x == 0) {
     int k = 0;
-    if (m > 0.f && m < INFINITY) {
+    if (m > 0.f) {
       k = 13 - ilogbf(m);  // -114 at least
       k = k > 126 ? 126 : k;  // 2^-126 is the smallest normal number
     }

@@ -32,3 +32,19 @@ def test_powers_of_two_of_the_loss_gradient(ra, T, k):
         off = (a.double() - b.double() * 2.0 ** -k).abs().max()
         assert float(off) <= 39 * 2.0 ** -150 * 2.0 ** -k
     ra.ra_sync_status()
+
+
+@pytest.mark.parametrize("T", [9, 40, 100])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_one_unusable_loss_gradient_leaves_the_other_tokens(ra, T, bad):
+    # small gradients beside it: without their power of two they would be fp16 subnormals
+    x, w, y, g = make(T, 64, 400, torch.float16, 19, ignored=0.0)
+    g *= 2.0 ** -30
+    g[4] = 0.0
+    _, lse = ra.xent_fwd(x, w, y)
+    want, _ = ra.xent_bwd(x, w, y, lse, g)
+    g[4] = bad
+    dx, _ = ra.xent_bwd(x, w, y, lse, g)
+    ra.ra_sync_status()
+    others = torch.arange(T, device="cuda") != 4
+    assert torch.equal(dx[others], want[others]) and not torch.isfinite(dx[4]).any()
