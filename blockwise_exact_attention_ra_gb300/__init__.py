@@ -471,6 +471,14 @@ def _allocate(stream, dev, *tensors):
     return [torch.empty(shape, dtype=dtype, device=dev) for shape, dtype in tensors]
 
 
+_INT_MAX = 2 ** 31 - 1  # ctypes passes the low 32 bits of a larger number
+
+
+def _fits(*sizes):
+    if max(sizes) > _INT_MAX:
+        raise RAError(1, f"sizes must be at most {_INT_MAX} (got {list(sizes)})")
+
+
 def _xent_check(x, w, targets):
     """(T, D, V, row stride of x, row stride of w); a single row passes 0."""
     shape, wshape = x.shape, w.shape
@@ -481,16 +489,22 @@ def _xent_check(x, w, targets):
     (xs, xc), (ws, wc) = x.stride(), w.stride()
     if D > 1 and (xc != 1 or wc != 1):
         raise RAError(1, f"x and w must have contiguous rows (strides {x.stride()}, {w.stride()})")
+    if V > _INT_MAX or D > _INT_MAX:
+        _fits(V, D)
     _vector(targets, "targets", T, torch.int64)
     return T, D, V, _stride(xs, T, "x"), _stride(ws, V, "w")
 
 
 def ra_xent_fwd_workspace_bytes(dtype, T, D, V):
+    if max(D, V) > _INT_MAX:
+        return 0  # as for other sizes that the call refuses
     return int(_lib().ra_xent_fwd_workspace_bytes(dtype, int(T), int(D), int(V)))
 
 
 def ra_xent_bwd_workspace_bytes(dtype, dx_dtype, T, D, V, block):
-    return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), int(block)))
+    if max(D, V) > _INT_MAX:
+        return 0
+    return int(_lib().ra_xent_bwd_workspace_bytes(dtype, dx_dtype, int(T), int(D), int(V), min(int(block), int(V))))
 
 
 def ra_xent_fwd(x, w, targets, loss, lse, workspace, ignore_index=-100, stream=None):
@@ -518,8 +532,8 @@ def ra_xent_bwd(x, w, targets, lse, dloss, block, dx, dw, workspace, ignore_inde
     T, D, V, xs, ws = sizes
     dev = _on_device(x, w, targets, lse, dloss, dx, dw, workspace)
     _check(_lib().ra_xent_bwd(x.data_ptr(), w.data_ptr(), _dt(x), T, D, V, xs, ws, targets.data_ptr(),
-                              int(ignore_index), lse.data_ptr(), dloss.data_ptr(), int(block), dx.data_ptr(), _dt(dx),
-                              dw.data_ptr(), _dt(dw), workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
+                              int(ignore_index), lse.data_ptr(), dloss.data_ptr(), min(int(block), V), dx.data_ptr(),
+                              _dt(dx), dw.data_ptr(), _dt(dw), workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
 
 
 # The two wrappers call the library themselves: host time bounds small losses, and each
@@ -546,7 +560,7 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
     _vector(dloss, "dloss", T, torch.float32)
     dev, lib, dtype = _on_device(x, w, targets, lse, dloss), _lib(), _dt(x)
     dx_code, dw_code = _code(dx_dtype), _code(dw_dtype)
-    block = V if block is None else int(block)
+    block = V if block is None else min(int(block), V)
     nbytes = lib.ra_xent_bwd_workspace_bytes(dtype, dx_code, T, D, V, block)
     dx, dw, workspace = _allocate(stream, dev, ((T, D), dx_dtype), ((V, D), dw_dtype), (nbytes, torch.uint8))
     code = lib.ra_xent_bwd(x.data_ptr(), w.data_ptr(), dtype, T, D, V, xs, ws, targets.data_ptr(), int(ignore_index),
@@ -558,6 +572,8 @@ def xent_bwd(x, w, targets, lse, dloss, block=None, dx_dtype=torch.float32, dw_d
 
 
 def ra_newton_schulz_workspace_bytes(batch, rows, cols):
+    if max(batch, rows, cols) > _INT_MAX:
+        return 0
     return int(_lib().ra_newton_schulz_workspace_bytes(int(batch), int(rows), int(cols)))
 
 
@@ -568,6 +584,7 @@ def _ns_layout(t, name):
     if n not in (2, 3):
         raise RAError(1, f"{name} must be [rows, cols] or [batch, rows, cols] (got {list(t.shape)})")
     batch, rows, cols = t.shape if n == 3 else (1, *t.shape)
+    _fits(batch, rows, cols)
     strides = t.stride()
     if strides[-1] != 1 and cols > 1:
         raise RAError(1, f"{name} must have contiguous rows (strides {strides})")
@@ -581,7 +598,7 @@ _Float3 = ctypes.c_float * 3
 def _newton_schulz(layout, g, out, out_strides, workspace, nbytes, steps, coeffs, eps, stream, dev):
     if len(coeffs) != 3:
         raise RAError(1, f"coeffs must be three numbers (got {len(coeffs)})")
-    _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), *layout, _Float3(*coeffs), int(steps), float(eps),
+    _check(_lib().ra_newton_schulz(g.data_ptr(), _dt(g), *layout, _Float3(*coeffs), min(int(steps), _INT_MAX), float(eps),
                                    out.data_ptr(), _dt(out), *out_strides, workspace.data_ptr(), nbytes,
                                    _handle(stream, dev)))
 
