@@ -1794,7 +1794,10 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
     if (*d.rs == 0) *d.rs = cols;
     const long long extent = (long long)(rows - 1) * *d.rs + cols;
     if (*d.bs == 0) *d.bs = extent;
-    if (*d.rs < cols || *d.rs > (1ll << 40) || *d.bs < extent || *d.bs > (1ll << 45))
+    // one matrix after the other, or all matrices' rows between two rows of one
+    const bool apart = *d.bs >= extent, between = *d.bs >= cols && *d.bs <= (1ll << 45) &&
+                                                  *d.rs >= (batch - 1) * *d.bs + cols;
+    if (*d.rs < cols || *d.rs > (1ll << 40) || *d.bs > (1ll << 45) || !(apart || between))
       return fail(RA_ERR_INVALID_ARG, "%s strides (%lld, %lld) make rows or matrices overlap", d.name, *d.bs, *d.rs);
   }
   const NsWs l = ns_layout(s);

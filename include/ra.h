@@ -393,7 +393,8 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  * with (a, b, c) = coeffs[0..2], read on the host; (3.4445, -4.7750, 2.0315) and five
  * steps bring every singular value that is not tiny near 1.
  *   g [batch, rows, cols] in any dtype, out [batch, rows, cols] in any dtype; rows and
- *   matrices at the strides given (elements, 0 = packed).  out may be g itself where
+ *   matrices at the strides given (elements, 0 = packed): matrices one after the other, or
+ *   rows of all of them between two rows of one ([rows, batch, cols]).  out may be g itself where
  *   dtype and strides agree.  Sizes of any value up to 65536; each matrix of the
  *   batch is orthogonalised by itself.
  *   The products run on the tensor cores with fp16 operands (held times powers of two
