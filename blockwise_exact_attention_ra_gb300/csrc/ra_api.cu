@@ -1616,6 +1616,7 @@ struct NsShape {
   int batch, rows, cols, m;  // m: the smaller side
   long long ld, ldm;         // padded rows of X and of the m x m matrices
   double sx, sa, sb;         // powers of two by which X, A' and B' are held in fp16
+  double growth;             // log2 of the most by which a step lets a singular value grow
 };
 
 // The largest |p(s)| over s in [0, top], p(s) = a s + b s^3 + c s^5: at top or at a
@@ -1635,6 +1636,14 @@ double ns_bound(double a, double b, double c, double top) {
   }
   for (double r : roots)
     if (r > 0.0 && r < top * top && p(sqrt(r)) > best) best = p(sqrt(r));
+  return best;
+}
+// The largest |p(s) / s| over s in [0, top]: at an end or where a + b t + c t^2 turns, t = s^2.
+double ns_growth(double a, double b, double c, double top) {
+  auto q = [&](double t) { return fabs(a + t * (b + c * t)); };
+  double best = q(0.0) > q(top * top) ? q(0.0) : q(top * top);
+  const double turn = c != 0.0 ? -b / (2.0 * c) : -1.0;
+  if (turn > 0.0 && turn < top * top && q(turn) > best) best = q(turn);
   return best;
 }
 double pow2_below(double x) { return ldexp(1.0, ilogb(x)); }
@@ -1658,13 +1667,16 @@ int check_ns(int batch, int rows, int cols, const float* coeffs, int steps, floa
   // Singular values start at or below 1 and stay below `top`; from that follow the
   // largest entries of X, A' and B', which must fit fp16 times their powers of two.
   const double a = coeffs[0], b = coeffs[1], c = coeffs[2];
-  double top = 1.0, cur = 1.0;
+  double top = 1.0, cur = 1.0, growth = 1.0;
   for (int i = 0; i < steps; ++i) {
+    const double g = ns_growth(a, b, c, cur);
+    if (g > growth) growth = g;
     cur = ns_bound(a, b, c, cur);
     if (!(cur < 64.0))
       return fail(RA_ERR_UNSUPPORTED, "coeffs (%g, %g, %g) let singular values grow past 64", a, b, c);
     if (cur > top) top = cur;
   }
+  s.growth = log2(growth) * (1.0 + 1e-6);
   const double t2 = top * top, room = 32768.0;
   const double bmax = (fabs(b) + 2.0 * fabs(c) * t2) * t2 + fabs(c) * t2 * t2;
   s.sa = pow2_below(room / t2);
@@ -1721,7 +1733,7 @@ Cut ns_cut(const NsArgs& a, int kind, int pairs) {
   return Cut{narrow <= pairs ? 128 : 256, 1};
 }
 
-// barrier words and flags | norm parts | sums of X's squares (two buffers) | X high terms
+// words, flags, counts and shifts | norm parts | sums of X's squares (two buffers) | X high terms
 // (two buffers) | X low terms | A' | B' | sums of splits
 struct NsWs {
   size_t words, parts, sums[2], hi[2], lo, a, b, partials, total;
@@ -1741,7 +1753,7 @@ NsWs ns_layout(const NsShape& s) {
     return at;
   };
   const size_t x = (size_t)s.batch * s.rows * s.ld * 2, g = (size_t)s.batch * s.m * s.ldm * 2;
-  w.words = take(((size_t)kNsWords + s.batch) * 4);
+  w.words = take(((size_t)kNsWords + 2 * s.batch) * 4);
   w.parts = take((size_t)s.batch * kNsParts * 3 * 4);
   for (size_t& at : w.sums) at = take((size_t)s.batch * ns_sums(s) * 4);
   w.hi[0] = take(x);
@@ -1853,6 +1865,8 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
   for (int i = 0; i < 2; ++i) a.sums[i] = reinterpret_cast<float*>(base + l.sums[i]);
   a.sums_ld = (long long)ns_sums(s);
   a.counts = a.words + kNsWords;
+  a.shifts = reinterpret_cast<int*>(a.counts + batch);
+  a.growth = (float)s.growth;
   uint16_t* hi[2] = {reinterpret_cast<uint16_t*>(base + l.hi[0]), reinterpret_cast<uint16_t*>(base + l.hi[1])};
   a.hi0 = hi[0];
   a.lo = reinterpret_cast<uint16_t*>(base + l.lo);

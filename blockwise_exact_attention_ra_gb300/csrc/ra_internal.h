@@ -345,6 +345,8 @@ struct NsArgs {
   long long out_ld, out_bstride;
   unsigned int* words;  // zeroed at first: the mark of a launch that gave up, the flags, the counts
   unsigned int* counts; // per matrix: warps that have scaled it and halves of tiles written
+  int* shifts;          // per matrix: X is held times 2^shift at first
+  float growth;         // log2 of the most by which a step lets X grow: what the shift falls by
   unsigned int* flags;  // per warp of a split: the last phase whose sums for the others it has written
   float* partials;      // sums that splits leave each other, [unit][CTA][warp][128 columns][32 rows]
   int* status;

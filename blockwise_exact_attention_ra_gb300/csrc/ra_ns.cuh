@@ -86,8 +86,10 @@ __device__ __forceinline__ void ns_add_square(float x, float* s) {
 }
 
 // mul / (|G|_F + eps) as f 2^e0 2^e1 (in range for every norm), by one warp; the parts
-// are added in a fixed order, in 64 bits.
-__device__ __forceinline__ void ns_factor(const float* parts, int num_parts, float mul, float eps, float* f) {
+// are added in a fixed order, in 64 bits.  With `shift`, times the power of two that brings
+// |G|_F / (|G|_F + eps) to 1/2 ... 1, if it is less: 2^*shift.
+__device__ __forceinline__ void ns_factor(const float* parts, int num_parts, float mul, float eps, float* f,
+                                          int* shift = nullptr) {
   double s = 0.0;
   for (int i = lane_id(); i < num_parts; i += 32) {
     const float* p = parts + 3 * i;
@@ -95,9 +97,17 @@ __device__ __forceinline__ void ns_factor(const float* parts, int num_parts, flo
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  const double norm = sqrt(s) + (double)eps;
-  const double inv = norm > 0.0 ? (double)mul / norm : 0.0;
+  const double own = sqrt(s), norm = own + (double)eps;
+  double inv = norm > 0.0 ? (double)mul / norm : 0.0;
   int e = 0;
+  if (shift) {
+    *shift = 0;
+    if (own > 0.0 && own < 0.5 * norm) {  // neither 0 nor NaN
+      (void)frexp(own / norm, &e);
+      *shift = -e;
+      inv = ldexp(inv, -e);
+    }
+  }
   f[2] = (float)frexp(inv, &e);
   f[0] = ldexpf(1.f, e / 2);
   f[1] = ldexpf(1.f, e - e / 2);

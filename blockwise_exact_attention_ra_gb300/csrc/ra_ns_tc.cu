@@ -9,7 +9,10 @@
 // which is a X + (b A + c A^2) X with A = A' + alpha I.  The products' operands are fp16
 // (times powers of two); taking alpha I out keeps the rounding of the Gram matrix's
 // large common diagonal out of the result, and X is carried as two fp16 terms (hi the
-// operand, hi + lo the state).  A' and B' are symmetric: blocks left of the diagonal are
+// operand, hi + lo the state).  Where |G| is far below eps, X is tiny at first and grows by
+// the polynomial's slope at each step: it is held times a power of two that falls from step
+// to step (without, norms of 1e-5 eps left errors of 3e-3, and of 1e-8 eps nothing).  A' and
+// B' are symmetric: blocks left of the diagonal are
 // neither computed nor held, the products read their mirror images (ra_pair.cuh).
 //
 // One launch because the chain of a small matrix is all latency: as launches of their
@@ -84,6 +87,9 @@ __device__ __forceinline__ float warp_total(const float* p, int n) {
   }
   return warp_sum(((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7])));
 }
+
+// 2^e for e of at most 0; 0 below fp32's normal numbers.
+__device__ __forceinline__ float pow2(int e) { return e < -126 ? 0.f : __int_as_float((e + 127) << 23); }
 
 // Tiles of a symmetric product: only those that reach the diagonal or lie right of it.
 __device__ __forceinline__ Tile tile_sym(int t, int tn, int bn) {
@@ -293,7 +299,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const unsigned id = (blockIdx.x / teams) * 256 + (threadIdx.x - 64), all = ns_team_size(a, team) * 256;
       for (int b = team; b < a.batch; b += teams) {
         float f[3];
-        ns_factor(a.parts + (long long)b * kNsParts * 3, a.num_parts, a.sx, a.eps, f);
+        int shift;
+        ns_factor(a.parts + (long long)b * kNsParts * 3, a.num_parts, a.sx, a.eps, f, &shift);
+        if (id == 0) a.shifts[b] = shift;
         for (unsigned i = id; i < per; i += all * kNsBatch) {
           NsRaw g[kNsBatch];
 #pragma unroll
@@ -389,14 +397,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           int next = 0;  // the next piece to finish
           while (next < cols && !finishes(next)) next += 64;
           if (next < cols) prefetch(next);
-          // alpha: the mean of the Gram matrix's diagonal, 1 / m at first
+          // X is held times 2^held in this step, its Gram matrix without; the new X times 2^then,
+          // the result without
+          const float shift = (float)__ldcg(a.shifts + b);
+          const int held = max((int)floorf(shift - step * a.growth), 0);
+          const int then = last ? 0 : max((int)floorf(shift - (step + 1) * a.growth), 0);
+          const float gram_mul = pow2(-2 * held), new_mul = pow2(then - held);
+          // alpha: the mean of the Gram matrix's diagonal, at first about 1 / m
           const float alpha =
-              step ? warp_total(sums + (long long)b * a.sums_ld, 16 * a.per[NS_UPDATE] * a.splits[NS_UPDATE]) * a.alpha_mul
-                   : 1.f / (float)a.m;
+              gram_mul *
+              (step ? warp_total(sums + (long long)b * a.sums_ld, 16 * a.per[NS_UPDATE] * a.splits[NS_UPDATE]) * a.alpha_mul
+                    : 1.f / (float)a.m);
           float sq = 0.f;  // UPDATE: squares of this warp's part of the new X
           const float lin = (a.cb + 2.f * a.cc * alpha) * a.square_lin;
-          const float own = a.ca + alpha * (a.cb + a.cc * alpha);
-          const float shift = alpha * a.sa;
+          const float own = (a.ca + alpha * (a.cb + a.cc * alpha)) * new_mul, update_acc = a.update_acc * new_mul;
+          const float gram_acc = a.gram_acc * gram_mul;
+          const float diagonal = alpha * a.sa;
           if (!p.wait(p.acc_full(acc), (lt >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
           if (f.splits > 1) {
@@ -454,7 +470,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (kind == NS_GRAM) {
               const int diag = row - col0 - c;  // this row's column of the diagonal
 #pragma unroll
-              for (int j = 0; j < 64; ++j) v[j] = fmaf(v[j], a.gram_acc, j == diag ? -shift : 0.f);
+              for (int j = 0; j < 64; ++j) v[j] = fmaf(v[j], gram_acc, j == diag ? -diagonal : 0.f);
             } else if (kind == NS_SQUARE) {
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
@@ -475,8 +491,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                   const float2 g = unpack_half2(qq[i]), e = unpack_half2(rr[i]);
-                  v[8 * j + 2 * i] = fmaf(v[8 * j + 2 * i], a.update_acc, own * (g.x + e.x));
-                  v[8 * j + 2 * i + 1] = fmaf(v[8 * j + 2 * i + 1], a.update_acc, own * (g.y + e.y));
+                  v[8 * j + 2 * i] = fmaf(v[8 * j + 2 * i], update_acc, own * (g.x + e.x));
+                  v[8 * j + 2 * i + 1] = fmaf(v[8 * j + 2 * i + 1], update_acc, own * (g.y + e.y));
                 }
               }
             }
