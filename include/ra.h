@@ -391,7 +391,9 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *     X = G / (|G|_F + eps);   `steps` times:  A = X X^T (X^T X where rows > cols),
  *     X <- a X + (b A + c A^2) X
  * with (a, b, c) = coeffs[0..2], read on the host; (3.4445, -4.7750, 2.0315) and five
- * steps bring every singular value that is not tiny near 1.
+ * steps bring every singular value that is not tiny near 1.  (The iteration: Kovarik 1970,
+ * Bjorck and Bowie 1971; these coefficients: K. Jordan et al., "Muon: An optimizer for
+ * hidden layers in neural networks", 2024.)
  *   g [batch, rows, cols] in any dtype, out [batch, rows, cols] in any dtype; rows and
  *   matrices at the strides given (elements, 0 = packed): matrices one after the other, or
  *   rows of all of them between two rows of one ([rows, batch, cols]).  out may be g itself where
@@ -401,11 +403,16 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *   that follow from the size and the coefficients, so that nothing leaves fp16's
  *   range) and fp32 sums; X is carried as two fp16 terms, and the Gram matrix without
  *   the mean of its diagonal, which enters in fp32, so that its rounding is no common
- *   factor of the result.  For gradients with sides of 32 or more the result is within
- *   about 2e-3 (relative, 2-norm) of exact arithmetic; with a side of 8 or less and
- *   singular values a thousand apart it is within 5e-2.  G = 0 gives 0;
- *   infinities and NaN in a matrix give NaN.  Coefficients that let the singular
- *   values grow past 64 return RA_ERR_UNSUPPORTED.
+ *   factor of the result.  What the operands' roundings leave along directions of zero or
+ *   tiny singular values is multiplied by up to a per step.  With (3.4445, -4.7750, 2.0315)
+ *   and five steps the result is within (relative, 2-norm, m the smaller side)
+ *     2.5e-3 of exact arithmetic for singular values that are spread (Gaussian, or decaying
+ *            to a thousandth) and m >= 32,
+ *     0.12 / sqrt(m) for any others: for ranks of an eighth to a quarter of m, the worst,
+ *            8e-3 was measured at m = 32, 4e-3 at 128, 3e-3 at 256 and 8e-2 at 2.
+ *   Norms far below eps lose nothing.  G = 0 gives 0; infinities and NaN in a matrix give
+ *   NaN.  Coefficients that let the singular values grow past 64 return
+ *   RA_ERR_UNSUPPORTED.
  *   workspace: device memory, 256-byte aligned, about 6 bytes per element of g, 4 per
  *   element of a square matrix of the smaller side, and up to 20 MB for each of the
  *   three products that is split.  It must not be in use by work that overlaps the call
