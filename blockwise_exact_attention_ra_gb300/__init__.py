@@ -14,8 +14,8 @@ Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 additionally allocate outputs and workspace with torch; so do ``ffn_fwd`` /
 ``ffn_bwd`` (a feed-forward layer), ``xent_fwd`` / ``xent_bwd`` (the cross
 entropy of its output against a vocabulary) and ``newton_schulz`` (the
-orthogonalised update of a weight's gradient), the last three on the stream they
-are given.
+orthogonalised update of a weight's gradient).  What they allocate belongs to the
+stream they are given.
 """
 import ctypes
 import os
@@ -414,8 +414,9 @@ def ffn_fwd(x, w1, w2, block=None, y_dtype=None, stream=None):
     """Convenience wrapper: allocates y and the workspace."""
     T, dm, dh = _ffn_check(x, w1, w2)
     block = T if block is None else block
-    y = torch.empty(T, dm, dtype=y_dtype or x.dtype, device=x.device)
-    ws = _workspace(ra_ffn_workspace_bytes(_dt(x), T, dm, dh, block, False), x.device)
+    with torch.cuda.stream(stream):
+        y = torch.empty(T, dm, dtype=y_dtype or x.dtype, device=x.device)
+        ws = _workspace(ra_ffn_workspace_bytes(_dt(x), T, dm, dh, block, False), x.device)
     ra_ffn_fwd(x, w1, w2, block, y, ws, stream)
     return y
 
@@ -423,10 +424,11 @@ def ffn_fwd(x, w1, w2, block=None, y_dtype=None, stream=None):
 def ffn_bwd(x, w1, w2, dy, block=None, dx_dtype=torch.float32, stream=None):
     T, dm, dh = _ffn_check(x, w1, w2)
     block = T if block is None else block
-    dx = torch.empty(T, dm, dtype=dx_dtype, device=x.device)
-    dw1 = torch.empty(dh, dm, dtype=torch.float32, device=x.device)
-    dw2 = torch.empty(dm, dh, dtype=torch.float32, device=x.device)
-    ws = _workspace(ra_ffn_workspace_bytes(_dt(x), T, dm, dh, block, True), x.device)
+    with torch.cuda.stream(stream):
+        dx = torch.empty(T, dm, dtype=dx_dtype, device=x.device)
+        dw1 = torch.empty(dh, dm, dtype=torch.float32, device=x.device)
+        dw2 = torch.empty(dm, dh, dtype=torch.float32, device=x.device)
+        ws = _workspace(ra_ffn_workspace_bytes(_dt(x), T, dm, dh, block, True), x.device)
     ra_ffn_bwd(x, w1, w2, dy, block, dx, dw1, dw2, ws, stream)
     return dx, dw1, dw2
 
@@ -652,9 +654,10 @@ def ring_attention_fwd(q, k, v, P, causal=True, scale=None, o_dtype=torch.float3
     if scale is None:
         scale = q.shape[-1] ** -0.5
     B, N, Hq, d = q.shape
-    o = empty_like_layout(q, o_dtype)  # the q group's layout
-    lse = torch.empty(B, Hq, N, dtype=torch.float32, device=q.device)
-    ws = _workspace(ra_ring_fwd_workspace_bytes(_dt(q), shape_of(q, k), P), q.device)
+    with torch.cuda.stream(stream):  # what is allocated belongs to the stream it is used on
+        o = empty_like_layout(q, o_dtype)  # the q group's layout
+        lse = torch.empty(B, Hq, N, dtype=torch.float32, device=q.device)
+        ws = _workspace(ra_ring_fwd_workspace_bytes(_dt(q), shape_of(q, k), P), q.device)
     if host_len is not None:
         if striped:
             raise RAError(1, "striped layouts do not combine with per-host lengths")
@@ -670,11 +673,11 @@ def ring_attention_bwd(q, k, v, o, lse, dO, P, causal=True, scale=None,
     """Allocate dQ, dK, dV (grad_dtype) and workspace and run the ring backward."""
     if scale is None:
         scale = q.shape[-1] ** -0.5
-    dq = empty_like_layout(q, grad_dtype)
-    dk = empty_like_layout(k, grad_dtype)
-    dv = empty_like_layout(k, grad_dtype)
-    ws = _workspace(ra_ring_bwd_workspace_bytes(_dt(q), _DTYPES[grad_dtype], shape_of(q, k), P),
-                    q.device)
+    with torch.cuda.stream(stream):
+        dq = empty_like_layout(q, grad_dtype)
+        dk = empty_like_layout(k, grad_dtype)
+        dv = empty_like_layout(k, grad_dtype)
+        ws = _workspace(ra_ring_bwd_workspace_bytes(_dt(q), _DTYPES[grad_dtype], shape_of(q, k), P), q.device)
     if host_len is not None:
         if striped:
             raise RAError(1, "striped layouts do not combine with per-host lengths")
