@@ -6,8 +6,8 @@
 // rows (bn / 2) r .. of B, so each SM loads half of the shared operand: against the
 // 128 x 256 tiles of a single CTA that cuts the operand bytes an SM takes from L2 by a
 // third, which is what bounds those (the feed-forward products reach 1470-1505
-// TFLOP/s that way; these 1760 on 4096 x 32768 x 2048 logits alone and 1670 on 8192 x
-// 131072 x 2048, 2.6 ms at the power limit).
+// TFLOP/s that way; these 1760 on 4096 x 32768 x 2048 logits alone and 1640-1670 on 8192 x
+// 131072 x 2048, 2.6-2.7 ms for calls back to back at the power limit, 2.5 in a cool run).
 //   warp 0      TMA producer (both CTAs): the CTA's halves of the A and B k-slabs,
 //               64 deep, into a ring of stages; all bytes are counted on the
 //               leader's (CTA 0's) barrier

@@ -1,7 +1,7 @@
 // The tensor-core products of the vocabulary cross entropy, on CTA pairs
 // (ra_pair.cuh):
 //   PAIR_STATS    logits' softmax statistics and the target's logit (forward)
-//   PAIR_DLOGITS  gradient of one block's logits, recomputed from x and w
+//   PAIR_DLOGITS  gradient of one block's logits, recomputed from x and w in the same pieces
 //   PAIR_STORE    dx = d W and dw = d^T x, whole or split along K, in one launch
 // The logits themselves stay in TMEM.
 #include <cuda_bf16.h>
@@ -25,8 +25,11 @@ constexpr int kThreads = 384;
 // The logits' kernels add the tensor core's sums of at most 12 k-slabs (768 products) up in
 // registers: the accumulator rounds towards zero, which over 2048 products left logits of
 // 16 off by 1e-5 and the loss of a sure token by as much.  Errors of loss and lse on 8192 x
-// 131072 x 2048 (2-norm, relative), and the time: whole 1.5e-6, 2.37 ms; 16 slabs 7e-7,
-// 2.46 ms; 12 slabs 5e-7, 2.49 ms; 4 slabs 2e-7, 2.80 ms; a sum in fp32 has 4e-7.
+// 131072 x 2048 (2-norm, relative), and the time of the kernel by itself: whole 1.5e-6, 2.37
+// ms; 16 slabs 7e-7, 2.46 ms; 12 slabs 5e-7, 2.49 ms; 4 slabs 2e-7, 2.80 ms; a sum in fp32 has
+// 4e-7.  The backward needs the forward's very logits: with sums of its own over the whole of D
+// the gradients of tokens with losses of 1e-4 to 1e-3 were off by 0.13 to 0.75 of their norm (now
+// 4e-3), for 1382 us a step instead of 1415 (4096 x 32768 x 2048).
 constexpr int kChunk = 12;
 __device__ __forceinline__ int chunk_slabs(int slabs) {
   const int chunks = (slabs + kChunk - 1) / kChunk;

@@ -354,12 +354,12 @@ int ra_ffn_bwd(const void* x, const void* w1, const void* w2, const void* dy, ra
  *   other target outside [0, V) gives loss NaN, no gradient, and RA_ERR_INVALID_ARG in
  *   the status word.
  *   loss, lse [T] fp32.  Products accumulate in fp32; the softmax's maxima and sums
- *   are fp32.  Infinities and NaN among the logits give NaN, as the formula does; a
- *   row whose logits are all -inf has lse = -inf and loss NaN.
+ *   are fp32.  +inf and NaN among the logits give NaN; a logit of -inf is an entry of
+ *   probability zero; a row whose logits are all -inf has lse = -inf and loss NaN.
  *   workspace: device memory, 256-byte aligned, of the size given (about T V / 8
- *   bytes for the forward; 2 T block bytes (4 for up to 64 tokens), 4 T D where dx is 16-bit and there is more
- *   than one block, and up to 20 MB each for dx and dw where their products are split,
- *   for the backward).  It must not be in use by work that overlaps the call on the
+ *   bytes for the forward; 2 T block bytes (4 for up to 64 tokens), 4 T D where dx is
+ *   16-bit and there is more than one block, and up to 20 MB each for dx and dw where
+ *   their products are split, for the backward).  It must not be in use by work that overlaps the call on the
  *   GPU.  Outputs overlap neither each other nor the inputs or the workspace. */
 size_t ra_xent_fwd_workspace_bytes(ra_dtype dtype, long long T, int D, int V);
 int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,
@@ -372,11 +372,14 @@ int ra_xent_fwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  *   lse from ra_xent_fwd of the same x, w, targets; dloss [T] fp32 (1 / T for a mean;
  *   values at ignored tokens are not used).
  *   dx [T, D] in dx_dtype and dw [V, D] in dw_dtype, packed, fully overwritten.  d is
- *   rounded to `dtype` before the two products (it is a tensor-core operand: half a
- *   unit of 2^-8 relative for bf16, of 2^-11 for fp16, whose values are brought into
- *   range by a power of two from max |dloss|), and kept as two such terms for up to 64
- *   tokens, where no sum averages its roundings out; the sums, over blocks too, are fp32.
- *   The results do not vary from run to run. */
+ *   rounded to `dtype` before the two products (it is a tensor-core operand: by up to
+ *   2^-8 relative for bf16, 2^-11 for fp16, whose values are brought into range by a power
+ *   of two from the largest finite |dloss|, 2^-113 at least), and kept as two such terms
+ *   for up to 64 tokens, where no sum averages its roundings out.  The logits are those of
+ *   the forward bit for bit, so that tokens the model is sure of keep their gradients.  The
+ *   sums, over blocks too, are fp32; the tensor core's round towards zero, which over
+ *   131072 tokens took up to 9e-5 of dw (x of one sign; 2e-5 otherwise).  The results do
+ *   not vary from run to run, nor dx with the type of dw or dw with that of dx. */
 size_t ra_xent_bwd_workspace_bytes(ra_dtype dtype, ra_dtype dx_dtype, long long T, int D, int V,
                                    int block);
 int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D, int V,
@@ -396,9 +399,9 @@ int ra_xent_bwd(const void* x, const void* w, ra_dtype dtype, long long T, int D
  * hidden layers in neural networks", 2024.)
  *   g [batch, rows, cols] in any dtype, out [batch, rows, cols] in any dtype; rows and
  *   matrices at the strides given (elements, 0 = packed): matrices one after the other, or
- *   rows of all of them between two rows of one ([rows, batch, cols]).  out may be g itself where
- *   dtype and strides agree.  Sizes of any value up to 65536; each matrix of the
- *   batch is orthogonalised by itself.
+ *   rows of all of them between two rows of one ([rows, batch, cols]).  out may be g
+ *   itself where dtype and strides agree.  Sizes of any value up to 65536; each matrix of
+ *   the batch is orthogonalised by itself.
  *   The products run on the tensor cores with fp16 operands (held times powers of two
  *   that follow from the size and the coefficients, so that nothing leaves fp16's
  *   range) and fp32 sums; X is carried as two fp16 terms, and the Gram matrix without
