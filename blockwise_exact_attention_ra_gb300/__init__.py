@@ -13,9 +13,12 @@ Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 ``RAError`` on a non-OK status.  ``ring_attention_fwd`` / ``ring_attention_bwd``
 additionally allocate outputs and workspace with torch; so do ``ffn_fwd`` /
 ``ffn_bwd`` (a feed-forward layer), ``xent_fwd`` / ``xent_bwd`` (the cross
-entropy of its output against a vocabulary) and ``newton_schulz`` (the
-orthogonalised update of a weight's gradient).  What they allocate belongs to the
-stream they are given.
+entropy of its output against a vocabulary), ``newton_schulz`` (the orthogonalised
+update of a weight's gradient), ``rotary_fwd`` / ``rotary_bwd`` and
+``norm_rotary_fwd`` / ``norm_rotary_bwd`` (rotary positions of queries and keys, with
+the norms of their heads in the same pass) and ``grad_norm`` / ``grad_clip`` (the norm
+of the gradients of many tensors, and their clipping by it).  What they allocate
+belongs to the stream they are given.
 """
 import ctypes
 import os
@@ -31,15 +34,18 @@ __all__ = [
     "ra_ring_step_host_workspace_bytes", "ra_ffn_workspace_bytes", "ra_ffn_fwd", "ra_ffn_bwd",
     "ra_xent_fwd_workspace_bytes", "ra_xent_fwd", "ra_xent_bwd_workspace_bytes", "ra_xent_bwd",
     "ra_newton_schulz_workspace_bytes", "ra_newton_schulz", "ffn_fwd", "ffn_bwd", "xent_fwd", "xent_bwd",
-    "newton_schulz",
+    "newton_schulz", "RaRotary", "ra_rotary_frequencies", "ra_rotary_fwd", "ra_rotary_bwd", "ra_norm_rotary_fwd",
+    "ra_norm_rotary_bwd_workspace_bytes", "ra_norm_rotary_bwd", "rotary_frequencies", "rotary_fwd", "rotary_bwd",
+    "norm_rotary_fwd", "norm_rotary_bwd", "ra_grad_workspace_bytes", "ra_grad_norm", "ra_grad_clip", "grad_norm",
+    "grad_clip",
     "ra_sync_status", "ra_last_error", "ra_launch_count", "ra_selftest_timeout", "ra_debug_visit_log",
     "ra_kernel_timing", "ra_kernel_timing_read",
     "ring_attention_fwd", "ring_attention_bwd", "RA_F32", "RA_BF16", "RA_F16",
-    "RA_CAUSAL", "RA_PRECISE", "RA_STRIPED",
+    "RA_CAUSAL", "RA_PRECISE", "RA_STRIPED", "RA_INTERLEAVED",
 ]
 
 RA_F32, RA_BF16, RA_F16 = 0, 1, 2
-RA_CAUSAL, RA_PRECISE, RA_STRIPED = 1, 2, 4
+RA_CAUSAL, RA_PRECISE, RA_STRIPED, RA_INTERLEAVED = 1, 2, 4, 8
 STATUS = {0: "RA_OK", 1: "RA_ERR_INVALID_ARG", 2: "RA_ERR_UNSUPPORTED", 3: "RA_ERR_CUDA",
           4: "RA_ERR_RANGE", 5: "RA_ERR_TIMEOUT"}
 _DTYPES = {torch.float32: RA_F32, torch.bfloat16: RA_BF16, torch.float16: RA_F16}
@@ -64,6 +70,12 @@ class RaShape(ctypes.Structure):
                 ("kv_rstride", ctypes.c_longlong), ("kv_hstride", ctypes.c_longlong)]
 
 
+class RaRotary(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int), ("freq", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("pos_bstride", ctypes.c_longlong), ("pos_off", ctypes.c_longlong), ("P", ctypes.c_int),
+                ("amplitude", ctypes.c_float)]
+
+
 def _load():
     if not os.path.exists(_LIBPATH):
         raise ImportError(
@@ -72,6 +84,7 @@ def _load():
     L = ctypes.CDLL(_LIBPATH)
     vp, i, f, ll, sz, sh = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_longlong,
                             ctypes.c_size_t, RaShape)
+    dbl, rot = ctypes.c_double, RaRotary
     sig = {
         "ra_acc_init": (i, [vp, vp, vp, sh, vp]),
         "ra_block_fwd": (i, [vp, vp, vp, i, vp, vp, vp, sh, ll, ll, i, f, vp, sz, vp]),
@@ -96,6 +109,15 @@ def _load():
         "ra_ring_bwd_varlen": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, vp, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd_workspace_bytes": (sz, [i, i, sh, i]),
+        "ra_rotary_frequencies": (i, [i, dbl, dbl, i, dbl, dbl, dbl, vp]),
+        "ra_rotary_fwd": (i, [vp, vp, i, sh, rot, i, vp, vp, sh, vp]),
+        "ra_rotary_bwd": (i, [vp, vp, i, sh, rot, i, vp, vp, i, sh, vp]),
+        "ra_norm_rotary_fwd": (i, [vp, vp, i, sh, vp, vp, i, f, rot, i, vp, vp, sh, vp]),
+        "ra_norm_rotary_bwd_workspace_bytes": (sz, [i]),
+        "ra_norm_rotary_bwd": (i, [vp, vp, i, sh, vp, vp, i, sh, vp, vp, i, f, rot, i, vp, vp, i, sh, vp, vp, vp, sz, vp]),
+        "ra_grad_workspace_bytes": (sz, [i]),
+        "ra_grad_norm": (i, [vp, vp, vp, i, vp, vp, sz, vp]),
+        "ra_grad_clip": (i, [vp, vp, vp, i, f, f, vp, vp, vp, vp, sz, vp]),
         "ra_sync_status": (i, [vp]),
         "ra_last_error": (ctypes.c_char_p, []),
         "ra_launch_count": (ctypes.c_ulonglong, []),
@@ -624,6 +646,324 @@ def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, strea
     out, workspace = _allocate(stream, dev, (g.shape, out_dtype or g.dtype), (nbytes, torch.uint8))
     _newton_schulz(layout, g, out, (0, 0), workspace, nbytes, steps, coeffs, eps, stream, dev)
     return out
+
+
+# ------------------------------------------------ rotary positions, norms of heads
+_ROTARY_METHODS = {"linear": 0, "base": 1, "parts": 2}
+
+
+def ra_rotary_frequencies(rot, base, scale, method, trained, fast, slow, freq):
+    """freq (float64 host tensor of rot / 2) <- the frequencies of a method (0, 1, 2)."""
+    if freq.is_cuda or freq.dtype != torch.float64 or freq.shape != (rot // 2,) or not freq.is_contiguous():
+        raise RAError(1, f"freq must be a contiguous float64 host tensor [{rot // 2}]")
+    _check(_lib().ra_rotary_frequencies(int(rot), float(base), float(scale), int(method), float(trained), float(fast),
+                                        float(slow), freq.data_ptr()))
+
+
+def rotary_frequencies(rot, base=10000.0, scale=1.0, method="linear", trained=0, fast=32.0, slow=1.0, device="cuda"):
+    """Frequencies of `rot` rotated columns, in radians per position (float64 tensor on
+    `device`), stretched to `scale` times the trained length: "linear" (positions
+    interpolated), "base" (a larger base) or "parts" (by the turns that each makes in the
+    `trained` length).  See include/ra.h."""
+    if method not in _ROTARY_METHODS:
+        raise RAError(1, f"method must be one of {sorted(_ROTARY_METHODS)} (got {method!r})")
+    freq = torch.empty(max(0, int(rot)) // 2, dtype=torch.float64)
+    ra_rotary_frequencies(int(rot), base, scale, _ROTARY_METHODS[method], trained, fast, slow, freq)
+    return freq.to(device)
+
+
+def _rot_strides(t, name):
+    s = t.stride()
+    if len(s) != 4:
+        raise RAError(1, f"{name} must be [B, N, H, d]")
+    n = t.shape
+    if s[3] != 1 and n[3] > 1:
+        raise RAError(1, f"{name} must have a contiguous last (head) dimension (strides {s})")
+    out = [s[i] if n[i] > 1 else 0 for i in range(3)]
+    for i in range(3):
+        if n[i] > 1 and s[i] == 0:
+            raise RAError(1, f"{name} must not be expanded (stride 0)")
+    return out
+
+
+def _rot_shape(q, k, qn="q", kn="k"):
+    """RaShape of queries and keys of the same rows; k may be None."""
+    qb, qr, qh = _rot_strides(q, qn)
+    B, N, Hq, d = q.shape
+    if max(B, N, Hq, d) > _INT_MAX:
+        _fits(B, N, Hq, d)
+    if k is None:
+        return RaShape(B, N, N, Hq, 1, d, qb, 0, qr, qh, 0, 0)
+    kb, kr, kh = _rot_strides(k, kn)
+    kB, kN, Hkv, kd = k.shape
+    if (kB, kN, kd) != (B, N, d) or k.dtype != q.dtype:
+        raise RAError(1, f"{qn} and {kn} must have the same batch, rows, head dimension and dtype (got {list(q.shape)} "
+                         f"{q.dtype}, {list(k.shape)} {k.dtype})")
+    if Hkv > _INT_MAX:
+        _fits(Hkv)
+    return RaShape(B, N, N, Hq, Hkv, d, qb, kb, qr, qh, kr, kh)
+
+
+def _same_shape(t, ref, name):
+    if (t is None) != (ref is None) or (t is not None and t.shape != ref.shape):
+        raise RAError(1, f"{name} must have the shape of what it belongs to (got "
+                         f"{None if t is None else list(t.shape)}, {None if ref is None else list(ref.shape)})")
+
+
+def _rotary(shape, freq, positions, pos_off, amplitude, P):
+    """RaRotary; freq None: no rotation."""
+    if freq is None:
+        return RaRotary(0, None, None, 0, 0, 1, 1.0)
+    if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
+        raise RAError(1, f"freq must be a contiguous float64 tensor [rot / 2] (got {freq.dtype} {list(freq.shape)})")
+    if P > _INT_MAX or 2 * freq.shape[0] > _INT_MAX:
+        _fits(P, 2 * freq.shape[0])
+    ptr, bstride = None, 0
+    if positions is not None:
+        B, N = shape.B, shape.N_q
+        n = positions.shape
+        if positions.dtype != torch.int64 or (n != (N,) and n != (B, N) and n != (1, N)):
+            raise RAError(1, f"positions must be int64 [N] or [B, N] (got {positions.dtype} {list(n)})")
+        st = positions.stride()
+        if N > 1 and st[-1] != 1:
+            raise RAError(1, f"positions must be contiguous along the rows (strides {st})")
+        if len(n) == 2 and n[0] > 1 and st[0] != 0:
+            bstride = st[0]
+        ptr = positions.data_ptr()
+    return RaRotary(2 * freq.shape[0], freq.data_ptr(), ptr, bstride, pos_off, P, amplitude)
+
+
+def _rot_flags(interleaved, striped):
+    return (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
+
+
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _there(*tensors):
+    return [t for t in tensors if t is not None]
+
+
+def _rot_weights(d, q_weight, k_weight):
+    """dtype code of the weights [d] of a norm (either may be None)."""
+    code = None
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is None:
+            continue
+        if t.shape != (d,) or not t.is_contiguous():
+            raise RAError(1, f"{name} must be contiguous [{d}] (got {list(t.shape)})")
+        if code not in (None, _dt(t)):
+            raise RAError(1, "q_weight and k_weight must have one dtype")
+        code = _dt(t)
+    return RA_F32 if code is None else code
+
+
+def ra_rotary_fwd(q, k, freq, q_out, k_out, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1,
+                  striped=False, stream=None):
+    """q_out, k_out <- q, k rotated by their positions (q_out may be q, k_out k; k and
+    k_out may be None).  See include/ra.h."""
+    _rotary_call(False, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream)
+
+
+def ra_rotary_bwd(dq_out, dk_out, freq, dq, dk, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1,
+                  striped=False, stream=None):
+    """dq, dk <- the gradients of q and k from those of ra_rotary_fwd's results."""
+    _rotary_call(True, dq_out, dk_out, freq, dq, dk, positions, pos_off, interleaved, amplitude, P, striped, stream)
+
+
+def _rotary_call(grad, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream):
+    shape = _rot_shape(q, k)
+    _same_shape(q_out, q, "the result of q")
+    _same_shape(k_out, k, "the result of k")
+    if freq is None:
+        raise RAError(1, "freq is None")
+    out_shape = _rot_shape(q_out, k_out)
+    rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
+    dev = _on_device(q, *_there(k, freq, q_out, k_out, positions))
+    dtype, out_dtype, flags = _dt(q), _dt(q_out), _rot_flags(interleaved, striped)
+    ptrs = q_out.data_ptr(), _data(k_out)
+    if grad:
+        code = _lib().ra_rotary_bwd(q.data_ptr(), _data(k), dtype, shape, rot, flags, *ptrs, out_dtype, out_shape,
+                                    _handle(stream, dev))
+    else:
+        if dtype != out_dtype:
+            raise RAError(1, f"the results must have the dtype of q and k (got {q_out.dtype}, {q.dtype})")
+        code = _lib().ra_rotary_fwd(q.data_ptr(), _data(k), dtype, shape, rot, flags, *ptrs, out_shape,
+                                    _handle(stream, dev))
+    if code:
+        _check(code)
+
+
+def _empty_pair(stream, dev, q, k, dtype):
+    if k is None:
+        return _allocate(stream, dev, (q.shape, dtype)) + [None]
+    return _allocate(stream, dev, (q.shape, dtype), (k.shape, dtype))
+
+
+def rotary_fwd(q, k, freq, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1, striped=False,
+               stream=None):
+    """Convenience wrapper: allocates the results (packed)."""
+    q_out, k_out = _empty_pair(stream, _on_device(q), q, k, q.dtype)
+    _rotary_call(False, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream)
+    return q_out, k_out
+
+
+def rotary_bwd(dq_out, dk_out, freq, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1, striped=False,
+               grad_dtype=None, stream=None):
+    """Convenience wrapper: allocates dq, dk (packed, dq_out's dtype by default)."""
+    dq, dk = _empty_pair(stream, _on_device(dq_out), dq_out, dk_out, grad_dtype or dq_out.dtype)
+    _rotary_call(True, dq_out, dk_out, freq, dq, dk, positions, pos_off, interleaved, amplitude, P, striped, stream)
+    return dq, dk
+
+
+def ra_norm_rotary_fwd(q, k, q_weight, k_weight, freq, q_out, k_out, eps=1e-6, positions=None, pos_off=0,
+                       interleaved=False, amplitude=1.0, P=1, striped=False, stream=None):
+    """q_out, k_out <- q, k normed for each head (weights [d] or None) and rotated (freq
+    None: not rotated).  See include/ra.h."""
+    shape = _rot_shape(q, k)
+    _same_shape(q_out, q, "the result of q")
+    _same_shape(k_out, k, "the result of k")
+    out_shape = _rot_shape(q_out, k_out)
+    if q.dtype != q_out.dtype:
+        raise RAError(1, f"the results must have the dtype of q and k (got {q_out.dtype}, {q.dtype})")
+    w_dtype = _rot_weights(shape.d, q_weight, k_weight)
+    rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
+    dev = _on_device(q, *_there(k, freq, q_out, k_out, positions, q_weight, k_weight))
+    code = _lib().ra_norm_rotary_fwd(q.data_ptr(), _data(k), _dt(q), shape, _data(q_weight), _data(k_weight), w_dtype, eps,
+                                     rot, _rot_flags(interleaved, striped), q_out.data_ptr(), _data(k_out), out_shape,
+                                     _handle(stream, dev))
+    if code:
+        _check(code)
+
+
+def norm_rotary_fwd(q, k, q_weight, k_weight, freq, eps=1e-6, positions=None, pos_off=0, interleaved=False,
+                    amplitude=1.0, P=1, striped=False, stream=None):
+    """Convenience wrapper: allocates the results (packed)."""
+    q_out, k_out = _empty_pair(stream, _on_device(q), q, k, q.dtype)
+    ra_norm_rotary_fwd(q, k, q_weight, k_weight, freq, q_out, k_out, eps, positions, pos_off, interleaved, amplitude, P,
+                       striped, stream)
+    return q_out, k_out
+
+
+def ra_norm_rotary_bwd_workspace_bytes(d):
+    return int(_lib().ra_norm_rotary_bwd_workspace_bytes(int(d)))
+
+
+def ra_norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dq_weight, dk_weight, workspace,
+                       eps=1e-6, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1, striped=False,
+                       stream=None):
+    """Gradients of ra_norm_rotary_fwd: dq, dk, and fp32 dq_weight, dk_weight [d] (or None)."""
+    shape = _rot_shape(q, k)
+    for t, ref, name in ((dq_out, q, "dq_out"), (dk_out, k, "dk_out"), (dq, q, "dq"), (dk, k, "dk")):
+        _same_shape(t, ref, name)
+    dout_shape, grad_shape = _rot_shape(dq_out, dk_out, "dq_out", "dk_out"), _rot_shape(dq, dk, "dq", "dk")
+    w_dtype = _rot_weights(shape.d, q_weight, k_weight)
+    for t, name in ((dq_weight, "dq_weight"), (dk_weight, "dk_weight")):
+        if t is not None:
+            _vector(t, name, shape.d, torch.float32)
+    rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
+    dev = _on_device(q, *_there(k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dq_weight, dk_weight, positions),
+                     workspace)
+    _check(_lib().ra_norm_rotary_bwd(q.data_ptr(), _data(k), _dt(q), shape, dq_out.data_ptr(), _data(dk_out), _dt(dq_out),
+                                     dout_shape, _data(q_weight), _data(k_weight), w_dtype, eps, rot,
+                                     _rot_flags(interleaved, striped), dq.data_ptr(), _data(dk), _dt(dq), grad_shape,
+                                     _data(dq_weight), _data(dk_weight), workspace.data_ptr(), _nbytes(workspace),
+                                     _handle(stream, dev)))
+
+
+def norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, eps=1e-6, positions=None, pos_off=0,
+                    interleaved=False, amplitude=1.0, P=1, striped=False, grad_dtype=None, stream=None):
+    """Convenience wrapper: allocates dq, dk (packed, q's dtype by default), the fp32
+    gradients of the weights (None for a tensor that is None, ones for weights) and the
+    workspace.  Returns dq, dk, dq_weight, dk_weight."""
+    dev, d = _on_device(q), q.shape[-1]
+    dq, dk = _empty_pair(stream, dev, q, k, grad_dtype or q.dtype)
+    dqw, dkw, ws = _allocate(stream, dev, ((d,), torch.float32), ((d,), torch.float32),
+                             ((ra_norm_rotary_bwd_workspace_bytes(d),), torch.uint8))
+    if k is None:
+        dkw = None
+    ra_norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dqw, dkw, ws, eps, positions, pos_off,
+                       interleaved, amplitude, P, striped, stream)
+    return dq, dk, dqw, dkw
+
+
+# ------------------------------------------------ norm and clipping of many tensors
+def ra_grad_workspace_bytes(count):
+    return int(_lib().ra_grad_workspace_bytes(min(int(count), _INT_MAX)))
+
+
+def _grad_arrays(tensors, name, dev):
+    """Host arrays of addresses, sizes and dtypes."""
+    n = len(tensors)
+    if n < 1:
+        raise RAError(1, f"{name} is empty")
+    codes = []
+    for t in tensors:
+        code = _DTYPES.get(t.dtype)
+        if code is None or t.device != dev or not t.is_contiguous():
+            raise RAError(1, f"{name} must be contiguous fp32, bf16 or fp16 tensors on one device (got {t.dtype} on "
+                             f"{t.device}, strides {t.stride()})")
+        codes.append(code)
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_longlong * n)(*[t.numel() for t in tensors]),
+            (ctypes.c_int * n)(*codes))
+
+
+def ra_grad_norm(grads, norm, workspace, stream=None):
+    """norm [1] or [] fp32 <- the 2-norm of all elements of all tensors of the list."""
+    if not len(grads):
+        raise RAError(1, "grads is empty")
+    dev = _on_device(grads[0], norm, workspace)
+    _norm_tensor(norm)
+    arrays = _grad_arrays(grads, "grads", dev)
+    _check(_lib().ra_grad_norm(*arrays, len(grads), norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
+                               _handle(stream, dev)))
+
+
+def _norm_tensor(norm):
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise RAError(1, f"norm must be one fp32 element (got {norm.dtype} {list(norm.shape)})")
+
+
+def ra_grad_clip(grads, max_norm, norm, workspace, outs=None, eps=1e-6, stream=None):
+    """norm <- the 2-norm of all tensors; outs (None: the gradients themselves) <- grads
+    times min(1, max_norm / (norm + eps)).  See include/ra.h."""
+    if not len(grads):
+        raise RAError(1, "grads is empty")
+    dev = _on_device(grads[0], norm, workspace)
+    _norm_tensor(norm)
+    ptrs, sizes, dtypes = _grad_arrays(grads, "grads", dev)
+    out_ptrs = out_dtypes = None
+    if outs is not None:
+        if len(outs) != len(grads):
+            raise RAError(1, f"outs must have {len(grads)} tensors (got {len(outs)})")
+        out_ptrs, out_sizes, out_dtypes = _grad_arrays(outs, "outs", dev)
+        if bytes(out_sizes) != bytes(sizes):
+            raise RAError(1, "outs must have the sizes of grads")
+    _check(_lib().ra_grad_clip(ptrs, sizes, dtypes, len(grads), max_norm, eps, out_ptrs, out_dtypes, norm.data_ptr(),
+                               workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
+
+
+def _grad_buffers(grads, stream):
+    if not len(grads):
+        raise RAError(1, "grads is empty")
+    return _allocate(stream, _on_device(grads[0]), ((), torch.float32),
+                     ((ra_grad_workspace_bytes(len(grads)),), torch.uint8))
+
+
+def grad_norm(grads, stream=None):
+    """Convenience wrapper: allocates the norm (returned, fp32 []) and the workspace."""
+    norm, ws = _grad_buffers(grads, stream)
+    ra_grad_norm(grads, norm, ws, stream)
+    return norm
+
+
+def grad_clip(grads, max_norm, outs=None, eps=1e-6, stream=None):
+    """Convenience wrapper: allocates the norm (returned, fp32 []) and the workspace; the
+    gradients are clipped in place, or into `outs`."""
+    norm, ws = _grad_buffers(grads, stream)
+    ra_grad_clip(grads, max_norm, norm, ws, outs, eps, stream)
+    return norm
 
 
 def ra_ring_bwd_workspace_bytes(dtype, grad_dtype, shape, P):

@@ -7,6 +7,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 #include <string>
@@ -1917,6 +1918,364 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
   TimedLaunch tl(RA_KERNEL_PAIR_TC, static_cast<cudaStream_t>(stream));
   e = launch_ns(a, pairs, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "Newton-Schulz launch");
+}
+
+#pragma GCC visibility pop
+}  // extern "C"
+
+// ------------------------------------------------ rotary positions, norms of heads
+namespace ra {
+namespace {
+
+// One tensor group's layout, rows on 16-byte boundaries.
+int rot_layout(const char* name, const ra_shape& sh, int dtype, Shape* out) {
+  int rc;
+  if ((rc = check_shape(sh, out))) return rc;
+  if (sh.d % 8 || sh.d > kRotMaxHead)
+    return fail(RA_ERR_UNSUPPORTED, "d must be a multiple of 8 up to %d (got %d)", kRotMaxHead, sh.d);
+  const long long unit = 16 / (long long)dtype_size(dtype);
+  for (const Lay* L : {&out->ql, &out->kvl})
+    if ((L->bs % unit) || (L->rs % unit) || (L->hs % unit))
+      return fail(RA_ERR_INVALID_ARG, "%s strides must be multiples of 16 bytes (%lld elements)", name, unit);
+  return RA_OK;
+}
+int same_extents(const char* name, const ra_shape& a, const ra_shape& b) {
+  if (a.B != b.B || a.N_q != b.N_q || a.N_kv != b.N_kv || a.Hq != b.Hq || a.Hkv != b.Hkv || a.d != b.d)
+    return fail(RA_ERR_INVALID_ARG, "%s does not have the extents of the inputs", name);
+  return RA_OK;
+}
+int check_pair(const void* q, const void* k, bool with_k, const char* qn, const char* kn) {
+  int rc;
+  if ((rc = check_ptr(q, qn))) return rc;
+  if (with_k) return check_ptr(k, kn);
+  if (k) return fail(RA_ERR_INVALID_ARG, "%s is given but k is NULL", kn);
+  return RA_OK;
+}
+
+// Everything but the tensors.
+int rot_common(const ra_shape& sh, const Shape& s, const ra_rotary& r, int flags, bool with_k, RotaryArgs* a) {
+  if (flags & ~(RA_INTERLEAVED | RA_STRIPED)) return fail(RA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
+  if (sh.N_q != sh.N_kv)
+    return fail(RA_ERR_INVALID_ARG, "queries and keys have the same rows (N_q=%d N_kv=%d)", sh.N_q, sh.N_kv);
+  if (r.rot < 0 || r.rot % 2 || r.rot > s.d)
+    return fail(RA_ERR_INVALID_ARG, "rot must be even and in [0, d=%d] (got %d)", s.d, r.rot);
+  if (!isfinite(r.amplitude)) return fail(RA_ERR_INVALID_ARG, "amplitude must be finite");
+  memset(a, 0, sizeof *a);
+  if (r.rot) {
+    if (!r.freq || (reinterpret_cast<uintptr_t>(r.freq) & 7u))
+      return fail(RA_ERR_INVALID_ARG, "freq must be a non-NULL, 8-byte aligned device array of doubles");
+    if (reinterpret_cast<uintptr_t>(r.positions) & 7u)
+      return fail(RA_ERR_INVALID_ARG, "positions must be 8-byte aligned");
+    if (r.positions && (flags & RA_STRIPED))
+      return fail(RA_ERR_INVALID_ARG, "RA_STRIPED does not combine with given positions");
+    if (r.positions && r.pos_bstride != 0 && (r.pos_bstride < s.Nq || r.pos_bstride > (1ll << 50)))
+      return fail(RA_ERR_INVALID_ARG, "pos_bstride must be 0 or at least N=%d (got %lld)", s.Nq, r.pos_bstride);
+    if ((flags & RA_STRIPED) && (r.P < 1 || s.Nq % r.P))
+      return fail(RA_ERR_INVALID_ARG, "P=%d must divide N=%d", r.P, s.Nq);
+    a->freq = r.freq;
+    a->positions = r.positions;
+    a->pos_bstride = r.pos_bstride;
+    a->pos_off = r.pos_off;
+    a->striped = (flags & RA_STRIPED) != 0;
+    a->P = a->striped ? r.P : 1;
+    a->S = s.Nq / a->P;
+  }
+  a->tokens = (long long)s.B * s.Nq;
+  a->N = s.Nq;
+  a->d = s.d;
+  a->rot = r.rot;
+  a->amplitude = r.amplitude;
+  a->side[0].H = s.Hq;
+  a->side[1].H = with_k ? s.Hkv : 0;
+  return RA_OK;
+}
+
+int check_norm(const void* qw, const void* kw, int w_dtype, float eps) {
+  if ((qw || kw) && !valid_dtype(w_dtype)) return fail(RA_ERR_INVALID_ARG, "bad weight dtype %d", w_dtype);
+  const uintptr_t mask = w_dtype == RA_F32 ? 3u : 1u;
+  if ((reinterpret_cast<uintptr_t>(qw) | reinterpret_cast<uintptr_t>(kw)) & mask)
+    return fail(RA_ERR_INVALID_ARG, "weights must be aligned to their elements");
+  if (!(eps >= 0.f) || !isfinite(eps)) return fail(RA_ERR_INVALID_ARG, "eps must be finite and >= 0 (got %g)", (double)eps);
+  return RA_OK;
+}
+
+int rotary_call(const void* q, const void* k, int dtype, const ra_shape& shape, const ra_rotary& rotary, int flags,
+                void* q_out, void* k_out, int out_dtype, const ra_shape& out_shape, bool norm, const void* qw,
+                const void* kw, int w_dtype, float eps, bool grad, void* stream) {
+  Shape s, o;
+  RotaryArgs a;
+  int rc;
+  if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return fail(RA_ERR_INVALID_ARG, "bad dtype");
+  if (out_dtype != dtype && dtype != RA_F32)
+    return fail(RA_ERR_UNSUPPORTED, "16-bit gradients are returned in their own type");
+  if ((rc = rot_layout("input", shape, dtype, &s)) || (rc = same_extents("out_shape", shape, out_shape)) ||
+      (rc = rot_layout("output", out_shape, out_dtype, &o)) || (rc = rot_common(shape, s, rotary, flags, k, &a)) ||
+      (rc = check_pair(q, k, k, "q", "k")) || (rc = check_pair(q_out, k_out, k, "the result of q", "the result of k")))
+    return rc;
+  if (norm && (rc = check_norm(qw, kw, w_dtype, eps))) return rc;
+  int* st;
+  if ((rc = status_ptr(&st))) return rc;
+  a.side[0].x = q; a.side[0].y = q_out; a.side[0].w = qw; a.side[0].xl = s.ql; a.side[0].yl = o.ql;
+  a.side[1].x = k; a.side[1].y = k_out; a.side[1].w = kw; a.side[1].xl = s.kvl; a.side[1].yl = o.kvl;
+  a.w_dtype = w_dtype;
+  a.eps = eps;
+  const cudaError_t e = launch_rotary(a, flags & RA_INTERLEAVED, dtype, out_dtype, norm, grad, device_sms(),
+                                      static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "rotary launch");
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+int ra_rotary_frequencies(int rot, double base, double scale, int method, double trained, double fast, double slow,
+                          double* freq) {
+  if (rot < 2 || rot % 2 || rot > kRotMaxHead)
+    return fail(RA_ERR_INVALID_ARG, "rot must be even and in [2, %d] (got %d)", kRotMaxHead, rot);
+  if (!(base > 1.) || !isfinite(base) || !(scale >= 1.) || !isfinite(scale))
+    return fail(RA_ERR_INVALID_ARG, "base must be above 1 and scale at least 1 (got %g, %g)", base, scale);
+  if (!freq) return fail(RA_ERR_INVALID_ARG, "freq is NULL");
+  if (method != RA_ROTARY_LINEAR && method != RA_ROTARY_BASE && method != RA_ROTARY_PARTS)
+    return fail(RA_ERR_INVALID_ARG, "unknown method %d", method);
+  if (method == RA_ROTARY_BASE && rot < 4) return fail(RA_ERR_INVALID_ARG, "a scaled base needs rot > 2");
+  if (method == RA_ROTARY_PARTS && (!(trained > 0.) || !isfinite(trained) || !(slow >= 0.) || !(fast > slow) || !isfinite(fast)))
+    return fail(RA_ERR_INVALID_ARG, "needs trained > 0 and fast > slow >= 0 (got %g, %g, %g)", trained, fast, slow);
+  if (method == RA_ROTARY_BASE) base *= pow(scale, (double)rot / (rot - 2));
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = pow(base, -2. * i / rot);
+    if (method == RA_ROTARY_LINEAR) {
+      freq[i] = f / scale;
+    } else if (method == RA_ROTARY_BASE) {
+      freq[i] = f;
+    } else {
+      const double t = (trained * f / 6.283185307179586 - slow) / (fast - slow);
+      const double slowed = f / scale;
+      freq[i] = t >= 1. ? f : t <= 0. ? slowed : slowed + t * (f - slowed);
+    }
+  }
+  return RA_OK;
+}
+
+int ra_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape, ra_rotary rotary, int flags, void* q_out,
+                  void* k_out, ra_shape out_shape, void* stream) {
+  return rotary_call(q, k, dtype, shape, rotary, flags, q_out, k_out, dtype, out_shape, false, nullptr, nullptr, RA_F32,
+                     0.f, false, stream);
+}
+
+int ra_rotary_bwd(const void* dq_out, const void* dk_out, ra_dtype dtype, ra_shape shape, ra_rotary rotary, int flags,
+                  void* dq, void* dk, ra_dtype grad_dtype, ra_shape grad_shape, void* stream) {
+  return rotary_call(dq_out, dk_out, dtype, shape, rotary, flags, dq, dk, grad_dtype, grad_shape, false, nullptr, nullptr,
+                     RA_F32, 0.f, true, stream);
+}
+
+int ra_norm_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape, const void* q_weight,
+                       const void* k_weight, ra_dtype w_dtype, float eps, ra_rotary rotary, int flags, void* q_out,
+                       void* k_out, ra_shape out_shape, void* stream) {
+  return rotary_call(q, k, dtype, shape, rotary, flags, q_out, k_out, dtype, out_shape, true, q_weight, k_weight, w_dtype,
+                     eps, false, stream);
+}
+
+size_t ra_norm_rotary_bwd_workspace_bytes(int d) {
+  if (d < 1 || d > kRotMaxHead) return 0;
+  return align256((size_t)kRotParts * 2 * d * 4);
+}
+
+int ra_norm_rotary_bwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape, const void* dq_out,
+                       const void* dk_out, ra_dtype dout_dtype, ra_shape dout_shape, const void* q_weight,
+                       const void* k_weight, ra_dtype w_dtype, float eps, ra_rotary rotary, int flags, void* dq, void* dk,
+                       ra_dtype grad_dtype, ra_shape grad_shape, float* dq_weight, float* dk_weight, void* workspace,
+                       size_t ws_bytes, void* stream) {
+  Shape s, g, o;
+  RotaryArgs a;
+  int rc;
+  if (!valid_dtype(dtype) || !valid_dtype(dout_dtype) || !valid_dtype(grad_dtype))
+    return fail(RA_ERR_INVALID_ARG, "bad dtype");
+  if ((dout_dtype != dtype && dout_dtype != RA_F32) || (grad_dtype != dtype && grad_dtype != RA_F32))
+    return fail(RA_ERR_UNSUPPORTED, "gradients are of the inputs' type or fp32");
+  if ((rc = rot_layout("input", shape, dtype, &s)) || (rc = same_extents("dout_shape", shape, dout_shape)) ||
+      (rc = rot_layout("gradient", dout_shape, dout_dtype, &g)) || (rc = same_extents("grad_shape", shape, grad_shape)) ||
+      (rc = rot_layout("output", grad_shape, grad_dtype, &o)) || (rc = rot_common(shape, s, rotary, flags, k, &a)) ||
+      (rc = check_pair(q, k, k, "q", "k")) || (rc = check_pair(dq_out, dk_out, k, "dq_out", "dk_out")) ||
+      (rc = check_pair(dq, dk, k, "dq", "dk")) || (rc = check_norm(q_weight, k_weight, w_dtype, eps)) ||
+      (dq_weight && (rc = check_floats(dq_weight, "dq_weight"))) || (dk_weight && (rc = check_floats(dk_weight, "dk_weight"))) ||
+      (rc = check_workspace(workspace, ws_bytes, ra_norm_rotary_bwd_workspace_bytes(s.d))))
+    return rc;
+  if (dk_weight && !k) return fail(RA_ERR_INVALID_ARG, "dk_weight is given but k is NULL");
+  int* st;
+  if ((rc = status_ptr(&st))) return rc;
+  a.side[0].x = q; a.side[0].dy = dq_out; a.side[0].y = dq; a.side[0].w = q_weight;
+  a.side[0].xl = s.ql; a.side[0].dyl = g.ql; a.side[0].yl = o.ql;
+  a.side[1].x = k; a.side[1].dy = dk_out; a.side[1].y = dk; a.side[1].w = k_weight;
+  a.side[1].xl = s.kvl; a.side[1].dyl = g.kvl; a.side[1].yl = o.kvl;
+  a.w_dtype = w_dtype;
+  a.eps = eps;
+  a.dw_parts = static_cast<float*>(workspace);
+  const cudaError_t e = launch_norm_rotary_bwd(a, flags & RA_INTERLEAVED, dtype, dout_dtype, grad_dtype, dq_weight,
+                                               dk_weight, device_sms(), static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "norm and rotary backward launch");
+}
+
+#pragma GCC visibility pop
+}  // extern "C"
+
+// ------------------------------------------------ norm and clipping of many tensors
+namespace ra {
+namespace {
+
+int grad_check(const void* const* grads, const long long* sizes, const int* dtypes, int count, const float* norm,
+               const void* workspace, size_t ws_bytes, long long* total) {
+  if (count < 1 || count > (1 << 20)) return fail(RA_ERR_INVALID_ARG, "count must be in [1, 2^20] (got %d)", count);
+  if (!grads || !sizes || !dtypes) return fail(RA_ERR_INVALID_ARG, "grads, sizes or dtypes is NULL");
+  *total = 0;
+  for (int i = 0; i < count; ++i) {
+    if (!valid_dtype(dtypes[i])) return fail(RA_ERR_INVALID_ARG, "bad dtype %d of gradient %d", dtypes[i], i);
+    if (sizes[i] < 0 || sizes[i] > (1ll << 40))
+      return fail(RA_ERR_INVALID_ARG, "gradient %d has %lld elements", i, sizes[i]);
+    if (sizes[i] && (!grads[i] || (reinterpret_cast<uintptr_t>(grads[i]) % dtype_size(dtypes[i]))))
+      return fail(RA_ERR_INVALID_ARG, "gradient %d is NULL or not aligned to its elements", i);
+    *total += sizes[i];
+    if (*total > (1ll << 40)) return fail(RA_ERR_INVALID_ARG, "more than 2^40 elements");
+  }
+  int rc;
+  if ((rc = check_floats(norm, "norm"))) return rc;
+  return check_workspace(workspace, ws_bytes, ra_grad_workspace_bytes(count));
+}
+
+// No output may overlap another tensor: neither another output nor an input other than the
+// one it is made of, and that one only from the same address on in the same type.
+int grad_overlap(const void* const* grads, const long long* sizes, const int* dtypes, int count, void* const* outs,
+                 const int* out_dtypes) {
+  struct Range {
+    uintptr_t lo, hi;
+    int i;
+  };
+  std::vector<Range> o;
+  o.reserve(count);
+  for (int i = 0; i < count; ++i) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(outs[i]);
+    if (sizes[i]) o.push_back({p, p + sizes[i] * dtype_size(out_dtypes[i]), i});
+  }
+  std::sort(o.begin(), o.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+  for (size_t j = 1; j < o.size(); ++j)
+    if (o[j].lo < o[j - 1].hi)
+      return fail(RA_ERR_INVALID_ARG, "the outputs of gradients %d and %d overlap", o[j - 1].i, o[j].i);
+  for (int i = 0; i < count; ++i) {
+    if (!sizes[i]) continue;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(grads[i]), hi = lo + sizes[i] * dtype_size(dtypes[i]);
+    auto j = std::upper_bound(o.begin(), o.end(), lo, [](uintptr_t v, const Range& r) { return v < r.hi; });
+    for (; j != o.end() && j->lo < hi; ++j)
+      if (j->i != i || j->lo != lo || dtypes[i] != out_dtypes[i])
+        return fail(RA_ERR_INVALID_ARG, "the output of gradient %d overlaps gradient %d", j->i, i);
+  }
+  return RA_OK;
+}
+
+// Runs `launch(list)` for each group of up to MAX tensors.
+template <int MAX, typename Launch>
+int grad_lists(const void* const* grads, const long long* sizes, const int* dtypes, int count, void* const* outs,
+               const int* out_dtypes, int chunk, Launch launch) {
+  GradList<MAX> a;
+  int i = 0, rc;
+  do {
+    a.count = 0;
+    a.chunk = chunk;
+    a.first[0] = 0;
+    for (; i < count && a.count < MAX; ++i) {
+      if (!sizes[i]) continue;
+      const int k = a.count++;
+      a.in[k] = grads[i];
+      a.out[k] = outs ? outs[i] : const_cast<void*>(grads[i]);
+      a.n[k] = sizes[i];
+      a.types[k] = (unsigned char)(dtypes[i] + 16 * (out_dtypes ? out_dtypes[i] : dtypes[i]));
+      a.first[k + 1] = a.first[k] + (int)((sizes[i] + chunk - 1) / chunk);
+    }
+    if (a.count && (rc = launch(a))) return rc;
+  } while (i < count);
+  return RA_OK;
+}
+
+// Elements of a chunk: enough chunks for every block, each long enough that a block's
+// start does not show.
+int grad_chunk(long long total, int sms) {
+  long long c = 2048;
+  while (c < 65536 && total / (2 * c) >= 8ll * sms) c *= 2;
+  return (int)c;
+}
+
+template <int MAX>
+int grad_call(const void* const* grads, const long long* sizes, const int* dtypes, int count, long long total, bool clip,
+              float max_norm, float eps, void* const* outs, const int* out_dtypes, float* norm, double* parts,
+              cudaStream_t st) {
+  const int sms = device_sms(), chunk = grad_chunk(total, sms);
+  int used = 0, rc;
+  rc = grad_lists<MAX>(grads, sizes, dtypes, count, outs, out_dtypes, chunk, [&](const GradList<MAX>& a) {
+    int n = 0;
+    const cudaError_t e = launch_grad_squares(a, parts + used, &n, sms, st);
+    used += n;
+    return e == cudaSuccess ? (int)RA_OK : cuda_fail(e, "gradient norm launch");
+  });
+  if (rc) return rc;
+  if (!clip || !used) {
+    const cudaError_t e = launch_grad_norm(parts, used, norm, st);
+    return e == cudaSuccess ? RA_OK : cuda_fail(e, "gradient norm launch");
+  }
+  return grad_lists<MAX>(grads, sizes, dtypes, count, outs, out_dtypes, chunk, [&](const GradList<MAX>& a) {
+    const cudaError_t e = launch_grad_scale(a, parts, used, max_norm, eps, norm, sms, st);
+    norm = nullptr;  // the first launch writes it
+    return e == cudaSuccess ? (int)RA_OK : cuda_fail(e, "gradient clipping launch");
+  });
+}
+
+int grad_any(const void* const* grads, const long long* sizes, const int* dtypes, int count, bool clip, float max_norm,
+             float eps, void* const* outs, const int* out_dtypes, float* norm, void* workspace, size_t ws_bytes,
+             void* stream) {
+  long long total;
+  int rc, *status;
+  if ((rc = grad_check(grads, sizes, dtypes, count, norm, workspace, ws_bytes, &total))) return rc;
+  if (clip) {
+    if (!(max_norm >= 0.f) || !isfinite(max_norm) || !(eps >= 0.f) || !isfinite(eps))
+      return fail(RA_ERR_INVALID_ARG, "max_norm and eps must be finite and >= 0 (got %g, %g)", (double)max_norm, (double)eps);
+    if (!outs != !out_dtypes) return fail(RA_ERR_INVALID_ARG, "outs and out_dtypes go together");
+    for (int i = 0; outs && i < count; ++i)
+      if (!valid_dtype(out_dtypes[i]) ||
+          (sizes[i] && (!outs[i] || (reinterpret_cast<uintptr_t>(outs[i]) % dtype_size(out_dtypes[i])))))
+        return fail(RA_ERR_INVALID_ARG, "output %d is NULL, not aligned to its elements or of a bad dtype", i);
+    try {
+      if ((rc = grad_overlap(grads, sizes, dtypes, count, outs ? outs : const_cast<void* const*>(grads),
+                             outs ? out_dtypes : dtypes)))
+        return rc;
+    } catch (...) {
+      return fail(RA_ERR_INVALID_ARG, "no host memory for %d tensors", count);
+    }
+  }
+  if ((rc = status_ptr(&status))) return rc;
+  double* parts = static_cast<double*>(workspace);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return count <= kClipFew ? grad_call<kClipFew>(grads, sizes, dtypes, count, total, clip, max_norm, eps, outs, out_dtypes, norm, parts, st)
+                           : grad_call<kClipMany>(grads, sizes, dtypes, count, total, clip, max_norm, eps, outs, out_dtypes, norm, parts, st);
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+size_t ra_grad_workspace_bytes(int count) {
+  if (count < 1 || count > (1 << 20)) return 0;
+  return align256(((size_t)count + kClipMany - 1) / kClipMany * kClipParts * sizeof(double));
+}
+
+int ra_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int count, float* norm,
+                 void* workspace, size_t ws_bytes, void* stream) {
+  return grad_any(grads, sizes, dtypes, count, false, 0.f, 0.f, nullptr, nullptr, norm, workspace, ws_bytes, stream);
+}
+
+int ra_grad_clip(const void* const* grads, const long long* sizes, const int* dtypes, int count, float max_norm, float eps,
+                 void* const* outs, const int* out_dtypes, float* norm, void* workspace, size_t ws_bytes, void* stream) {
+  return grad_any(grads, sizes, dtypes, count, true, max_norm, eps, outs, out_dtypes, norm, workspace, ws_bytes, stream);
 }
 
 #pragma GCC visibility pop

@@ -305,6 +305,58 @@ cudaError_t launch_xent_scale(const float* grad, const long long* targets, long 
 // out (dtype) <- the sum of `planes` fp32 planes of n elements each (n a multiple of 8)
 cudaError_t launch_sum_planes(const float* planes, int count, long long n, void* out, int dtype, cudaStream_t st);
 
+// -------------------------------------------- rotary positions, norms of heads
+struct RotarySide {  // queries, or keys
+  const void* x;
+  const void* dy;    // backward
+  void* y;           // result, or gradient of x
+  const void* w;     // weights of the norm [d], or NULL: ones
+  Lay xl, dyl, yl;
+  int H;             // 0: there are none
+};
+struct RotaryArgs {
+  RotarySide side[2];
+  long long tokens;  // B N
+  int N, d, rot;
+  const double* freq;          // [rot / 2], radians per position
+  const long long* positions;  // [B or 1, N], or NULL: pos_off + row
+  long long pos_bstride, pos_off;
+  int striped, P, S;           // row i S + l holds position l P + i
+  float amplitude, eps;
+  int w_dtype;
+  float* dw_parts;             // [2][blocks][d], backward
+  // set by the launch
+  int G, parts;
+  long long units;
+};
+constexpr int kRotMaxHead = 256;
+constexpr int kRotParts = 608;  // blocks of the backward kernel
+cudaError_t launch_rotary(RotaryArgs& a, int interleaved, int dtype, int out_dtype, int norm, int grad, int sms,
+                          cudaStream_t st);
+cudaError_t launch_norm_rotary_bwd(RotaryArgs& a, int interleaved, int dtype, int g_dtype, int grad_dtype, float* dwq,
+                                   float* dwk, int sms, cudaStream_t st);
+int rot_exchange(int rot, int interleaved);
+void rot_units(RotaryArgs& a, int sms);
+
+// -------------------------------------------- norm and clipping of many tensors
+constexpr int kClipFew = 48, kClipMany = 1024;  // tensors a launch takes
+constexpr int kClipParts = 608;                 // blocks of a launch
+template <int MAX>
+struct GradList {
+  int count, chunk;        // tensors; elements of a chunk, a multiple of 8
+  const void* in[MAX];
+  void* out[MAX];
+  long long n[MAX];        // at least 1
+  int first[MAX + 1];      // a tensor's first chunk
+  unsigned char types[MAX];  // dtype of in + 16 times that of out
+};
+template <int MAX>
+cudaError_t launch_grad_squares(const GradList<MAX>& a, double* parts, int* used, int sms, cudaStream_t st);
+template <int MAX>
+cudaError_t launch_grad_scale(const GradList<MAX>& a, const double* parts, int count, float max_norm, float eps,
+                              float* norm, int sms, cudaStream_t st);
+cudaError_t launch_grad_norm(const double* parts, int count, float* norm, cudaStream_t st);
+
 // -------------------------------------------- Newton-Schulz
 struct NsInput {
   const void* g;

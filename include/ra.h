@@ -93,8 +93,10 @@ typedef enum { RA_F32 = 0, RA_BF16 = 1, RA_F16 = 2 } ra_dtype;
  *             backward pass a key tile's gradients go round the ring once per
  *             local query tile they meet (each lap in ring order), which keeps
  *             the query tiles that concurrent work units read in cache; only
- *             rounding depends on that order.  Ignored without RA_CAUSAL. */
-enum { RA_CAUSAL = 1, RA_PRECISE = 2, RA_STRIPED = 4 };
+ *             rounding depends on that order.  Ignored without RA_CAUSAL.
+ *             Also taken by the rotary entry points, for rows in that order.
+ * RA_INTERLEAVED  rotary entry points: pairs are columns (2i, 2i + 1). */
+enum { RA_CAUSAL = 1, RA_PRECISE = 2, RA_STRIPED = 4, RA_INTERLEAVED = 8 };
 
 typedef enum {
   RA_OK = 0,
@@ -426,6 +428,114 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
                      long long g_bstride, long long g_rstride, const float* coeffs, int steps,
                      float eps, void* out, ra_dtype out_dtype, long long out_bstride,
                      long long out_rstride, void* workspace, size_t ws_bytes, void* stream);
+
+/* Rotary positions.  Row (b, n, h) of q and of k at position p has its first `rot` columns
+ * turned in pairs, pair i by the angle p freq[i]:
+ *     (x, y) -> amplitude (x cos - y sin, x sin + y cos),
+ * pair i being columns (i, i + rot / 2), or (2i, 2i + 1) with RA_INTERLEAVED; columns from
+ * rot on are copied.  q and k of one call go through one launch, between the projections
+ * and ra_ring_fwd (backward: between ra_ring_bwd and the projections' gradients).
+ *   freq       device array of rot / 2 doubles, radians per position (ra_rotary_frequencies
+ *              makes some); angles keep an error of at most 2^-31 + |p| 2^-56 turns.
+ *   positions  device array of 64-bit integers, element (b, n) at b * pos_bstride + n (0:
+ *              every batch has the same N), any values; or NULL: row n is at pos_off + n,
+ *              or with RA_STRIPED, where row i S + l (S = N / P) is the l-th of virtual host
+ *              i, at pos_off + l P + i.  (Per-host lengths: pass positions.)
+ *   P          with RA_STRIPED the number of hosts, which divides N; ignored otherwise. */
+typedef struct {
+  int rot;                    /* even, 0 (no rotation) to d */
+  const double* freq;
+  const long long* positions; /* 8-byte aligned, or NULL */
+  long long pos_bstride;
+  long long pos_off;
+  int P;
+  float amplitude;            /* 1, or what a scaling method multiplies cos and sin by */
+} ra_rotary;
+
+/* How ra_rotary_frequencies stretches frequencies to `scale` times the trained length.
+ * With f = base^(-2i / rot):
+ * RA_ROTARY_LINEAR  f / scale (positions interpolated).
+ * RA_ROTARY_BASE    the same with base scale^(rot / (rot - 2)) base: the fastest pair keeps its
+ *                   frequency, the slowest is divided by scale.  rot > 2.
+ * RA_ROTARY_PARTS   by the turns t = trained f / 2 pi that a pair makes in the trained length:
+ *                   f from `fast` turns on, f / scale up to `slow` turns, in between the mean
+ *                   of both with weights that go linearly with t ("YaRN: Efficient Context
+ *                   Window Extension of Large Language Models", Peng et al. 2023, section 3.2,
+ *                   which also multiplies cos and sin by 1 + 0.1 ln scale: `amplitude`). */
+enum { RA_ROTARY_LINEAR = 0, RA_ROTARY_BASE = 1, RA_ROTARY_PARTS = 2 };
+
+/* freq[0 .. rot / 2) (host memory) of a method.  base > 1, scale >= 1; trained > 0 and
+ * fast > slow >= 0 for RA_ROTARY_PARTS (ignored otherwise). */
+int ra_rotary_frequencies(int rot, double base, double scale, int method, double trained,
+                          double fast, double slow, double* freq);
+
+/* q [B, N, Hq, d], k [B, N, Hkv, d] (shape.N_q = shape.N_kv = N) -> q_out, k_out, same type,
+ * at the strides of out_shape (whose extents are those of shape).  k and k_out may both be
+ * NULL: q alone.  q_out may be q itself (and k_out k) where the strides agree; otherwise
+ * outputs overlap no input.  flags: RA_INTERLEAVED, RA_STRIPED.
+ *   Sizes: d a multiple of 8 up to 256; rows start on 16-byte boundaries.  Any dtype; sums
+ *   and products fp32, rounded once.  Columns from rot on are copied bit for bit. */
+int ra_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape, ra_rotary rotary,
+                  int flags, void* q_out, void* k_out, ra_shape out_shape, void* stream);
+
+/* Gradients of ra_rotary_fwd: dq, dk from the gradients dq_out, dk_out of its results (in
+ * dtype, at the strides of shape), written in grad_dtype (dtype, or any type where dtype is
+ * RA_F32) at the strides of grad_shape.  In place as above. */
+int ra_rotary_bwd(const void* dq_out, const void* dk_out, ra_dtype dtype, ra_shape shape,
+                  ra_rotary rotary, int flags, void* dq, void* dk, ra_dtype grad_dtype,
+                  ra_shape grad_shape, void* stream);
+
+/* Norm of each head and rotary positions in one pass over q and k:
+ *     r = (mean_c x_c^2 + eps)^-1/2,   y = rotate(x r w)
+ * for each row (b, n, h), the mean over all d columns, w q_weight or k_weight [d] in
+ * w_dtype (NULL: ones).  rotary.rot = 0 norms without a rotation (for queries and keys of
+ * cross attention, say).  eps >= 0; rows whose squares leave fp32's range are scaled first.
+ * Other arguments as for ra_rotary_fwd. */
+int ra_norm_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape,
+                       const void* q_weight, const void* k_weight, ra_dtype w_dtype, float eps,
+                       ra_rotary rotary, int flags, void* q_out, void* k_out, ra_shape out_shape,
+                       void* stream);
+
+/* Gradients of ra_norm_rotary_fwd, with g = rotate^T(dy) and n = x r:
+ *     dx = r (g w - n mean_c(g_c w_c n_c)),   dw_c = sum over rows of g_c n_c.
+ *   q, k the inputs of the forward pass (dtype, shape); dq_out, dk_out the gradients of its
+ *   results in dout_dtype (dtype or RA_F32) at the strides of dout_shape; dq, dk in
+ *   grad_dtype (dtype or RA_F32) at the strides of grad_shape, which may be dq_out, dk_out
+ *   (or q, k) themselves where type and strides agree; dq_weight, dk_weight [d] fp32,
+ *   overwritten, NULL where not wanted.  Results do not vary from run to run.
+ *   workspace: device memory, 256-byte aligned, ra_norm_rotary_bwd_workspace_bytes(d)
+ *   bytes.  It must not be in use by work that overlaps the call on the GPU. */
+size_t ra_norm_rotary_bwd_workspace_bytes(int d);
+int ra_norm_rotary_bwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape,
+                       const void* dq_out, const void* dk_out, ra_dtype dout_dtype,
+                       ra_shape dout_shape, const void* q_weight, const void* k_weight,
+                       ra_dtype w_dtype, float eps, ra_rotary rotary, int flags, void* dq, void* dk,
+                       ra_dtype grad_dtype, ra_shape grad_shape, float* dq_weight,
+                       float* dk_weight, void* workspace, size_t ws_bytes, void* stream);
+
+/* The norm of the gradients of many tensors taken together, n = (sum g^2)^1/2 over all
+ * elements of all of them, and their clipping by it ("Ring Attention: Train 1M Tokens on 8GB
+ * GPUs in 2026", section "Gotchas and Failure Modes", clips gradients through the ring):
+ *     c = min(1, max_norm / (n + eps)),   out = c g.
+ *   grads, sizes, dtypes, outs, out_dtypes  host arrays of `count` entries, read during the
+ *   call: device addresses (aligned to an element), numbers of elements (0 allowed), types;
+ *   a tensor's elements are contiguous.  outs NULL: in place (where c = 1 nothing is
+ *   written); an entry of outs may be that of grads where the types agree; otherwise no
+ *   output overlaps another tensor.  A tensor that is listed twice counts twice, and cannot
+ *   be written twice.
+ *   norm [1] fp32 on the device.  Sums are fp64 (fp32 over up to 64 elements): gradients of
+ *   any size, from fp32's smallest to its largest, have their norm.  An infinite n gives
+ *   c = 0 and NaN gives NaN, as the formula says: read norm to skip such a step.  The
+ *   results do not vary from run to run.
+ *   max_norm >= 0, eps >= 0 (with both 0 and n = 0, c is NaN).
+ *   workspace: device memory, 256-byte aligned, ra_grad_workspace_bytes(count) bytes.  It
+ *   must not be in use by work that overlaps the call on the GPU. */
+size_t ra_grad_workspace_bytes(int count);
+int ra_grad_norm(const void* const* grads, const long long* sizes, const int* dtypes, int count,
+                 float* norm, void* workspace, size_t ws_bytes, void* stream);
+int ra_grad_clip(const void* const* grads, const long long* sizes, const int* dtypes, int count,
+                 float max_norm, float eps, void* const* outs, const int* out_dtypes, float* norm,
+                 void* workspace, size_t ws_bytes, void* stream);
 
 /* Synchronise `stream`, then return and clear the device status word
  * (RA_OK, RA_ERR_RANGE, RA_ERR_TIMEOUT, or RA_ERR_INVALID_ARG for a target outside

@@ -1,6 +1,6 @@
 """fp64 CPU oracle for blockwise exact attention, the blockwise feed-forward
-layer, the vocabulary cross entropy and the Newton-Schulz update (test
-infrastructure only).
+layer, the vocabulary cross entropy, the Newton-Schulz update, rotary positions,
+norms of heads, cross attention and gradient clipping (test infrastructure only).
 
 Only the test suite, ``__graft_entry__.smoke()`` and the CPU-baseline leg of
 ``bench.py`` may import this package.  The CUDA product path never imports,
@@ -35,4 +35,13 @@ from .train import (  # noqa: F401
     xent_bwd,
     newton_schulz,
     singular_map,
+)
+from .layer import (  # noqa: F401
+    rotary,
+    rows_to_positions,
+    head_norm,
+    head_norm_bwd,
+    cross_attention,
+    global_norm,
+    clip_factor,
 )
