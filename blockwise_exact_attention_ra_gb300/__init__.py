@@ -14,7 +14,8 @@ Functions with the C names (``ra_block_fwd``, ``ra_merge``, ``ra_ring_fwd``,
 additionally allocate outputs and workspace with torch; so do ``ffn_fwd`` /
 ``ffn_bwd`` (a feed-forward layer), ``xent_fwd`` / ``xent_bwd`` (the cross
 entropy of its output against a vocabulary), ``newton_schulz`` (the orthogonalised
-update of a weight's gradient), ``rotary_fwd`` / ``rotary_bwd`` and
+update of a weight's gradient), ``cross_attention_fwd`` / ``cross_attention_bwd``
+(attention to keys of another length), ``rotary_fwd`` / ``rotary_bwd`` and
 ``norm_rotary_fwd`` / ``norm_rotary_bwd`` (rotary positions of queries and keys, with
 the norms of their heads in the same pass) and ``grad_norm`` / ``grad_clip`` (the norm
 of the gradients of many tensors, and their clipping by it).  What they allocate
@@ -37,7 +38,8 @@ __all__ = [
     "newton_schulz", "RaRotary", "ra_rotary_frequencies", "ra_rotary_fwd", "ra_rotary_bwd", "ra_norm_rotary_fwd",
     "ra_norm_rotary_bwd_workspace_bytes", "ra_norm_rotary_bwd", "rotary_frequencies", "rotary_fwd", "rotary_bwd",
     "norm_rotary_fwd", "norm_rotary_bwd", "ra_grad_workspace_bytes", "ra_grad_norm", "ra_grad_clip", "grad_norm",
-    "grad_clip",
+    "grad_clip", "ra_cross_fwd_workspace_bytes", "ra_cross_fwd", "ra_cross_bwd_workspace_bytes", "ra_cross_bwd",
+    "cross_attention_fwd", "cross_attention_bwd",
     "ra_sync_status", "ra_last_error", "ra_launch_count", "ra_selftest_timeout", "ra_debug_visit_log",
     "ra_kernel_timing", "ra_kernel_timing_read",
     "ring_attention_fwd", "ring_attention_bwd", "RA_F32", "RA_BF16", "RA_F16",
@@ -109,6 +111,10 @@ def _load():
         "ra_ring_bwd_varlen": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, vp, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, i, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_ring_bwd_workspace_bytes": (sz, [i, i, sh, i]),
+        "ra_cross_fwd_workspace_bytes": (sz, [i, sh, i]),
+        "ra_cross_fwd": (i, [vp, vp, vp, i, sh, vp, i, f, vp, i, vp, vp, sz, vp]),
+        "ra_cross_bwd_workspace_bytes": (sz, [i, sh]),
+        "ra_cross_bwd": (i, [vp, vp, vp, vp, i, vp, vp, i, sh, vp, i, f, vp, vp, vp, i, vp, sz, vp]),
         "ra_rotary_frequencies": (i, [i, dbl, dbl, i, dbl, dbl, dbl, vp]),
         "ra_rotary_fwd": (i, [vp, vp, i, sh, rot, i, vp, vp, sh, vp]),
         "ra_rotary_bwd": (i, [vp, vp, i, sh, rot, i, vp, vp, i, sh, vp]),
@@ -648,6 +654,116 @@ def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, strea
     return out
 
 
+# ------------------------------------------------ cross attention
+def _strides_of(t, name):
+    """Batch, row and head strides of a [B, N, H, d] tensor; 0 (the library's packed default)
+    for an axis of extent 1, whose stride is arbitrary."""
+    s, n = t.stride(), t.shape
+    if len(s) != 4:
+        raise RAError(1, f"{name} must be [B, N, H, d]")
+    if s[3] != 1 and n[3] > 1:
+        raise RAError(1, f"{name} must have a contiguous last (head) dimension (strides {s})")
+    if max(n) > _INT_MAX:
+        _fits(*n)
+    out = []
+    for i in range(3):
+        if n[i] == 1:
+            out.append(0)
+        elif s[i] == 0:
+            raise RAError(1, f"{name} must not be expanded (stride 0)")
+        else:
+            out.append(s[i])
+    return out
+
+
+def _cross_shape(q, k, v, kv_len, **others):
+    """RaShape; `others` maps a name to (tensor, "q" or "k"): of that tensor's shape and strides."""
+    qs, ks = _strides_of(q, "q"), _strides_of(k, "k")
+    B, Nq, Hq, d = q.shape
+    kB, Nkv, Hkv, kd = k.shape
+    if kB != B or kd != d or k.dtype != q.dtype:
+        raise RAError(1, f"q and k must have the same batch, head dimension and dtype (got {list(q.shape)} {q.dtype}, "
+                         f"{list(k.shape)} {k.dtype})")
+    for name, (t, like) in dict(others, v=(v, "k")).items():
+        ref, strides = (q, qs) if like == "q" else (k, ks)
+        if t.shape != ref.shape or _strides_of(t, name) != strides:
+            raise RAError(1, f"{name} must have the shape and strides of {like} ({list(t.shape)} {t.stride()} vs "
+                             f"{list(ref.shape)} {ref.stride()})")
+    if v.dtype != k.dtype:
+        raise RAError(1, f"k and v must have the same dtype (got {k.dtype}, {v.dtype})")
+    if kv_len is not None:
+        _vector(kv_len, "kv_len", B, torch.int32)
+    return RaShape(B, Nq, Nkv, Hq, Hkv, d, qs[0], ks[0], qs[1], qs[2], ks[1], ks[2])
+
+
+def _row_floats(t, name, q):
+    B, Nq, Hq, _ = q.shape
+    if t.dtype != torch.float32 or t.shape != (B, Hq, Nq) or not t.is_contiguous():
+        raise RAError(1, f"{name} must be packed fp32 [{B}, {Hq}, {Nq}] (got {t.dtype} {list(t.shape)})")
+
+
+def ra_cross_fwd_workspace_bytes(dtype, shape, flags=0):
+    return int(_lib().ra_cross_fwd_workspace_bytes(dtype, shape, flags))
+
+
+def ra_cross_bwd_workspace_bytes(dtype, shape):
+    return int(_lib().ra_cross_bwd_workspace_bytes(dtype, shape))
+
+
+def ra_cross_fwd(q, k, v, scale, o, lse, workspace, kv_len=None, stream=None, precise=False):
+    """o, lse <- softmax(scale q k^T) v over the first kv_len[b] keys (int32 device tensor
+    [B], None: all).  See include/ra.h."""
+    shape = _cross_shape(q, k, v, kv_len, o=(o, "q"))
+    _row_floats(lse, "lse", q)
+    dev = _on_device(q, k, v, o, lse, workspace, *_there(kv_len))
+    _check(_lib().ra_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), shape, _data(kv_len),
+                               RA_PRECISE if precise else 0, float(scale), o.data_ptr(), _dt(o), lse.data_ptr(),
+                               workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
+
+
+def ra_cross_bwd(q, k, v, o, dO, lse, scale, dq, dk, dv, workspace, kv_len=None, stream=None, precise=False):
+    """Gradients of sum(o * dO) (overwritten).  See include/ra.h."""
+    shape = _cross_shape(q, k, v, kv_len, o=(o, "q"), dO=(dO, "q"), dq=(dq, "q"), dk=(dk, "k"), dv=(dv, "k"))
+    _row_floats(lse, "lse", q)
+    if dO.dtype != q.dtype or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
+        raise RAError(1, f"dO must have q's dtype, dk and dv dq's (got {dO.dtype}, {dk.dtype}, {dv.dtype})")
+    dev = _on_device(q, k, v, o, dO, lse, dq, dk, dv, workspace, *_there(kv_len))
+    _check(_lib().ra_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _dt(o), dO.data_ptr(),
+                               lse.data_ptr(), _dt(q), shape, _data(kv_len), RA_PRECISE if precise else 0, float(scale),
+                               dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dt(dq), workspace.data_ptr(),
+                               _nbytes(workspace), _handle(stream, dev)))
+
+
+def cross_attention_fwd(q, k, v, kv_len=None, scale=None, o_dtype=torch.float32, stream=None, precise=False):
+    """Allocate o (o_dtype, q's layout) and lse [B, Hq, Nq] fp32 and run ra_cross_fwd."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    shape = _cross_shape(q, k, v, kv_len)
+    dev = _on_device(q)
+    nbytes = ra_cross_fwd_workspace_bytes(_dt(q), shape, RA_PRECISE if precise else 0)
+    B, Nq, Hq, _ = q.shape
+    with torch.cuda.stream(stream):
+        o = empty_like_layout(q, o_dtype)
+    lse, ws = _allocate(stream, dev, ((B, Hq, Nq), torch.float32), ((nbytes,), torch.uint8))
+    ra_cross_fwd(q, k, v, scale, o, lse, ws, kv_len, stream, precise)
+    return o, lse
+
+
+def cross_attention_bwd(q, k, v, o, lse, dO, kv_len=None, scale=None, grad_dtype=torch.float32, stream=None,
+                        precise=False):
+    """Allocate dq, dk, dv (grad_dtype, the layouts of q and k) and run ra_cross_bwd."""
+    if scale is None:
+        scale = q.shape[-1] ** -0.5
+    shape = _cross_shape(q, k, v, kv_len)
+    dev = _on_device(q)
+    nbytes = ra_cross_bwd_workspace_bytes(_dt(q), shape)
+    with torch.cuda.stream(stream):
+        dq, dk, dv = empty_like_layout(q, grad_dtype), empty_like_layout(k, grad_dtype), empty_like_layout(k, grad_dtype)
+    ws, = _allocate(stream, dev, ((nbytes,), torch.uint8))
+    ra_cross_bwd(q, k, v, o, dO, lse, scale, dq, dk, dv, ws, kv_len, stream, precise)
+    return dq, dk, dv
+
+
 # ------------------------------------------------ rotary positions, norms of heads
 _ROTARY_METHODS = {"linear": 0, "base": 1, "parts": 2}
 
@@ -672,35 +788,17 @@ def rotary_frequencies(rot, base=10000.0, scale=1.0, method="linear", trained=0,
     return freq.to(device)
 
 
-def _rot_strides(t, name):
-    s = t.stride()
-    if len(s) != 4:
-        raise RAError(1, f"{name} must be [B, N, H, d]")
-    n = t.shape
-    if s[3] != 1 and n[3] > 1:
-        raise RAError(1, f"{name} must have a contiguous last (head) dimension (strides {s})")
-    out = [s[i] if n[i] > 1 else 0 for i in range(3)]
-    for i in range(3):
-        if n[i] > 1 and s[i] == 0:
-            raise RAError(1, f"{name} must not be expanded (stride 0)")
-    return out
-
-
 def _rot_shape(q, k, qn="q", kn="k"):
     """RaShape of queries and keys of the same rows; k may be None."""
-    qb, qr, qh = _rot_strides(q, qn)
+    qb, qr, qh = _strides_of(q, qn)
     B, N, Hq, d = q.shape
-    if max(B, N, Hq, d) > _INT_MAX:
-        _fits(B, N, Hq, d)
     if k is None:
         return RaShape(B, N, N, Hq, 1, d, qb, 0, qr, qh, 0, 0)
-    kb, kr, kh = _rot_strides(k, kn)
+    kb, kr, kh = _strides_of(k, kn)
     kB, kN, Hkv, kd = k.shape
     if (kB, kN, kd) != (B, N, d) or k.dtype != q.dtype:
         raise RAError(1, f"{qn} and {kn} must have the same batch, rows, head dimension and dtype (got {list(q.shape)} "
                          f"{q.dtype}, {list(k.shape)} {k.dtype})")
-    if Hkv > _INT_MAX:
-        _fits(Hkv)
     return RaShape(B, N, N, Hq, Hkv, d, qb, kb, qr, qh, kr, kh)
 
 

@@ -13,7 +13,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libra.so")
 SOURCES = ["ra_api.cu", "ra_simt.cu", "ra_fwd_tc.cu", "ra_bwd_tc.cu", "ra_gemm_tc.cu", "ra_noalloc.cu",
            "ra_xent_tc.cu", "ra_xent_few.cu", "ra_ns_tc.cu", "ra_ns_small.cu", "ra_train.cu", "ra_rotary.cu",
-           "ra_rotary_bwd.cu", "ra_clip.cu"]
+           "ra_rotary_bwd.cu", "ra_clip.cu", "ra_cross.cu", "ra_cross_few.cu"]
 HEADERS = ["ra_device.cuh", "ra_internal.h", "ra_pair.cuh", "ra_ns.cuh", "ra_rotary.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

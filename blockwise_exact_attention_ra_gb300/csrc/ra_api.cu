@@ -2280,3 +2280,273 @@ int ra_grad_clip(const void* const* grads, const long long* sizes, const int* dt
 
 #pragma GCC visibility pop
 }  // extern "C"
+
+// ------------------------------------------------ cross attention
+namespace ra {
+namespace {
+
+constexpr int kPlanSms = 152;  // plans are made for a whole GB300, so that sizes do not vary
+
+int check_cross(const ra_shape& shape, int dtype, int flags, Shape* s) {
+  if (flags & ~RA_PRECISE) return fail(RA_ERR_INVALID_ARG, "unknown flag bits 0x%x", flags);
+  if (dtype != RA_BF16 && dtype != RA_F16) {
+    if (dtype == RA_F32) return fail(RA_ERR_UNSUPPORTED, "cross attention takes bf16 or fp16 inputs");
+    return fail(RA_ERR_INVALID_ARG, "bad dtype %d", dtype);
+  }
+  int rc;
+  if ((rc = check_shape(shape, s))) return rc;
+  if (s->d != 64 && s->d != 128) return fail(RA_ERR_UNSUPPORTED, "cross attention supports d in {64, 128} (got %d)", s->d);
+  const long long tiles = ((long long)s->Nq + 127) / 128, keys = ((long long)s->Nkv + 127) / 128;
+  if ((long long)s->B * s->Hq * tiles > (1 << 22) || (long long)s->B * s->Hkv * keys > (1 << 22) ||
+      tiles * (s->Hq / s->Hkv) >= (1 << 20))
+    return fail(RA_ERR_UNSUPPORTED, "too many tiles of queries or keys");
+  return RA_OK;
+}
+
+struct CrossPlan {
+  bool few, bf16_p;
+  int splits;
+  size_t v16, parts, m, l, total;
+};
+
+// Parts of the keys, by what a call takes (us; measured): the waves of units, a tile of 128
+// keys `tile` and a unit's start and end `ends`, and the join, which reads every part's state.
+int cross_parts(long long units, long long tiles, double tile, double ends, double part_bytes, int most) {
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= most && s <= tiles; ++s) {
+    const double waves = (double)((units * s + kPlanSms - 1) / kPlanSms);
+    const double t = waves * ((tiles + s - 1) / s * tile + ends) + (s > 1 ? 4. + s * part_bytes / 5e6 : 0.);
+    if (t < least * 0.97) {
+      least = t;
+      best = s;
+    }
+  }
+  return best;
+}
+
+CrossPlan cross_plan(const Shape& s, int dtype, int flags) {
+  CrossPlan p{};
+  const int group = s.Hq / s.Hkv;
+  const long long tiles = (s.Nkv + 127) / 128;
+  p.few = (long long)s.Nq * group <= kCrossFewRows;
+  if (p.few) {
+    const long long units = (long long)s.B * s.Hkv, want = (608 + units - 1) / units, most = (s.Nkv + 255) / 256;
+    p.splits = (int)(want < most ? want : most);
+  } else {
+    p.bf16_p = dtype == RA_BF16 && !(flags & RA_PRECISE) && (long long)s.Nq * group <= 512;
+    const int pairs = ((s.Nq + 127) / 128 + 1) / 2;
+    const double tile = (s.Nq <= 128 ? 1.2 : 2.) * s.d / 128.;
+    p.splits = cross_parts((long long)s.B * s.Hq * pairs, tiles, tile, 4., 8. * s.B * s.Nq * s.Hq * s.d, 64);
+  }
+  p.v16 = 256;
+  p.parts = p.v16;
+  if (!p.few && dtype == RA_BF16 && !p.bf16_p) p.parts += align256((size_t)s.B * s.Nkv * s.Hkv * s.d * 2);
+  p.m = p.l = p.total = p.parts;
+  if (p.splits > 1) {
+    const size_t states = (size_t)p.splits * s.B * s.Nq * s.Hq;
+    p.m = p.parts + align256(states * s.d * 4);
+    p.l = p.m + align256(states * 4);
+    p.total = p.l + align256(states * 4);
+  }
+  return p;
+}
+
+int check_len(const int* kv_len) {
+  if (reinterpret_cast<uintptr_t>(kv_len) & 3u) return fail(RA_ERR_INVALID_ARG, "kv_len is not 4-byte aligned");
+  return RA_OK;
+}
+
+// Backward workspace: D, lse2 [B, Hq, Np] fp32 | dq accumulator [B, Nq, Hq, d] fp32 | unit
+// counter | fp16 copies | planes of dK and dV.
+struct CrossBwdPlan {
+  int Np, q_splits;
+  size_t D, lse2, dq, sched, q16, do16, k16, v16, parts, total;
+};
+CrossBwdPlan cross_bwd_plan(const Shape& s, int dtype) {
+  CrossBwdPlan p{};
+  const long long nqt = (s.Nq + 127) / 128, nkt = (s.Nkv + 127) / 128, units = (long long)s.B * s.Hkv * nkt;
+  const int group = s.Hq / s.Hkv;
+  const size_t rows = (size_t)s.B * s.Hq * nqt * 128, qel = (size_t)s.B * s.Nq * s.Hq * s.d;
+  const size_t kvel = (size_t)s.B * s.Nkv * s.Hkv * s.d;
+  p.Np = (int)(nqt * 128);
+  const int most = cross_parts(units, nqt, 2.6 * group * s.d / 128., 5., 16. * kvel, 32);
+  const long long per = (nqt + most - 1) / most;
+  p.q_splits = (int)((nqt + per - 1) / per);  // none of them empty
+  size_t off = 0;
+  p.D = off; off += align256(rows * 4);
+  p.lse2 = off; off += align256(rows * 4);
+  p.dq = off; off += align256(qel * 4);
+  p.sched = off; off += 256;
+  if (dtype == RA_BF16) {
+    p.q16 = off; off += align256(qel * 2);
+    p.do16 = off; off += align256(qel * 2);
+  }
+  p.k16 = off; off += align256(kvel * 2);
+  p.v16 = off; off += align256(kvel * 2);
+  p.parts = off;
+  if (p.q_splits > 1) off += align256(2 * kvel * 4 * p.q_splits);
+  p.total = off;
+  return p;
+}
+
+}  // namespace
+}  // namespace ra
+
+extern "C" {
+#pragma GCC visibility push(default)
+
+size_t ra_cross_fwd_workspace_bytes(ra_dtype dtype, ra_shape shape, int flags) {
+  Shape s;
+  if (check_cross(shape, dtype, flags, &s)) return 0;
+  return cross_plan(s, dtype, flags).total;
+}
+
+int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra_shape shape, const int* kv_len, int flags,
+                 float scale, void* o, ra_dtype o_dtype, float* lse, void* workspace, size_t ws_bytes, void* stream) {
+  Shape s;
+  int rc, *st;
+  if ((rc = check_cross(shape, dtype, flags, &s))) return rc;
+  if (!valid_dtype(o_dtype)) return fail(RA_ERR_INVALID_ARG, "bad dtype");
+  if ((rc = check_scale(scale)) || (rc = check_ptr(q, "q")) || (rc = check_ptr(k, "k")) || (rc = check_ptr(v, "v")) ||
+      (rc = check_ptr(o, "o")) || (rc = check_floats(lse, "lse")) || (rc = check_len(kv_len)))
+    return rc;
+  const CrossPlan p = cross_plan(s, dtype, flags);
+  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const CrossState part{reinterpret_cast<float*>(ws + p.parts), reinterpret_cast<float*>(ws + p.m),
+                        reinterpret_cast<float*>(ws + p.l)};
+  const int bf = dtype == RA_BF16;
+  cudaError_t e;
+  if (p.few) {
+    CrossFewArgs a;
+    memset(&a, 0, sizeof a);
+    a.q = q; a.k = k; a.v = v; a.bf16 = bf;
+    a.B = s.B; a.Nq = s.Nq; a.Nkv = s.Nkv; a.Hq = s.Hq; a.Hkv = s.Hkv; a.d = s.d;
+    a.ql = s.ql; a.kvl = s.kvl; a.ol = s.ql;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.kv_len = kv_len; a.splits = p.splits; a.part = part;
+    a.o = o; a.o_dtype = o_dtype; a.lse = lse;
+    e = launch_cross_few(a, cs);
+  } else {
+    const long long units = (long long)s.B * s.Hq * (((s.Nq + 127) / 128 + 1) / 2) * p.splits;
+    const void* v16 = v;
+    if (bf && !p.bf16_p) {
+      v16 = ws + p.v16;
+      if ((e = launch_cross_keys(nullptr, v, 1, s.kvl, nullptr, ws + p.v16, s.B, s.Nkv, s.Hkv, s.d, kv_len, st, cs)) != cudaSuccess)
+        return cuda_fail(e, "v -> fp16 launch");
+    }
+    TcFwdArgs a;
+    memset(&a, 0, sizeof a);
+    if ((rc = make_map(&a.tm_q, q, bf, s.B, s.Nq, s.Hq, s.d, s.ql)) || (rc = make_map(&a.tm_k, k, bf, s.B, s.Nkv, s.Hkv, s.d, s.kvl)) ||
+        (rc = make_map(&a.tm_v, v16, v16 == v && bf, s.B, s.Nkv, s.Hkv, s.d, v16 == v ? s.kvl : packed_lay(s.Nkv, s.Hkv, s.d))))
+      return rc;
+    a.qk_bf16 = bf; a.cross = 1; a.splits = p.splits; a.bf16_p = p.bf16_p; a.kv_len = kv_len;
+    a.B = s.B; a.Nq = s.Nq; a.Nkv = s.Nkv; a.Hq = s.Hq; a.Hkv = s.Hkv; a.d = s.d;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.precise = (flags & RA_PRECISE) != 0;
+    a.mode = p.splits > 1 ? 2 : 0;
+    a.o_acc = part.o; a.m_acc = part.m; a.l_acc = part.l;
+    a.o_out = o; a.o_dtype = o_dtype; a.ol = s.ql; a.lse = lse;
+    a.status = st;
+    a.wait_limit_ns = wait_limit_ns();
+    a.log = visit_log();
+    a.num_units = (int)units;
+    if (units > device_sms()) {  // drawn from a counter: batch entries differ in length
+      a.sched = static_cast<unsigned int*>(workspace);
+      if ((e = cudaMemsetAsync(workspace, 0, 256, cs)) != cudaSuccess) return cuda_fail(e, "zero unit counter");
+    }
+    TimedLaunch tl(RA_KERNEL_FWD_TC, cs);
+    e = launch_tc_fwd(a, device_sms(), cs);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "cross attention forward launch");
+  if (p.splits > 1) {
+    e = launch_cross_join(part, p.splits, s.B, s.Nq, s.Hq, s.d, o, o_dtype, s.ql, lse, cs);
+    if (e != cudaSuccess) return cuda_fail(e, "cross attention join launch");
+  }
+  return RA_OK;
+}
+
+size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape) {
+  Shape s;
+  if (check_cross(shape, dtype, 0, &s)) return 0;
+  return cross_bwd_plan(s, dtype).total;
+}
+
+int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype, const void* dO,
+                 const float* lse, ra_dtype dtype, ra_shape shape, const int* kv_len, int flags, float scale, void* dq,
+                 void* dk, void* dv, ra_dtype grad_dtype, void* workspace, size_t ws_bytes, void* stream) {
+  Shape s;
+  int rc, *st;
+  if ((rc = check_cross(shape, dtype, flags, &s))) return rc;
+  if (!valid_dtype(o_dtype) || !valid_dtype(grad_dtype)) return fail(RA_ERR_INVALID_ARG, "bad dtype");
+  if ((rc = check_scale(scale)) || (rc = check_ptr(q, "q")) || (rc = check_ptr(k, "k")) || (rc = check_ptr(v, "v")) ||
+      (rc = check_ptr(o, "o")) || (rc = check_ptr(dO, "dO")) || (rc = check_floats(lse, "lse")) ||
+      (rc = check_ptr(dq, "dq")) || (rc = check_ptr(dk, "dk")) || (rc = check_ptr(dv, "dv")) || (rc = check_len(kv_len)))
+    return rc;
+  const CrossBwdPlan p = cross_bwd_plan(s, dtype);
+  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const int bf = dtype == RA_BF16;
+  cudaError_t e;
+  CrossRowsArgs r;
+  memset(&r, 0, sizeof r);
+  r.q = q; r.dO = dO; r.o = o; r.lse = lse;
+  r.bf16 = bf; r.o_dtype = o_dtype;
+  r.B = s.B; r.Nq = s.Nq; r.Np = p.Np; r.Hq = s.Hq; r.d = s.d;
+  r.ql = s.ql;
+  if (bf) {
+    r.q16 = ws + p.q16;
+    r.do16 = ws + p.do16;
+  }
+  r.D = reinterpret_cast<float*>(ws + p.D);
+  r.lse2 = reinterpret_cast<float*>(ws + p.lse2);
+  r.dq_acc = reinterpret_cast<float*>(ws + p.dq);
+  r.sched = reinterpret_cast<unsigned int*>(ws + p.sched);
+  r.status = st;
+  if ((e = launch_cross_rows(r, cs)) != cudaSuccess) return cuda_fail(e, "cross attention row terms launch");
+  const void *q16 = bf ? r.q16 : q, *do16 = bf ? r.do16 : dO, *k16 = k, *v16 = v;
+  const Lay q_l = bf ? packed_lay(s.Nq, s.Hq, s.d) : s.ql;
+  Lay kv_l = s.kvl;
+  if (bf || kv_len) {  // keys past the length as zeros: what they hold would reach dq
+    k16 = ws + p.k16;
+    v16 = ws + p.v16;
+    kv_l = packed_lay(s.Nkv, s.Hkv, s.d);
+    if ((e = launch_cross_keys(k, v, bf, s.kvl, ws + p.k16, ws + p.v16, s.B, s.Nkv, s.Hkv, s.d, kv_len, st, cs)) != cudaSuccess)
+      return cuda_fail(e, "fp16 operand copy launch");
+  }
+  TcBwdArgs a;
+  memset(&a, 0, sizeof a);
+  if ((rc = make_map(&a.tm_q, q16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) || (rc = make_map(&a.tm_do, do16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) ||
+      (rc = make_map(&a.tm_k, k16, 0, s.B, s.Nkv, s.Hkv, s.d, kv_l)) || (rc = make_map(&a.tm_v, v16, 0, s.B, s.Nkv, s.Hkv, s.d, kv_l)) ||
+      (rc = make_map_f32(&a.tm_dq, r.dq_acc, s.B, s.Nq, s.Hq, s.d)))
+    return rc;
+  a.cross = 1; a.N = s.Nq; a.Nkv = s.Nkv; a.Np = p.Np; a.q_splits = p.q_splits; a.kv_len = kv_len;
+  a.parts = reinterpret_cast<float*>(ws + p.parts);
+  a.B = s.B; a.Hq = s.Hq; a.Hkv = s.Hkv; a.d = s.d;
+  a.scale = scale;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.precise = (flags & RA_PRECISE) != 0;
+  a.lse = r.lse2; a.Dvec = r.D; a.dq_acc = r.dq_acc;
+  a.dk = dk; a.dv = dv; a.grad_dtype = grad_dtype; a.kvl = s.kvl;
+  a.status = st;
+  a.wait_limit_ns = wait_limit_ns();
+  a.log = visit_log();
+  a.num_units = s.B * s.Hkv * ((s.Nkv + 127) / 128) * p.q_splits;
+  a.sched = r.sched;
+  {
+    TimedLaunch tl(RA_KERNEL_BWD_TC, cs);
+    e = launch_tc_bwd(a, device_sms(), cs);
+  }
+  if (e != cudaSuccess) return cuda_fail(e, "cross attention backward launch");
+  if (p.q_splits > 1 &&
+      (e = launch_cross_sum(a.parts, p.q_splits, s.B, s.Nkv, s.Hkv, s.d, dk, dv, grad_dtype, s.kvl, cs)) != cudaSuccess)
+    return cuda_fail(e, "cross attention gradient sum launch");
+  e = launch_cross_dq(r.dq_acc, scale, s.B, s.Nq, s.Hq, s.d, dq, grad_dtype, s.ql, cs);
+  return e == cudaSuccess ? RA_OK : cuda_fail(e, "dq conversion launch");
+}
+
+#pragma GCC visibility pop
+}  // extern "C"

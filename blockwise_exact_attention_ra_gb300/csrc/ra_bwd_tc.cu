@@ -83,6 +83,7 @@ struct BwdSmem {
 
 struct BwdUnit {
   int b, g, jt;
+  int first, part;  // cross attention: first query tile, part of the query tiles
   int count;  // query tiles per head
   int n_iter; // count * group
   int host, tk, per_block;  // striped layouts: key host, local key tile, query tiles per block
@@ -99,9 +100,24 @@ struct BwdUnit {
 // units end the launch.
 __device__ __forceinline__ int host_len_at(const int* hl, int j, int S);
 
-template <bool STRIPED, bool VARLEN>
+template <bool STRIPED, bool VARLEN, bool CROSS>
 __device__ __forceinline__ BwdUnit bwd_unit(const TcBwdArgs& a, int u) {
   BwdUnit r;
+  if (CROSS) {
+    // a key tile meets every query tile of its part; one past the length meets none
+    const int nkt = (a.Nkv + 127) / 128, nqt = a.Np / 128, per = (nqt + a.q_splits - 1) / a.q_splits;
+    const int head = nkt * a.q_splits, bg = u / head, rest = u - bg * head;
+    r.b = bg / a.Hkv;
+    r.g = bg - r.b * a.Hkv;
+    r.part = rest / nkt;
+    r.jt = rest - r.part * nkt;
+    r.first = r.part * per;
+    r.count = min(per, nqt - r.first);
+    r.count_m = div_magic((unsigned)r.count);
+    r.n_iter = r.count * (a.Hq / a.Hkv);
+    if (a.kv_len && r.jt * 128 >= host_len_at(a.kv_len, r.b, a.Nkv)) r.n_iter = 0;
+    return r;
+  }
   const int nT = a.N / 128;
   const int bg = u / nT;
   r.jt = u % nT;
@@ -135,12 +151,16 @@ __device__ __forceinline__ BwdUnit bwd_unit(const TcBwdArgs& a, int u) {
 }
 
 // Query head and query tile of iteration it, in ring order.
-template <bool STRIPED>
+template <bool STRIPED, bool CROSS>
 __device__ __forceinline__ void bwd_iter(const TcBwdArgs& a, const BwdUnit& u, int it, int* h,
                                          int* qt) {
   const int group = a.Hq / a.Hkv;
   const int hh = div_by(it, u.count_m), k = it - hh * u.count;
   *h = u.g * group + hh;
+  if (CROSS) {
+    *qt = u.first + k;
+    return;
+  }
   if (STRIPED) {
     // The key tile goes round the ring once per local query tile it meets:
     // lap t takes local query tile tk + t of hosts (j + s) mod P, s = 0..P-1.
@@ -211,14 +231,15 @@ __device__ __forceinline__ uint32_t dq_box(int s, int cc) {
   return L::kDO0 + s * L::kTile + cc * 16384;
 }
 
-// Ring layouts, one kernel build each: contiguous hosts, striped rows, and
-// contiguous hosts with variable valid lengths.
-enum { kLayoutContiguous = 0, kLayoutStriped = 1, kLayoutVarlen = 2 };
+// Layouts, one kernel build each: contiguous hosts of the ring, striped rows,
+// contiguous hosts with variable valid lengths; and queries against keys of another
+// length (cross attention).
+enum { kLayoutContiguous = 0, kLayoutStriped = 1, kLayoutVarlen = 2, kLayoutCross = 3 };
 
 template <int D, bool PRECISE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_constant__ TcBwdArgs a) {
   using L = BwdSmem<D>;
-  constexpr bool STRIPED = LAYOUT == kLayoutStriped, VARLEN = LAYOUT == kLayoutVarlen;
+  constexpr bool STRIPED = LAYOUT == kLayoutStriped, VARLEN = LAYOUT == kLayoutVarlen, CROSS = LAYOUT == kLayoutCross;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
   if (sbase & 1023u) {  // the swizzled tiles need 1024-byte alignment
@@ -318,8 +339,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         unit_ring[slot] = u;
         mbar_arrive(bar_unit_full(slot));
         if (u >= a.num_units) break;
-        const BwdUnit bu = bwd_unit<STRIPED, VARLEN>(a, u);
-        if (VARLEN && bu.n_iter == 0) continue;
+        const BwdUnit bu = bwd_unit<STRIPED, VARLEN, CROSS>(a, u);
+        if ((VARLEN || CROSS) && bu.n_iter == 0) continue;
         if (!mbar_wait(BAR_KV_EMPTY, (k & 1) ^ 1, abort_flag, a.status, lim)) { ok = false; break; }
         mbar_arrive_expect_tx(BAR_KV_FULL, 2 * L::kTile);
 #pragma unroll
@@ -330,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         ++k;
         for (int it = 0; it < bu.n_iter; ++it) {
           int h, qt;
-          bwd_iter<STRIPED>(a, bu, it, &h, &qt);
+          bwd_iter<STRIPED, CROSS>(a, bu, it, &h, &qt);
           if (VARLEN && !q_tile_valid<VARLEN>(a, qt)) continue;
           if (a.log.entries) log_visit(a.log, 1u, bu.b * a.Hq + h, qt, bu.jt);
           const int s = qd_cnt & 1;
@@ -340,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
 #pragma unroll
           for (int c = 0; c < D / 64; ++c)
             tma_load_4d(sbase + L::kQ0 + s * L::kTile + c * 16384, &a.tm_q, bar_q_full(s), c * 64, h, qt * 128, bu.b, pol_q);
-          const long long vrow = ((long long)bu.b * a.Hq + h) * a.N + (long long)qt * 128;
+          const long long vrow = ((long long)bu.b * a.Hq + h) * (CROSS ? a.Np : a.N) + (long long)qt * 128;
           bulk_load(sbase + L::kVec0 + s * 1024, a.lse + vrow, 512, bar_q_full(s));
           bulk_load(sbase + L::kVec0 + s * 1024 + 512, a.Dvec + vrow, 512, bar_q_full(s));
           q_issued[s] = 1;
@@ -400,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       auto next_valid = [&](const BwdUnit& bu, int it) {
         for (; it < bu.n_iter; ++it) {
           int h, qt;
-          bwd_iter<STRIPED>(a, bu, it, &h, &qt);
+          bwd_iter<STRIPED, CROSS>(a, bu, it, &h, &qt);
           if (q_tile_valid<VARLEN>(a, qt)) break;
         }
         return it;
@@ -408,8 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       for (int n = 0; ok; ++n) {
         int u;
         if (!take_unit(n, &u) || u >= a.num_units) break;
-        const BwdUnit bu = bwd_unit<STRIPED, VARLEN>(a, u);
-        if (VARLEN && bu.n_iter == 0) continue;
+        const BwdUnit bu = bwd_unit<STRIPED, VARLEN, CROSS>(a, u);
+        if ((VARLEN || CROSS) && bu.n_iter == 0) continue;
         if (!wait(BAR_KV_FULL, k & 1)) break;
         // prologue: S(0), dP(0)
         uint32_t s = qd_cnt & 1;
@@ -539,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
     for (int n = 0; ok; ++n) {
       int u;
       if (!take_unit(n, &u) || u >= a.num_units) break;
-      const BwdUnit bu = bwd_unit<STRIPED, VARLEN>(a, u);
+      const BwdUnit bu = bwd_unit<STRIPED, VARLEN, CROSS>(a, u);
       // padding: key rows of this tile from kvalid on (variable host lengths)
       int kvalid = 128;
       if (VARLEN) {
@@ -547,6 +568,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         const int j = div_by(bu.jt, a.T_m);
         kvalid = host_len_at(a.host_len, j, a.ring_S) - (bu.jt - j * T) * 128;
       }
+      if (CROSS) kvalid = (a.kv_len ? host_len_at(a.kv_len, bu.b, a.Nkv) : a.Nkv) - bu.jt * 128;
       // kq: position in the current query head's sweep, enough to place the
       // diagonal tiles without the query tile index
       int kq = 0;
@@ -554,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         const int kpos = kq;
         if (++kq == bu.count) kq = 0;
         int h = 0, qt = 0;
-        if (VARLEN) bwd_iter<STRIPED>(a, bu, it, &h, &qt);
+        if (VARLEN) bwd_iter<STRIPED, CROSS>(a, bu, it, &h, &qt);
         // padding: query columns of this tile from qvalid on; a tile wholly in
         // padding is skipped by every role
         int qvalid = 128;
@@ -581,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         // striped layout the same local tile of any host pair, the sweep's
         // first lap (query hosts j, j+1, ... in ring order), strict (c > r)
         // where the query's host index has wrapped below the key's
-        const bool pad = VARLEN && (qvalid < 128 || kvalid < 128);
+        const bool pad = (VARLEN || CROSS) && (qvalid < 128 || kvalid < 128);
         bool diag;
         int strict = 0;
         if (STRIPED) {
@@ -609,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         // a padded key row, are zero
         if (diag || pad) {
           const int c_lo = diag ? r + strict - half * 64 : 0;
-          const int c_hi = VARLEN ? (r < kvalid ? qvalid - half * 64 : 0) : 64;
+          const int c_hi = VARLEN || CROSS ? (r < kvalid ? qvalid - half * 64 : 0) : 64;
 #pragma unroll
           for (int c = 0; c < 64; ++c)
             if (c < c_lo || c >= c_hi) pr[c] = 0u;
@@ -680,11 +702,57 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
     for (int n = 0; ok; ++n) {
       int u;
       if (!take_unit(n, &u) || u >= a.num_units) break;
-      const BwdUnit bu = bwd_unit<STRIPED, VARLEN>(a, u);
+      const BwdUnit bu = bwd_unit<STRIPED, VARLEN, CROSS>(a, u);
       if (VARLEN && bu.n_iter == 0) continue;
+      const long long row = (long long)bu.jt * 128 + r;
+      // this row of dK (which 0) or dV, 32 columns from c on
+      auto write = [&](int which, int c, const uint32_t (&v)[32], float mul) {
+        if (CROSS && row >= a.Nkv) return;
+        long long base = lay_at(a.kvl, bu.b, row, bu.g);
+        void* outp = which == 0 ? a.dk : a.dv;
+        int dtype = a.grad_dtype;
+        if (CROSS && a.q_splits > 1) {
+          outp = a.parts;
+          dtype = RA_F32;
+          base = ((((long long)which * a.q_splits + bu.part) * a.B + bu.b) * a.Nkv + row) * a.Hkv * D + bu.g * D;
+        }
+        if (dtype == RA_F32) {
+          float* op = static_cast<float*>(outp) + base + c;
+#pragma unroll
+          for (int j = 0; j < 32; j += 4)
+            *reinterpret_cast<float4*>(op + j) =
+                make_float4(__uint_as_float(v[j]) * mul, __uint_as_float(v[j + 1]) * mul,
+                            __uint_as_float(v[j + 2]) * mul, __uint_as_float(v[j + 3]) * mul);
+        } else {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            const float f0 = __uint_as_float(v[j]) * mul, f1 = __uint_as_float(v[j + 1]) * mul;
+            if (dtype == RA_BF16) {
+              __nv_bfloat162 t = __floats2bfloat162_rn(f0, f1);
+              pk[j / 2] = *reinterpret_cast<uint32_t*>(&t);
+            } else {
+              pk[j / 2] = pack_half2(f0, f1);
+            }
+          }
+          uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(outp) + base + c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) op[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        }
+      };
+      if (CROSS && bu.n_iter == 0) {  // keys past the length have no gradient
+        uint32_t v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = 0u;
+        for (int c = 0; c < D; c += 32) {
+          write(0, c, v, 1.f);
+          write(1, c, v, 1.f);
+        }
+        continue;
+      }
       for (int it = 0; it < bu.n_iter; ++it) {
         int h, qt;
-        bwd_iter<STRIPED>(a, bu, it, &h, &qt);
+        bwd_iter<STRIPED, CROSS>(a, bu, it, &h, &qt);
         if (VARLEN && !q_tile_valid<VARLEN>(a, qt)) continue;
         if (!mbar_wait(BAR_DQ_FULL, dq_cnt & 1, abort_flag, a.status, lim)) { ok = false; break; }
         ++dq_cnt;
@@ -709,6 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
           __syncwarp();
         };
         auto reduce = [&](int rd) {  // lane 0: this warp's rows of round rd
+          if (CROSS && qt * 128 + (int)quarter * 32 >= a.N) return;  // none of them is a row
 #pragma unroll
           for (int cc = 0; cc < BPR; ++cc)
             tma_reduce_add_4d(&a.tm_dq, sbase + dq_box<D>(s, cc) + quarter * 32 * 128, rd * HALF + 32 * cc, h,
@@ -745,41 +814,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       if (!ok) break;
       if (!mbar_wait(BAR_DKV_FULL, k & 1, abort_flag, a.status, lim)) { ok = false; break; }
       tc_fence_after();
-      const long long row = (long long)bu.jt * 128 + r;
-      const long long base = lay_at(a.kvl, bu.b, row, bu.g);
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint32_t src = (which == 0 ? T_DK : T_DV) + lane_off;
         const float mul = which == 0 ? a.scale : 1.f;
-        void* outp = which == 0 ? a.dk : a.dv;
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t v[32];
           RA_TMEM_LD32(src + c, v);
           tmem_ld_wait();
-          if (a.grad_dtype == RA_F32) {
-            float* op = static_cast<float*>(outp) + base + c;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(op + j) =
-                  make_float4(__uint_as_float(v[j]) * mul, __uint_as_float(v[j + 1]) * mul,
-                              __uint_as_float(v[j + 2]) * mul, __uint_as_float(v[j + 3]) * mul);
-          } else {
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 32; j += 2) {
-              const float f0 = __uint_as_float(v[j]) * mul, f1 = __uint_as_float(v[j + 1]) * mul;
-              if (a.grad_dtype == RA_BF16) {
-                __nv_bfloat162 t = __floats2bfloat162_rn(f0, f1);
-                pk[j / 2] = *reinterpret_cast<uint32_t*>(&t);
-              } else {
-                pk[j / 2] = pack_half2(f0, f1);
-              }
-            }
-            uint4* op = reinterpret_cast<uint4*>(static_cast<uint16_t*>(outp) + base + c);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) op[j] = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-          }
+          write(which, c, v, mul);
         }
       }
       tc_fence_before();
@@ -808,7 +852,10 @@ cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st) {
     return cudaSuccess;
   };
   if (a.d == 128) {
-    if (a.striped)
+    if (a.cross)
+      e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutCross>, BwdSmem<128>::kBytes)
+                    : run(tc_bwd_kernel<128, false, kLayoutCross>, BwdSmem<128>::kBytes);
+    else if (a.striped)
       e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutStriped>, BwdSmem<128>::kBytes)
                     : run(tc_bwd_kernel<128, false, kLayoutStriped>, BwdSmem<128>::kBytes);
     else if (a.host_len)
@@ -818,7 +865,10 @@ cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st) {
       e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutContiguous>, BwdSmem<128>::kBytes)
                     : run(tc_bwd_kernel<128, false, kLayoutContiguous>, BwdSmem<128>::kBytes);
   } else if (a.d == 64) {
-    if (a.striped)
+    if (a.cross)
+      e = a.precise ? run(tc_bwd_kernel<64, true, kLayoutCross>, BwdSmem<64>::kBytes)
+                    : run(tc_bwd_kernel<64, false, kLayoutCross>, BwdSmem<64>::kBytes);
+    else if (a.striped)
       e = a.precise ? run(tc_bwd_kernel<64, true, kLayoutStriped>, BwdSmem<64>::kBytes)
                     : run(tc_bwd_kernel<64, false, kLayoutStriped>, BwdSmem<64>::kBytes);
     else if (a.host_len)

@@ -1,0 +1,292 @@
+// The kernels around cross attention's products: the join of states over parts of the keys,
+// fp16 operand copies, the backward pass's row terms and its last conversions.  All are
+// bound by what they read and write.
+#include <math.h>
+
+#include "ra_device.cuh"
+
+namespace ra {
+namespace {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kThreads = 256;
+
+__device__ __forceinline__ int len_at(const int* kv_len, int b, int Nkv) {
+  if (!kv_len) return Nkv;
+  const int v = __ldg(kv_len + b);
+  return v < 0 ? 0 : v > Nkv ? Nkv : v;
+}
+
+// Eight values as `dtype` at element i of p.
+__device__ __forceinline__ void put8(void* p, int dtype, long long i, const float (&f)[8]) {
+  if (dtype == RA_F32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
+    o[0] = make_float4(f[0], f[1], f[2], f[3]);
+    o[1] = make_float4(f[4], f[5], f[6], f[7]);
+  } else if (dtype == RA_BF16) {
+    __align__(16) __nv_bfloat16 e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = __float2bfloat16_rn(f[j]);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p) + i) = *reinterpret_cast<const uint4*>(e);
+  } else {
+    __align__(16) __half e[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) e[j] = __float2half_rn(f[j]);
+    *reinterpret_cast<uint4*>(static_cast<__half*>(p) + i) = *reinterpret_cast<const uint4*>(e);
+  }
+}
+__device__ __forceinline__ void get8(const void* p, int dtype, long long i, float (&f)[8]) {
+  if (dtype == RA_F32) {
+    const float4* s = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    const float4 a = s[0], b = s[1];
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    return;
+  }
+  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+  if (dtype == RA_BF16) {
+    const __nv_bfloat16* e = reinterpret_cast<const __nv_bfloat16*>(&v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __bfloat162float(e[j]);
+  } else {
+    const __half* e = reinterpret_cast<const __half*>(&v);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __half2float(e[j]);
+  }
+}
+__device__ __forceinline__ bool past_fp16(const float (&f)[8]) {
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) bad |= fabsf(f[j]) > 65504.f && fabsf(f[j]) < INFINITY;
+  return bad;
+}
+
+// A warp joins the states (m_s, l_s, o_s) of one row: m = max m_s, w_s = e^{m_s - m},
+// o = sum w_s o_s / sum w_s l_s, lse = m + ln sum w_s l_s.  Parts that saw no key left no
+// o_s.  A lane holds d / 32 columns.
+__global__ void __launch_bounds__(kThreads) cross_join_kernel(CrossState p, int splits, int B, int Nq, int Hq, int d, void* o,
+                                                              int o_dtype, Lay ol, float* lse) {
+  pdl_trigger();
+  pdl_wait();
+  const long long rows = (long long)B * Nq * Hq, row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= rows) return;
+  const int h = (int)(row % Hq);
+  const long long bn = row / Hq;
+  const int n = (int)(bn % Nq), b = (int)(bn / Nq);
+  const long long at = ((long long)b * Hq + h) * Nq + n;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, p.m[s * rows + at]);
+  m = warp_max(m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s0 = 0; s0 < splits; s0 += 32) {
+    float w = 0.f;
+    if (s0 + lane < splits) {
+      w = ex2_approx((p.m[(s0 + lane) * rows + at] - ref) * kLog2e);
+      const float ls = p.l[(s0 + lane) * rows + at];
+      // a NaN stays one, whatever its part's maximum
+      if (w > 0.f || ls != ls) l += w * ls;
+    }
+    const int last = min(32, splits - s0);
+#pragma unroll 4
+    for (int j = 0; j < last; ++j) {
+      const float ws = __shfl_sync(0xffffffffu, w, j);
+      if (!(ws > 0.f)) continue;
+      const float* src = p.o + ((s0 + j) * rows + row) * d;
+      if (d == 128) {
+        const float4 v = reinterpret_cast<const float4*>(src)[lane];
+        acc.x = fmaf(ws, v.x, acc.x);
+        acc.y = fmaf(ws, v.y, acc.y);
+        acc.z = fmaf(ws, v.z, acc.z);
+        acc.w = fmaf(ws, v.w, acc.w);
+      } else {
+        const float2 v = reinterpret_cast<const float2*>(src)[lane];
+        acc.x = fmaf(ws, v.x, acc.x);
+        acc.y = fmaf(ws, v.y, acc.y);
+      }
+    }
+  }
+  l = warp_sum(l);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  acc.x *= inv;
+  acc.y *= inv;
+  acc.z *= inv;
+  acc.w *= inv;
+  const long long out = lay_at(ol, b, n, h);
+  if (d == 128) {
+    if (o_dtype == RA_F32) {
+      reinterpret_cast<float4*>(static_cast<float*>(o) + out)[lane] = acc;
+    } else {
+      uint2 v;
+      if (o_dtype == RA_BF16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(acc.x, acc.y), y = __floats2bfloat162_rn(acc.z, acc.w);
+        v = make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+      } else {
+        v = make_uint2(pack_half2(acc.x, acc.y), pack_half2(acc.z, acc.w));
+      }
+      reinterpret_cast<uint2*>(static_cast<uint16_t*>(o) + out)[lane] = v;
+    }
+  } else if (o_dtype == RA_F32) {
+    reinterpret_cast<float2*>(static_cast<float*>(o) + out)[lane] = make_float2(acc.x, acc.y);
+  } else if (o_dtype == RA_BF16) {
+    reinterpret_cast<__nv_bfloat162*>(static_cast<uint16_t*>(o) + out)[lane] = __floats2bfloat162_rn(acc.x, acc.y);
+  } else {
+    reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(o) + out)[lane] = pack_half2(acc.x, acc.y);
+  }
+  if (lane == 0) lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+__global__ void __launch_bounds__(kThreads) cross_keys_kernel(const void* k, const void* v, int dtype, Lay kvl, __half* k16,
+                                                              __half* v16, int B, int Nkv, int Hkv, int d, const int* kv_len,
+                                                              int* status) {
+  const int per_row = Hkv * d / 8;
+  const long long total = (long long)B * Nkv * per_row;
+  bool bad = false;
+  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < total; t += (long long)gridDim.x * kThreads) {
+    const long long bn = t / per_row;
+    const int e = (int)(t - bn * per_row) * 8, g = e / d, b = (int)(bn / Nkv), n = (int)(bn - (long long)b * Nkv);
+    const bool there = n < len_at(kv_len, b, Nkv);
+    const long long src = lay_at(kvl, b, n, g) + (e - g * d);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const void* x = i ? v : k;
+      __half* y = i ? v16 : k16;
+      if (!y) continue;
+      float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (there) {
+        get8(x, dtype, src, f);
+        bad |= past_fp16(f);
+      }
+      put8(y, RA_F16, t * 8, f);
+    }
+  }
+  if (bad) report(status, RA_ERR_RANGE);
+}
+
+// d / 8 lanes a row (b, n, h), n up to Np.
+__global__ void __launch_bounds__(kThreads) cross_rows_kernel(const __grid_constant__ CrossRowsArgs a) {
+  const int G = a.d / 8, lane = threadIdx.x % G, in_dtype = a.bf16 ? RA_BF16 : RA_F16;
+  const long long rows = (long long)a.B * a.Np * a.Hq, step = (long long)gridDim.x * (kThreads / G);
+  if (blockIdx.x == 0 && threadIdx.x < 64) a.sched[threadIdx.x] = 0u;
+  bool bad = false;
+  // the warp's rows end together: its lanes meet in the sums
+  const long long first = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / G;
+  for (long long base = first - (threadIdx.x % 32) / G; base < rows; base += step) {
+    const long long i = base + (threadIdx.x % 32) / G;
+    const int h = (int)(i % a.Hq);
+    const long long bn = i / a.Hq;
+    const int b = (int)(bn / a.Np), n = (int)(bn - (long long)b * a.Np);
+    const bool there = i < rows && n < a.Nq;
+    float dot = 0.f;
+    if (there) {
+      const long long src = lay_at(a.ql, b, n, h) + 8 * lane;
+      const long long row = (((long long)b * a.Nq + n) * a.Hq + h) * a.d + 8 * lane;
+      float f[8], g[8];
+      get8(a.dO, in_dtype, src, f);
+      get8(a.o, a.o_dtype, src, g);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dot = fmaf(f[j], g[j], dot);
+      if (a.do16) {
+        bad |= past_fp16(f);
+        put8(a.do16, RA_F16, row, f);
+        get8(a.q, in_dtype, src, g);
+        bad |= past_fp16(g);
+        put8(a.q16, RA_F16, row, g);
+      }
+      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      put8(a.dq_acc, RA_F32, row, zero);
+    }
+    for (int o = G >> 1; o; o >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, o);
+    if (lane == 0 && i < rows) {
+      const long long at = ((long long)b * a.Hq + h) * a.Np + n;
+      const float lse = there ? a.lse[((long long)b * a.Hq + h) * a.Nq + n] : -INFINITY;
+      const bool seen = lse != -INFINITY;
+      a.D[at] = seen ? -dot : 0.f;
+      a.lse2[at] = seen ? -(lse * kLog2e) : -INFINITY;  // P = 0
+    }
+  }
+  if (bad) report(a.status, RA_ERR_RANGE);
+}
+
+__global__ void __launch_bounds__(kThreads) cross_sum_kernel(const float* parts, int splits, int B, int Nkv, int Hkv, int d,
+                                                             void* dk, void* dv, int dtype, Lay kvl) {
+  const int per_row = Hkv * d / 8;
+  const long long plane = (long long)B * Nkv * Hkv * d, total = plane / 8;
+  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < 2 * total; i += (long long)gridDim.x * kThreads) {
+    const int which = i >= total;
+    const long long t = i - which * total, bn = t / per_row;
+    const int e = (int)(t - bn * per_row) * 8, g = e / d, b = (int)(bn / Nkv), n = (int)(bn - (long long)b * Nkv);
+    float f[8], x[8];
+    const float* src = parts + (long long)which * splits * plane + t * 8;
+    get8(src, RA_F32, 0, f);
+    for (int s = 1; s < splits; ++s) {
+      get8(src, RA_F32, s * plane, x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] += x[j];
+    }
+    put8(which ? dv : dk, dtype, lay_at(kvl, b, n, g) + (e - g * d), f);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) cross_dq_kernel(const float* acc, float mul, int B, int Nq, int Hq, int d, void* dq,
+                                                            int dtype, Lay ql) {
+  const int per_row = Hq * d / 8;
+  const long long total = (long long)B * Nq * per_row;
+  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < total; t += (long long)gridDim.x * kThreads) {
+    const long long bn = t / per_row;
+    const int e = (int)(t - bn * per_row) * 8, h = e / d, b = (int)(bn / Nq), n = (int)(bn - (long long)b * Nq);
+    float f[8];
+    get8(acc, RA_F32, t * 8, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] *= mul;
+    put8(dq, dtype, lay_at(ql, b, n, h) + (e - h * d), f);
+  }
+}
+
+unsigned blocks_for(long long threads) {
+  const long long b = (threads + kThreads - 1) / kThreads;
+  return (unsigned)(b < 1 ? 1 : b > 152 * 16 ? 152 * 16 : b);
+}
+
+}  // namespace
+
+cudaError_t launch_cross_join(const CrossState& part, int splits, int B, int Nq, int Hq, int d, void* o, int o_dtype,
+                              Lay ol, float* lse, cudaStream_t st) {
+  const long long blocks = ((long long)B * Nq * Hq * 32 + kThreads - 1) / kThreads;
+  const cudaError_t e = launch_pdl(cross_join_kernel, (int)blocks, kThreads, 0, st, part, splits, B, Nq, Hq, d, o, o_dtype, ol, lse);
+  if (e == cudaSuccess) count_launch();
+  return e;
+}
+
+cudaError_t launch_cross_keys(const void* k, const void* v, int bf16, Lay kvl, void* k16, void* v16, int B, int Nkv,
+                              int Hkv, int d, const int* kv_len, int* status, cudaStream_t st) {
+  cross_keys_kernel<<<blocks_for((long long)B * Nkv * Hkv * d / 8), kThreads, 0, st>>>(
+      k, v, bf16 ? RA_BF16 : RA_F16, kvl, static_cast<__half*>(k16), static_cast<__half*>(v16), B, Nkv, Hkv, d, kv_len, status);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cross_rows(const CrossRowsArgs& a, cudaStream_t st) {
+  cross_rows_kernel<<<blocks_for((long long)a.B * a.Np * a.Hq * a.d / 8), kThreads, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
+                             Lay kvl, cudaStream_t st) {
+  cross_sum_kernel<<<blocks_for((long long)B * Nkv * Hkv * d / 4), kThreads, 0, st>>>(parts, splits, B, Nkv, Hkv, d, dk, dv,
+                                                                                      dtype, kvl);
+  count_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_cross_dq(const float* dq_acc, float mul, int B, int Nq, int Hq, int d, void* dq, int dtype, Lay ql,
+                            cudaStream_t st) {
+  cross_dq_kernel<<<blocks_for((long long)B * Nq * Hq * d / 8), kThreads, 0, st>>>(dq_acc, mul, B, Nq, Hq, d, dq, dtype, ql);
+  count_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace ra

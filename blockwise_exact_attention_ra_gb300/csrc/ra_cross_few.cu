@@ -1,0 +1,334 @@
+// Cross attention of a few queries (single tokens, drafted ones) against many keys: bound
+// by reading K and V once.
+//
+// A block takes one key/value head of one batch entry and one part of its keys; the query
+// rows of the heads that share it (Nq Hq / Hkv <= 32) are the rows of m16n8k16 products, so
+// that K and V are read once for all of them.  Its four warps take blocks of 16 keys in
+// turn, each through a ring of its own in shared memory that cp.async fills (rows past the
+// length with zeros: 0 x NaN would not be 0), and keep their own online-softmax state;
+// nothing is waited for but a warp's own copies until the four states are joined at the end.
+//
+// Products are fp32 sums of the inputs as they are; P enters the second as two terms of
+// their type, hi and P - hi (rounding 2^-17 relative for bf16, 2^-23 for fp16: the tensor
+// cores have time for it).  The running maximum is raised lazily, as in ra_fwd_tc.cu.
+#include <math.h>
+
+#include <type_traits>
+
+#include "ra_device.cuh"
+
+namespace ra {
+namespace {
+
+constexpr int kWarps = 4, kThreads = 32 * kWarps, kKeys = 16, kStages = 3;
+constexpr float kRescaleThreshold = 8.0f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct FewSmem {
+  static constexpr int kTile = kKeys * D * 2;          // K or V of 16 keys
+  static constexpr int kWarp = kStages * 2 * kTile;
+  static constexpr int kBytes = kWarps * kWarp;
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t a) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(a)
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// x, y as a pair of T, and what that rounding takes from them as another
+template <typename T>
+__device__ __forceinline__ void two_terms(float x, float y, uint32_t* hi, uint32_t* lo) {
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(x - __low2float(h), y - __high2float(h));
+    *hi = *reinterpret_cast<const uint32_t*>(&h);
+    *lo = *reinterpret_cast<const uint32_t*>(&l);
+  } else {
+    *hi = pack_half2(x, y);
+    const float2 h = unpack_half2(*hi);
+    *lo = pack_half2(x - h.x, y - h.y);
+  }
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_constant__ CrossFewArgs a) {
+  using L = FewSmem<D>;
+  constexpr int kChunks = D / 8, kRows = 32 / kChunks;  // 16-byte pieces of a row; rows a warp copies at a time
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 states[kWarps][16 * MT];
+  pdl_trigger();
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = a.Hq / a.Hkv, rows = a.Nq * group;
+  const int unit = blockIdx.x / a.splits, split = blockIdx.x - unit * a.splits;
+  const int b = unit / a.Hkv, g = unit - b * a.Hkv;
+  int len = a.Nkv;
+  if (a.kv_len) {
+    const int v = __ldg(a.kv_len + b);
+    len = v < 0 ? 0 : v > a.Nkv ? a.Nkv : v;
+  }
+  const int blocks = (len + kKeys - 1) / kKeys, per = (blocks + a.splits - 1) / a.splits;
+  const int first = split * per, last = min(blocks, first + per);
+  const int count = last > first + warp ? (last - first - warp + kWarps - 1) / kWarps : 0;  // of this warp
+  const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+  const T* kbase = static_cast<const T*>(a.k) + lay_at(a.kvl, b, 0, g);
+  const T* vbase = static_cast<const T*>(a.v) + lay_at(a.kvl, b, 0, g);
+  const int cc = lane % kChunks, cr = lane / kChunks;
+  auto load = [&](int i) {  // the warp's block i
+    if (i < count) {
+      const int key0 = (first + warp + i * kWarps) * kKeys;
+      const uint32_t dst = ring + (i % kStages) * 2 * L::kTile;
+#pragma unroll
+      for (int j = 0; j < kKeys / kRows; ++j) {
+        const int r = j * kRows + cr, key = key0 + r;
+        const bool there = key < len;
+        const long long at = (long long)(there ? key : 0) * a.kvl.rs + cc * 8;
+        const uint32_t to = dst + r * (D * 2) + ((cc ^ (r & 7)) << 4);
+        copy16(to, kbase + at, there);
+        copy16(to + L::kTile, vbase + at, there);
+      }
+    }
+    copy_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) load(i);
+
+  // query rows: row r is query r / group of head g group + r % group
+  uint32_t qf[MT][D / 16][4];
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int r = t * 16 + half * 8 + (lane >> 2);
+      const int n = r / group, h = g * group + r - n * group;
+      const T* src = static_cast<const T*>(a.q) + (r < rows ? lay_at(a.ql, b, n, h) : 0) + 2 * (lane & 3);
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        qf[t][k][half] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k) : 0u;
+        qf[t][k][2 + half] = r < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * k + 8) : 0u;
+      }
+    }
+  float o[MT][D / 8][4], m[MT][2], l[MT][2];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    m[t][0] = m[t][1] = -INFINITY;
+    l[t][0] = l[t][1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.f;
+  }
+  const float sl2 = a.scale_log2;
+  const int mat = lane >> 3, mr = lane & 7;
+  for (int i = 0; i < count; ++i) {
+    copy_wait<kStages - 2>();
+    __syncwarp();
+    load(i + kStages - 1);  // into the place that the last turn read
+    const uint32_t kt = ring + (i % kStages) * 2 * L::kTile, vt = kt + L::kTile;
+    float s[MT][2][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[t][j][0] = s[t][j][1] = s[t][j][2] = s[t][j][3] = 0.f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      uint32_t f[4];
+      const int key = (mat >> 1) * 8 + mr, chunk = 2 * k + (mat & 1);
+      ldsm4(f, kt + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        mma16816<T>(s[t][0], qf[t][k], f[0], f[1]);
+        mma16816<T>(s[t][1], qf[t][k], f[2], f[3]);
+      }
+    }
+    const int left = len - (first + warp + i * kWarps) * kKeys;
+    if (left < kKeys) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (j * 8 + 2 * (lane & 3) + (c & 1) >= left) s[t][j][c] = -INFINITY;
+    }
+    uint32_t hi[MT][4], lo[MT][4];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      float alpha[2];
+      bool raise = false;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        float mx = fmaxf(fmaxf(s[t][0][2 * half], s[t][0][2 * half + 1]), fmaxf(s[t][1][2 * half], s[t][1][2 * half + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * sl2;
+        const bool up = mx > m[t][half] + kRescaleThreshold;  // also from -inf
+        alpha[half] = up ? ex2_approx(m[t][half] - mx) : 1.f;
+        if (up) m[t][half] = mx;
+        raise |= up;
+      }
+      if (__any_sync(0xffffffffu, raise)) {
+        l[t][0] *= alpha[0];
+        l[t][1] *= alpha[1];
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) {
+          o[t][j][0] *= alpha[0];
+          o[t][j][1] *= alpha[0];
+          o[t][j][2] *= alpha[1];
+          o[t][j][3] *= alpha[1];
+        }
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const float neg = m[t][half] == -INFINITY ? 0.f : -m[t][half];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float x = ex2_approx(fmaf(s[t][j][2 * half], sl2, neg));
+          const float y = ex2_approx(fmaf(s[t][j][2 * half + 1], sl2, neg));
+          l[t][half] += x + y;
+          two_terms<T>(x, y, &hi[t][2 * j + half], &lo[t][2 * j + half]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+      uint32_t f[4];
+      const int key = (mat & 1) * 8 + mr, chunk = 2 * j + (mat >> 1);
+      ldsm4t(f, vt + key * (D * 2) + ((chunk ^ (key & 7)) << 4));
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        mma16816<T>(o[t][2 * j], hi[t], f[0], f[1]);
+        mma16816<T>(o[t][2 * j + 1], hi[t], f[2], f[3]);
+        mma16816<T>(o[t][2 * j], lo[t], f[0], f[1]);
+        mma16816<T>(o[t][2 * j + 1], lo[t], f[2], f[3]);
+      }
+    }
+    __syncwarp();
+  }
+  copy_wait<0>();
+  // the warps' states, joined: each leaves (m, l) and O in its own ring
+  float* mine = reinterpret_cast<float*>(smem + warp * L::kWarp);
+  static_assert(16 * MT * D * 4 <= L::kWarp, "a warp's O fits its ring");
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      float sum = l[t][half];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      const int r = t * 16 + half * 8 + (lane >> 2);
+      if ((lane & 3) == 0) states[warp][r] = make_float2(m[t][half], sum);
+    }
+  __syncwarp();
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int r = t * 16 + half * 8 + (lane >> 2);
+        *reinterpret_cast<float2*>(mine + r * D + 8 * j + 2 * (lane & 3)) =
+            make_float2(o[t][j][2 * half], o[t][j][2 * half + 1]);
+      }
+  __syncthreads();
+  for (int i = threadIdx.x; i < rows * kChunks; i += kThreads) {
+    const int r = i / kChunks, c = (i - r * kChunks) * 8, n = r / group, h = g * group + r - n * group;
+    float top = -INFINITY, sum = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, states[w][r].x);
+    const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float2 st = states[w][r];
+      const float weight = ex2_approx(st.x - ref);
+      sum += weight * st.y;
+      const float* src = reinterpret_cast<const float*>(smem + w * L::kWarp) + r * D + c;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[j] = fmaf(weight, src[j], acc[j]);
+    }
+    const long long at = ((long long)(split * a.B + b) * a.Hq + h) * a.Nq + n;
+    if (a.splits > 1) {
+      float* out = a.part.o + (((long long)(split * a.B + b) * a.Nq + n) * a.Hq + h) * D + c;
+      reinterpret_cast<float4*>(out)[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      reinterpret_cast<float4*>(out)[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+      if (c == 0) {
+        a.part.m[at] = top == -INFINITY ? top : top * kLn2;
+        a.part.l[at] = sum;
+      }
+      continue;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const long long out = lay_at(a.ol, b, n, h) + c;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] *= inv;
+    if (a.o_dtype == RA_F32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.o) + out);
+      p[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+      p[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    } else {
+      uint32_t p[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (a.o_dtype == RA_BF16) {
+          const __nv_bfloat162 v = __floats2bfloat162_rn(acc[2 * j], acc[2 * j + 1]);
+          p[j] = *reinterpret_cast<const uint32_t*>(&v);
+        } else {
+          p[j] = pack_half2(acc[2 * j], acc[2 * j + 1]);
+        }
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + out) = make_uint4(p[0], p[1], p[2], p[3]);
+    }
+    if (c == 0) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_cross_few(const CrossFewArgs& a, cudaStream_t st) {
+  const int rows = a.Nq * (a.Hq / a.Hkv);
+  if (rows > kCrossFewRows) return cudaErrorInvalidValue;
+  auto run = [&](auto kernel, int smem) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(kernel, a.B * a.Hkv * a.splits, kThreads, smem, st, a);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  };
+  auto typed = [&](auto t) {
+    using T = decltype(t);
+    if (a.d == 128)
+      return rows <= 16 ? run(cross_few_kernel<T, 128, 1>, FewSmem<128>::kBytes)
+                        : run(cross_few_kernel<T, 128, 2>, FewSmem<128>::kBytes);
+    if (a.d == 64)
+      return rows <= 16 ? run(cross_few_kernel<T, 64, 1>, FewSmem<64>::kBytes)
+                        : run(cross_few_kernel<T, 64, 2>, FewSmem<64>::kBytes);
+    return cudaErrorInvalidValue;
+  };
+  return a.bf16 ? typed(__nv_bfloat16{}) : typed(__half{});
+}
+
+}  // namespace ra

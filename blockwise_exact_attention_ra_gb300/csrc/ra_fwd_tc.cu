@@ -37,6 +37,16 @@
 // the rounding of P from 2^-12 relative to about 2^-24.  The running
 // maximum is updated lazily: O and l are rescaled only when the maximum
 // grows by more than 8 (log2 units), so P <= 2^8, well inside fp16.
+//
+// CROSS: queries against keys of another length, without a mask but for the
+// keys' lengths per batch entry, units (head, part of the keys, query tiles):
+// few query tiles leave SMs idle unless the keys are split, whose partial
+// states are joined by a kernel of its own (ra_cross.cu).  A unit visits its
+// tiles from the last to the first.  V's rows past a length that ends inside
+// a tile are set to zero in shared memory, since 0 x NaN is not 0; K's need
+// nothing, their scores are replaced.  With BF16P the two terms of P are bf16
+// and V is taken as it is, without the fp16 copy of it that few queries would
+// not repay (rounding of P 2^-17 relative).
 #include <math.h>
 
 #include <type_traits>
@@ -72,6 +82,7 @@ struct FwdSmem {
 
 struct UnitInfo {
   int b, h, g;
+  int split, nkv;  // cross attention: part of the keys, keys there are
   int qa_row0;    // tensor row of tile A (tile B = qa_row0 + 128)
   int has_b;
   int n_iter;     // key/value tiles visited
@@ -161,10 +172,33 @@ __device__ __forceinline__ int last_visible_tile(const TcFwdArgs& a, long long q
 // lightest units end the launch.
 // VARLEN selects the kernel built for variable host lengths; the other
 // builds see no length array and compile its checks away.
-template <bool VARLEN, bool STRIPED>
+template <bool VARLEN, bool STRIPED, bool CROSS>
 __device__ __forceinline__ UnitInfo unit_info(const TcFwdArgs& a, int u) {
   UnitInfo r;
   int per_head;
+  if (CROSS) {
+    const int pairs = ((a.Nq + 127) / 128 + 1) / 2;
+    per_head = pairs * a.splits;
+    const int bh = u / per_head, rest = u - bh * per_head;
+    r.b = bh / a.Hq;
+    r.h = bh - r.b * a.Hq;
+    r.g = r.h / (a.Hq / a.Hkv);
+    r.split = rest / pairs;
+    r.qa_row0 = (rest - r.split * pairs) * 256;
+    r.has_b = r.qa_row0 + 128 < a.Nq;
+    r.qpos0[0] = r.qpos0[1] = 0;
+    r.nkv = a.Nkv;
+    if (a.kv_len) r.nkv = host_len_at(a.kv_len, r.b, a.Nkv);
+    r.nkt = (r.nkv + 127) / 128;
+    const int per = (r.nkt + a.splits - 1) / a.splits, first = r.split * per;
+    const int last = first + per < r.nkt ? first + per : r.nkt;
+    r.n_iter = last > first ? last - first : 0;
+    r.kt0 = last - 1;
+    r.wrap = r.striped = 0;
+    r.start[0] = 0;
+    r.start[1] = r.has_b ? 0 : r.n_iter;
+    return r;
+  }
   if (a.ring_P > 0) {
     const int T = a.ring_S / 128;
     per_head = a.ring_P * ((T + 1) / 2);
@@ -270,7 +304,7 @@ __device__ __forceinline__ UnitInfo unit_info(const TcFwdArgs& a, int u) {
   return r;
 }
 
-template <int D, bool PRECISE, bool VARLEN, bool STRIPED>
+template <int D, bool PRECISE, bool VARLEN, bool STRIPED, bool CROSS = false, bool BF16P = false>
 __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_constant__ TcFwdArgs a) {
   using L = FwdSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -363,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
         unit_ring[slot] = u;
         mbar_arrive(bar_unit_full(slot));
         if (u >= a.num_units) break;
-        const UnitInfo ui = unit_info<VARLEN, STRIPED>(a, u);
+        const UnitInfo ui = unit_info<VARLEN, STRIPED, CROSS>(a, u);
         if (ui.n_iter == 0) continue;  // no key of this block is visible to the unit
         if (!mbar_wait(BAR_Q_EMPTY, (k & 1) ^ 1, abort_flag, a.status, lim)) { ok = false; break; }
         ++k;
@@ -411,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc_qk = idesc_f16(a.qk_bf16 ? 1u : 0u, 0, 0, 128, 128);
-      const uint32_t idesc_pv = idesc_f16(0, 0, 1, 128, D);
+      const uint32_t idesc_pv = idesc_f16(BF16P ? 1u : 0u, 0, 1, 128, D);
       const uint32_t tS[2] = {tmem + 0u, tmem + 128u};
       const uint32_t tO[2] = {tmem + 256u, tmem + 256u + (uint32_t)D};
       uint32_t L_cnt = 0;
@@ -446,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       for (int n = 0; ok; ++n) {
         int u;
         if (!take_unit(n, &u) || u >= a.num_units) break;
-        const UnitInfo ui = unit_info<VARLEN, STRIPED>(a, u);
+        const UnitInfo ui = unit_info<VARLEN, STRIPED, CROSS>(a, u);
         if (ui.n_iter == 0) continue;
         if (!mbar_wait(BAR_Q_FULL, k & 1, abort_flag, a.status, lim)) { ok = false; break; }
         ++k;
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           if (active(ui, x, it0)) issue_s(x, sk);
         mma_commit(bar_kv_empty(sk));
         ++L_cnt;
-        bool first_pv[2] = {a.mode == 0, a.mode == 0};
+        bool first_pv[2] = {a.mode != 1, a.mode != 1};
         // A unit takes an even number of K/V loads (its first K, then V(it)
         // and K(it+1) per iteration, V alone at the last), so V(it) sits in
         // stage 1 or 3 and K(it+1) in the stage after it, alternating from one
@@ -521,11 +555,29 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
     const uint32_t tO = tmem + 256u + (x == 0 ? 0u : (uint32_t)D) + lane_off;
     const float sl2 = a.scale_log2;
     uint32_t s_cnt = 0, o_cnt = 0;
+    uint32_t kv_loads = 0;  // CROSS: K/V loads of the units before
     bool ok = true;
     for (int n = 0; ok; ++n) {
       int u;
       if (!take_unit(n, &u) || u >= a.num_units) break;
-      const UnitInfo ui = unit_info<VARLEN, STRIPED>(a, u);
+      const UnitInfo ui = unit_info<VARLEN, STRIPED, CROSS>(a, u);
+      if (CROSS && ui.n_iter == 0) {  // no key: nothing seen
+        const int row = ui.qa_row0 + x * 128 + r;
+        if (row < a.Nq) {
+          const long long at = ((long long)(ui.split * a.B + ui.b) * a.Hq + ui.h) * a.Nq + row;
+          if (a.mode == 0) {
+            a.lse[at] = -INFINITY;
+            const long long out = lay_at(a.ol, ui.b, row, ui.h);
+            const int step = a.o_dtype == RA_F32 ? 4 : 8;
+            for (int c = 0; c < D; c += step)
+              *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.o_out) + (out + c) * (16 / step)) = make_uint4(0u, 0u, 0u, 0u);
+          } else {
+            a.m_acc[at] = -INFINITY;
+            a.l_acc[at] = 0.f;
+          }
+        }
+        continue;
+      }
       if ((VARLEN && ui.n_iter == 0) || !ever_active(ui, x)) continue;  // this tile sees no key in this unit
       const int row = ui.qa_row0 + x * 128 + r;  // tensor row
       // with variable host lengths, rows past their host's valid length are padding
@@ -533,8 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       const long long qpos = ui.qpos0[x] + r;
       float m_run = -INFINITY, l_run = 0.f;
       // row offsets of the state (m, l: [B, Hq, N]; o: [B, N, Hq, D]), formed where used
-      auto sidx = [&]() { return ((long long)ui.b * a.Hq + ui.h) * a.Nq + row; };
-      auto oidx = [&]() { return (((long long)ui.b * a.Nq + row) * a.Hq + ui.h) * D; };
+      auto sidx = [&]() { return ((long long)(CROSS ? ui.split * a.B + ui.b : ui.b) * a.Hq + ui.h) * a.Nq + row; };
+      auto oidx = [&]() { return (((long long)(CROSS ? ui.split * a.B + ui.b : ui.b) * a.Nq + row) * a.Hq + ui.h) * D; };
       if (a.mode == 1) {
         // load the running state into registers and TMEM
         if (row_ok) {
@@ -584,12 +636,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           need_mask = tk == ui.tq[x];
           lim_c = r - (blk > ui.host ? 1 : 0);
         } else {
-          need_mask = (a.causal && kvpos0 + 127 > ui.qpos0[x]) || (kt * 128 + 128 > a.Nkv);
-          lim_c = a.causal ? qpos - kvpos0 : 127;
+          need_mask = CROSS ? kt * 128 + 128 > ui.nkv : (a.causal && kvpos0 + 127 > ui.qpos0[x]) || (kt * 128 + 128 > a.Nkv);
+          lim_c = !CROSS && a.causal ? qpos - kvpos0 : 127;
         }
         if (VARLEN && kv_len < 128) need_mask = true;  // keys past the host's valid length
         if (need_mask) {
-          const int nvalid = VARLEN ? min(a.Nkv - kt * 128, kv_len) : a.Nkv - kt * 128;
+          const int nvalid = CROSS ? ui.nkv - kt * 128 : VARLEN ? min(a.Nkv - kt * 128, kv_len) : a.Nkv - kt * 128;
 #pragma unroll
           for (int c = 0; c < 128; ++c)
             if (c > lim_c || c >= nvalid) sr[c] = __float_as_uint(-INFINITY);
@@ -627,10 +679,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
                                         sl2x2, nm2);
             const float p0 = ex2_approx(e.x), p1 = ex2_approx(e.y);
             rs2[(j / 2) & 1] = __fadd2_rn(rs2[(j / 2) & 1], make_float2(p0, p1));
-            pk[j / 2] = pack_half2(p0, p1);
-            if (PRECISE) {
-              const float2 hi = unpack_half2(pk[j / 2]);
-              pl[j / 2] = pack_half2(p0 - hi.x, p1 - hi.y);
+            if (BF16P) {
+              const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+              const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - __low2float(hi), p1 - __high2float(hi));
+              pk[j / 2] = *reinterpret_cast<const uint32_t*>(&hi);
+              pl[j / 2] = *reinterpret_cast<const uint32_t*>(&lo);
+            } else {
+              pk[j / 2] = pack_half2(p0, p1);
+              if (PRECISE) {
+                const float2 hi = unpack_half2(pk[j / 2]);
+                pl[j / 2] = pack_half2(p0 - hi.x, p1 - hi.y);
+              }
             }
           }
           RA_TMEM_ST16(tS + c / 2, pk);
@@ -651,11 +710,27 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
           }
         }
         o_valid = true;
+        if (CROSS && x == 0 && need_mask && ui.nkv < a.Nkv) {
+          // the unit's first tile: V's rows past the length, before either product that
+          // reads them (tile A's comes first and waits for this warpgroup)
+          const uint32_t load = kv_loads + 1;
+          if (!mbar_wait(bar_kv_full(load % kStages), (load / kStages) & 1, abort_flag, a.status, lim)) { ok = false; break; }
+          if (kt * 128 + r >= ui.nkv) {
+            uint8_t* v = smem + L::kStage0 + (load % kStages) * L::kTileBytes + r * 128;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) *reinterpret_cast<uint4*>(v + c * 16384 + j * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+          }
+          fence_proxy_async_smem();
+        }
         tmem_st_wait();
         tc_fence_before();
         mbar_arrive(bar_p_full(x));
       }
       if (!ok) break;
+      if (CROSS) kv_loads += 2 * ui.n_iter;
       if (!mbar_wait(bar_o_full(x), o_cnt & 1, abort_flag, a.status, lim)) { ok = false; break; }
       ++o_cnt;
       tc_fence_after();
@@ -742,6 +817,10 @@ cudaError_t launch_tc_fwd(TcFwdArgs& a, int num_sms, cudaStream_t st) {
     constexpr int DD = decltype(d_c)::value;
     constexpr int smem = FwdSmem<DD>::kAlloc;
     const bool striped = a.ring_P > 0 && a.striped;
+    if (a.cross)
+      return a.bf16_p    ? run(tc_fwd_kernel<DD, true, false, false, true, true>, smem)
+             : a.precise ? run(tc_fwd_kernel<DD, true, false, false, true>, smem)
+                         : run(tc_fwd_kernel<DD, false, false, false, true>, smem);
     if (a.host_len)
       return a.precise ? run(tc_fwd_kernel<DD, true, true, false>, smem) : run(tc_fwd_kernel<DD, false, true, false>, smem);
     if (striped)

@@ -138,7 +138,11 @@ struct TcFwdArgs {
   int striped;         // ring mode, causal: rows are in striped order (position l*P + host)
   const int* host_len; // ring mode, optional: valid rows per host (device, P entries)
   // outputs
-  int mode;         // 0: ring (finalise), 1: block (read/write state)
+  // cross attention: queries against keys of another length (ring_P 0, causal 0)
+  int cross, splits;   // parts of the keys
+  int bf16_p;          // P as two bf16 terms, v in bf16
+  const int* kv_len;   // optional: keys per batch entry (device)
+  int mode;         // 0: finalise, 1: block (read/write state), 2: cross: write the parts' states
   float* o_acc;     // block mode: [B, Nq, Hq, d] fp32
   float* m_acc;     // [B, Hq, Nq] (natural-log units)
   float* l_acc;
@@ -170,6 +174,11 @@ struct TcBwdArgs {
   unsigned long long P_m;  // div_magic(ring_P)
   int striped;  // causal, rows in striped order (position l*P + host)
   const int* host_len;  // optional: valid rows per host (device, P entries)
+  // cross attention: N query rows, Nkv key rows, lse and Dvec with rows of Np (a multiple
+  // of 128, -inf and 0 from N on); units (head, part of the query tiles, key tile)
+  int cross, Nkv, Np, q_splits;
+  const int* kv_len;    // optional: keys per batch entry (device)
+  float* parts;         // q_splits > 1: dK then dV [q_splits][B, Nkv, Hkv, d]
   const float* lse;   // [B, Hq, N]: -LSE * log2(e)
   const float* Dvec;  // [B, Hq, N]: -D
   float* dq_acc;      // packed fp32 [B, N, Hq, d], pre-zeroed, reduce-added
@@ -184,6 +193,54 @@ struct TcBwdArgs {
   VisitLog log;     // debug record of the query tiles loaded (off when log.entries is NULL)
 };
 cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st);
+
+// -------------------------------------------- cross attention
+// A few queries (Nq * Hq / Hkv <= kCrossFewRows) on warp-level products: bound by reading
+// K and V.  Results, or with splits > 1 the parts' states.
+struct CrossState {   // [splits][B, Nq, Hq, d], [splits][B, Hq, Nq] (natural-log units)
+  float *o, *m, *l;
+};
+constexpr int kCrossFewRows = 32;
+struct CrossFewArgs {
+  const void *q, *k, *v;
+  int bf16, B, Nq, Nkv, Hq, Hkv, d;
+  Lay ql, kvl, ol;
+  float scale_log2;
+  const int* kv_len;
+  int splits;
+  CrossState part;
+  void* o;
+  int o_dtype;
+  float* lse;
+};
+cudaError_t launch_cross_few(const CrossFewArgs& a, cudaStream_t st);
+// o, lse <- the parts' states joined
+cudaError_t launch_cross_join(const CrossState& part, int splits, int B, int Nq, int Hq, int d, void* o, int o_dtype,
+                              Lay ol, float* lse, cudaStream_t st);
+// dst (packed fp16) <- src (16-bit) of one or two key-side tensors, rows from kv_len[b] on
+// zero; values beyond the fp16 range set RA_ERR_RANGE in *status
+cudaError_t launch_cross_keys(const void* k, const void* v, int bf16, Lay kvl, void* k16, void* v16, int B, int Nkv,
+                              int Hkv, int d, const int* kv_len, int* status, cudaStream_t st);
+// what the backward kernel needs of the query side: lse2 = -lse log2(e), D = -dO . O (rows
+// of Np; -inf and 0 where there is no row or it saw no key), fp16 copies of q and dO (bf16
+// inputs), and dq_acc = 0
+struct CrossRowsArgs {
+  const void *q, *dO, *o;
+  const float* lse;
+  int bf16, o_dtype, B, Nq, Np, Hq, d;
+  Lay ql;
+  void *q16, *do16;  // NULL for fp16 inputs
+  float *D, *lse2, *dq_acc;
+  unsigned int* sched;
+  int* status;
+};
+cudaError_t launch_cross_rows(const CrossRowsArgs& a, cudaStream_t st);
+// dk, dv <- sums of the parts' planes
+cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
+                             Lay kvl, cudaStream_t st);
+// out (dtype, layout) <- mul x (packed fp32)
+cudaError_t launch_cross_dq(const float* dq_acc, float mul, int B, int Nq, int Hq, int d, void* dq, int dtype, Lay ql,
+                            cudaStream_t st);
 
 // Counts kernel launches (ra_launch_count).
 void count_launch(unsigned n = 1);

@@ -429,6 +429,39 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
                      float eps, void* out, ra_dtype out_dtype, long long out_bstride,
                      long long out_rstride, void* workspace, size_t ws_bytes, void* stream);
 
+/* Attention of queries to the keys and values of another sequence of any length (cross
+ * attention to an encoder's states):
+ *     s_ij = scale q_i . k_j,   P = softmax over j < kv_len[b],   o = P v,
+ *     lse_i = ln sum_j e^{s_ij}.
+ *   q, o [B, N_q, Hq, d], k, v [B, N_kv, Hkv, d], any N_q, N_kv >= 1, in `dtype` (RA_BF16 or
+ *   RA_F16), d 64 or 128; o in o_dtype, lse [B, Hq, N_q] fp32.  Strides as in ra_shape.
+ *   kv_len  device array of B int32 (clamped to [0, N_kv]), or NULL: every key is there.
+ *     Keys and values from kv_len[b] on may hold anything (infinities and NaN too).  A batch
+ *     entry without keys has o = 0, lse = -inf.
+ *   flags   RA_PRECISE.
+ *   A few queries (N_q Hq / Hkv <= 32; single tokens) run on a kernel bound by reading k
+ *   and v once; where there are few query tiles the keys are split over the SMs and the parts
+ *   joined.  P is rounded to fp16 (two terms with RA_PRECISE) against v in fp16 (bf16 v
+ *   copied, with RA_ERR_RANGE, as for the ring), or enters as two terms of the inputs' type (a few
+ *   queries, and bf16 where the copy would take longer than the products).
+ *   workspace: device memory, 256-byte aligned, ra_cross_fwd_workspace_bytes() bytes.  It
+ *   must not be in use by work that overlaps the call on the GPU.  o overlaps no input. */
+size_t ra_cross_fwd_workspace_bytes(ra_dtype dtype, ra_shape shape, int flags);
+int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra_shape shape,
+                 const int* kv_len, int flags, float scale, void* o, ra_dtype o_dtype, float* lse,
+                 void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradients of L = sum(o * dO): dq [B, N_q, Hq, d], dk, dv [B, N_kv, Hkv, d] in grad_dtype,
+ * fully overwritten (rows from kv_len[b] on with zeros), by the formulas of ra_ring_bwd; o in
+ * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  Operands are
+ * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  dq is summed over the key
+ * tiles in fp32 in an order that varies; dk and dv do not vary from run to run. */
+size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape);
+int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype,
+                 const void* dO, const float* lse, ra_dtype dtype, ra_shape shape,
+                 const int* kv_len, int flags, float scale, void* dq, void* dk, void* dv,
+                 ra_dtype grad_dtype, void* workspace, size_t ws_bytes, void* stream);
+
 /* Rotary positions.  Row (b, n, h) of q and of k at position p has its first `rot` columns
  * turned in pairs, pair i by the angle p freq[i]:
  *     (x, y) -> amplitude (x cos - y sin, x sin + y cos),
