@@ -24,6 +24,7 @@ belongs to the stream they are given.
 import ctypes
 import os
 import threading
+from array import array
 
 import torch
 
@@ -655,16 +656,37 @@ def newton_schulz(g, steps=5, coeffs=_NS_COEFFS, eps=1e-7, out_dtype=None, strea
 
 
 # ------------------------------------------------ cross attention
+# Host time bounds small calls of these operators (a single token): shapes of contiguous tensors
+# take no strides, and the wrappers check what they are given but not what they allocate.
+def _device_index(ref, *tensors):
+    """The index of the device that ref and the tensors (None: left out) lie on, the current one."""
+    i = ref.get_device()
+    if i < 0 or i != torch.cuda.current_device():
+        raise RAError(1, f"tensors must be on the current CUDA device (got {ref.device})")
+    for t in tensors:
+        if t is not None and t.get_device() != i:
+            raise RAError(1, f"tensors must be on one device (got {t.device} and {ref.device})")
+    return i
+
+
+def _stream_handle(stream, index):
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(index) if _raw_stream else torch.cuda.current_stream().cuda_stream
+
+
 def _strides_of(t, name):
     """Batch, row and head strides of a [B, N, H, d] tensor; 0 (the library's packed default)
     for an axis of extent 1, whose stride is arbitrary."""
     s, n = t.stride(), t.shape
     if len(s) != 4:
         raise RAError(1, f"{name} must be [B, N, H, d]")
+    if t.numel() > _INT_MAX:
+        _fits(*n)
+    if t.is_contiguous():
+        return 0, 0, 0
     if s[3] != 1 and n[3] > 1:
         raise RAError(1, f"{name} must have a contiguous last (head) dimension (strides {s})")
-    if max(n) > _INT_MAX:
-        _fits(*n)
     out = []
     for i in range(3):
         if n[i] == 1:
@@ -676,24 +698,31 @@ def _strides_of(t, name):
     return out
 
 
-def _cross_shape(q, k, v, kv_len, **others):
-    """RaShape; `others` maps a name to (tensor, "q" or "k"): of that tensor's shape and strides."""
-    qs, ks = _strides_of(q, "q"), _strides_of(k, "k")
+def _data(t):
+    return None if t is None else t.data_ptr()
+
+
+def _cross_shape(q, k, v, kv_len):
+    """RaShape of queries and of keys and values."""
+    qb, qr, qh = _strides_of(q, "q")
+    ks = _strides_of(k, "k")
     B, Nq, Hq, d = q.shape
     kB, Nkv, Hkv, kd = k.shape
-    if kB != B or kd != d or k.dtype != q.dtype:
-        raise RAError(1, f"q and k must have the same batch, head dimension and dtype (got {list(q.shape)} {q.dtype}, "
-                         f"{list(k.shape)} {k.dtype})")
-    for name, (t, like) in dict(others, v=(v, "k")).items():
-        ref, strides = (q, qs) if like == "q" else (k, ks)
-        if t.shape != ref.shape or _strides_of(t, name) != strides:
-            raise RAError(1, f"{name} must have the shape and strides of {like} ({list(t.shape)} {t.stride()} vs "
-                             f"{list(ref.shape)} {ref.stride()})")
-    if v.dtype != k.dtype:
-        raise RAError(1, f"k and v must have the same dtype (got {k.dtype}, {v.dtype})")
+    if kB != B or kd != d or k.dtype != q.dtype or v.dtype != q.dtype:
+        raise RAError(1, f"q, k and v must have one batch, head dimension and dtype (got {list(q.shape)} {q.dtype}, "
+                         f"{list(k.shape)} {k.dtype}, {v.dtype})")
+    if v.shape != k.shape or _strides_of(v, "v") != ks:
+        raise RAError(1, f"v must have the shape and strides of k ({list(v.shape)} {v.stride()} vs {list(k.shape)} "
+                         f"{k.stride()})")
     if kv_len is not None:
         _vector(kv_len, "kv_len", B, torch.int32)
-    return RaShape(B, Nq, Nkv, Hq, Hkv, d, qs[0], ks[0], qs[1], qs[2], ks[1], ks[2])
+    return RaShape(B, Nq, Nkv, Hq, Hkv, d, qb, ks[0], qr, qh, ks[1], ks[2])
+
+
+def _like(t, ref, name, ref_name):
+    if t.shape != ref.shape or list(_strides_of(t, name)) != list(_strides_of(ref, ref_name)):
+        raise RAError(1, f"{name} must have the shape and strides of {ref_name} ({list(t.shape)} {t.stride()} vs "
+                         f"{list(ref.shape)} {ref.stride()})")
 
 
 def _row_floats(t, name, q):
@@ -713,54 +742,84 @@ def ra_cross_bwd_workspace_bytes(dtype, shape):
 def ra_cross_fwd(q, k, v, scale, o, lse, workspace, kv_len=None, stream=None, precise=False):
     """o, lse <- softmax(scale q k^T) v over the first kv_len[b] keys (int32 device tensor
     [B], None: all).  See include/ra.h."""
-    shape = _cross_shape(q, k, v, kv_len, o=(o, "q"))
+    shape = _cross_shape(q, k, v, kv_len)
+    _like(o, q, "o", "q")
     _row_floats(lse, "lse", q)
-    dev = _on_device(q, k, v, o, lse, workspace, *_there(kv_len))
+    dev = _device_index(q, k, v, o, lse, workspace, kv_len)
     _check(_lib().ra_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), _dt(q), shape, _data(kv_len),
-                               RA_PRECISE if precise else 0, float(scale), o.data_ptr(), _dt(o), lse.data_ptr(),
-                               workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
+                               RA_PRECISE if precise else 0, scale, o.data_ptr(), _dt(o), lse.data_ptr(),
+                               workspace.data_ptr(), _nbytes(workspace), _stream_handle(stream, dev)))
+
+
+def _check_cross_bwd(q, k, o, lse, dO):
+    _like(o, q, "o", "q")
+    _like(dO, q, "dO", "q")
+    _row_floats(lse, "lse", q)
+    if dO.dtype != q.dtype:
+        raise RAError(1, f"dO must have q's dtype (got {dO.dtype}, {q.dtype})")
 
 
 def ra_cross_bwd(q, k, v, o, dO, lse, scale, dq, dk, dv, workspace, kv_len=None, stream=None, precise=False):
     """Gradients of sum(o * dO) (overwritten).  See include/ra.h."""
-    shape = _cross_shape(q, k, v, kv_len, o=(o, "q"), dO=(dO, "q"), dq=(dq, "q"), dk=(dk, "k"), dv=(dv, "k"))
-    _row_floats(lse, "lse", q)
-    if dO.dtype != q.dtype or dk.dtype != dq.dtype or dv.dtype != dq.dtype:
-        raise RAError(1, f"dO must have q's dtype, dk and dv dq's (got {dO.dtype}, {dk.dtype}, {dv.dtype})")
-    dev = _on_device(q, k, v, o, dO, lse, dq, dk, dv, workspace, *_there(kv_len))
+    shape = _cross_shape(q, k, v, kv_len)
+    _check_cross_bwd(q, k, o, lse, dO)
+    _like(dq, q, "dq", "q")
+    _like(dk, k, "dk", "k")
+    _like(dv, k, "dv", "k")
+    if dk.dtype != dq.dtype or dv.dtype != dq.dtype:
+        raise RAError(1, f"dq, dk and dv must have one dtype (got {dq.dtype}, {dk.dtype}, {dv.dtype})")
+    dev = _device_index(q, k, v, o, dO, lse, dq, dk, dv, workspace, kv_len)
     _check(_lib().ra_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _dt(o), dO.data_ptr(),
-                               lse.data_ptr(), _dt(q), shape, _data(kv_len), RA_PRECISE if precise else 0, float(scale),
+                               lse.data_ptr(), _dt(q), shape, _data(kv_len), RA_PRECISE if precise else 0, scale,
                                dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _dt(dq), workspace.data_ptr(),
-                               _nbytes(workspace), _handle(stream, dev)))
+                               _nbytes(workspace), _stream_handle(stream, dev)))
+
+
+def _in_layout(t, dtype):
+    """A new tensor in t's layout (as empty_like_layout, quicker where that is packed)."""
+    if t.is_contiguous():
+        return torch.empty_like(t) if t.dtype == dtype else torch.empty(t.shape, dtype=dtype, device=t.device)
+    return empty_like_layout(t, dtype)
 
 
 def cross_attention_fwd(q, k, v, kv_len=None, scale=None, o_dtype=torch.float32, stream=None, precise=False):
     """Allocate o (o_dtype, q's layout) and lse [B, Hq, Nq] fp32 and run ra_cross_fwd."""
-    if scale is None:
-        scale = q.shape[-1] ** -0.5
+    if stream is not None:
+        with torch.cuda.stream(stream):  # what is allocated belongs to the stream it is used on
+            return cross_attention_fwd(q, k, v, kv_len, scale, o_dtype, None, precise)
     shape = _cross_shape(q, k, v, kv_len)
-    dev = _on_device(q)
-    nbytes = ra_cross_fwd_workspace_bytes(_dt(q), shape, RA_PRECISE if precise else 0)
-    B, Nq, Hq, _ = q.shape
-    with torch.cuda.stream(stream):
-        o = empty_like_layout(q, o_dtype)
-    lse, ws = _allocate(stream, dev, ((B, Hq, Nq), torch.float32), ((nbytes,), torch.uint8))
-    ra_cross_fwd(q, k, v, scale, o, lse, ws, kv_len, stream, precise)
+    dev, lib, dtype, device = _device_index(q, k, v, kv_len), _lib(), _dt(q), q.device
+    flags = RA_PRECISE if precise else 0
+    nbytes = lib.ra_cross_fwd_workspace_bytes(dtype, shape, flags)
+    o = _in_layout(q, o_dtype)
+    lse = torch.empty((shape.B, shape.Hq, shape.N_q), dtype=torch.float32, device=device)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    code = lib.ra_cross_fwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), dtype, shape, _data(kv_len), flags,
+                            shape.d ** -0.5 if scale is None else scale, o.data_ptr(), _code(o_dtype), lse.data_ptr(),
+                            ws.data_ptr(), nbytes, _stream_handle(None, dev))
+    if code:
+        _check(code)
     return o, lse
 
 
 def cross_attention_bwd(q, k, v, o, lse, dO, kv_len=None, scale=None, grad_dtype=torch.float32, stream=None,
                         precise=False):
     """Allocate dq, dk, dv (grad_dtype, the layouts of q and k) and run ra_cross_bwd."""
-    if scale is None:
-        scale = q.shape[-1] ** -0.5
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return cross_attention_bwd(q, k, v, o, lse, dO, kv_len, scale, grad_dtype, None, precise)
     shape = _cross_shape(q, k, v, kv_len)
-    dev = _on_device(q)
-    nbytes = ra_cross_bwd_workspace_bytes(_dt(q), shape)
-    with torch.cuda.stream(stream):
-        dq, dk, dv = empty_like_layout(q, grad_dtype), empty_like_layout(k, grad_dtype), empty_like_layout(k, grad_dtype)
-    ws, = _allocate(stream, dev, ((nbytes,), torch.uint8))
-    ra_cross_bwd(q, k, v, o, dO, lse, scale, dq, dk, dv, ws, kv_len, stream, precise)
+    _check_cross_bwd(q, k, o, lse, dO)
+    dev, lib, dtype = _device_index(q, k, v, o, lse, dO, kv_len), _lib(), _dt(q)
+    nbytes = lib.ra_cross_bwd_workspace_bytes(dtype, shape)
+    dq, dk, dv = _in_layout(q, grad_dtype), _in_layout(k, grad_dtype), _in_layout(k, grad_dtype)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    code = lib.ra_cross_bwd(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _dt(o), dO.data_ptr(), lse.data_ptr(),
+                            dtype, shape, _data(kv_len), RA_PRECISE if precise else 0,
+                            shape.d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                            _code(grad_dtype), ws.data_ptr(), nbytes, _stream_handle(None, dev))
+    if code:
+        _check(code)
     return dq, dk, dv
 
 
@@ -790,15 +849,24 @@ def rotary_frequencies(rot, base=10000.0, scale=1.0, method="linear", trained=0,
 
 def _rot_shape(q, k, qn="q", kn="k"):
     """RaShape of queries and keys of the same rows; k may be None."""
-    qb, qr, qh = _strides_of(q, qn)
-    B, N, Hq, d = q.shape
+    n = q.shape
+    if len(n) != 4:
+        raise RAError(1, f"{qn} must be [B, N, H, d]")
+    B, N, Hq, d = n
     if k is None:
-        return RaShape(B, N, N, Hq, 1, d, qb, 0, qr, qh, 0, 0)
-    kb, kr, kh = _strides_of(k, kn)
-    kB, kN, Hkv, kd = k.shape
-    if (kB, kN, kd) != (B, N, d) or k.dtype != q.dtype:
-        raise RAError(1, f"{qn} and {kn} must have the same batch, rows, head dimension and dtype (got {list(q.shape)} "
-                         f"{q.dtype}, {list(k.shape)} {k.dtype})")
+        Hkv, packed = 1, q.is_contiguous()
+    else:
+        m = k.shape
+        if len(m) != 4 or m[0] != B or m[1] != N or m[3] != d or k.dtype != q.dtype:
+            raise RAError(1, f"{qn} and {kn} must be [B, N, H, d] of one batch, rows, head dimension and dtype (got "
+                             f"{list(n)} {q.dtype}, {list(m)} {k.dtype})")
+        Hkv, packed = m[2], q.is_contiguous() and k.is_contiguous()
+    if packed and q.numel() <= _INT_MAX:
+        if Hkv > _INT_MAX:
+            _fits(Hkv)
+        return RaShape(B, N, N, Hq, Hkv, d)
+    qb, qr, qh = _strides_of(q, qn)
+    kb, kr, kh = (0, 0, 0) if k is None else _strides_of(k, kn)
     return RaShape(B, N, N, Hq, Hkv, d, qb, kb, qr, qh, kr, kh)
 
 
@@ -812,35 +880,21 @@ def _rotary(shape, freq, positions, pos_off, amplitude, P):
     """RaRotary; freq None: no rotation."""
     if freq is None:
         return RaRotary(0, None, None, 0, 0, 1, 1.0)
-    if freq.dtype != torch.float64 or freq.dim() != 1 or not freq.is_contiguous():
-        raise RAError(1, f"freq must be a contiguous float64 tensor [rot / 2] (got {freq.dtype} {list(freq.shape)})")
-    if P > _INT_MAX or 2 * freq.shape[0] > _INT_MAX:
-        _fits(P, 2 * freq.shape[0])
-    ptr, bstride = None, 0
-    if positions is not None:
-        B, N = shape.B, shape.N_q
-        n = positions.shape
-        if positions.dtype != torch.int64 or (n != (N,) and n != (B, N) and n != (1, N)):
-            raise RAError(1, f"positions must be int64 [N] or [B, N] (got {positions.dtype} {list(n)})")
-        st = positions.stride()
-        if N > 1 and st[-1] != 1:
-            raise RAError(1, f"positions must be contiguous along the rows (strides {st})")
-        if len(n) == 2 and n[0] > 1 and st[0] != 0:
-            bstride = st[0]
-        ptr = positions.data_ptr()
-    return RaRotary(2 * freq.shape[0], freq.data_ptr(), ptr, bstride, pos_off, P, amplitude)
-
-
-def _rot_flags(interleaved, striped):
-    return (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
-
-
-def _data(t):
-    return None if t is None else t.data_ptr()
-
-
-def _there(*tensors):
-    return [t for t in tensors if t is not None]
+    n = freq.shape
+    if freq.dtype != torch.float64 or len(n) != 1 or not freq.is_contiguous():
+        raise RAError(1, f"freq must be a contiguous float64 tensor [rot / 2] (got {freq.dtype} {list(n)})")
+    if P > _INT_MAX or 2 * n[0] > _INT_MAX:
+        _fits(P, 2 * n[0])
+    if positions is None:
+        return RaRotary(2 * n[0], freq.data_ptr(), None, 0, pos_off, P, amplitude)
+    m, B, N = positions.shape, shape.B, shape.N_q
+    if positions.dtype != torch.int64 or (m != (B, N) and m != (N,) and m != (1, N)):
+        raise RAError(1, f"positions must be int64 [N] or [B, N] (got {positions.dtype} {list(m)})")
+    st = positions.stride()
+    if N > 1 and st[-1] != 1:
+        raise RAError(1, f"positions must be contiguous along the rows (strides {st})")
+    return RaRotary(2 * n[0], freq.data_ptr(), positions.data_ptr(), st[0] if len(m) == 2 and m[0] > 1 else 0, pos_off, P,
+                    amplitude)
 
 
 def _rot_weights(d, q_weight, k_weight):
@@ -851,9 +905,10 @@ def _rot_weights(d, q_weight, k_weight):
             continue
         if t.shape != (d,) or not t.is_contiguous():
             raise RAError(1, f"{name} must be contiguous [{d}] (got {list(t.shape)})")
-        if code not in (None, _dt(t)):
+        if code is None:
+            code = _dt(t)
+        elif code != _dt(t):
             raise RAError(1, "q_weight and k_weight must have one dtype")
-        code = _dt(t)
     return RA_F32 if code is None else code
 
 
@@ -870,78 +925,108 @@ def ra_rotary_bwd(dq_out, dk_out, freq, dq, dk, positions=None, pos_off=0, inter
     _rotary_call(True, dq_out, dk_out, freq, dq, dk, positions, pos_off, interleaved, amplitude, P, striped, stream)
 
 
-def _rotary_call(grad, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream):
+def _rotary_call(grad, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream,
+                 out_dtype=None):
+    """q_out None: both results are allocated (packed, out_dtype) and returned."""
     shape = _rot_shape(q, k)
-    _same_shape(q_out, q, "the result of q")
-    _same_shape(k_out, k, "the result of k")
     if freq is None:
         raise RAError(1, "freq is None")
-    out_shape = _rot_shape(q_out, k_out)
     rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
-    dev = _on_device(q, *_there(k, freq, q_out, k_out, positions))
-    dtype, out_dtype, flags = _dt(q), _dt(q_out), _rot_flags(interleaved, striped)
-    ptrs = q_out.data_ptr(), _data(k_out)
-    if grad:
-        code = _lib().ra_rotary_bwd(q.data_ptr(), _data(k), dtype, shape, rot, flags, *ptrs, out_dtype, out_shape,
-                                    _handle(stream, dev))
+    if q_out is None:
+        dev = _device_index(q, k, freq, positions)
+        q_out, k_out = _empty_pair(q, k, out_dtype)
+        out_shape = RaShape(shape.B, shape.N_q, shape.N_kv, shape.Hq, shape.Hkv, shape.d)
     else:
-        if dtype != out_dtype:
+        _same_shape(q_out, q, "the result of q")
+        _same_shape(k_out, k, "the result of k")
+        out_shape = _rot_shape(q_out, k_out)
+        if not grad and q_out.dtype != q.dtype:
             raise RAError(1, f"the results must have the dtype of q and k (got {q_out.dtype}, {q.dtype})")
-        code = _lib().ra_rotary_fwd(q.data_ptr(), _data(k), dtype, shape, rot, flags, *ptrs, out_shape,
-                                    _handle(stream, dev))
+        dev = _device_index(q, k, freq, q_out, k_out, positions)
+    flags = (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
+    if grad:
+        code = _lib().ra_rotary_bwd(q.data_ptr(), _data(k), _dt(q), shape, rot, flags, q_out.data_ptr(), _data(k_out),
+                                    _dt(q_out), out_shape, _stream_handle(stream, dev))
+    else:
+        code = _lib().ra_rotary_fwd(q.data_ptr(), _data(k), _dt(q), shape, rot, flags, q_out.data_ptr(), _data(k_out),
+                                    out_shape, _stream_handle(stream, dev))
     if code:
         _check(code)
+    return q_out, k_out
 
 
-def _empty_pair(stream, dev, q, k, dtype):
+def _empty_pair(q, k, dtype):
+    """New packed tensors of the shapes of q and k (None for None)."""
+    if q.dtype == dtype and q.is_contiguous():
+        a = torch.empty_like(q)
+    else:
+        a = torch.empty(q.shape, dtype=dtype, device=q.device)
     if k is None:
-        return _allocate(stream, dev, (q.shape, dtype)) + [None]
-    return _allocate(stream, dev, (q.shape, dtype), (k.shape, dtype))
+        return a, None
+    if k.dtype == dtype and k.is_contiguous():
+        return a, torch.empty_like(k)
+    return a, torch.empty(k.shape, dtype=dtype, device=k.device)
 
 
 def rotary_fwd(q, k, freq, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1, striped=False,
                stream=None):
     """Convenience wrapper: allocates the results (packed)."""
-    q_out, k_out = _empty_pair(stream, _on_device(q), q, k, q.dtype)
-    _rotary_call(False, q, k, freq, q_out, k_out, positions, pos_off, interleaved, amplitude, P, striped, stream)
-    return q_out, k_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _rotary_call(False, q, k, freq, None, None, positions, pos_off, interleaved, amplitude, P, striped, None,
+                                q.dtype)
+    return _rotary_call(False, q, k, freq, None, None, positions, pos_off, interleaved, amplitude, P, striped, None, q.dtype)
 
 
 def rotary_bwd(dq_out, dk_out, freq, positions=None, pos_off=0, interleaved=False, amplitude=1.0, P=1, striped=False,
                grad_dtype=None, stream=None):
     """Convenience wrapper: allocates dq, dk (packed, dq_out's dtype by default)."""
-    dq, dk = _empty_pair(stream, _on_device(dq_out), dq_out, dk_out, grad_dtype or dq_out.dtype)
-    _rotary_call(True, dq_out, dk_out, freq, dq, dk, positions, pos_off, interleaved, amplitude, P, striped, stream)
-    return dq, dk
+    with torch.cuda.stream(stream):
+        return _rotary_call(True, dq_out, dk_out, freq, None, None, positions, pos_off, interleaved, amplitude, P, striped,
+                            None, grad_dtype or dq_out.dtype)
 
 
 def ra_norm_rotary_fwd(q, k, q_weight, k_weight, freq, q_out, k_out, eps=1e-6, positions=None, pos_off=0,
                        interleaved=False, amplitude=1.0, P=1, striped=False, stream=None):
     """q_out, k_out <- q, k normed for each head (weights [d] or None) and rotated (freq
     None: not rotated).  See include/ra.h."""
+    _norm_rotary_call(q, k, q_weight, k_weight, freq, q_out, k_out, eps, positions, pos_off, interleaved, amplitude, P,
+                      striped, stream)
+
+
+def _norm_rotary_call(q, k, q_weight, k_weight, freq, q_out, k_out, eps, positions, pos_off, interleaved, amplitude, P,
+                      striped, stream):
     shape = _rot_shape(q, k)
-    _same_shape(q_out, q, "the result of q")
-    _same_shape(k_out, k, "the result of k")
-    out_shape = _rot_shape(q_out, k_out)
-    if q.dtype != q_out.dtype:
-        raise RAError(1, f"the results must have the dtype of q and k (got {q_out.dtype}, {q.dtype})")
     w_dtype = _rot_weights(shape.d, q_weight, k_weight)
     rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
-    dev = _on_device(q, *_there(k, freq, q_out, k_out, positions, q_weight, k_weight))
+    if q_out is None:
+        dev = _device_index(q, k, freq, positions, q_weight, k_weight)
+        q_out, k_out = _empty_pair(q, k, q.dtype)
+        out_shape = RaShape(shape.B, shape.N_q, shape.N_kv, shape.Hq, shape.Hkv, shape.d)
+    else:
+        _same_shape(q_out, q, "the result of q")
+        _same_shape(k_out, k, "the result of k")
+        out_shape = _rot_shape(q_out, k_out)
+        if q.dtype != q_out.dtype:
+            raise RAError(1, f"the results must have the dtype of q and k (got {q_out.dtype}, {q.dtype})")
+        dev = _device_index(q, k, freq, q_out, k_out, positions, q_weight, k_weight)
+    flags = (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
     code = _lib().ra_norm_rotary_fwd(q.data_ptr(), _data(k), _dt(q), shape, _data(q_weight), _data(k_weight), w_dtype, eps,
-                                     rot, _rot_flags(interleaved, striped), q_out.data_ptr(), _data(k_out), out_shape,
-                                     _handle(stream, dev))
+                                     rot, flags, q_out.data_ptr(), _data(k_out), out_shape, _stream_handle(stream, dev))
     if code:
         _check(code)
+    return q_out, k_out
 
 
 def norm_rotary_fwd(q, k, q_weight, k_weight, freq, eps=1e-6, positions=None, pos_off=0, interleaved=False,
                     amplitude=1.0, P=1, striped=False, stream=None):
     """Convenience wrapper: allocates the results (packed)."""
-    q_out, k_out = _empty_pair(stream, _on_device(q), q, k, q.dtype)
-    ra_norm_rotary_fwd(q, k, q_weight, k_weight, freq, q_out, k_out, eps, positions, pos_off, interleaved, amplitude, P,
-                       striped, stream)
-    return q_out, k_out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _norm_rotary_call(q, k, q_weight, k_weight, freq, None, None, eps, positions, pos_off, interleaved,
+                                     amplitude, P, striped, None)
+    return _norm_rotary_call(q, k, q_weight, k_weight, freq, None, None, eps, positions, pos_off, interleaved, amplitude,
+                             P, striped, None)
 
 
 def ra_norm_rotary_bwd_workspace_bytes(d):
@@ -961,28 +1046,44 @@ def ra_norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, d
         if t is not None:
             _vector(t, name, shape.d, torch.float32)
     rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
-    dev = _on_device(q, *_there(k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dq_weight, dk_weight, positions),
-                     workspace)
+    dev = _device_index(q, k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dq_weight, dk_weight, positions, workspace)
+    flags = (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
     _check(_lib().ra_norm_rotary_bwd(q.data_ptr(), _data(k), _dt(q), shape, dq_out.data_ptr(), _data(dk_out), _dt(dq_out),
-                                     dout_shape, _data(q_weight), _data(k_weight), w_dtype, eps, rot,
-                                     _rot_flags(interleaved, striped), dq.data_ptr(), _data(dk), _dt(dq), grad_shape,
-                                     _data(dq_weight), _data(dk_weight), workspace.data_ptr(), _nbytes(workspace),
-                                     _handle(stream, dev)))
+                                     dout_shape, _data(q_weight), _data(k_weight), w_dtype, eps, rot, flags, dq.data_ptr(),
+                                     _data(dk), _dt(dq), grad_shape, _data(dq_weight), _data(dk_weight),
+                                     workspace.data_ptr(), _nbytes(workspace), _stream_handle(stream, dev)))
 
 
 def norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, eps=1e-6, positions=None, pos_off=0,
                     interleaved=False, amplitude=1.0, P=1, striped=False, grad_dtype=None, stream=None):
     """Convenience wrapper: allocates dq, dk (packed, q's dtype by default), the fp32
-    gradients of the weights (None for a tensor that is None, ones for weights) and the
+    gradients of the weights (of ones where a weight is None; None where k is) and the
     workspace.  Returns dq, dk, dq_weight, dk_weight."""
-    dev, d = _on_device(q), q.shape[-1]
-    dq, dk = _empty_pair(stream, dev, q, k, grad_dtype or q.dtype)
-    dqw, dkw, ws = _allocate(stream, dev, ((d,), torch.float32), ((d,), torch.float32),
-                             ((ra_norm_rotary_bwd_workspace_bytes(d),), torch.uint8))
-    if k is None:
-        dkw = None
-    ra_norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, dq, dk, dqw, dkw, ws, eps, positions, pos_off,
-                       interleaved, amplitude, P, striped, stream)
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_rotary_bwd(q, k, dq_out, dk_out, q_weight, k_weight, freq, eps, positions, pos_off, interleaved,
+                                   amplitude, P, striped, grad_dtype, None)
+    shape = _rot_shape(q, k)
+    _same_shape(dq_out, q, "dq_out")
+    _same_shape(dk_out, k, "dk_out")
+    dout_shape = _rot_shape(dq_out, dk_out, "dq_out", "dk_out")
+    grad_shape = RaShape(shape.B, shape.N_q, shape.N_kv, shape.Hq, shape.Hkv, shape.d)
+    w_dtype = _rot_weights(shape.d, q_weight, k_weight)
+    rot = _rotary(shape, freq, positions, pos_off, amplitude, P)
+    dev, lib, device, d = _device_index(q, k, dq_out, dk_out, q_weight, k_weight, freq, positions), _lib(), q.device, shape.d
+    grad_dtype = grad_dtype or q.dtype
+    dq, dk = _empty_pair(q, k, grad_dtype)
+    dqw = torch.empty(d, dtype=torch.float32, device=device)
+    dkw = None if k is None else torch.empty(d, dtype=torch.float32, device=device)
+    nbytes = lib.ra_norm_rotary_bwd_workspace_bytes(d)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    flags = (RA_INTERLEAVED if interleaved else 0) | (RA_STRIPED if striped else 0)
+    code = lib.ra_norm_rotary_bwd(q.data_ptr(), _data(k), _dt(q), shape, dq_out.data_ptr(), _data(dk_out), _dt(dq_out),
+                                  dout_shape, _data(q_weight), _data(k_weight), w_dtype, eps, rot, flags, dq.data_ptr(),
+                                  _data(dk), _code(grad_dtype), grad_shape, dqw.data_ptr(), _data(dkw), ws.data_ptr(),
+                                  nbytes, _stream_handle(None, dev))
+    if code:
+        _check(code)
     return dq, dk, dqw, dkw
 
 
@@ -991,77 +1092,90 @@ def ra_grad_workspace_bytes(count):
     return int(_lib().ra_grad_workspace_bytes(min(int(count), _INT_MAX)))
 
 
+_data_ptr, _numel, _contiguous, _get_device = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous,
+                                               torch.Tensor.get_device)
+
+
 def _grad_arrays(tensors, name, dev):
-    """Host arrays of addresses, sizes and dtypes."""
-    n = len(tensors)
-    if n < 1:
-        raise RAError(1, f"{name} is empty")
-    codes = []
-    for t in tensors:
-        code = _DTYPES.get(t.dtype)
-        if code is None or t.device != dev or not t.is_contiguous():
-            raise RAError(1, f"{name} must be contiguous fp32, bf16 or fp16 tensors on one device (got {t.dtype} on "
-                             f"{t.device}, strides {t.stride()})")
-        codes.append(code)
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in tensors]), (ctypes.c_longlong * n)(*[t.numel() for t in tensors]),
-            (ctypes.c_int * n)(*codes))
+    """Host arrays of addresses, sizes and dtype codes.  A list may have hundreds of tensors:
+    each property is taken of all of them at once."""
+    if {*map(_get_device, tensors)} != {dev} or not all(map(_contiguous, tensors)):
+        raise RAError(1, f"{name} must be contiguous tensors on one device")
+    dtypes = [t.dtype for t in tensors]
+    codes = {t: _code(t) for t in {*dtypes}}
+    return (array("q", map(_data_ptr, tensors)), array("q", map(_numel, tensors)), array("i", map(codes.get, dtypes)))
+
+
+def _address(a):
+    return a.buffer_info()[0]
+
+
+def _grad_call(grads, norm, workspace, nbytes, max_norm, outs, eps, stream, dev):
+    """max_norm None: the norm alone."""
+    n, lib = len(grads), _lib()
+    ptrs, sizes, dtypes = _grad_arrays(grads, "grads", dev)
+    handle = _stream_handle(stream, dev)
+    if max_norm is None:
+        code = lib.ra_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), n, norm.data_ptr(),
+                                workspace.data_ptr(), nbytes, handle)
+    elif outs is None:
+        code = lib.ra_grad_clip(_address(ptrs), _address(sizes), _address(dtypes), n, max_norm, eps, None, None,
+                                norm.data_ptr(), workspace.data_ptr(), nbytes, handle)
+    else:
+        if len(outs) != n:
+            raise RAError(1, f"outs must have {n} tensors (got {len(outs)})")
+        out_ptrs, out_sizes, out_dtypes = _grad_arrays(outs, "outs", dev)
+        if out_sizes != sizes:
+            raise RAError(1, "outs must have the sizes of grads")
+        code = lib.ra_grad_clip(_address(ptrs), _address(sizes), _address(dtypes), n, max_norm, eps, _address(out_ptrs),
+                                _address(out_dtypes), norm.data_ptr(), workspace.data_ptr(), nbytes, handle)
+    if code:
+        _check(code)
+
+
+def _norm_tensor(grads, norm, workspace):
+    if not len(grads):
+        raise RAError(1, "grads is empty")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise RAError(1, f"norm must be one fp32 element (got {norm.dtype} {list(norm.shape)})")
+    return _device_index(norm, workspace)
 
 
 def ra_grad_norm(grads, norm, workspace, stream=None):
     """norm [1] or [] fp32 <- the 2-norm of all elements of all tensors of the list."""
-    if not len(grads):
-        raise RAError(1, "grads is empty")
-    dev = _on_device(grads[0], norm, workspace)
-    _norm_tensor(norm)
-    arrays = _grad_arrays(grads, "grads", dev)
-    _check(_lib().ra_grad_norm(*arrays, len(grads), norm.data_ptr(), workspace.data_ptr(), _nbytes(workspace),
-                               _handle(stream, dev)))
-
-
-def _norm_tensor(norm):
-    if norm.dtype != torch.float32 or norm.numel() != 1:
-        raise RAError(1, f"norm must be one fp32 element (got {norm.dtype} {list(norm.shape)})")
+    dev = _norm_tensor(grads, norm, workspace)
+    _grad_call(grads, norm, workspace, _nbytes(workspace), None, None, 0.0, stream, dev)
 
 
 def ra_grad_clip(grads, max_norm, norm, workspace, outs=None, eps=1e-6, stream=None):
     """norm <- the 2-norm of all tensors; outs (None: the gradients themselves) <- grads
     times min(1, max_norm / (norm + eps)).  See include/ra.h."""
-    if not len(grads):
-        raise RAError(1, "grads is empty")
-    dev = _on_device(grads[0], norm, workspace)
-    _norm_tensor(norm)
-    ptrs, sizes, dtypes = _grad_arrays(grads, "grads", dev)
-    out_ptrs = out_dtypes = None
-    if outs is not None:
-        if len(outs) != len(grads):
-            raise RAError(1, f"outs must have {len(grads)} tensors (got {len(outs)})")
-        out_ptrs, out_sizes, out_dtypes = _grad_arrays(outs, "outs", dev)
-        if bytes(out_sizes) != bytes(sizes):
-            raise RAError(1, "outs must have the sizes of grads")
-    _check(_lib().ra_grad_clip(ptrs, sizes, dtypes, len(grads), max_norm, eps, out_ptrs, out_dtypes, norm.data_ptr(),
-                               workspace.data_ptr(), _nbytes(workspace), _handle(stream, dev)))
+    dev = _norm_tensor(grads, norm, workspace)
+    _grad_call(grads, norm, workspace, _nbytes(workspace), float(max_norm), outs, eps, stream, dev)
 
 
-def _grad_buffers(grads, stream):
+def _grad_allocate(grads, max_norm, outs, eps, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _grad_allocate(grads, max_norm, outs, eps, None)
     if not len(grads):
         raise RAError(1, "grads is empty")
-    return _allocate(stream, _on_device(grads[0]), ((), torch.float32),
-                     ((ra_grad_workspace_bytes(len(grads)),), torch.uint8))
+    dev, device = _device_index(grads[0]), grads[0].device
+    nbytes = _lib().ra_grad_workspace_bytes(min(len(grads), _INT_MAX))
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    _grad_call(grads, norm, torch.empty(nbytes, dtype=torch.uint8, device=device), nbytes, max_norm, outs, eps, None, dev)
+    return norm
 
 
 def grad_norm(grads, stream=None):
     """Convenience wrapper: allocates the norm (returned, fp32 []) and the workspace."""
-    norm, ws = _grad_buffers(grads, stream)
-    ra_grad_norm(grads, norm, ws, stream)
-    return norm
+    return _grad_allocate(grads, None, None, 0.0, stream)
 
 
 def grad_clip(grads, max_norm, outs=None, eps=1e-6, stream=None):
     """Convenience wrapper: allocates the norm (returned, fp32 []) and the workspace; the
     gradients are clipped in place, or into `outs`."""
-    norm, ws = _grad_buffers(grads, stream)
-    ra_grad_clip(grads, max_norm, norm, ws, outs, eps, stream)
-    return norm
+    return _grad_allocate(grads, float(max_norm), outs, eps, stream)
 
 
 def ra_ring_bwd_workspace_bytes(dtype, grad_dtype, shape, P):

@@ -13,7 +13,10 @@
 //
 // Bound by reading the gradients twice (the factor depends on all of them) and writing
 // them once.  The second pass goes through the chunks from the last to the first: what the
-// first one read last is still in L2.
+// first one read last is still in L2.  Its chunks are small, a block each: what the GPU has
+// open at a time then lies close together (2^29 bf16: 7.0 TB/s; 4.6 TB/s with blocks that
+// each go through chunks of 128 KB), for which a block of its own forms the factor.  Few
+// chunks are taken by blocks that form it each: a launch less.
 #include <math.h>
 
 #include "ra_device.cuh"
@@ -187,7 +190,7 @@ __device__ __forceinline__ void scale_chunk(const T* p, TO* out, const Chunk& c,
     uint4 v[kScaleBatch];
 #pragma unroll
     for (int k = 0; k < kScaleBatch; ++k)
-      if (i + k * kThreads < vectors) v[k] = __ldcs(q + i + k * kThreads);
+      if (i + k * kThreads < vectors) v[k] = q[i + k * kThreads];
 #pragma unroll
     for (int k = 0; k < kScaleBatch; ++k) {
       if (i + k * kThreads >= vectors) break;
@@ -212,19 +215,30 @@ __device__ __forceinline__ void scale_to(const T* p, void* out, int type, const 
   else scale_chunk(p, static_cast<__half*>(out), c, mul);
 }
 
+// The factor, in two steps: one below fp32's smallest normal number would lose its digits.
+// A norm that is infinite gives 0 and one that is NaN gives NaN.
+__device__ __forceinline__ float2 factor_of(double norm, float max_norm, float eps) {
+  const double factor = (double)max_norm / (norm + (double)eps);
+  return factor >= 1.     ? make_float2(1.f, 1.f)
+         : factor < 1e-30 ? make_float2(9.094947017729282e-13f, (float)(factor * 1099511627776.))
+                          : make_float2((float)factor, 1.f);
+}
+
+// factor NULL: from the parts; else what grad_norm_kernel left there.
 template <int MAX>
 __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_constant__ GradList<MAX> a, const double* parts,
-                                                              int count, float max_norm, float eps, float* norm) {
+                                                              int count, float max_norm, float eps, float* norm,
+                                                              const float2* factor) {
   pdl_trigger();
   pdl_wait();
-  const double n = norm_of(parts, count);
-  if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
-  // a norm that is infinite gives 0 and one that is NaN gives NaN
-  const double factor = (double)max_norm / (n + (double)eps);
-  // in two steps, as a factor below fp32's smallest normal number would lose its digits
-  const float2 mul = factor >= 1.        ? make_float2(1.f, 1.f)
-                     : factor < 1e-30    ? make_float2(9.094947017729282e-13f, (float)(factor * 1099511627776.))
-                                         : make_float2((float)factor, 1.f);
+  float2 mul;
+  if (factor) {
+    mul = *factor;
+  } else {
+    const double n = norm_of(parts, count);
+    if (norm && blockIdx.x == 0 && threadIdx.x == 0) *norm = (float)n;
+    mul = factor_of(n, max_norm, eps);
+  }
   for (int k = blockIdx.x; k < a.first[a.count]; k += gridDim.x) {
     const Chunk c = find_chunk(a, a.first[a.count] - 1 - k);
     const int t = a.types[c.tensor] & 15, to = a.types[c.tensor] >> 4;
@@ -237,11 +251,14 @@ __global__ void __launch_bounds__(kThreads, 4) grad_scale_kernel(const __grid_co
   }
 }
 
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* parts, int count, float* norm) {
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const double* parts, int count, float max_norm, float eps,
+                                                             float* norm, float2* factor) {
   pdl_trigger();
   pdl_wait();
   const double n = norm_of(parts, count);
-  if (threadIdx.x == 0) *norm = (float)n;
+  if (threadIdx.x) return;
+  *norm = (float)n;
+  if (factor) *factor = factor_of(n, max_norm, eps);
 }
 
 template <int MAX>
@@ -262,21 +279,24 @@ cudaError_t launch_grad_squares(const GradList<MAX>& a, double* parts, int* used
 }
 template <int MAX>
 cudaError_t launch_grad_scale(const GradList<MAX>& a, const double* parts, int count, float max_norm, float eps,
-                              float* norm, int sms, cudaStream_t st) {
-  const cudaError_t e =
-      launch_pdl(grad_scale_kernel<MAX>, grid_of(a, sms), kThreads, 0, st, a, parts, count, max_norm, eps, norm);
+                              float* norm, const float2* factor, int sms, cudaStream_t st) {
+  const cudaError_t e = launch_pdl(grad_scale_kernel<MAX>, factor ? a.first[a.count] : grid_of(a, sms), kThreads, 0, st, a,
+                                   parts, count, max_norm, eps, norm, factor);
   if (e == cudaSuccess) count_launch();
   return e;
 }
-cudaError_t launch_grad_norm(const double* parts, int count, float* norm, cudaStream_t st) {
-  const cudaError_t e = launch_pdl(grad_norm_kernel, 1, kThreads, 0, st, parts, count, norm);
+cudaError_t launch_grad_norm(const double* parts, int count, float max_norm, float eps, float* norm, float2* factor,
+                             cudaStream_t st) {
+  const cudaError_t e = launch_pdl(grad_norm_kernel, 1, kThreads, 0, st, parts, count, max_norm, eps, norm, factor);
   if (e == cudaSuccess) count_launch();
   return e;
 }
 
 template cudaError_t launch_grad_squares(const GradList<kClipFew>&, double*, int*, int, cudaStream_t);
+template cudaError_t launch_grad_squares(const GradList<kClipSome>&, double*, int*, int, cudaStream_t);
 template cudaError_t launch_grad_squares(const GradList<kClipMany>&, double*, int*, int, cudaStream_t);
-template cudaError_t launch_grad_scale(const GradList<kClipFew>&, const double*, int, float, float, float*, int, cudaStream_t);
-template cudaError_t launch_grad_scale(const GradList<kClipMany>&, const double*, int, float, float, float*, int, cudaStream_t);
+template cudaError_t launch_grad_scale(const GradList<kClipFew>&, const double*, int, float, float, float*, const float2*, int, cudaStream_t);
+template cudaError_t launch_grad_scale(const GradList<kClipSome>&, const double*, int, float, float, float*, const float2*, int, cudaStream_t);
+template cudaError_t launch_grad_scale(const GradList<kClipMany>&, const double*, int, float, float, float*, const float2*, int, cudaStream_t);
 
 }  // namespace ra

@@ -61,54 +61,76 @@ __device__ __forceinline__ bool past_fp16(const float (&f)[8]) {
   return bad;
 }
 
-// A warp joins the states (m_s, l_s, o_s) of one row: m = max m_s, w_s = e^{m_s - m},
+// Joins the states (m_s, l_s, o_s) of a row: m = max m_s, w_s = e^{m_s - m},
 // o = sum w_s o_s / sum w_s l_s, lse = m + ln sum w_s l_s.  Parts that saw no key left no
-// o_s.  A lane holds d / 32 columns.
+// o_s.  W warps share a row's parts (a single one would wait for each four of up to 256 in
+// turn: 45 us) and add up their sums in order; a lane holds d / 32 columns.
+template <int W>
 __global__ void __launch_bounds__(kThreads) cross_join_kernel(CrossState p, int splits, int B, int Nq, int Hq, int d, void* o,
                                                               int o_dtype, Lay ol, float* lse) {
+  __shared__ float4 sums[kThreads / 32][32];
+  __shared__ float totals[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  const long long rows = (long long)B * Nq * Hq, row = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (row >= rows) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, share = warp % W;
+  const long long rows = (long long)B * Nq * Hq, row = (long long)blockIdx.x * (kThreads / 32 / W) + warp / W;
+  const bool there = row < rows;
   const int h = (int)(row % Hq);
   const long long bn = row / Hq;
   const int n = (int)(bn % Nq), b = (int)(bn / Nq);
   const long long at = ((long long)b * Hq + h) * Nq + n;
-  float m = -INFINITY;
-  for (int s = lane; s < splits; s += 32) m = fmaxf(m, p.m[s * rows + at]);
-  m = warp_max(m);
-  const float ref = m == -INFINITY ? 0.f : m;
-  float l = 0.f;
+  float m = -INFINITY, l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < splits; s0 += 32) {
-    float w = 0.f;
-    if (s0 + lane < splits) {
-      w = ex2_approx((p.m[(s0 + lane) * rows + at] - ref) * kLog2e);
-      const float ls = p.l[(s0 + lane) * rows + at];
-      // a NaN stays one, whatever its part's maximum
-      if (w > 0.f || ls != ls) l += w * ls;
-    }
-    const int last = min(32, splits - s0);
-#pragma unroll 4
-    for (int j = 0; j < last; ++j) {
-      const float ws = __shfl_sync(0xffffffffu, w, j);
-      if (!(ws > 0.f)) continue;
-      const float* src = p.o + ((s0 + j) * rows + row) * d;
-      if (d == 128) {
-        const float4 v = reinterpret_cast<const float4*>(src)[lane];
-        acc.x = fmaf(ws, v.x, acc.x);
-        acc.y = fmaf(ws, v.y, acc.y);
-        acc.z = fmaf(ws, v.z, acc.z);
-        acc.w = fmaf(ws, v.w, acc.w);
-      } else {
-        const float2 v = reinterpret_cast<const float2*>(src)[lane];
-        acc.x = fmaf(ws, v.x, acc.x);
-        acc.y = fmaf(ws, v.y, acc.y);
+  if (there) {
+    for (int s = lane; s < splits; s += 32) m = fmaxf(m, p.m[s * rows + at]);
+    m = warp_max(m);
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int s0 = share; s0 < splits; s0 += 32 * W) {  // lane j looks at part s0 + j W
+      float w = 0.f;
+      const int mine = s0 + lane * W;
+      if (mine < splits) {
+        w = ex2_approx((p.m[mine * rows + at] - ref) * kLog2e);
+        const float ls = p.l[mine * rows + at];
+        // a NaN stays one, whatever its part's maximum
+        if (w > 0.f || ls != ls) l += w * ls;
+      }
+      const int last = min(32, (splits - s0 + W - 1) / W);
+#pragma unroll 8
+      for (int j = 0; j < last; ++j) {
+        const float ws = __shfl_sync(0xffffffffu, w, j);
+        if (!(ws > 0.f)) continue;
+        const float* src = p.o + ((s0 + j * W) * rows + row) * d;
+        if (d == 128) {
+          const float4 v = reinterpret_cast<const float4*>(src)[lane];
+          acc.x = fmaf(ws, v.x, acc.x);
+          acc.y = fmaf(ws, v.y, acc.y);
+          acc.z = fmaf(ws, v.z, acc.z);
+          acc.w = fmaf(ws, v.w, acc.w);
+        } else {
+          const float2 v = reinterpret_cast<const float2*>(src)[lane];
+          acc.x = fmaf(ws, v.x, acc.x);
+          acc.y = fmaf(ws, v.y, acc.y);
+        }
       }
     }
+    l = warp_sum(l);
   }
-  l = warp_sum(l);
+  if (W > 1) {
+    sums[warp][lane] = acc;
+    if (lane == 0) totals[warp] = l;
+    __syncthreads();
+    if (share) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      const float4 v = sums[warp + w][lane];
+      acc.x += v.x;
+      acc.y += v.y;
+      acc.z += v.z;
+      acc.w += v.w;
+      l += totals[warp + w];
+    }
+  }
+  if (!there) return;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   acc.x *= inv;
   acc.y *= inv;
@@ -254,8 +276,12 @@ unsigned blocks_for(long long threads) {
 
 cudaError_t launch_cross_join(const CrossState& part, int splits, int B, int Nq, int Hq, int d, void* o, int o_dtype,
                               Lay ol, float* lse, cudaStream_t st) {
-  const long long blocks = ((long long)B * Nq * Hq * 32 + kThreads - 1) / kThreads;
-  const cudaError_t e = launch_pdl(cross_join_kernel, (int)blocks, kThreads, 0, st, part, splits, B, Nq, Hq, d, o, o_dtype, ol, lse);
+  const long long rows = (long long)B * Nq * Hq;
+  auto run = [&](auto kernel, int warps) {
+    const int per = kThreads / 32 / warps;
+    return launch_pdl(kernel, (int)((rows + per - 1) / per), kThreads, 0, st, part, splits, B, Nq, Hq, d, o, o_dtype, ol, lse);
+  };
+  const cudaError_t e = splits > 8 ? run(cross_join_kernel<8>, 8) : splits > 2 ? run(cross_join_kernel<2>, 2) : run(cross_join_kernel<1>, 1);
   if (e == cudaSuccess) count_launch();
   return e;
 }

@@ -383,8 +383,9 @@ struct RotaryArgs {
   int w_dtype;
   float* dw_parts;             // [2][blocks][d], backward
   // set by the launch
-  int G, parts;
-  long long units;
+  int flat;                   // every tensor's token t is at t rs
+  int G, heads, tile, parts;  // lanes of a row; heads and tokens of a warp's rows; parts of the heads
+  long long units;            // tiles of tokens x parts
 };
 constexpr int kRotMaxHead = 256;
 constexpr int kRotParts = 608;  // blocks of the backward kernel
@@ -396,7 +397,7 @@ int rot_exchange(int rot, int interleaved);
 void rot_units(RotaryArgs& a, int sms);
 
 // -------------------------------------------- norm and clipping of many tensors
-constexpr int kClipFew = 48, kClipMany = 1024;  // tensors a launch takes
+constexpr int kClipFew = 48, kClipSome = 320, kClipMany = 1024;  // tensors a launch takes
 constexpr int kClipParts = 608;                 // blocks of a launch
 template <int MAX>
 struct GradList {
@@ -411,8 +412,10 @@ template <int MAX>
 cudaError_t launch_grad_squares(const GradList<MAX>& a, double* parts, int* used, int sms, cudaStream_t st);
 template <int MAX>
 cudaError_t launch_grad_scale(const GradList<MAX>& a, const double* parts, int count, float max_norm, float eps,
-                              float* norm, int sms, cudaStream_t st);
-cudaError_t launch_grad_norm(const double* parts, int count, float* norm, cudaStream_t st);
+                              float* norm, const float2* factor, int sms, cudaStream_t st);
+// norm, and the factor where it is not NULL
+cudaError_t launch_grad_norm(const double* parts, int count, float max_norm, float eps, float* norm, float2* factor,
+                             cudaStream_t st);
 
 // -------------------------------------------- Newton-Schulz
 struct NsInput {

@@ -1,19 +1,26 @@
 // What the forward and the backward kernel of the rotary positions (with or without the
-// norm of each head) share: angles, and the exchange between the two columns of a pair.
+// norm of each head) share: angles, the layout of rows in a warp, and the exchange between
+// the two columns of a pair.
 //
 // Mathematics.  Pair i of a row at position p is turned by the angle p f_i:
 //   (x, y) -> A (x cos - y sin, x sin + y cos),
 // columns (i, i + rot/2) or (2i, 2i+1).  A frequency is held as F = round(2^64 f / 2 pi),
 // the 64-bit fixed-point fraction of a turn per position; p F mod 2^64 is the phase, so
 // that whole turns fall away by the wrap-around of an integer product and positions of any
-// size keep an error of at most |p| 2^-54 f / 2 pi turns (that of f itself, a double) plus
+// size keep an error of at most |p| 2^-56 turns (a double's rounding of f / 2 pi) plus
 // 2^-33.  No table is read.
 //
-// Organisation.  G lanes (d / 8 of them, rounded up to a power of two) hold one row, eight
-// columns (16 bytes of a 16-bit type) each; a warp holds 32 / G rows, of as many tokens,
-// and goes through their heads, so that the angles of a token are formed once, by the warp
-// that uses them, and stay in registers.  The kernels are bound by reading and writing the
-// rows.
+// Organisation.  A lane holds two pieces of eight columns (16 bytes of a 16-bit type) of a
+// row, so chosen that they hold whole pairs where rot/2 is a multiple of 8 (or pairs are
+// neighbours): the two columns of a pair meet in a thread, without an exchange.  G lanes
+// (d / 16, rounded up to a power of two) hold a row, a warp 32 / G rows: `heads` heads of a
+// token next to each other (of several tokens where there are fewer heads), and it goes
+// through the token's heads.  What the angles, and the norm's weights, do to a row is a
+// factor for each column and one for the column that shares its pair; a warp forms them
+// once for a token, in shared memory, from where each row's lanes read them: held in
+// registers they took a third of those, and of the warps that cover DRAM's latency.
+// Arithmetic is on pairs of fp32 (packed operations).  The kernels are bound by reading and
+// writing the rows, next to which issuing their instructions takes about as long.
 #pragma once
 
 #include "ra_device.cuh"
@@ -22,53 +29,80 @@ namespace ra {
 
 constexpr int kRotThreads = 256, kRotWarps = kRotThreads / 32;
 constexpr int kRotMaxD = kRotMaxHead;
+constexpr int kRotSmemSm = 227 * 1024;  // shared memory of an SM that blocks may have
 
-// How the other column of a pair is reached: within the thread; in a lane rot/16 further
-// (rot a multiple of 16); through shared memory.
-enum RotExchange { ROT_THREAD = 0, ROT_SHUFFLE = 1, ROT_STAGE = 2 };
+// Where the other column of a pair is: in the same piece; in the lane's other piece (rot a
+// multiple of 16); anywhere in the row, reached through shared memory.
+enum RotExchange { ROT_PIECE = 0, ROT_OTHER = 1, ROT_STAGE = 2 };
+
+// Dynamic shared memory of a block: frequencies | weights | per warp: the factors of its
+// tokens' columns, C then S (tile d floats each), and where q and k have weights of their own
+// another pair; staged rows (ROT_STAGE); sums of the weights' gradients (backward).
+template <int EX, bool BWD>
+struct RotSmem {
+  static constexpr int kWeights = kRotMaxD / 2 * 8;
+  static constexpr int kWarps = kWeights + 2 * kRotMaxD * 4;
+  static constexpr int kStageRow = 65;  // floats of one column in eight
+  int stage, sums, warp, bytes;         // in a warp's part; a warp's part; a block's
+  __host__ __device__ RotSmem(const RotaryArgs& a, int sides) {
+    stage = sides * 2 * a.tile * a.d * 4;
+    sums = stage + (EX == ROT_STAGE ? 8 * kStageRow * 4 + 32 : 0);  // 2112: a multiple of 16
+    warp = sums + (BWD ? 2 * (32 / a.G) * a.d * 4 : 0);
+    bytes = kWarps + kRotWarps * warp;
+  }
+};
 
 // Eight columns of one row as they are in memory.
 template <typename T>
 struct Raw8 {
   uint4 v[sizeof(T) / 2];
 };
+// What is not there keeps what r held.
 template <typename T>
-__device__ __forceinline__ Raw8<T> load8(const T* p, bool there) {
-  Raw8<T> r;
+__device__ __forceinline__ void load8(Raw8<T>& r, const T* p, bool there) {
+  if (there) {
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    r.v[i] = there ? reinterpret_cast<const uint4*>(p)[i] : make_uint4(0u, 0u, 0u, 0u);
-  return r;
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = reinterpret_cast<const uint4*>(p)[i];
+  }
 }
 template <typename T>
-__device__ __forceinline__ void unpack8(const Raw8<T>& r, float (&f)[8]) {
-  const T* e = reinterpret_cast<const T*>(r.v);
+__device__ __forceinline__ void zero8(Raw8<T>& r) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = to_f32(e[j]);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.v[i] = make_uint4(0u, 0u, 0u, 0u);
 }
+__device__ __forceinline__ float2 pair_of(uint32_t v, __nv_bfloat16) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 pair_of(uint32_t v, __half) { return unpack_half2(v); }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
+__device__ __forceinline__ void unpack8(const Raw8<T>& r, float2 (&f)[4]) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
-  } else {
-    __align__(16) T e[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = from_f32<T>(f[j]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(e);
+    for (int i = 0; i < 2; ++i) {
+      f[2 * i] = make_float2(__uint_as_float(r.v[i].x), __uint_as_float(r.v[i].y));
+      f[2 * i + 1] = make_float2(__uint_as_float(r.v[i].z), __uint_as_float(r.v[i].w));
+    }
+  } else {
+    f[0] = pair_of(r.v[0].x, T());
+    f[1] = pair_of(r.v[0].y, T());
+    f[2] = pair_of(r.v[0].z, T());
+    f[3] = pair_of(r.v[0].w, T());
   }
 }
+__device__ __forceinline__ uint32_t pack_pair(float2 f, __nv_bfloat16) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_pair(float2 f, __half) { return pack_half2(f.x, f.y); }
 template <typename T>
-__device__ __forceinline__ Raw8<T> shuffle8(const Raw8<T>& r, int lane) {
-  Raw8<T> o;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-    o.v[i].x = __shfl_sync(0xffffffffu, r.v[i].x, lane);
-    o.v[i].y = __shfl_sync(0xffffffffu, r.v[i].y, lane);
-    o.v[i].z = __shfl_sync(0xffffffffu, r.v[i].z, lane);
-    o.v[i].w = __shfl_sync(0xffffffffu, r.v[i].w, lane);
+__device__ __forceinline__ void store8(T* p, const float2 (&f)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  } else {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack_pair(f[0], T()), pack_pair(f[1], T()), pack_pair(f[2], T()), pack_pair(f[3], T()));
   }
-  return o;
 }
 
 __device__ __forceinline__ float load_any(const void* p, int dtype, int i) {
@@ -105,10 +139,10 @@ __device__ __forceinline__ unsigned long long fixed_turns(double f) {
   return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
 }
 
-__device__ __forceinline__ long long rot_position(const RotaryArgs& a, long long b, long long n) {
+__device__ __forceinline__ long long rot_position(const RotaryArgs& a, long long b, int n) {
   if (a.positions) return __ldg(a.positions + b * a.pos_bstride + n);
   if (a.striped) {
-    const long long host = n / a.S;
+    const int host = n / a.S;
     n = (n - host * a.S) * a.P + host;
   }
   return a.pos_off + n;
@@ -116,109 +150,179 @@ __device__ __forceinline__ long long rot_position(const RotaryArgs& a, long long
 
 // Sum over the G lanes of a row.
 __device__ __forceinline__ float group_sum(float v, int G) {
-  for (int o = G >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+    if (o < G) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// A warp's place: lane c of group g, which holds the row of token t0 + g.
+// A lane's place: group g holds the row of a token (t0 + token) and a head (h + head), this
+// lane its columns e[0] .. + 8 and e[1] .. + 8 where they are there.
 struct RotLane {
-  int g, c, partner;   // partner: lane that holds the pairs' other columns (ROT_SHUFFLE)
-  bool column;         // this lane holds columns of the row
-  uint32_t turned;     // bit j: column 8 c + j belongs to a pair
+  int g, s, token, head;
+  int e[2];
+  bool there[2];
+  uint32_t turned[2];  // bit j: column e + j belongs to a pair
 };
 template <int EX>
 __device__ __forceinline__ RotLane rot_lane(const RotaryArgs& a) {
   RotLane l;
-  const int lane = (int)lane_id();
+  const int lane = (int)lane_id(), pieces = a.d / 8;
   l.g = lane / a.G;
-  l.c = lane - l.g * a.G;
-  l.column = l.c * 8 < a.d;
-  const int left = a.rot - 8 * l.c;
-  l.turned = left >= 8 ? 0xffu : left > 0 ? (1u << left) - 1u : 0u;
-  l.partner = lane;
-  if (EX == ROT_SHUFFLE && left > 0) l.partner = l.c * 16 < a.rot ? lane + a.rot / 16 : lane - a.rot / 16;
+  l.s = lane - l.g * a.G;
+  l.token = l.g / a.heads;
+  l.head = l.g - l.token * a.heads;
+  int p[2];
+  const int pairs = EX == ROT_OTHER ? a.rot / 16 : 0;  // lanes that hold pairs of pieces
+  if (l.s < pairs) {
+    p[0] = l.s;
+    p[1] = l.s + pairs;
+  } else {
+    const int rest = pieces - 2 * pairs, step = (rest + 1) / 2;
+    p[0] = 2 * pairs + l.s - pairs;
+    p[1] = p[0] + step;
+    if (l.s - pairs >= step) p[0] = p[1] = pieces;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    l.there[i] = p[i] < pieces;
+    l.e[i] = 8 * p[i];
+    const int left = a.rot - l.e[i];
+    l.turned[i] = !l.there[i] || left <= 0 ? 0u : left >= 8 ? 0xffu : (1u << left) - 1u;
+  }
   return l;
 }
 
-// The other columns of the pairs of this lane's eight (0 for columns of no pair, whose
-// factor is -0: x 1 + 0 (-0) is x, whatever the neighbour holds).  `stage`: 8 x 33 floats
-// of the warp; column p of a group's row sits at [p % 8][g G + p / 8], so that neither the
-// writes nor the reads, at any distance, meet in a bank.
-template <int EX, typename T>
-__device__ __forceinline__ void other_columns(const RotaryArgs& a, const RotLane& l, const Raw8<T>& raw,
-                                              const float (&f)[8], float (&p)[8], float* stage) {
-  if constexpr (EX == ROT_THREAD) {
+// The other columns of the pairs of this lane's columns; 0 for columns of no pair, whose
+// factor is -0 (x 1 + 0 (-0) is x, whatever the neighbour holds).  ALL: every column
+// belongs to a pair.  `stage`: column p of a group's row sits at [p % 8][g 2G + p / 8], so
+// that neither the writes nor the reads, at any distance, meet in a bank.
+template <int EX, bool ALL>
+__device__ __forceinline__ void other_columns(const RotaryArgs& a, const RotLane& l, const float2 (&f)[2][4],
+                                              float2 (&p)[2][4], float* stage) {
+  if constexpr (EX == ROT_STAGE) {
+    constexpr int R = RotSmem<EX, false>::kStageRow;
+    const int half = a.rot / 2, row = l.g * 2 * a.G;
+    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) p[j] = (l.turned >> j) & 1u ? f[j ^ 1] : 0.f;
-  } else if constexpr (EX == ROT_SHUFFLE) {
-    unpack8(shuffle8(raw, l.partner), p);
-    if (!l.turned) {
+    for (int i = 0; i < 2; ++i)
+      if (l.there[i]) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) p[j] = 0.f;
-    }
+        for (int j = 0; j < 4; ++j) {
+          stage[2 * j * R + row + l.e[i] / 8] = f[i][j].x;
+          stage[(2 * j + 1) * R + row + l.e[i] / 8] = f[i][j].y;
+        }
+      }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = l.e[i] + j, at = e < half ? e + half : e - half;
+        const float v = (l.turned[i] >> j) & 1u ? stage[(at & 7) * R + row + (at >> 3)] : 0.f;
+        if (j & 1) p[i][j / 2].y = v;
+        else p[i][j / 2].x = v;
+      }
   } else {
-    const int lane = (int)lane_id(), half = a.rot / 2;
-    __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) stage[j * 33 + lane] = f[j];
-    __syncwarp();
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = 8 * l.c + j, at = e < half ? e + half : e - half;
-      p[j] = (l.turned >> j) & 1u ? stage[(at & 7) * 33 + l.g * a.G + (at >> 3)] : 0.f;
-    }
+      for (int j = 0; j < 4; ++j) {
+        const float2 o = EX == ROT_OTHER ? f[1 - i][j] : make_float2(f[i][j].y, f[i][j].x);
+        const bool turned = ALL || ((EX == ROT_OTHER ? l.turned[i] : l.turned[i] >> (2 * j)) & 1u);
+        p[i][j] = turned ? o : make_float2(0.f, 0.f);
+      }
   }
 }
 
-// Factors of this lane's columns and of their pairs' other columns.  DIR: 1 turns by the
-// angle, -1 by its opposite (the transpose, for gradients).
-template <int EX, int DIR>
-__device__ __forceinline__ void rot_factors(const RotaryArgs& a, const RotLane& l, const float2* cs, float (&C)[8],
-                                            float (&S)[8]) {
-  const int half = a.rot / 2;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const int e = 8 * l.c + j;
-    C[j] = 1.f;
-    S[j] = -0.f;
-    if ((l.turned >> j) & 1u) {
-      const bool second = EX == ROT_THREAD ? j & 1 : e >= half;
-      const float2 t = cs[l.g * half + (EX == ROT_THREAD ? e >> 1 : second ? e - half : e)];
-      C[j] = t.x;
-      S[j] = (second ? DIR : -DIR) * t.y;
-    }
+// Column c of a token's factors: the first four of each eight, then the others, so that the
+// lanes' reads of four lie beside each other.
+__device__ __forceinline__ int rot_column(int d, int c) { return (c & 4 ? d / 2 : 0) + (c >> 3) * 4 + (c & 3); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// Eight columns' values: at p, and `half` floats further.
+__device__ __forceinline__ void columns8(float2 (&v)[4], const float* p, int half) {
+  const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + half);
+  v[0] = make_float2(x.x, x.y);
+  v[1] = make_float2(x.z, x.w);
+  v[2] = make_float2(y.x, y.y);
+  v[3] = make_float2(y.z, y.w);
+}
+
+// Batch entry and row of a token.
+__device__ __forceinline__ void rot_token(const RotaryArgs& a, long long t, long long* b, long long* n) {
+  if (a.N == a.tokens) {
+    *b = 0;
+    *n = t;
+  } else if (a.tokens < (1ll << 31)) {
+    const uint32_t q = (uint32_t)t / (uint32_t)a.N;
+    *b = q;
+    *n = (uint32_t)t - q * (uint32_t)a.N;
+  } else {
+    *b = t / a.N;
+    *n = t - *b * a.N;
   }
 }
 
-// The column that shares a pair with column e.
+// Offset of row (token t, head h); t = b N + n.
+__device__ __forceinline__ long long rot_offset(const RotaryArgs& a, const Lay& L, long long t, long long b, long long n, int h) {
+  return a.flat ? t * L.rs + h * L.hs : lay_at(L, b, n, h);
+}
+
+// The columns of a pair.
 template <int EX>
-__device__ __forceinline__ int other_column(const RotaryArgs& a, int e) {
-  if (EX == ROT_THREAD) return e ^ 1;
-  return e < a.rot / 2 ? e + a.rot / 2 : e - a.rot / 2;
+__device__ __forceinline__ void rot_pair(const RotaryArgs& a, int pair, int* x, int* y) {
+  *x = EX == ROT_PIECE ? 2 * pair : pair;
+  *y = EX == ROT_PIECE ? 2 * pair + 1 : pair + a.rot / 2;
 }
 
-// cos and sin of every pair of the warp's tokens.
-template <bool FAST>
-__device__ __forceinline__ void rot_angles(const RotaryArgs& a, const unsigned long long* freq, long long t0,
-                                           float2* cs) {
-  const int half = a.rot / 2, rows = 32 / a.G;
+// The factors of a warp's tokens t0, t0 + 1, ...: C of each column, S of the column that
+// shares its pair (1 and -0 where none does).  With WEIGHTS those of q, then those of k, times
+// the weights (w, w + d) of the columns that they multiply.  DIR: 1 turns by the angle, -1 by
+// its opposite (the transpose, for gradients).
+template <int EX, bool FAST, int DIR, bool WEIGHTS>
+__device__ __forceinline__ void rot_factors(const RotaryArgs& a, const unsigned long long* freq, const float* w, long long t0,
+                                            float* factors) {
+  const int half = a.rot / 2, S = a.tile * a.d;
   __syncwarp();
-  if (half)
-    for (int i = (int)lane_id(); i < rows * half; i += 32) {
-      const int g = i / half;
-      const long long t = t0 + g;
-      if (t < a.tokens) {
-        const long long b = t / a.N;
-        cs[i] = turn<FAST>(freq[i - g * half], rot_position(a, b, t - b * a.N), a.amplitude);
+  for (int g = 0; g < a.tile && t0 + g < a.tokens; ++g, factors += a.d) {
+    if (half) {
+      long long b, n;
+      rot_token(a, t0 + g, &b, &n);
+      const long long pos = rot_position(a, b, (int)n);
+      for (int j = (int)lane_id(); j < half; j += 32) {
+        const float2 t = turn<FAST>(freq[j], pos, a.amplitude);
+        int x, y;
+        rot_pair<EX>(a, j, &x, &y);
+        float* const fx = factors + rot_column(a.d, x);
+        float* const fy = factors + rot_column(a.d, y);
+#pragma unroll
+        for (int side = 0; side < (WEIGHTS ? 2 : 1); ++side) {
+          const float wx = WEIGHTS ? w[side * a.d + x] : 1.f, wy = WEIGHTS ? w[side * a.d + y] : 1.f;
+          fx[2 * side * S] = t.x * wx;
+          fy[2 * side * S] = t.x * wy;
+          fx[(2 * side + 1) * S] = -DIR * t.y * wy;
+          fy[(2 * side + 1) * S] = DIR * t.y * wx;
+        }
       }
     }
+    for (int c = a.rot + (int)lane_id(); c < a.d; c += 32) {
+      float* const f = factors + rot_column(a.d, c);
+#pragma unroll
+      for (int side = 0; side < (WEIGHTS ? 2 : 1); ++side) {
+        f[2 * side * S] = WEIGHTS ? w[side * a.d + c] : 1.f;
+        f[(2 * side + 1) * S] = -0.f;
+      }
+    }
+  }
   __syncwarp();
 }
 
-// Heads [first, last) of part `part` of `parts`.
-__device__ __forceinline__ void rot_heads(int H, int part, int parts, int* first, int* last) {
-  *first = (int)((long long)H * part / parts);
-  *last = (int)((long long)H * (part + 1) / parts);
+// Heads [first, last) of part `part` of a.parts, whole steps of a warp but for the last.
+__device__ __forceinline__ void rot_heads(const RotaryArgs& a, int H, int part, int* first, int* last) {
+  const int steps = (H + a.heads - 1) / a.heads;
+  *first = a.parts == 1 ? 0 : steps * part / a.parts * a.heads;
+  *last = a.parts == 1 ? H : min(H, steps * (part + 1) / a.parts * a.heads);
 }
 
 // 2^-70 where the sum of squares left fp32's range (or is NaN), else 1.

@@ -11,116 +11,165 @@
 namespace ra {
 namespace {
 
+// Blocks of an SM: 128 registers a thread.  (131072 tokens of 16 + 4 heads of 128, bf16: 440
+// us; with three, whose 80 registers spill, 500 at best.)
+constexpr int kBlocks = 2;
+
+template <typename T, typename TG, typename TO, int EX, bool ALL>
+__device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane& l, const RotarySide& side, const float* weight,
+                                              const float* factors, const T* x, const TG* dy,
+                                              TO* out, bool token, int h0, int h1, float* stage, float* sums) {
+  const long long x_step = a.heads * side.xl.hs, dy_step = a.heads * side.dyl.hs, out_step = a.heads * side.yl.hs;
+  const float inv_d = 1.f / (float)a.d;
+  Raw8<T> rx[2];   // zeros, or rows before, in columns that are not there
+  Raw8<TG> rg[2];
+  float2 dw[2][4];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    zero8(rx[i]);
+    zero8(rg[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dw[i][j] = both(0.f);
+  const float *C[2], *W[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    C[i] = factors + l.token * a.d + (l.there[i] ? l.e[i] / 2 : 0);
+    W[i] = weight + (l.there[i] ? l.e[i] : 0);
+  }
+  for (int h = h0; h < h1; h += a.heads, x += x_step, dy += dy_step, out += out_step) {
+    const bool row = token && h + l.head < h1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      load8(rx[i], x + l.e[i], row && l.there[i]);
+      load8(rg[i], dy + l.e[i], row && l.there[i]);
+    }
+    float2 f[2][4], g[2][4], p[2][4], s2 = both(0.f), d2 = both(0.f);
+    unpack8(rg[0], g[0]);
+    unpack8(rg[1], g[1]);
+    other_columns<EX, ALL>(a, l, g, p, stage);
+    unpack8(rx[0], f[0]);
+    unpack8(rx[1], f[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 c[4], sn[4], w[4];
+      columns8(c, C[i], a.d / 2);
+      columns8(sn, C[i] + a.tile * a.d, a.d / 2);
+      columns8(w, W[i], 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        g[i][j] = __ffma2_rn(g[i][j], c[j], __fmul2_rn(p[i][j], sn[j]));
+        p[i][j] = __fmul2_rn(g[i][j], w[j]);
+        s2 = __ffma2_rn(f[i][j], f[i][j], s2);
+        d2 = __ffma2_rn(p[i][j], f[i][j], d2);
+      }
+    }
+    float sum = group_sum(s2.x + s2.y, a.G), dot = group_sum(d2.x + d2.y, a.G), eps = a.eps, sc = 1.f;
+    if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
+      sc = rot_scale(sum);
+      sum = dot = 0.f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f[i][j] = __fmul2_rn(f[i][j], both(sc));
+          sum = fmaf(f[i][j].y, f[i][j].y, fmaf(f[i][j].x, f[i][j].x, sum));
+          dot = fmaf(p[i][j].y, f[i][j].y, fmaf(p[i][j].x, f[i][j].x, dot));
+        }
+      sum = group_sum(sum, a.G);
+      dot = group_sum(dot, a.G);
+      eps *= sc * sc;
+    }
+    const float r = rsqrtf(fmaf(sum, inv_d, eps));
+    const float2 r2 = both(r), along = both(-dot * r * inv_d), rs = both(r * sc);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float2 dx[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 normed = __fmul2_rn(f[i][j], r2);
+        if (row) dw[i][j] = __ffma2_rn(g[i][j], normed, dw[i][j]);
+        dx[j] = __fmul2_rn(rs, __ffma2_rn(normed, along, p[i][j]));
+      }
+      if (row && l.there[i]) store8(out + l.e[i], dx);
+    }
+  }
+  // this lane's own sums in shared memory
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (l.there[i]) {
+      float4* p = reinterpret_cast<float4*>(sums + l.g * a.d + l.e[i]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float4 v = p[j];
+        v.x += dw[i][2 * j].x;
+        v.y += dw[i][2 * j].y;
+        v.z += dw[i][2 * j + 1].x;
+        v.w += dw[i][2 * j + 1].y;
+        p[j] = v;
+      }
+    }
+}
+
 template <typename T, typename TG, typename TO, int EX>
-__global__ void __launch_bounds__(kRotThreads, 2) norm_rotary_bwd_kernel(const __grid_constant__ RotaryArgs a) {
-  __shared__ unsigned long long freq[kRotMaxD / 2];
-  __shared__ float weight[2][kRotMaxD];
-  __shared__ float2 angles[kRotWarps][kRotMaxD / 2];
-  __shared__ float stages[EX == ROT_STAGE ? kRotWarps : 1][EX == ROT_STAGE ? 8 * 33 : 1];
-  __shared__ float sums[kRotWarps][kRotMaxD];
-  constexpr int U = 2;  // rows in flight
-  const int warp = threadIdx.x >> 5;
+__global__ void __launch_bounds__(kRotThreads, kBlocks) norm_rotary_bwd_kernel(const __grid_constant__ RotaryArgs a) {
+  using Smem = RotSmem<EX, true>;
+  const Smem L(a, 1);
+  extern __shared__ __align__(16) uint8_t smem[];
+  unsigned long long* freq = reinterpret_cast<unsigned long long*>(smem);
+  float* weight = reinterpret_cast<float*>(smem + Smem::kWeights);
+  const int warp = threadIdx.x >> 5, groups = 32 / a.G;
+  auto of_warp = [&](int w, int at) { return smem + Smem::kWarps + w * L.warp + at; };
+  float* factors = reinterpret_cast<float*>(of_warp(warp, 0));
+  float* stage = reinterpret_cast<float*>(of_warp(warp, L.stage));
+  float* sums = reinterpret_cast<float*>(of_warp(warp, L.sums));  // [side][group][d]
+  const RotLane l = rot_lane<EX>(a);
+  const long long first = (long long)blockIdx.x * kRotWarps + warp, step = (long long)gridDim.x * kRotWarps;
   for (int i = threadIdx.x; i < a.rot / 2; i += kRotThreads) freq[i] = fixed_turns(a.freq[i]);
   for (int i = threadIdx.x; i < 2 * a.d; i += kRotThreads) {
     const int side = i >= a.d, c = i - side * a.d;
-    weight[side][c] = a.side[side].w ? load_any(a.side[side].w, a.w_dtype, c) : 1.f;
+    weight[i] = a.side[side].w ? load_any(a.side[side].w, a.w_dtype, c) : 1.f;
   }
+  for (int i = (int)lane_id(); i < 2 * groups * a.d; i += 32) sums[i] = 0.f;
   __syncthreads();
-  const RotLane l = rot_lane<EX>(a);
-  float2* cs = angles[warp];
-  float* stage = stages[EX == ROT_STAGE ? warp : 0];
-  const float inv_d = 1.f / (float)a.d;
-  float dw[2][8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) dw[0][j] = dw[1][j] = 0.f;
-  const long long first = (long long)blockIdx.x * kRotWarps + warp, step = (long long)gridDim.x * kRotWarps;
   for (long long unit = first; unit < a.units; unit += step) {
-    const long long tile = unit / a.parts;
+    const long long tile = a.parts == 1 ? unit : unit / a.parts;
     const int part = (int)(unit - tile * a.parts);
-    const long long t0 = tile * (32 / a.G), t = t0 + l.g;
-    rot_angles<sizeof(T) == 2>(a, freq, t0, cs);
-    const bool there = l.column && t < a.tokens;
-    const long long b = t / a.N, n = t - b * a.N;
-    float C[8], S[8];
-    rot_factors<EX, -1>(a, l, cs, C, S);
-    auto rows = [&](const RotarySide& s, const float* ws, float (&dws)[8]) {
+    const long long t0 = tile * a.tile;
+    rot_factors<EX, sizeof(T) == 2, -1, false>(a, freq, nullptr, t0, factors);
+    const bool token = t0 + l.token < a.tokens;
+    const long long t = token ? t0 + l.token : t0;
+    long long b, n;
+    rot_token(a, t, &b, &n);
+#pragma unroll 1
+    for (int side = 0; side < 2; ++side) {
+      const RotarySide& s = a.side[side];
       int h0, h1;
-      rot_heads(s.H, part, a.parts, &h0, &h1);
-      if (h0 == h1) return;
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = l.column ? ws[8 * l.c + j] : 0.f;
-      const T* x = static_cast<const T*>(s.x) + lay_at(s.xl, b, n, 0) + 8 * l.c;
-      const TG* dy = static_cast<const TG*>(s.dy) + lay_at(s.dyl, b, n, 0) + 8 * l.c;
-      TO* out = static_cast<TO*>(s.y) + lay_at(s.yl, b, n, 0) + 8 * l.c;
-      for (int h = h0; h < h1; h += U) {
-        Raw8<T> rx[U];
-        Raw8<TG> rg[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          rx[u] = load8(x + (h + u) * s.xl.hs, there && h + u < h1);
-          rg[u] = load8(dy + (h + u) * s.dyl.hs, there && h + u < h1);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (h + u >= h1) break;
-          float f[8], g[8], p[8], dx[8];
-          unpack8(rg[u], g);
-          other_columns<EX>(a, l, rg[u], g, p, stage);
-          unpack8(rx[u], f);
-          float sum = 0.f, dot = 0.f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            g[j] = fmaf(g[j], C[j], p[j] * S[j]);
-            sum = fmaf(f[j], f[j], sum);
-            dot = fmaf(g[j] * w[j], f[j], dot);
-          }
-          sum = group_sum(sum, a.G);
-          dot = group_sum(dot, a.G);
-          float eps = a.eps, sc = 1.f;
-          if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
-            sc = rot_scale(sum);
-            sum = dot = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              f[j] *= sc;
-              sum = fmaf(f[j], f[j], sum);
-              dot = fmaf(g[j] * w[j], f[j], dot);
-            }
-            sum = group_sum(sum, a.G);
-            dot = group_sum(dot, a.G);
-            eps *= sc * sc;
-          }
-          const float r = rsqrtf(fmaf(sum, inv_d, eps)), along = dot * r * inv_d, rs = r * sc;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float normed = f[j] * r;
-            dws[j] = fmaf(g[j], normed, dws[j]);
-            dx[j] = rs * fmaf(-normed, along, g[j] * w[j]);
-          }
-          if (there) store8(out + (h + u) * s.yl.hs, dx);
-        }
-      }
-    };
-    rows(a.side[0], weight[0], dw[0]);
-    rows(a.side[1], weight[1], dw[1]);
+      rot_heads(a, s.H, part, &h0, &h1);
+      if (h0 == h1) continue;
+      const T* x = static_cast<const T*>(s.x) + rot_offset(a, s.xl, t, b, n, h0 + l.head);
+      const TG* dy = static_cast<const TG*>(s.dy) + rot_offset(a, s.dyl, t, b, n, h0 + l.head);
+      TO* out = static_cast<TO*>(s.y) + rot_offset(a, s.yl, t, b, n, h0 + l.head);
+      if (EX != ROT_STAGE && a.rot == a.d)
+        gradient_rows<T, TG, TO, EX, EX != ROT_STAGE>(a, l, s, weight + side * a.d, factors, x, dy, out, token, h0, h1, stage,
+                                                      sums + side * groups * a.d);
+      else
+        gradient_rows<T, TG, TO, EX, false>(a, l, s, weight + side * a.d, factors, x, dy, out, token, h0, h1, stage,
+                                            sums + side * groups * a.d);
+    }
   }
-  // the block's sums: over the rows of a warp, then over its warps, in order
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float v = dw[side][j];
-      for (int o = a.G; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (l.g == 0 && l.column) sums[warp][8 * l.c + j] = v;
+  // the block's sums, over groups and warps in order
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.d; i += kRotThreads) {
+    const int side = i >= a.d, c = i - side * a.d;
+    float v = 0.f;
+    for (int w = 0; w < kRotWarps; ++w) {
+      const float* from = reinterpret_cast<const float*>(of_warp(w, L.sums)) + side * groups * a.d + c;
+      for (int g = 0; g < groups; ++g) v += from[g * a.d];
     }
-    __syncthreads();
-    for (int c = threadIdx.x; c < a.d; c += kRotThreads) {
-      float v = sums[0][c];
-      for (int i = 1; i < kRotWarps; ++i) v += sums[i][c];
-      a.dw_parts[((long long)side * gridDim.x + blockIdx.x) * a.d + c] = v;
-    }
-    __syncthreads();
+    a.dw_parts[((long long)side * gridDim.x + blockIdx.x) * a.d + c] = v;
   }
 }
 
@@ -145,18 +194,20 @@ __global__ void __launch_bounds__(1024) rotary_dw_kernel(const float* parts, int
 
 template <typename T, typename TG, typename TO>
 cudaError_t run(const RotaryArgs& a, int exchange, float* dwq, float* dwk, int sms, cudaStream_t st) {
-  auto go = [&](auto kernel) {
-    const long long want = (a.units + kRotWarps - 1) / kRotWarps, most = 2ll * sms < kRotParts ? 2ll * sms : kRotParts;
+  auto go = [&](auto kernel, int smem) {
+    const long long want = (a.units + kRotWarps - 1) / kRotWarps, most = (long long)kBlocks * sms < kRotParts ? (long long)kBlocks * sms : kRotParts;
     const int blocks = (int)(want < most ? want : most);
-    kernel<<<blocks, kRotThreads, 0, st>>>(a);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<blocks, kRotThreads, smem, st>>>(a);
+    e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_pdl(rotary_dw_kernel, (a.d + 31) / 32 * 2, 1024, 0, st, a.dw_parts, blocks, a.d, dwq, dwk);
     if (e == cudaSuccess) count_launch(2);
     return e;
   };
-  if (exchange == ROT_THREAD) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_THREAD>);
-  if (exchange == ROT_SHUFFLE) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_SHUFFLE>);
-  return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_STAGE>);
+  if (exchange == ROT_PIECE) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_PIECE>, RotSmem<ROT_PIECE, true>(a, 1).bytes);
+  if (exchange == ROT_OTHER) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_OTHER>, RotSmem<ROT_OTHER, true>(a, 1).bytes);
+  return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_STAGE>, RotSmem<ROT_STAGE, true>(a, 1).bytes);
 }
 
 }  // namespace
