@@ -25,6 +25,7 @@ import ctypes
 import os
 import threading
 from array import array
+from operator import attrgetter
 
 import torch
 
@@ -1094,16 +1095,20 @@ def ra_grad_workspace_bytes(count):
 
 _data_ptr, _numel, _contiguous, _get_device = (torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.is_contiguous,
                                                torch.Tensor.get_device)
+_dtype_of = attrgetter("dtype")
 
 
 def _grad_arrays(tensors, name, dev):
-    """Host arrays of addresses, sizes and dtype codes.  A list may have hundreds of tensors:
-    each property is taken of all of them at once."""
+    """Addresses and dtype codes (arrays) and sizes (a list).  There may be hundreds of tensors:
+    each property is taken of all of them at once (0.3 us a tensor)."""
     if {*map(_get_device, tensors)} != {dev} or not all(map(_contiguous, tensors)):
         raise RAError(1, f"{name} must be contiguous tensors on one device")
-    dtypes = [t.dtype for t in tensors]
-    codes = {t: _code(t) for t in {*dtypes}}
-    return (array("q", map(_data_ptr, tensors)), array("q", map(_numel, tensors)), array("i", map(codes.get, dtypes)))
+    codes = {t: _code(t) for t in {*map(_dtype_of, tensors)}}
+    if len(codes) == 1:
+        types = array("i", codes.values()) * len(tensors)
+    else:
+        types = array("i", [codes[t.dtype] for t in tensors])
+    return array("q", list(map(_data_ptr, tensors))), list(map(_numel, tensors)), types
 
 
 def _address(a):
@@ -1113,8 +1118,8 @@ def _address(a):
 def _grad_call(grads, norm, workspace, nbytes, max_norm, outs, eps, stream, dev):
     """max_norm None: the norm alone."""
     n, lib = len(grads), _lib()
-    ptrs, sizes, dtypes = _grad_arrays(grads, "grads", dev)
-    handle = _stream_handle(stream, dev)
+    ptrs, numels, dtypes = _grad_arrays(grads, "grads", dev)
+    sizes, handle = array("q", numels), _stream_handle(stream, dev)
     if max_norm is None:
         code = lib.ra_grad_norm(_address(ptrs), _address(sizes), _address(dtypes), n, norm.data_ptr(),
                                 workspace.data_ptr(), nbytes, handle)
@@ -1125,7 +1130,7 @@ def _grad_call(grads, norm, workspace, nbytes, max_norm, outs, eps, stream, dev)
         if len(outs) != n:
             raise RAError(1, f"outs must have {n} tensors (got {len(outs)})")
         out_ptrs, out_sizes, out_dtypes = _grad_arrays(outs, "outs", dev)
-        if out_sizes != sizes:
+        if out_sizes != numels:
             raise RAError(1, "outs must have the sizes of grads")
         code = lib.ra_grad_clip(_address(ptrs), _address(sizes), _address(dtypes), n, max_norm, eps, _address(out_ptrs),
                                 _address(out_dtypes), norm.data_ptr(), workspace.data_ptr(), nbytes, handle)

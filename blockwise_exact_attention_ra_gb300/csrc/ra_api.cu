@@ -2316,7 +2316,7 @@ int check_cross(const ra_shape& shape, int dtype, int flags, Shape* s) {
   if ((rc = check_shape(shape, s))) return rc;
   if (s->d != 64 && s->d != 128) return fail(RA_ERR_UNSUPPORTED, "cross attention supports d in {64, 128} (got %d)", s->d);
   const long long tiles = ((long long)s->Nq + 127) / 128, keys = ((long long)s->Nkv + 127) / 128;
-  if ((long long)s->B * s->Hq * tiles > (1 << 22) || (long long)s->B * s->Hkv * keys > (1 << 22) ||
+  if ((long long)s->B * s->Hq * tiles > (1 << 24) || (long long)s->B * s->Hkv * keys > (1 << 24) ||
       tiles * (s->Hq / s->Hkv) >= (1 << 20))
     return fail(RA_ERR_UNSUPPORTED, "too many tiles of queries or keys");
   return RA_OK;
@@ -2344,14 +2344,32 @@ int cross_parts(long long units, long long tiles, double tile, double ends, doub
   return best;
 }
 
-CrossPlan cross_plan(const Shape& s, int dtype, int flags) {
+// The same for a few queries: `slots` blocks at a time share 6.2 TB/s (us; a block's start and
+// end, and the join, measured).  Where batch entries differ in length no wave is waited for.
+int cross_few_parts(const Shape& s, int slots, bool ragged) {
+  const double units = (double)s.B * s.Hkv, alone = (double)s.Nkv * s.d * 4. * slots / 6.2e6;
+  const int most = (s.Nkv + 127) / 128 < 256 ? (s.Nkv + 127) / 128 : 256;
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n <= most; ++n) {
+    const double w = units * n / slots, waves = w < 1. ? 1. : ragged ? w : ceil(w);
+    const double t = waves * (alone / n + 3.) + (n > 1 ? 4. + 0.03 * n : 0.);
+    if (t < least * 0.99) {
+      least = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
+CrossPlan cross_plan(const Shape& s, int dtype, int flags, bool ragged) {
   CrossPlan p{};
   const int group = s.Hq / s.Hkv;
   const long long tiles = (s.Nkv + 127) / 128;
   p.few = (long long)s.Nq * group <= kCrossFewRows;
   if (p.few) {
-    const long long units = (long long)s.B * s.Hkv, want = (608 + units - 1) / units, most = (s.Nkv + 255) / 256;
-    p.splits = (int)(want < most ? want : most);
+    const int blocks = s.d == 128 ? 2 : s.Nq * group <= 16 ? 4 : 3;  // of an SM
+    p.splits = cross_few_parts(s, blocks * kPlanSms, ragged);
   } else {
     p.bf16_p = dtype == RA_BF16 && !(flags & RA_PRECISE) && (long long)s.Nq * group <= 512;
     const int pairs = ((s.Nq + 127) / 128 + 1) / 2;
@@ -2418,7 +2436,8 @@ extern "C" {
 size_t ra_cross_fwd_workspace_bytes(ra_dtype dtype, ra_shape shape, int flags) {
   Shape s;
   if (check_cross(shape, dtype, flags, &s)) return 0;
-  return cross_plan(s, dtype, flags).total;
+  const size_t a = cross_plan(s, dtype, flags, false).total, b = cross_plan(s, dtype, flags, true).total;
+  return a > b ? a : b;
 }
 
 int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra_shape shape, const int* kv_len, int flags,
@@ -2430,7 +2449,7 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
   if ((rc = check_scale(scale)) || (rc = check_ptr(q, "q")) || (rc = check_ptr(k, "k")) || (rc = check_ptr(v, "v")) ||
       (rc = check_ptr(o, "o")) || (rc = check_floats(lse, "lse")) || (rc = check_len(kv_len)))
     return rc;
-  const CrossPlan p = cross_plan(s, dtype, flags);
+  const CrossPlan p = cross_plan(s, dtype, flags, kv_len != nullptr);
   if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
@@ -2453,8 +2472,8 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
     const void* v16 = v;
     if (bf && !p.bf16_p) {
       v16 = ws + p.v16;
-      if ((e = launch_cross_keys(nullptr, v, 1, s.kvl, nullptr, ws + p.v16, s.B, s.Nkv, s.Hkv, s.d, kv_len, st, cs)) != cudaSuccess)
-        return cuda_fail(e, "v -> fp16 launch");
+      const CrossKeysArgs c{nullptr, v, nullptr, ws + p.v16, 1, s.B, s.Nkv, s.Hkv, s.d, s.kvl, kv_len, st};
+      if ((e = launch_cross_keys(c, cs)) != cudaSuccess) return cuda_fail(e, "v -> fp16 launch");
     }
     TcFwdArgs a;
     memset(&a, 0, sizeof a);
@@ -2520,12 +2539,15 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
     r.q16 = ws + p.q16;
     r.do16 = ws + p.do16;
   }
+  // dS times 2^m: a key's share of a row's probability is about 1 / Nkv, and a dS of 2^10 still fits
+  int m = 0;
+  while (m < 6 && (1ll << (m + 10)) < s.Nkv) ++m;
+  r.d_mul = ldexpf(1.f, m - kCrossP);
   r.D = reinterpret_cast<float*>(ws + p.D);
   r.lse2 = reinterpret_cast<float*>(ws + p.lse2);
   r.dq_acc = reinterpret_cast<float*>(ws + p.dq);
   r.sched = reinterpret_cast<unsigned int*>(ws + p.sched);
   r.status = st;
-  if ((e = launch_cross_rows(r, cs)) != cudaSuccess) return cuda_fail(e, "cross attention row terms launch");
   const void *q16 = bf ? r.q16 : q, *do16 = bf ? r.do16 : dO, *k16 = k, *v16 = v;
   const Lay q_l = bf ? packed_lay(s.Nq, s.Hq, s.d) : s.ql;
   Lay kv_l = s.kvl;
@@ -2533,9 +2555,10 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
     k16 = ws + p.k16;
     v16 = ws + p.v16;
     kv_l = packed_lay(s.Nkv, s.Hkv, s.d);
-    if ((e = launch_cross_keys(k, v, bf, s.kvl, ws + p.k16, ws + p.v16, s.B, s.Nkv, s.Hkv, s.d, kv_len, st, cs)) != cudaSuccess)
-      return cuda_fail(e, "fp16 operand copy launch");
   }
+  const CrossKeysArgs keys{k, v, k16 == k ? nullptr : ws + p.k16, ws + p.v16, bf, s.B, s.Nkv, s.Hkv, s.d,
+                           s.kvl, kv_len, st};
+  if ((e = launch_cross_prepare(r, keys, cs)) != cudaSuccess) return cuda_fail(e, "cross attention operands launch");
   TcBwdArgs a;
   memset(&a, 0, sizeof a);
   if ((rc = make_map(&a.tm_q, q16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) || (rc = make_map(&a.tm_do, do16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) ||
@@ -2548,6 +2571,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.precise = (flags & RA_PRECISE) != 0;
+  a.dp_mul = r.d_mul; a.dk_mul = ldexpf(scale, -m); a.dv_mul = ldexpf(1.f, -kCrossP);
   a.lse = r.lse2; a.Dvec = r.D; a.dq_acc = r.dq_acc;
   a.dk = dk; a.dv = dv; a.grad_dtype = grad_dtype; a.kvl = s.kvl;
   a.status = st;
@@ -2563,7 +2587,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   if (p.q_splits > 1 &&
       (e = launch_cross_sum(a.parts, p.q_splits, s.B, s.Nkv, s.Hkv, s.d, dk, dv, grad_dtype, s.kvl, cs)) != cudaSuccess)
     return cuda_fail(e, "cross attention gradient sum launch");
-  e = launch_cross_dq(r.dq_acc, scale, s.B, s.Nq, s.Hq, s.d, dq, grad_dtype, s.ql, cs);
+  e = launch_cross_dq(r.dq_acc, a.dk_mul, s.B, s.Nq, s.Hq, s.d, dq, grad_dtype, s.ql, cs);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "dq conversion launch");
 }
 

@@ -45,6 +45,10 @@
 // those columns after dK(i), which also leaves the next Q tile's load more
 // time; dQ(i) leaves TMEM while dK(i) and S(i+1) run, before dP(i+1) needs
 // its columns.
+// Cross attention (kLayoutCross): P and dS are held times 2^12 and 2^m, so that those of
+// long sequences (P about 1 / N) are normal fp16 numbers (131072 keys: dV within 1.3e-3
+// without, 3e-4 with): the first by adding to -LSE log2(e), the second by the factor that dP
+// and D enter dS with; dK, dV and dQ are scaled back.
 // With PRECISE, dS enters the dK product as two fp16 terms (hi from shared
 // memory, lo = fp16(dS - hi) from TMEM columns of dP^T that have already been
 // read: [128+64h, 128+64h+32) for query half h), so its rounding drops from
@@ -664,7 +668,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
           for (int j = 0; j < 32; j += 2) {
             // dS = P * (dP - D), two columns per fp32x2 add and multiply
             const float2 ndd = *reinterpret_cast<const float2*>(ndvec + c + j);
-            const float2 diff = __fadd2_rn(make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1])), ndd);
+            // (CROSS: of D and P times powers of two, dS times another)
+            const float2 dpj = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
+            const float2 diff = CROSS ? __ffma2_rn(dpj, make_float2(a.dp_mul, a.dp_mul), ndd) : __fadd2_rn(dpj, ndd);
             const float2 ds = __fmul2_rn(make_float2(__uint_as_float(pr[c + j]), __uint_as_float(pr[c + j + 1])), diff);
             const float d0 = ds.x, d1 = ds.y;
             pk[j / 2] = pack_half2(d0, d1);
@@ -817,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint32_t src = (which == 0 ? T_DK : T_DV) + lane_off;
-        const float mul = which == 0 ? a.scale : 1.f;
+        const float mul = which == 0 ? (CROSS ? a.dk_mul : a.scale) : (CROSS ? a.dv_mul : 1.f);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t v[32];

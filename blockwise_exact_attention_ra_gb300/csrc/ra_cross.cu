@@ -160,21 +160,20 @@ __global__ void __launch_bounds__(kThreads) cross_join_kernel(CrossState p, int 
   if (lane == 0) lse[at] = l == 0.f ? -INFINITY : m + logf(l);
 }
 
-__global__ void __launch_bounds__(kThreads) cross_keys_kernel(const void* k, const void* v, int dtype, Lay kvl, __half* k16,
-                                                              __half* v16, int B, int Nkv, int Hkv, int d, const int* kv_len,
-                                                              int* status) {
-  const int per_row = Hkv * d / 8;
-  const long long total = (long long)B * Nkv * per_row;
+// Keys and values as fp16, by blocks block, block + blocks, ...
+__device__ __forceinline__ void copy_keys(const CrossKeysArgs& a, long long block, long long blocks) {
+  const int per_row = a.Hkv * a.d / 8, dtype = a.bf16 ? RA_BF16 : RA_F16;
+  const long long total = (long long)a.B * a.Nkv * per_row;
   bool bad = false;
-  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < total; t += (long long)gridDim.x * kThreads) {
+  for (long long t = block * kThreads + threadIdx.x; t < total; t += blocks * kThreads) {
     const long long bn = t / per_row;
-    const int e = (int)(t - bn * per_row) * 8, g = e / d, b = (int)(bn / Nkv), n = (int)(bn - (long long)b * Nkv);
-    const bool there = n < len_at(kv_len, b, Nkv);
-    const long long src = lay_at(kvl, b, n, g) + (e - g * d);
+    const int e = (int)(t - bn * per_row) * 8, g = e / a.d, b = (int)(bn / a.Nkv), n = (int)(bn - (long long)b * a.Nkv);
+    const bool there = n < len_at(a.kv_len, b, a.Nkv);
+    const long long src = lay_at(a.kvl, b, n, g) + (e - g * a.d);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const void* x = i ? v : k;
-      __half* y = i ? v16 : k16;
+      const void* x = i ? a.v : a.k;
+      void* y = i ? a.v16 : a.k16;
       if (!y) continue;
       float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       if (there) {
@@ -184,13 +183,23 @@ __global__ void __launch_bounds__(kThreads) cross_keys_kernel(const void* k, con
       put8(y, RA_F16, t * 8, f);
     }
   }
-  if (bad) report(status, RA_ERR_RANGE);
+  if (bad) report(a.status, RA_ERR_RANGE);
 }
 
-// d / 8 lanes a row (b, n, h), n up to Np.
-__global__ void __launch_bounds__(kThreads) cross_rows_kernel(const __grid_constant__ CrossRowsArgs a) {
+__global__ void __launch_bounds__(kThreads) cross_keys_kernel(const __grid_constant__ CrossKeysArgs a) {
+  copy_keys(a, blockIdx.x, gridDim.x);
+}
+
+// What the backward kernel needs, the query side by the first row_blocks blocks (d / 8 lanes
+// a row (b, n, h), n up to Np), the key side by the others.
+__global__ void __launch_bounds__(kThreads) cross_prepare_kernel(const __grid_constant__ CrossRowsArgs a,
+                                                                 const __grid_constant__ CrossKeysArgs keys, int row_blocks) {
+  if ((int)blockIdx.x >= row_blocks) {
+    copy_keys(keys, blockIdx.x - row_blocks, gridDim.x - row_blocks);
+    return;
+  }
   const int G = a.d / 8, lane = threadIdx.x % G, in_dtype = a.bf16 ? RA_BF16 : RA_F16;
-  const long long rows = (long long)a.B * a.Np * a.Hq, step = (long long)gridDim.x * (kThreads / G);
+  const long long rows = (long long)a.B * a.Np * a.Hq, step = (long long)row_blocks * (kThreads / G);
   if (blockIdx.x == 0 && threadIdx.x < 64) a.sched[threadIdx.x] = 0u;
   bool bad = false;
   // the warp's rows end together: its lanes meet in the sums
@@ -225,8 +234,8 @@ __global__ void __launch_bounds__(kThreads) cross_rows_kernel(const __grid_const
       const long long at = ((long long)b * a.Hq + h) * a.Np + n;
       const float lse = there ? a.lse[((long long)b * a.Hq + h) * a.Nq + n] : -INFINITY;
       const bool seen = lse != -INFINITY;
-      a.D[at] = seen ? -dot : 0.f;
-      a.lse2[at] = seen ? -(lse * kLog2e) : -INFINITY;  // P = 0
+      a.D[at] = seen ? -dot * a.d_mul : 0.f;
+      a.lse2[at] = seen ? (float)kCrossP - lse * kLog2e : -INFINITY;  // P = 0
     }
   }
   if (bad) report(a.status, RA_ERR_RANGE);
@@ -286,16 +295,16 @@ cudaError_t launch_cross_join(const CrossState& part, int splits, int B, int Nq,
   return e;
 }
 
-cudaError_t launch_cross_keys(const void* k, const void* v, int bf16, Lay kvl, void* k16, void* v16, int B, int Nkv,
-                              int Hkv, int d, const int* kv_len, int* status, cudaStream_t st) {
-  cross_keys_kernel<<<blocks_for((long long)B * Nkv * Hkv * d / 8), kThreads, 0, st>>>(
-      k, v, bf16 ? RA_BF16 : RA_F16, kvl, static_cast<__half*>(k16), static_cast<__half*>(v16), B, Nkv, Hkv, d, kv_len, status);
+cudaError_t launch_cross_keys(const CrossKeysArgs& a, cudaStream_t st) {
+  cross_keys_kernel<<<blocks_for((long long)a.B * a.Nkv * a.Hkv * a.d / 8), kThreads, 0, st>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
-cudaError_t launch_cross_rows(const CrossRowsArgs& a, cudaStream_t st) {
-  cross_rows_kernel<<<blocks_for((long long)a.B * a.Np * a.Hq * a.d / 8), kThreads, 0, st>>>(a);
+cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& keys, cudaStream_t st) {
+  const unsigned rows = blocks_for((long long)a.B * a.Np * a.Hq * a.d / 8);
+  const unsigned more = keys.k16 ? blocks_for((long long)keys.B * keys.Nkv * keys.Hkv * keys.d / 8) : 0;
+  cross_prepare_kernel<<<rows + more, kThreads, 0, st>>>(a, keys, (int)rows);
   count_launch();
   return cudaGetLastError();
 }

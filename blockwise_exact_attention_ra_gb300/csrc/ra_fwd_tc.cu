@@ -736,7 +736,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
       tc_fence_after();
       // epilogue
       if (a.mode == 0) {
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
+        // CROSS: a row that holds a NaN has NaN here too
+        const float inv = (CROSS ? l_run != 0.f : l_run > 0.f) ? 1.f / l_run : 0.f;
         const long long out = lay_at(a.ol, ui.b, row, ui.h);
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
@@ -769,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_fwd_kernel(const __grid_consta
             }
           }
         }
-        if (row_ok) a.lse[sidx()] = l_run > 0.f ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
+        if (row_ok) a.lse[sidx()] = (CROSS ? l_run != 0.f : l_run > 0.f) ? (m_run + log2f(l_run)) * kLn2 : -INFINITY;
       } else {
 #pragma unroll
         for (int c = 0; c < D; c += 32) {

@@ -179,6 +179,7 @@ struct TcBwdArgs {
   int cross, Nkv, Np, q_splits;
   const int* kv_len;    // optional: keys per batch entry (device)
   float* parts;         // q_splits > 1: dK then dV [q_splits][B, Nkv, Hkv, d]
+  float dp_mul, dk_mul, dv_mul;  // lse is larger by kCrossP, Dvec is times dp_mul = 2^(m - kCrossP), dS times 2^m
   const float* lse;   // [B, Hq, N]: -LSE * log2(e)
   const float* Dvec;  // [B, Hq, N]: -D
   float* dq_acc;      // packed fp32 [B, N, Hq, d], pre-zeroed, reduce-added
@@ -201,6 +202,7 @@ struct CrossState {   // [splits][B, Nq, Hq, d], [splits][B, Hq, Nq] (natural-lo
   float *o, *m, *l;
 };
 constexpr int kCrossFewRows = 32;
+constexpr int kCrossP = 12;  // backward: P is held times 2^kCrossP
 struct CrossFewArgs {
   const void *q, *k, *v;
   int bf16, B, Nq, Nkv, Hq, Hkv, d;
@@ -217,24 +219,32 @@ cudaError_t launch_cross_few(const CrossFewArgs& a, cudaStream_t st);
 // o, lse <- the parts' states joined
 cudaError_t launch_cross_join(const CrossState& part, int splits, int B, int Nq, int Hq, int d, void* o, int o_dtype,
                               Lay ol, float* lse, cudaStream_t st);
-// dst (packed fp16) <- src (16-bit) of one or two key-side tensors, rows from kv_len[b] on
-// zero; values beyond the fp16 range set RA_ERR_RANGE in *status
-cudaError_t launch_cross_keys(const void* k, const void* v, int bf16, Lay kvl, void* k16, void* v16, int B, int Nkv,
-                              int Hkv, int d, const int* kv_len, int* status, cudaStream_t st);
-// what the backward kernel needs of the query side: lse2 = -lse log2(e), D = -dO . O (rows
-// of Np; -inf and 0 where there is no row or it saw no key), fp16 copies of q and dO (bf16
-// inputs), and dq_acc = 0
+// k16, v16 (packed fp16; NULL: not wanted) <- k, v (16-bit), rows from kv_len[b] on zero;
+// values beyond the fp16 range set RA_ERR_RANGE in *status
+struct CrossKeysArgs {
+  const void *k, *v;
+  void *k16, *v16;
+  int bf16, B, Nkv, Hkv, d;
+  Lay kvl;
+  const int* kv_len;
+  int* status;
+};
+cudaError_t launch_cross_keys(const CrossKeysArgs& a, cudaStream_t st);
+// what the backward kernel needs of the query side: lse2 = kCrossP - lse log2(e), D = -d_mul
+// dO . O (rows of Np; -inf and 0 where there is no row or it saw no key), fp16 copies of q and dO (bf16
+// inputs), dq_acc = 0 and the unit counter; and the key side as above where k16 is not NULL
 struct CrossRowsArgs {
   const void *q, *dO, *o;
   const float* lse;
   int bf16, o_dtype, B, Nq, Np, Hq, d;
   Lay ql;
+  float d_mul;
   void *q16, *do16;  // NULL for fp16 inputs
   float *D, *lse2, *dq_acc;
   unsigned int* sched;
   int* status;
 };
-cudaError_t launch_cross_rows(const CrossRowsArgs& a, cudaStream_t st);
+cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& keys, cudaStream_t st);
 // dk, dv <- sums of the parts' planes
 cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
                              Lay kvl, cudaStream_t st);

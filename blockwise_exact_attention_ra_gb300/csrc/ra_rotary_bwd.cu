@@ -180,8 +180,8 @@ __global__ void __launch_bounds__(1024) rotary_dw_kernel(const float* parts, int
   const int per = gridDim.x / 2, side = (int)blockIdx.x / per;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = ((int)blockIdx.x - side * per) * 32 + lane;
   float* out = side ? dwk : dwq;
+  pdl_wait();  // in every block: what comes after may wait for this kernel alone
   if (!out) return;
-  pdl_wait();
   float v = 0.f;
   if (c < d)
     for (int b = w; b < blocks; b += 32) v += parts[((long long)side * blocks + b) * d + c];

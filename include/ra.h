@@ -454,8 +454,10 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
 /* Gradients of L = sum(o * dO): dq [B, N_q, Hq, d], dk, dv [B, N_kv, Hkv, d] in grad_dtype,
  * fully overwritten (rows from kv_len[b] on with zeros), by the formulas of ra_ring_bwd; o in
  * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  Operands are
- * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  dq is summed over the key
- * tiles in fp32 in an order that varies; dk and dv do not vary from run to run. */
+ * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  P and dS are rounded to
+ * fp16 times powers of two, dS by 1 (N_kv <= 1024) to 64 (N_kv > 32768): an element of dS past
+ * 65504 divided by that overflows.  dq is summed over the key tiles in fp32 in an order that
+ * varies; dk and dv do not vary from run to run. */
 size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape);
 int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype,
                  const void* dO, const float* lse, ra_dtype dtype, ra_shape shape,

@@ -224,6 +224,11 @@ def test_extreme_scores(ra):
         q[0, 1, 0, 0] = float("nan")
         o2, lse2 = ra.cross_attention_fwd(q, k, v, None, 0.5)
         assert o2[0, 1, 0].isnan().all() and torch.equal(o2[0, 0], o[0, 0]) and torch.equal(o2[0, 1, 1], o[0, 1, 1])
+        assert lse2[0, 0, 1].isnan() and int(lse2.isnan().sum()) == 1
+        do = rand(q.shape, torch.float16, 53)
+        dq, dk, dv = ra.cross_attention_bwd(q, k, v, o2, lse2, do, None, 0.5)
+        assert dq[0, 1, 0].isnan().all() and not dq[0, 0].isnan().any() and not dq[0, 1, 1].isnan().any()
+        assert dk[:, :, 0].isnan().all() and dv[:, :, 0].isnan().all() and not dk[:, :, 1].isnan().any()
     ra.ra_sync_status()
 
 
