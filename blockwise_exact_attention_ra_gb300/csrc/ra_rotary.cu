@@ -70,7 +70,8 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, const RotLane& 
   }
 }
 
-template <typename T, typename TO, bool NORM, int EX, int DIR>
+// ALL: every column belongs to a pair.
+template <typename T, typename TO, bool NORM, int EX, int DIR, bool ALL>
 __global__ void __launch_bounds__(kRotThreads, kBlocks) rotary_kernel(const __grid_constant__ RotaryArgs a) {
   using Smem = RotSmem<EX, false>;
   const Smem L(a, NORM ? 2 : 1);
@@ -107,10 +108,7 @@ __global__ void __launch_bounds__(kRotThreads, kBlocks) rotary_kernel(const __gr
       const float* const own = factors + (NORM ? side * 2 * a.tile * a.d : 0);
       const T* in = static_cast<const T*>(s.x) + rot_offset(a, s.xl, t, b, n, h0 + l.head);
       TO* out = static_cast<TO*>(s.y) + rot_offset(a, s.yl, t, b, n, h0 + l.head);
-      if (EX != ROT_STAGE && a.rot == a.d)
-        rotate_rows<T, TO, NORM, EX, EX != ROT_STAGE>(a, l, s, own, in, out, token, h0, h1, stage);
-      else
-        rotate_rows<T, TO, NORM, EX, false>(a, l, s, own, in, out, token, h0, h1, stage);
+      rotate_rows<T, TO, NORM, EX, ALL>(a, l, s, own, in, out, token, h0, h1, stage);
     }
   }
 }
@@ -127,9 +125,14 @@ cudaError_t run(const RotaryArgs& a, int exchange, int sms, cudaStream_t st) {
     return cudaGetLastError();
   };
   constexpr int sides = NORM ? 2 : 1;
-  if (exchange == ROT_PIECE) return go(rotary_kernel<T, TO, NORM, ROT_PIECE, DIR>, RotSmem<ROT_PIECE, false>(a, sides).bytes);
-  if (exchange == ROT_OTHER) return go(rotary_kernel<T, TO, NORM, ROT_OTHER, DIR>, RotSmem<ROT_OTHER, false>(a, sides).bytes);
-  return go(rotary_kernel<T, TO, NORM, ROT_STAGE, DIR>, RotSmem<ROT_STAGE, false>(a, sides).bytes);
+  const int piece = RotSmem<ROT_PIECE, false>(a, sides).bytes, other = RotSmem<ROT_OTHER, false>(a, sides).bytes;
+  if (exchange == ROT_PIECE)
+    return a.rot == a.d ? go(rotary_kernel<T, TO, NORM, ROT_PIECE, DIR, true>, piece)
+                        : go(rotary_kernel<T, TO, NORM, ROT_PIECE, DIR, false>, piece);
+  if (exchange == ROT_OTHER)
+    return a.rot == a.d ? go(rotary_kernel<T, TO, NORM, ROT_OTHER, DIR, true>, other)
+                        : go(rotary_kernel<T, TO, NORM, ROT_OTHER, DIR, false>, other);
+  return go(rotary_kernel<T, TO, NORM, ROT_STAGE, DIR, false>, RotSmem<ROT_STAGE, false>(a, sides).bytes);
 }
 
 }  // namespace

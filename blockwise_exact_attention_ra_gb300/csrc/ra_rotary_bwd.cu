@@ -11,8 +11,8 @@
 namespace ra {
 namespace {
 
-// Blocks of an SM: 128 registers a thread.  (131072 tokens of 16 + 4 heads of 128, bf16: 440
-// us; with three, whose 80 registers spill, 500 at best.)
+// Blocks of an SM: 128 registers a thread.  (131072 tokens of 16 + 4 heads of 128, bf16: 430
+// us, 4.7 TB/s; with three, whose 80 registers spill, 519.)
 constexpr int kBlocks = 2;
 
 template <typename T, typename TG, typename TO, int EX, bool ALL>
@@ -21,77 +21,92 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
                                               TO* out, bool token, int h0, int h1, float* stage, float* sums) {
   const long long x_step = a.heads * side.xl.hs, dy_step = a.heads * side.dyl.hs, out_step = a.heads * side.yl.hs;
   const float inv_d = 1.f / (float)a.d;
-  Raw8<T> rx[2];   // zeros, or rows before, in columns that are not there
-  Raw8<TG> rg[2];
   float2 dw[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    zero8(rx[i]);
-    zero8(rg[i]);
-  }
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = both(0.f);
+  int at[2];  // columns that are there
   const float *C[2], *W[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    C[i] = factors + l.token * a.d + (l.there[i] ? l.e[i] / 2 : 0);
-    W[i] = weight + (l.there[i] ? l.e[i] : 0);
+    at[i] = l.there[i] ? l.e[i] : 0;
+    C[i] = factors + l.token * a.d + at[i] / 2;
+    W[i] = weight + at[i];
   }
   for (int h = h0; h < h1; h += a.heads, x += x_step, dy += dy_step, out += out_step) {
     const bool row = token && h + l.head < h1;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      load8(rx[i], x + l.e[i], row && l.there[i]);
-      load8(rg[i], dy + l.e[i], row && l.there[i]);
+    // x stays as it was read, in half the registers, and is unpacked twice.  A head that is
+    // not there reads the step's first.
+    Raw8<T> rx[2];
+    Raw8<TG> rg[2];
+    const T* px = x;
+    const TG* pg = dy;
+    if (h + a.heads > h1 && h + l.head >= h1) {
+      px -= l.head * side.xl.hs;
+      pg -= l.head * side.dyl.hs;
     }
-    float2 f[2][4], g[2][4], p[2][4], s2 = both(0.f), d2 = both(0.f);
-    unpack8(rg[0], g[0]);
-    unpack8(rg[1], g[1]);
-    other_columns<EX, ALL>(a, l, g, p, stage);
-    unpack8(rx[0], f[0]);
-    unpack8(rx[1], f[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float2 c[4], sn[4], w[4];
-      columns8(c, C[i], a.d / 2);
-      columns8(sn, C[i] + a.tile * a.d, a.d / 2);
-      columns8(w, W[i], 4);
+      load8(rx[i], px + at[i], true);
+      load8(rg[i], pg + at[i], true);
+    }
+    float2 g[2][4], s2[2], d2[2];
+    {
+      float2 y[2][4], p[2][4];
+      unpack8(rg[0], y[0]);
+      unpack8(rg[1], y[1]);
+      other_columns<EX, ALL>(a, l, y, p, stage);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        g[i][j] = __ffma2_rn(g[i][j], c[j], __fmul2_rn(p[i][j], sn[j]));
-        p[i][j] = __fmul2_rn(g[i][j], w[j]);
-        s2 = __ffma2_rn(f[i][j], f[i][j], s2);
-        d2 = __ffma2_rn(p[i][j], f[i][j], d2);
+      for (int i = 0; i < 2; ++i) {
+        float2 c[4], sn[4];
+        columns8(c, C[i], a.d / 2);
+        columns8(sn, C[i] + a.tile * a.d, a.d / 2);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[i][j] = __ffma2_rn(y[i][j], c[j], __fmul2_rn(p[i][j], sn[j]));
       }
     }
-    float sum = group_sum(s2.x + s2.y, a.G), dot = group_sum(d2.x + d2.y, a.G), eps = a.eps, sc = 1.f;
-    if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
-      sc = rot_scale(sum);
-      sum = dot = 0.f;
+    // the sums for the norm's factor; sc: what brings a row's squares into fp32's range
+    float sc = 1.f;
+    auto sums_of = [&] {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
+        float2 f[4], w[4];
+        unpack8(rx[i], f);
+        columns8(w, W[i], 4);
+        s2[i] = d2[i] = both(0.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          f[i][j] = __fmul2_rn(f[i][j], both(sc));
-          sum = fmaf(f[i][j].y, f[i][j].y, fmaf(f[i][j].x, f[i][j].x, sum));
-          dot = fmaf(p[i][j].y, f[i][j].y, fmaf(p[i][j].x, f[i][j].x, dot));
+          const float2 x2 = sc == 1.f ? f[j] : __fmul2_rn(f[j], both(sc));
+          s2[i] = __ffma2_rn(x2, x2, s2[i]);
+          d2[i] = __ffma2_rn(__fmul2_rn(g[i][j], w[j]), x2, d2[i]);
         }
-      sum = group_sum(sum, a.G);
-      dot = group_sum(dot, a.G);
+      }
+    };
+    sums_of();
+    auto of_row = [&](const float2 (&v)[2]) {
+      return group_sum((l.there[0] ? v[0].x + v[0].y : 0.f) + (l.there[1] ? v[1].x + v[1].y : 0.f), a.G);
+    };
+    float sum = of_row(s2), dot = of_row(d2), eps = a.eps;
+    if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
+      sc = rot_scale(sum);
+      sums_of();
+      sum = of_row(s2);
+      dot = of_row(d2);
       eps *= sc * sc;
     }
     const float r = rsqrtf(fmaf(sum, inv_d, eps));
-    const float2 r2 = both(r), along = both(-dot * r * inv_d), rs = both(r * sc);
+    const float2 rs = both(r * sc), along = both(-dot * r * inv_d);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float2 dx[4];
+      float2 f[4], w[4], dx[4];
+      unpack8(rx[i], f);
+      columns8(w, W[i], 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 normed = __fmul2_rn(f[i][j], r2);
+        const float2 normed = __fmul2_rn(f[j], rs);
         if (row) dw[i][j] = __ffma2_rn(g[i][j], normed, dw[i][j]);
-        dx[j] = __fmul2_rn(rs, __ffma2_rn(normed, along, p[i][j]));
+        dx[j] = __fmul2_rn(rs, __ffma2_rn(normed, along, __fmul2_rn(g[i][j], w[j])));
       }
       if (row && l.there[i]) store8(out + l.e[i], dx);
     }
@@ -113,7 +128,7 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
     }
 }
 
-template <typename T, typename TG, typename TO, int EX>
+template <typename T, typename TG, typename TO, int EX, bool ALL>
 __global__ void __launch_bounds__(kRotThreads, kBlocks) norm_rotary_bwd_kernel(const __grid_constant__ RotaryArgs a) {
   using Smem = RotSmem<EX, true>;
   const Smem L(a, 1);
@@ -152,12 +167,8 @@ __global__ void __launch_bounds__(kRotThreads, kBlocks) norm_rotary_bwd_kernel(c
       const T* x = static_cast<const T*>(s.x) + rot_offset(a, s.xl, t, b, n, h0 + l.head);
       const TG* dy = static_cast<const TG*>(s.dy) + rot_offset(a, s.dyl, t, b, n, h0 + l.head);
       TO* out = static_cast<TO*>(s.y) + rot_offset(a, s.yl, t, b, n, h0 + l.head);
-      if (EX != ROT_STAGE && a.rot == a.d)
-        gradient_rows<T, TG, TO, EX, EX != ROT_STAGE>(a, l, s, weight + side * a.d, factors, x, dy, out, token, h0, h1, stage,
-                                                      sums + side * groups * a.d);
-      else
-        gradient_rows<T, TG, TO, EX, false>(a, l, s, weight + side * a.d, factors, x, dy, out, token, h0, h1, stage,
-                                            sums + side * groups * a.d);
+      gradient_rows<T, TG, TO, EX, ALL>(a, l, s, weight + side * a.d, factors, x, dy, out, token, h0, h1, stage,
+                                        sums + side * groups * a.d);
     }
   }
   // the block's sums, over groups and warps in order
@@ -205,9 +216,14 @@ cudaError_t run(const RotaryArgs& a, int exchange, float* dwq, float* dwk, int s
     if (e == cudaSuccess) count_launch(2);
     return e;
   };
-  if (exchange == ROT_PIECE) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_PIECE>, RotSmem<ROT_PIECE, true>(a, 1).bytes);
-  if (exchange == ROT_OTHER) return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_OTHER>, RotSmem<ROT_OTHER, true>(a, 1).bytes);
-  return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_STAGE>, RotSmem<ROT_STAGE, true>(a, 1).bytes);
+  const int piece = RotSmem<ROT_PIECE, true>(a, 1).bytes, other = RotSmem<ROT_OTHER, true>(a, 1).bytes;
+  if (exchange == ROT_PIECE)
+    return a.rot == a.d ? go(norm_rotary_bwd_kernel<T, TG, TO, ROT_PIECE, true>, piece)
+                        : go(norm_rotary_bwd_kernel<T, TG, TO, ROT_PIECE, false>, piece);
+  if (exchange == ROT_OTHER)
+    return a.rot == a.d ? go(norm_rotary_bwd_kernel<T, TG, TO, ROT_OTHER, true>, other)
+                        : go(norm_rotary_bwd_kernel<T, TG, TO, ROT_OTHER, false>, other);
+  return go(norm_rotary_bwd_kernel<T, TG, TO, ROT_STAGE, false>, RotSmem<ROT_STAGE, true>(a, 1).bytes);
 }
 
 }  // namespace

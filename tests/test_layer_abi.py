@@ -140,6 +140,66 @@ def test_clip_refusals(ra):
     assert ra.ra_grad_workspace_bytes(1) > 0 and ra.ra_grad_workspace_bytes(1025) == 2 * ra.ra_grad_workspace_bytes(1024)
 
 
+def test_cross_refusals(ra):
+    lib = ra.lib
+
+    def fwd(*, q=VP, k=VP, v=VP, dt=ra.RA_BF16, sh=None, lens=None, flags=0, scale=0.1, o=VP, odt=ra.RA_F32, lse=VP, ws=VP,
+            n=BIG, **kw):
+        return lib.ra_cross_fwd(q, k, v, dt, sh or shape(ra, **kw), lens, flags, scale, o, odt, lse, ws, n, None)
+
+    def bwd(*, q=VP, k=VP, v=VP, dt=ra.RA_BF16, sh=None, lens=None, flags=0, scale=0.1, o=VP, odt=ra.RA_F32, lse=VP, ws=VP,
+            n=BIG, do=VP, dq=VP, dk=VP, dv=VP, gdt=ra.RA_F32, **kw):
+        return lib.ra_cross_bwd(q, k, v, o, odt, do, lse, dt, sh or shape(ra, **kw), lens, flags, scale, dq, dk, dv, gdt, ws, n,
+                                None)
+
+    for call in (fwd, bwd):
+        for size in (dict(N_q=1, N_kv=70), dict(N_q=300, N_kv=7)):       # both kernels
+            assert call(dt=ra.RA_F32, **size) == 2 and call(dt=7, **size) == 1 and call(odt=9, **size) == 1
+            assert call(B=0, **size) == 1 and call(Hq=3, **size) == 1 and call(d=32, **size) == 2 and call(d=96, **size) == 2
+            assert call(flags=1, **size) == 1 and call(flags=4, **size) == 1 and "flag" in ra.ra_last_error()
+            assert call(scale=0.0, **size) == 1 and call(scale=math.nan, **size) == 1
+            for name in ("q", "k", "v", "o"):
+                assert call(**{name: None}, **size) == 1 and call(**{name: ctypes.c_void_p(4104)}, **size) == 1
+            assert call(lse=None, **size) == 1 and call(lse=ctypes.c_void_p(4098), **size) == 1
+            assert call(lens=ctypes.c_void_p(4098), **size) == 1 and "kv_len" in ra.ra_last_error()
+            assert call(ws=None, **size) == 1 and call(n=ctypes.c_size_t(16), **size) == 1 and call(ws=ctypes.c_void_p(4224), **size) == 1
+            assert call(q_hstride=32, **size) == 1 and call(kv_bstride=100, **size) == 1
+        assert call(N_q=0) == 1 and call(N_kv=0) == 1
+        assert call(N_q=(1 << 30) - 1, B=64, Hq=64) == 2 and "tiles" in ra.ra_last_error()
+    for name in ("do", "dq", "dk", "dv"):
+        assert bwd(**{name: None}) == 1 and bwd(**{name: ctypes.c_void_p(8)}) == 1
+    assert bwd(gdt=5) == 1
+    f, b = ra.ra_cross_fwd_workspace_bytes, ra.ra_cross_bwd_workspace_bytes
+    long = shape(ra, B=1, N_q=4096, N_kv=10000, Hq=8, Hkv=8, d=128)
+    assert f(ra.RA_BF16, long) >= 10000 * 8 * 128 * 2 and f(ra.RA_F16, long) < f(ra.RA_BF16, long)
+    one = shape(ra, B=1, N_q=1, N_kv=100000, Hq=8, Hkv=8, d=128)
+    assert 8 * 128 * 4 * 8 < f(ra.RA_BF16, one) < 1 << 22           # parts' states, no copy of v
+    assert f(ra.RA_F32, long) == 0 and b(ra.RA_F32, long) == 0 and f(ra.RA_BF16, shape(ra, d=32)) == 0
+    assert b(ra.RA_BF16, long) >= 4096 * 8 * 128 * (4 + 2 + 2) + 2 * 10000 * 8 * 128 * 2
+
+
+def test_cross_binding_refuses_before_the_library(ra):
+    q, k = torch.zeros(2, 3, 4, 64).half(), torch.zeros(2, 9, 2, 64).half()
+    lse, ws, n = torch.zeros(2, 4, 3), torch.zeros(64, dtype=torch.uint8), torch.zeros(2, dtype=torch.int32)
+    for bad in (lambda: ra.cross_attention_fwd(q[:1], k, k), lambda: ra.cross_attention_fwd(q, k.float(), k),
+                lambda: ra.cross_attention_fwd(q, k, k.float()), lambda: ra.cross_attention_fwd(q, k, k[:, :8]),
+                lambda: ra.cross_attention_fwd(q[..., :32], k, k), lambda: ra.cross_attention_fwd(q[0], k, k),
+                lambda: ra.cross_attention_fwd(q, k, k.transpose(1, 2).contiguous().transpose(1, 2)),
+                lambda: ra.cross_attention_fwd(q, k, k, n.long()), lambda: ra.cross_attention_fwd(q, k, k, n[:1]),
+                lambda: ra.cross_attention_fwd(q, k, k, n.repeat(2)[::2]), lambda: ra.cross_attention_fwd(q, k, k),
+                lambda: ra.ra_cross_fwd(q, k, k, 0.1, q[:, :2], lse, ws), lambda: ra.ra_cross_fwd(q, k, k, 0.1, q, lse[:1], ws),
+                lambda: ra.ra_cross_fwd(q, k, k, 0.1, q, lse.double(), ws),
+                lambda: ra.cross_attention_bwd(q, k, k, q, lse, q.float()), lambda: ra.cross_attention_bwd(q, k, k, q, lse.transpose(1, 2), q),
+                lambda: ra.ra_cross_bwd(q, k, k, q, q, lse, 0.1, q, k, k.float(), ws),
+                lambda: ra.ra_cross_bwd(q, k, k, q, q, lse, 0.1, q, k, k[:, :3], ws)):
+        with pytest.raises(ra.RAError):
+            bad()
+    for i in range(3):
+        t = k.narrow(i, 0, 1).expand(*k.shape)
+        with pytest.raises(ra.RAError, match="expanded"):
+            ra.cross_attention_fwd(q, t, t)
+
+
 def test_binding_refuses_before_the_library(ra):
     q, k = torch.zeros(2, 8, 4, 16), torch.zeros(2, 8, 2, 16)
     f, w = torch.ones(8, dtype=torch.float64), torch.ones(16)
