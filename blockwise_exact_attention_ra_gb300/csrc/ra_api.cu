@@ -2324,7 +2324,7 @@ int check_cross(const ra_shape& shape, int dtype, int flags, Shape* s) {
 
 struct CrossPlan {
   bool few, bf16_p;
-  int splits;
+  int splits, cluster;  // parts of the keys; few queries: how many of them a cluster joins
   size_t v16, parts, m, l, total;
 };
 
@@ -2344,16 +2344,22 @@ int cross_parts(long long units, long long tiles, double tile, double ends, doub
   return best;
 }
 
-// The same for a few queries: `slots` blocks at a time share 6.2 TB/s (us; a block's start and
-// end, and the join, measured).  Where batch entries differ in length no wave is waited for.
+// Parts of the keys that a cluster of blocks joins: all of them up to eight.  (Clusters whose
+// states a kernel joins gain nothing: 76 parts of 131072 keys 56 us, clusters of four, which do
+// not all find SMs at once, 86 us; of eight of 72, 63 us.)
+int cross_cluster(int splits) { return splits <= 8 ? splits : 1; }
+
+// The parts for a few queries: `slots` blocks at a time share 6.2 TB/s (us; a block's start and
+// end, and the joins, measured).  Where batch entries differ in length no wave is waited for.
 int cross_few_parts(const Shape& s, int slots, bool ragged) {
   const double units = (double)s.B * s.Hkv, alone = (double)s.Nkv * s.d * 4. * slots / 6.2e6;
   const int most = (s.Nkv + 127) / 128 < 256 ? (s.Nkv + 127) / 128 : 256;
   int best = 1;
   double least = 1e30;
-  for (int n = 1; n <= most; ++n) {
+  for (int n = 1; n <= most; n += n < 8 ? n : 1) {
+    const int parts = n / cross_cluster(n);
     const double w = units * n / slots, waves = w < 1. ? 1. : ragged ? w : ceil(w);
-    const double t = waves * (alone / n + 3.) + (n > 1 ? 4. + 0.03 * n : 0.);
+    const double t = waves * (alone / n + 3.) + (n > 1 ? 1. : 0.) + (parts > 1 ? 4. + 0.03 * parts : 0.);
     if (t < least * 0.99) {
       least = t;
       best = n;
@@ -2370,6 +2376,7 @@ CrossPlan cross_plan(const Shape& s, int dtype, int flags, bool ragged) {
   if (p.few) {
     const int blocks = s.d == 128 ? 2 : s.Nq * group <= 16 ? 4 : 3;  // of an SM
     p.splits = cross_few_parts(s, blocks * kPlanSms, ragged);
+    p.cluster = cross_cluster(p.splits);
   } else {
     p.bf16_p = dtype == RA_BF16 && !(flags & RA_PRECISE) && (long long)s.Nq * group <= 512;
     const int pairs = ((s.Nq + 127) / 128 + 1) / 2;
@@ -2380,8 +2387,9 @@ CrossPlan cross_plan(const Shape& s, int dtype, int flags, bool ragged) {
   p.parts = p.v16;
   if (!p.few && dtype == RA_BF16 && !p.bf16_p) p.parts += align256((size_t)s.B * s.Nkv * s.Hkv * s.d * 2);
   p.m = p.l = p.total = p.parts;
-  if (p.splits > 1) {
-    const size_t states = (size_t)p.splits * s.B * s.Nq * s.Hq;
+  const int parts = p.few ? p.splits / p.cluster : p.splits;
+  if (parts > 1) {
+    const size_t states = (size_t)parts * s.B * s.Nq * s.Hq;
     p.m = p.parts + align256(states * s.d * 4);
     p.l = p.m + align256(states * 4);
     p.total = p.l + align256(states * 4);
@@ -2464,7 +2472,7 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
     a.B = s.B; a.Nq = s.Nq; a.Nkv = s.Nkv; a.Hq = s.Hq; a.Hkv = s.Hkv; a.d = s.d;
     a.ql = s.ql; a.kvl = s.kvl; a.ol = s.ql;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.kv_len = kv_len; a.splits = p.splits; a.part = part;
+    a.kv_len = kv_len; a.splits = p.splits; a.cluster = p.cluster; a.part = part;
     a.o = o; a.o_dtype = o_dtype; a.lse = lse;
     e = launch_cross_few(a, cs);
   } else {
@@ -2499,8 +2507,9 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
     e = launch_tc_fwd(a, device_sms(), cs);
   }
   if (e != cudaSuccess) return cuda_fail(e, "cross attention forward launch");
-  if (p.splits > 1) {
-    e = launch_cross_join(part, p.splits, s.B, s.Nq, s.Hq, s.d, o, o_dtype, s.ql, lse, cs);
+  const int parts = p.few ? p.splits / p.cluster : p.splits;
+  if (parts > 1) {
+    e = launch_cross_join(part, parts, s.B, s.Nq, s.Hq, s.d, o, o_dtype, s.ql, lse, cs);
     if (e != cudaSuccess) return cuda_fail(e, "cross attention join launch");
   }
   return RA_OK;

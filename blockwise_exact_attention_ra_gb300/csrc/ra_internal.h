@@ -197,7 +197,7 @@ cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st);
 
 // -------------------------------------------- cross attention
 // A few queries (Nq * Hq / Hkv <= kCrossFewRows) on warp-level products: bound by reading
-// K and V.  Results, or with splits > 1 the parts' states.
+// K and V.  Results, or with splits > cluster the clusters' states.
 struct CrossState {   // [splits][B, Nq, Hq, d], [splits][B, Hq, Nq] (natural-log units)
   float *o, *m, *l;
 };
@@ -209,7 +209,7 @@ struct CrossFewArgs {
   Lay ql, kvl, ol;
   float scale_log2;
   const int* kv_len;
-  int splits;
+  int splits, cluster;  // parts of the keys, and how many of them a cluster joins
   CrossState part;
   void* o;
   int o_dtype;

@@ -118,7 +118,7 @@ cudaError_t run(const RotaryArgs& a, int exchange, int sms, cudaStream_t st) {
   auto go = [&](auto kernel, int smem) {
     const int fit = kRotSmemSm / (smem + 1024);  // 3 where a warp's rows are of many tokens
     const long long blocks = (a.units + kRotWarps - 1) / kRotWarps, most = (long long)sms * (fit < kBlocks ? fit : kBlocks);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)(blocks < most ? blocks : most), kRotThreads, smem, st>>>(a);
     count_launch();

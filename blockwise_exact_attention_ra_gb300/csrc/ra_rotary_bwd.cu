@@ -208,7 +208,7 @@ cudaError_t run(const RotaryArgs& a, int exchange, float* dwq, float* dwk, int s
   auto go = [&](auto kernel, int smem) {
     const long long want = (a.units + kRotWarps - 1) / kRotWarps, most = (long long)kBlocks * sms < kRotParts ? (long long)kBlocks * sms : kRotParts;
     const int blocks = (int)(want < most ? want : most);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = smem > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) : cudaSuccess;
     if (e != cudaSuccess) return e;
     kernel<<<blocks, kRotThreads, smem, st>>>(a);
     e = cudaGetLastError();
