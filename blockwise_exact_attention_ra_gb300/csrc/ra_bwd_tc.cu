@@ -52,7 +52,8 @@
 // With PRECISE, dS enters the dK product as two fp16 terms (hi from shared
 // memory, lo = fp16(dS - hi) from TMEM columns of dP^T that have already been
 // read: [128+64h, 128+64h+32) for query half h), so its rounding drops from
-// 2^-12 relative to about 2^-24; dQ keeps the single fp16 term.  That mode
+// 2^-12 relative to about 2^-24; dQ keeps the single fp16 term, but for cross
+// attention with D = 64, where shared memory has room for its low terms.  That mode
 // keeps the order dV(i) S(i+1) dK(i) dQ(i) dP(i+1).
 #include <math.h>
 
@@ -83,6 +84,9 @@ struct BwdSmem {
   static constexpr int kUsed = kUnits + 16;
   // at least 120 KB so that one CTA (holding all 512 TMEM columns) occupies an SM
   static constexpr int kBytes = kUsed > 122880 ? kUsed : 122880;
+  // the low terms of dS^T for dQ, where there is room for them (cross attention, D = 64)
+  static constexpr int kDSLow = (kUsed + 1023) & ~1023;
+  static constexpr int kBytesLow = kDSLow + kDSBytes;
 };
 
 struct BwdUnit {
@@ -243,6 +247,7 @@ enum { kLayoutContiguous = 0, kLayoutStriped = 1, kLayoutVarlen = 2, kLayoutCros
 template <int D, bool PRECISE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_constant__ TcBwdArgs a) {
   using L = BwdSmem<D>;
+  constexpr bool kLowDQ = PRECISE && LAYOUT == kLayoutCross && D == 64;  // dQ takes dS in two terms
   constexpr bool STRIPED = LAYOUT == kLayoutStriped, VARLEN = LAYOUT == kLayoutVarlen, CROSS = LAYOUT == kLayoutCross;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -406,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       const uint64_t dK_k = smem_desc_sw128(sK, 16, 1024), dK_mn = smem_desc_sw128(sK, 16384, 1024);
       const uint64_t dV_k = smem_desc_sw128(sV, 16, 1024);
       const uint64_t dS_k = smem_desc_sw128(sDS, 16, 1024), dS_mn = smem_desc_sw128(sDS, 16384, 1024);
+      const uint64_t dS_low_mn = smem_desc_sw128(sbase + (kLowDQ ? L::kDSLow : L::kDS), 16384, 1024);
       const uint64_t dQ_k0 = smem_desc_sw128(sbase + L::kQ0, 16, 1024), dQ_mn0 = smem_desc_sw128(sbase + L::kQ0, 16384, 1024);
       const uint64_t dO_k0 = smem_desc_sw128(sbase + L::kDO0, 16, 1024), dO_mn0 = smem_desc_sw128(sbase + L::kDO0, 16384, 1024);
       constexpr uint32_t kStageStep = L::kTile >> 4;  // descriptor step between the two stages
@@ -512,6 +518,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ss(T_DP, desc_off(dS_mn, kk * 2048), desc_off(dK_mn, kk * 2048), id_dq, kk > 0 ? 1u : 0u);
+            if (kLowDQ) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                mma_ss(T_DP, desc_off(dS_low_mn, kk * 2048), desc_off(dK_mn, kk * 2048), id_dq, 1u);
+            }
             mma_commit(BAR_DQ_FULL);  // dO_i (read by dP_i, dV_i) is consumed too: the dQ warps stage dQ_i in its buffer
             ++dq_cnt;
           };
@@ -689,6 +700,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
             const int chunk = (c >> 3) + q4;
             *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (r & 7)) << 4)) =
                 make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
+            if constexpr (kLowDQ)
+              *reinterpret_cast<uint4*>(ds_row + (L::kDSLow - L::kDS) + ((chunk ^ (r & 7)) << 4)) =
+                  make_uint4(pl[4 * q4], pl[4 * q4 + 1], pl[4 * q4 + 2], pl[4 * q4 + 3]);
           }
         }
         fence_proxy_async_smem();
@@ -872,7 +886,7 @@ cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st) {
                     : run(tc_bwd_kernel<128, false, kLayoutContiguous>, BwdSmem<128>::kBytes);
   } else if (a.d == 64) {
     if (a.cross)
-      e = a.precise ? run(tc_bwd_kernel<64, true, kLayoutCross>, BwdSmem<64>::kBytes)
+      e = a.precise ? run(tc_bwd_kernel<64, true, kLayoutCross>, BwdSmem<64>::kBytesLow)
                     : run(tc_bwd_kernel<64, false, kLayoutCross>, BwdSmem<64>::kBytes);
     else if (a.striped)
       e = a.precise ? run(tc_bwd_kernel<64, true, kLayoutStriped>, BwdSmem<64>::kBytes)

@@ -438,7 +438,8 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
  *   kv_len  device array of B int32 (clamped to [0, N_kv]), or NULL: every key is there.
  *     Keys and values from kv_len[b] on may hold anything (infinities and NaN too).  A batch
  *     entry without keys has o = 0, lse = -inf.
- *   flags   RA_PRECISE.
+ *   flags   RA_PRECISE (the backward pass of fp16 inputs takes it anyway; with d = 64 it
+ *     carries dS in two terms for dq too).
  *   A few queries (N_q Hq / Hkv <= 32; single tokens) run on a kernel bound by reading k
  *   and v once; where there are few query tiles the keys are split over the SMs and the parts
  *   joined.  P is rounded to fp16 (two terms with RA_PRECISE) against v in fp16 (bf16 v
