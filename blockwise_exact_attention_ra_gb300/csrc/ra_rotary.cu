@@ -18,7 +18,7 @@ template <typename T, typename TO, bool NORM, int EX, bool ALL>
 __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, const RotLane& l, const RotarySide& side, const float* factors,
                                             const T* in, TO* out, bool token, int h0, int h1, float* stage) {
   const long long in_step = a.heads * side.xl.hs, out_step = a.heads * side.yl.hs;
-  const float inv_d = 1.f / (float)a.d;
+  const float inv_d = 1.f / (float)a.d, least = rot_least(a);
   const float* C[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) C[i] = factors + l.token * a.d + (l.there[i] ? l.e[i] / 2 : 0);
@@ -39,8 +39,8 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, const RotLane& 
 #pragma unroll
         for (int j = 0; j < 4; ++j) s2 = __ffma2_rn(f[i][j], f[i][j], s2);
       float sum = group_sum(s2.x + s2.y, a.G), eps = a.eps;
-      if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
-        const float sc = rot_scale(sum);
+      if (__any_sync(0xffffffffu, !(sum < 1e37f && sum >= least))) {
+        const float sc = rot_scale(sum, least);
         sum = 0.f;
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -50,7 +50,7 @@ __device__ __forceinline__ void rotate_rows(const RotaryArgs& a, const RotLane& 
             sum = fmaf(f[i][j].y, f[i][j].y, fmaf(f[i][j].x, f[i][j].x, sum));
           }
         sum = group_sum(sum, a.G);
-        eps *= sc * sc;
+        eps = eps * sc * sc;
       }
       r = both(rsqrtf(fmaf(sum, inv_d, eps)));
     }

@@ -95,14 +95,22 @@ __device__ __forceinline__ uint32_t pack_pair(float2 f, __nv_bfloat16) {
 }
 __device__ __forceinline__ uint32_t pack_pair(float2 f, __half) { return pack_half2(f.x, f.y); }
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float2 (&f)[4]) {
+__device__ __forceinline__ void pack8(Raw8<T>& r, const float2 (&f)[4]) {
   if constexpr (sizeof(T) == 4) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r.v[i] = make_uint4(__float_as_uint(f[2 * i].x), __float_as_uint(f[2 * i].y), __float_as_uint(f[2 * i + 1].x),
+                          __float_as_uint(f[2 * i + 1].y));
   } else {
-    *reinterpret_cast<uint4*>(p) =
-        make_uint4(pack_pair(f[0], T()), pack_pair(f[1], T()), pack_pair(f[2], T()), pack_pair(f[3], T()));
+    r.v[0] = make_uint4(pack_pair(f[0], T()), pack_pair(f[1], T()), pack_pair(f[2], T()), pack_pair(f[3], T()));
   }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float2 (&f)[4]) {
+  Raw8<T> r;
+  pack8(r, f);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(p)[i] = r.v[i];
 }
 
 __device__ __forceinline__ float load_any(const void* p, int dtype, int i) {
@@ -325,7 +333,11 @@ __device__ __forceinline__ void rot_heads(const RotaryArgs& a, int H, int part, 
   *last = a.parts == 1 ? H : min(H, steps * (part + 1) / a.parts * a.heads);
 }
 
-// 2^-70 where the sum of squares left fp32's range (or is NaN), else 1.
-__device__ __forceinline__ float rot_scale(float sum) { return sum < 1e37f ? 1.f : 8.470329472543003e-22f; }
+// A row whose sum of squares left fp32's range (or is NaN) is scaled, and its sum formed again:
+// by 2^-70, or by 2^100 where the squares may have vanished and eps would not hide it.
+__device__ __forceinline__ float rot_least(const RotaryArgs& a) { return a.eps < 1e-30f ? 1e-30f : 0.f; }
+__device__ __forceinline__ float rot_scale(float sum, float least) {
+  return sum < least ? 1.2676506002282294e30f : sum < 1e37f ? 1.f : 8.470329472543003e-22f;
+}
 
 }  // namespace ra

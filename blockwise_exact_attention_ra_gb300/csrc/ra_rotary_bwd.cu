@@ -20,7 +20,7 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
                                               const float* factors, const T* x, const TG* dy,
                                               TO* out, bool token, int h0, int h1, float* stage, float* sums) {
   const long long x_step = a.heads * side.xl.hs, dy_step = a.heads * side.dyl.hs, out_step = a.heads * side.yl.hs;
-  const float inv_d = 1.f / (float)a.d;
+  const float inv_d = 1.f / (float)a.d, least = rot_least(a);
   float2 dw[2][4];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -66,8 +66,7 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
         for (int j = 0; j < 4; ++j) g[i][j] = __ffma2_rn(y[i][j], c[j], __fmul2_rn(p[i][j], sn[j]));
       }
     }
-    // the sums for the norm's factor; sc: what brings a row's squares into fp32's range
-    float sc = 1.f;
+    // the sums for the norm's factor
     auto sums_of = [&] {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -77,9 +76,8 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
         s2[i] = d2[i] = both(0.f);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const float2 x2 = sc == 1.f ? f[j] : __fmul2_rn(f[j], both(sc));
-          s2[i] = __ffma2_rn(x2, x2, s2[i]);
-          d2[i] = __ffma2_rn(__fmul2_rn(g[i][j], w[j]), x2, d2[i]);
+          s2[i] = __ffma2_rn(f[j], f[j], s2[i]);
+          d2[i] = __ffma2_rn(__fmul2_rn(g[i][j], w[j]), f[j], d2[i]);
         }
       }
     };
@@ -87,13 +85,23 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
     auto of_row = [&](const float2 (&v)[2]) {
       return group_sum((l.there[0] ? v[0].x + v[0].y : 0.f) + (l.there[1] ? v[1].x + v[1].y : 0.f), a.G);
     };
-    float sum = of_row(s2), dot = of_row(d2), eps = a.eps;
-    if (__any_sync(0xffffffffu, !(sum < 1e37f))) {
-      sc = rot_scale(sum);
+    float sum = of_row(s2), dot = of_row(d2), eps = a.eps, sc = 1.f;
+    if (__any_sync(0xffffffffu, !(sum < 1e37f && sum >= least))) {
+      // x in place, in its type: a power of two loses only what is 2^-100 of the row's largest
+      // (fp16 rows get here with zeros, infinities and NaN only)
+      sc = rot_scale(sum, least);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float2 f[4];
+        unpack8(rx[i], f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[j] = __fmul2_rn(f[j], both(sc));
+        pack8(rx[i], f);
+      }
       sums_of();
       sum = of_row(s2);
       dot = of_row(d2);
-      eps *= sc * sc;
+      eps = eps * sc * sc;
     }
     const float r = rsqrtf(fmaf(sum, inv_d, eps));
     const float2 rs = both(r * sc), along = both(-dot * r * inv_d);
@@ -104,7 +112,7 @@ __device__ __forceinline__ void gradient_rows(const RotaryArgs& a, const RotLane
       columns8(w, W[i], 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float2 normed = __fmul2_rn(f[j], rs);
+        const float2 normed = __fmul2_rn(f[j], both(r));
         if (row) dw[i][j] = __ffma2_rn(g[i][j], normed, dw[i][j]);
         dx[j] = __fmul2_rn(rs, __ffma2_rn(normed, along, __fmul2_rn(g[i][j], w[j])));
       }

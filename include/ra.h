@@ -525,7 +525,8 @@ int ra_rotary_bwd(const void* dq_out, const void* dk_out, ra_dtype dtype, ra_sha
  *     r = (mean_c x_c^2 + eps)^-1/2,   y = rotate(x r w)
  * for each row (b, n, h), the mean over all d columns, w q_weight or k_weight [d] in
  * w_dtype (NULL: ones).  rotary.rot = 0 norms without a rotation (for queries and keys of
- * cross attention, say).  eps >= 0; rows whose squares leave fp32's range are scaled first.
+ * cross attention, say).  eps >= 0; rows whose squares leave fp32's range, up or down, are
+ * scaled first.
  * Other arguments as for ra_rotary_fwd. */
 int ra_norm_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape,
                        const void* q_weight, const void* k_weight, ra_dtype w_dtype, float eps,

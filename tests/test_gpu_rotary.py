@@ -237,6 +237,37 @@ def test_rows_of_any_size(ra):
     assert z[0, 5, 0, [3, 11]].isnan().all() and not z[0, 5, 0, plain].isnan().any()
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("eps", [0.0, 1e-36])
+def test_small_rows_without_eps(ra, dtype, eps):
+    """Rows whose squares vanish in fp32, with an eps that does not hide it, beside ordinary ones and
+    rows of zeros (0 with an eps, 0 / 0 without)."""
+    d, N = 64, 9
+    freq = frequencies(64)
+    x = rand((1, N, 2, d), dtype, 30)
+    small = 1e-5 if dtype == torch.float16 else 1e-25
+    x[0, 1::2] *= small
+    x[0, 3, 0] *= 0.125
+    x[0, 8, 1] = 0
+    w = rand((d,), torch.float32, 31)
+    y, _ = ra.norm_rotary_fwd(x, None, w, None, freq, eps=eps)
+    eps = float(np.float32(eps))
+    n, _ = oracle.head_norm(f64(x), f64(w), max(eps, 1e-300))
+    rows = N if eps else 8
+    near("rows", y[:, :rows], oracle.rotary(n, np.arange(N), freq.cpu().numpy())[:, :rows],
+         turned_size(n, freq, False, 1.0)[:, :rows], U[dtype], 2e-6)
+    assert eps or (y[0, 8, 1].isnan().all() and not y[0, 8, 0].isnan().any())
+    x, dy = x[:, :8].contiguous(), rand((1, 8, 2, d), dtype, 32)
+    dx, _, dw, _ = ra.norm_rotary_bwd(x, None, dy, None, w, None, freq, eps=eps, grad_dtype=torch.float32)
+    g = oracle.rotary(f64(dy), np.arange(8), freq.cpu().numpy(), transpose=True)
+    want, want_w = oracle.head_norm_bwd(f64(x), g, f64(w), eps)
+    n, r = oracle.head_norm(f64(x), None, eps)
+    gs = turned_size(f64(dy), freq, False, 1.0)
+    size = r * (gs * np.abs(f64(w)) + np.abs(n) * (gs * np.abs(f64(w)) * np.abs(n)).mean(axis=-1, keepdims=True))
+    near("dx", dx, want, size, U[torch.float32], 4e-6)
+    near("dw", dw, want_w, (gs * np.abs(n)).sum(axis=(0, 1, 2)), U[torch.float32], 1e-5)
+
+
 @pytest.mark.parametrize("rot,interleaved", [(64, False), (20, False), (64, True)])
 def test_differences(ra, rot, interleaved):
     """The gradients against differences of the forward pass (fp32; central, step h: h^2 / 6 of third
