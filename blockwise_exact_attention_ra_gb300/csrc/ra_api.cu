@@ -2568,6 +2568,15 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   const CrossKeysArgs keys{k, v, k16 == k ? nullptr : ws + p.k16, ws + p.v16, bf, s.B, s.Nkv, s.Hkv, s.d,
                            s.kvl, kv_len, st};
   if ((e = launch_cross_prepare(r, keys, cs)) != cudaSuccess) return cuda_fail(e, "cross attention operands launch");
+  // D = dO . O of rows that few keys share is formed again: the rounding of an o in 16 bits alone would
+  // be up to three times that of dq and dk with 3 keys, 1.6 times with 200 (d 128, rows that lean
+  // towards a key), and shows little past 4 d keys
+  const int dot_keys = flags & RA_PRECISE ? s.Nkv : 4 * s.d;
+  if (o_dtype != RA_F32 && (kv_len || s.Nkv <= dot_keys)) {
+    const CrossDotArgs f{q, k, v, dO, lse, bf, s.B, s.Nq, s.Nkv, p.Np, s.Hq, s.Hkv, s.d, dot_keys, s.ql, s.kvl,
+                         scale * 1.4426950408889634f, r.d_mul, kv_len, r.D};
+    if ((e = launch_cross_dot(f, cs)) != cudaSuccess) return cuda_fail(e, "cross attention dO . O launch");
+  }
   TcBwdArgs a;
   memset(&a, 0, sizeof a);
   if ((rc = make_map(&a.tm_q, q16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) || (rc = make_map(&a.tm_do, do16, 0, s.B, s.Nq, s.Hq, s.d, q_l)) ||
@@ -2579,8 +2588,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   a.B = s.B; a.Hq = s.Hq; a.Hkv = s.Hkv; a.d = s.d;
   a.scale = scale;
   a.scale_log2 = scale * 1.4426950408889634f;
-  // fp16 gradients, whose own rounding is 2.1e-4, show that of dS to one fp16 term: 3.1e-4 in all,
-  // 2.1e-4 with two terms, which take 8 to 18% more time
+  // fp16 gradients, whose own rounding is 2.1e-4, show that of P and dS to one fp16 term: 3.0e-4 in all
   a.precise = (flags & RA_PRECISE) != 0 || dtype == RA_F16;
   a.dp_mul = r.d_mul; a.dk_mul = ldexpf(scale, -m); a.dv_mul = ldexpf(1.f, -kCrossP);
   a.lse = r.lse2; a.Dvec = r.D; a.dq_acc = r.dq_acc;

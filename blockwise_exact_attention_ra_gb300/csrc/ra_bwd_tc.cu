@@ -52,9 +52,10 @@
 // With PRECISE, dS enters the dK product as two fp16 terms (hi from shared
 // memory, lo = fp16(dS - hi) from TMEM columns of dP^T that have already been
 // read: [128+64h, 128+64h+32) for query half h), so its rounding drops from
-// 2^-12 relative to about 2^-24; dQ keeps the single fp16 term, but for cross
-// attention with D = 64, where shared memory has room for its low terms.  That mode
-// keeps the order dV(i) S(i+1) dK(i) dQ(i) dP(i+1).
+// 2^-12 relative to about 2^-24; dQ keeps the single fp16 term, and dV that of P.  In cross
+// attention dQ has two of dS too, whose low terms lie in shared memory, beside the rest with
+// D = 64, with D = 128 in dO(i)'s place, once dV(i) has read that and before dQ(i) comes
+// out through it; and dV two of P (in TMEM, the S^T columns beside P^T).  PRECISE keeps the order dV(i) S(i+1) dK(i) dQ(i) dP(i+1).
 #include <math.h>
 
 #include "ra_device.cuh"
@@ -76,7 +77,7 @@ struct BwdSmem {
   static constexpr int kVec0 = kDS + kDSBytes;  // per stage: LSE*log2e [128], D [128]
   static constexpr int kBars = kVec0 + 2 * 1024;
   // kv_full, kv_empty, q_full[2], q_empty[2], s_full, dp_full, ds_full,
-  // ds_free, dq_full, dq_free, dkv_full, dkv_free, drain, (unused),
+  // ds_free, dq_full, dq_free, dkv_full, dkv_free, drain, dv,
   // do_full[2], do_empty[2], (unused), p_full, unit_full[4], unit_empty[4]
   static constexpr int kNumBars = 30;
   static constexpr int kMisc = kBars + kNumBars * 8;  // TMEM address, abort flag
@@ -84,9 +85,12 @@ struct BwdSmem {
   static constexpr int kUsed = kUnits + 16;
   // at least 120 KB so that one CTA (holding all 512 TMEM columns) occupies an SM
   static constexpr int kBytes = kUsed > 122880 ? kUsed : 122880;
-  // the low terms of dS^T for dQ, where there is room for them (cross attention, D = 64)
-  static constexpr int kDSLow = (kUsed + 1023) & ~1023;
-  static constexpr int kBytesLow = kDSLow + kDSBytes;
+  // the low terms of dS^T for dQ (cross attention): beside the rest where there is room, else
+  // in dO's stage
+  static constexpr bool kLowBeside = D == 64;
+  static constexpr int kDSLow = kLowBeside ? (kUsed + 1023) & ~1023 : kDO0;
+  static constexpr int kBytesLow = kLowBeside ? kDSLow + kDSBytes : kBytes;
+  static_assert(kLowBeside || kTile == kDSBytes, "the low terms fit a stage");
 };
 
 struct BwdUnit {
@@ -247,7 +251,7 @@ enum { kLayoutContiguous = 0, kLayoutStriped = 1, kLayoutVarlen = 2, kLayoutCros
 template <int D, bool PRECISE, int LAYOUT>
 __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_constant__ TcBwdArgs a) {
   using L = BwdSmem<D>;
-  constexpr bool kLowDQ = PRECISE && LAYOUT == kLayoutCross && D == 64;  // dQ takes dS in two terms
+  constexpr bool kLow = PRECISE && LAYOUT == kLayoutCross;  // dQ takes dS in two terms, dV P
   constexpr bool STRIPED = LAYOUT == kLayoutStriped, VARLEN = LAYOUT == kLayoutVarlen, CROSS = LAYOUT == kLayoutCross;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sbase = smem_u32(smem);
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
   volatile int* unit_ring = reinterpret_cast<volatile int*>(smem + L::kUnits);
   const uint32_t BAR_S_FULL = bar0 + 48, BAR_DP_FULL = bar0 + 56, BAR_DS_FULL = bar0 + 64,
                  BAR_DS_FREE = bar0 + 72, BAR_DQ_FULL = bar0 + 80, BAR_DQ_FREE = bar0 + 88,
-                 BAR_DKV_FULL = bar0 + 96, BAR_DKV_FREE = bar0 + 104, BAR_DRAIN = bar0 + 112;
+                 BAR_DKV_FULL = bar0 + 96, BAR_DKV_FREE = bar0 + 104, BAR_DRAIN = bar0 + 112, BAR_DV = bar0 + 120;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const uint32_t warp = warp_id();
@@ -291,6 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
     mbar_init(BAR_DKV_FULL, 1);
     mbar_init(BAR_DKV_FREE, 128);
     mbar_init(BAR_DRAIN, 1);
+    mbar_init(BAR_DV, 1);
     mbar_init(BAR_P_FULL, 256);
     // the producer draws the CTA's units and passes them on through a ring of
     // four slots; every consumer thread (MMA lane, 256 compute and 128 dQ
@@ -316,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (CROSS) pdl_wait();
   const uint32_t tmem = *tmem_slot;
   const uint64_t lim = a.wait_limit_ns;
   const uint32_t T_S = tmem, T_DP = tmem + 128, T_DK = tmem + 256, T_DV = tmem + 256 + D;
@@ -347,7 +353,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         const int u = (int)atomicAdd(a.sched, 1u);
         unit_ring[slot] = u;
         mbar_arrive(bar_unit_full(slot));
-        if (u >= a.num_units) break;
+        if (u >= a.num_units) {
+          if (CROSS) pdl_trigger();
+          break;
+        }
         const BwdUnit bu = bwd_unit<STRIPED, VARLEN, CROSS>(a, u);
         if ((VARLEN || CROSS) && bu.n_iter == 0) continue;
         if (!mbar_wait(BAR_KV_EMPTY, (k & 1) ^ 1, abort_flag, a.status, lim)) { ok = false; break; }
@@ -411,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       const uint64_t dK_k = smem_desc_sw128(sK, 16, 1024), dK_mn = smem_desc_sw128(sK, 16384, 1024);
       const uint64_t dV_k = smem_desc_sw128(sV, 16, 1024);
       const uint64_t dS_k = smem_desc_sw128(sDS, 16, 1024), dS_mn = smem_desc_sw128(sDS, 16384, 1024);
-      const uint64_t dS_low_mn = smem_desc_sw128(sbase + (kLowDQ ? L::kDSLow : L::kDS), 16384, 1024);
+      const uint64_t dS_low_mn0 = smem_desc_sw128(sbase + (kLow ? L::kDSLow : L::kDS), 16384, 1024);
       const uint64_t dQ_k0 = smem_desc_sw128(sbase + L::kQ0, 16, 1024), dQ_mn0 = smem_desc_sw128(sbase + L::kQ0, 16384, 1024);
       const uint64_t dO_k0 = smem_desc_sw128(sbase + L::kDO0, 16, 1024), dO_mn0 = smem_desc_sw128(sbase + L::kDO0, 16384, 1024);
       constexpr uint32_t kStageStep = L::kTile >> 4;  // descriptor step between the two stages
@@ -473,6 +482,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
             const uint32_t pa = T_S + (kk < 4 ? kk * 8 : 64 + (kk - 4) * 8);
             mma_ts(T_DV, pa, desc_off(dO_mn, kk * 2048), id_acc, (it > it0 || kk > 0) ? 1u : 0u);
           }
+          if (kLow) {  // + P_lo^T dO_i, P_lo^T in the S columns beside P^T
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk) {
+              const uint32_t la = T_S + (kk < 4 ? 32 + kk * 8 : 96 + (kk - 4) * 8);
+              mma_ts(T_DV, la, desc_off(dO_mn, kk * 2048), id_acc, 1u);
+            }
+            if (!L::kLowBeside) mma_commit(BAR_DV);
+          }
           if (!PRECISE) {
             // dQ(i), then dK(i) with dS^T from TMEM (the S columns P^T leaves
             // free: queries 0-63 at 32-63, 64-127 at 96-127), then S(i+1) over them
@@ -518,7 +535,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
 #pragma unroll
             for (int kk = 0; kk < 8; ++kk)
               mma_ss(T_DP, desc_off(dS_mn, kk * 2048), desc_off(dK_mn, kk * 2048), id_dq, kk > 0 ? 1u : 0u);
-            if (kLowDQ) {
+            if (kLow) {
+              const uint64_t dS_low_mn = dS_low_mn0 + (L::kLowBeside ? 0u : s * kStageStep);
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 mma_ss(T_DP, desc_off(dS_low_mn, kk * 2048), desc_off(dK_mn, kk * 2048), id_dq, 1u);
@@ -658,6 +676,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < 32; j += 2) pk[j / 2] = pack_half2(__uint_as_float(pr[c + j]), __uint_as_float(pr[c + j + 1]));
           RA_TMEM_ST16(tS + c / 2, pk);
+          if constexpr (kLow) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {
+              const float2 hi = unpack_half2(pk[j / 2]);
+              pk[j / 2] = pack_half2(__uint_as_float(pr[c + j]) - hi.x, __uint_as_float(pr[c + j + 1]) - hi.y);
+            }
+            RA_TMEM_ST16(tS + 32 + c / 2, pk);
+          }
         }
         // P^T is in TMEM (and S^T has been read): the MMA warp may start dV
         // and then overwrite these columns with the next S^T
@@ -668,6 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         tc_fence_after();
         // dS^T of the previous iteration must have been consumed by its MMAs
         if (gi > 0 && !mbar_wait(BAR_DS_FREE, (gi - 1) & 1, abort_flag, a.status, lim)) { ok = false; break; }
+        if (kLow && !L::kLowBeside && !mbar_wait(BAR_DV, gi & 1, abort_flag, a.status, lim)) { ok = false; break; }
+        uint8_t* const low_row = smem + L::kDSLow + (L::kLowBeside ? 0 : s * L::kTile) + half * 16384 + r * 128;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t dp[32];
@@ -700,8 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
             const int chunk = (c >> 3) + q4;
             *reinterpret_cast<uint4*>(ds_row + ((chunk ^ (r & 7)) << 4)) =
                 make_uint4(pk[4 * q4], pk[4 * q4 + 1], pk[4 * q4 + 2], pk[4 * q4 + 3]);
-            if constexpr (kLowDQ)
-              *reinterpret_cast<uint4*>(ds_row + (L::kDSLow - L::kDS) + ((chunk ^ (r & 7)) << 4)) =
+            if constexpr (kLow)
+              *reinterpret_cast<uint4*>(low_row + ((chunk ^ (r & 7)) << 4)) =
                   make_uint4(pl[4 * q4], pl[4 * q4 + 1], pl[4 * q4 + 2], pl[4 * q4 + 3]);
           }
         }
@@ -868,12 +896,13 @@ cudaError_t launch_tc_bwd(TcBwdArgs& a, int num_sms, cudaStream_t st) {
   auto run = [&](auto kernel, int smem) {
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (err != cudaSuccess) return err;
+    if (a.cross) return launch_pdl(kernel, grid, kThreads, smem, st, a);
     kernel<<<grid, kThreads, smem, st>>>(a);
     return cudaSuccess;
   };
   if (a.d == 128) {
     if (a.cross)
-      e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutCross>, BwdSmem<128>::kBytes)
+      e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutCross>, BwdSmem<128>::kBytesLow)
                     : run(tc_bwd_kernel<128, false, kLayoutCross>, BwdSmem<128>::kBytes);
     else if (a.striped)
       e = a.precise ? run(tc_bwd_kernel<128, true, kLayoutStriped>, BwdSmem<128>::kBytes)

@@ -194,6 +194,7 @@ __global__ void __launch_bounds__(kThreads) cross_keys_kernel(const __grid_const
 // a row (b, n, h), n up to Np), the key side by the others.
 __global__ void __launch_bounds__(kThreads) cross_prepare_kernel(const __grid_constant__ CrossRowsArgs a,
                                                                  const __grid_constant__ CrossKeysArgs keys, int row_blocks) {
+  pdl_trigger();
   if ((int)blockIdx.x >= row_blocks) {
     copy_keys(keys, blockIdx.x - row_blocks, gridDim.x - row_blocks);
     return;
@@ -243,6 +244,8 @@ __global__ void __launch_bounds__(kThreads) cross_prepare_kernel(const __grid_co
 
 __global__ void __launch_bounds__(kThreads) cross_sum_kernel(const float* parts, int splits, int B, int Nkv, int Hkv, int d,
                                                              void* dk, void* dv, int dtype, Lay kvl) {
+  pdl_trigger();
+  pdl_wait();
   const int per_row = Hkv * d / 8;
   const long long plane = (long long)B * Nkv * Hkv * d, total = plane / 8;
   for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < 2 * total; i += (long long)gridDim.x * kThreads) {
@@ -263,6 +266,7 @@ __global__ void __launch_bounds__(kThreads) cross_sum_kernel(const float* parts,
 
 __global__ void __launch_bounds__(kThreads) cross_dq_kernel(const float* acc, float mul, int B, int Nq, int Hq, int d, void* dq,
                                                             int dtype, Lay ql) {
+  pdl_wait();
   const int per_row = Hq * d / 8;
   const long long total = (long long)B * Nq * per_row;
   for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < total; t += (long long)gridDim.x * kThreads) {
@@ -311,17 +315,18 @@ cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& ke
 
 cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
                              Lay kvl, cudaStream_t st) {
-  cross_sum_kernel<<<blocks_for((long long)B * Nkv * Hkv * d / 4), kThreads, 0, st>>>(parts, splits, B, Nkv, Hkv, d, dk, dv,
-                                                                                      dtype, kvl);
-  count_launch();
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(cross_sum_kernel, (int)blocks_for((long long)B * Nkv * Hkv * d / 4), kThreads, 0, st, parts,
+                                   splits, B, Nkv, Hkv, d, dk, dv, dtype, kvl);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 cudaError_t launch_cross_dq(const float* dq_acc, float mul, int B, int Nq, int Hq, int d, void* dq, int dtype, Lay ql,
                             cudaStream_t st) {
-  cross_dq_kernel<<<blocks_for((long long)B * Nq * Hq * d / 8), kThreads, 0, st>>>(dq_acc, mul, B, Nq, Hq, d, dq, dtype, ql);
-  count_launch();
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(cross_dq_kernel, (int)blocks_for((long long)B * Nq * Hq * d / 8), kThreads, 0, st, dq_acc,
+                                   mul, B, Nq, Hq, d, dq, dtype, ql);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 }  // namespace ra

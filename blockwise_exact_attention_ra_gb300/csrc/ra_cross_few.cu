@@ -376,7 +376,118 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
   cluster_sync();  // what others read stays until they have
 }
 
+// Backward pass: D_i = sum_j P_ij (dO_i . v_j) of rows that few keys share, which is dO . o
+// without o's rounding.  A block takes 128 query rows of a head, a warp 16 of them with all
+// keys, 64 at a time in shared memory for all warps; P from the saved lse, everything else as
+// above.  It runs beside the operand copies and waits for them only before it writes.
+constexpr int kDotWarps = 8, kDotKeys = 64;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __grid_constant__ CrossDotArgs a) {
+  constexpr int kChunks = D / 8, kTile = kDotKeys * D * 2;
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tiles = (a.Nq + 127) / 128, unit = blockIdx.x / tiles, b = unit / a.Hq, h = unit - b * a.Hq;
+  const int row0 = (blockIdx.x - unit * tiles) * 128 + warp * 16, g = h / (a.Hq / a.Hkv);
+  int len = a.Nkv;
+  if (a.kv_len) {
+    const int v = __ldg(a.kv_len + b);
+    len = v < 0 ? 0 : v > a.Nkv ? a.Nkv : v;
+  }
+  if (len == 0 || len > a.max_keys) {
+    pdl_wait();  // what comes after waits for this kernel alone
+    return;
+  }
+  const T* kbase = static_cast<const T*>(a.k) + lay_at(a.kvl, b, 0, g);
+  const T* vbase = static_cast<const T*>(a.v) + lay_at(a.kvl, b, 0, g);
+  const uint32_t kt = smem_u32(smem), vt = kt + kTile;
+  uint32_t qf[D / 16][4], df[D / 16][4];
+  float lse2[2], sum[2] = {0.f, 0.f};
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int n = row0 + half * 8 + (lane >> 2);
+    const bool there = n < a.Nq;
+    const long long at = (there ? lay_at(a.ql, b, n, h) : 0) + 2 * (lane & 3);
+    const float lse = there ? a.lse[((long long)b * a.Hq + h) * a.Nq + n] : -INFINITY;
+    lse2[half] = lse == -INFINITY ? -INFINITY : -lse * 1.4426950408889634f;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      const T* q = static_cast<const T*>(a.q) + at + 16 * k;
+      const T* dO = static_cast<const T*>(a.dO) + at + 16 * k;
+      qf[k][half] = there ? *reinterpret_cast<const uint32_t*>(q) : 0u;
+      qf[k][2 + half] = there ? *reinterpret_cast<const uint32_t*>(q + 8) : 0u;
+      df[k][half] = there ? *reinterpret_cast<const uint32_t*>(dO) : 0u;
+      df[k][2 + half] = there ? *reinterpret_cast<const uint32_t*>(dO + 8) : 0u;
+    }
+  }
+  const int mat = lane >> 3, mr = lane & 7;
+  for (int key0 = 0; key0 < len; key0 += kDotKeys) {
+    if (key0) __syncthreads();
+    const int keys = min(kDotKeys, (len - key0 + 15) & ~15);  // of whole products
+    for (int i = threadIdx.x; i < keys * kChunks; i += 32 * kDotWarps) {
+      const int r = i / kChunks, c = i - r * kChunks;
+      const bool there = key0 + r < len;
+      const long long at = (long long)(there ? key0 + r : 0) * a.kvl.rs + c * 8;
+      const uint32_t to = r * (D * 2) + ((c ^ (r & 7)) << 4);
+      copy16(kt + to, kbase + at, there);
+      copy16(vt + to, vbase + at, there);
+    }
+    copy_commit();
+    copy_wait<0>();
+    __syncthreads();
+    for (int j0 = 0; j0 < keys; j0 += 16) {
+      float s[2][4], dp[2][4];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[j][c] = dp[j][c] = 0.f;
+      const uint32_t key = j0 + (mat >> 1) * 8 + mr;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t at = key * (D * 2) + (((2 * k + (mat & 1)) ^ (key & 7)) << 4);
+        uint32_t f[4];
+        ldsm4(f, kt + at);
+        mma16816<T>(s[0], qf[k], f[0], f[1]);
+        mma16816<T>(s[1], qf[k], f[2], f[3]);
+        ldsm4(f, vt + at);
+        mma16816<T>(dp[0], df[k], f[0], f[1]);
+        mma16816<T>(dp[1], df[k], f[2], f[3]);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float p = ex2_approx(fmaf(s[j][c], a.scale_log2, lse2[c >> 1]));
+          if (key0 + j0 + j * 8 + 2 * (lane & 3) + (c & 1) < len) sum[c >> 1] = fmaf(p, dp[j][c], sum[c >> 1]);
+        }
+    }
+  }
+  pdl_wait();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float v = sum[half];
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
+    const int n = row0 + half * 8 + (lane >> 2);
+    if ((lane & 3) == 0 && n < a.Nq && lse2[half] != -INFINITY) a.D[((long long)b * a.Hq + h) * a.Np + n] = -v * a.d_mul;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_cross_dot(const CrossDotArgs& a, cudaStream_t st) {
+  auto run = [&](auto kernel) {
+    const int smem = 2 * kDotKeys * a.d * 2;
+    const int blocks = a.B * a.Hq * ((a.Nq + 127) / 128);
+    const cudaError_t e = launch_pdl(kernel, blocks, 32 * kDotWarps, smem, st, a);
+    if (e == cudaSuccess) count_launch();
+    return e;
+  };
+  if (a.d == 128) return a.bf16 ? run(cross_dot_kernel<__nv_bfloat16, 128>) : run(cross_dot_kernel<__half, 128>);
+  if (a.d == 64) return a.bf16 ? run(cross_dot_kernel<__nv_bfloat16, 64>) : run(cross_dot_kernel<__half, 64>);
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_cross_few(const CrossFewArgs& a, cudaStream_t st) {
   const int rows = a.Nq * (a.Hq / a.Hkv);

@@ -245,6 +245,17 @@ struct CrossRowsArgs {
   int* status;
 };
 cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& keys, cudaStream_t st);
+// D (as above) <- -d_mul sum_j P_ij dO_i . v_j for the rows of batch entries with up to max_keys keys
+struct CrossDotArgs {
+  const void *q, *k, *v, *dO;
+  const float* lse;
+  int bf16, B, Nq, Nkv, Np, Hq, Hkv, d, max_keys;
+  Lay ql, kvl;
+  float scale_log2, d_mul;
+  const int* kv_len;
+  float* D;
+};
+cudaError_t launch_cross_dot(const CrossDotArgs& a, cudaStream_t st);
 // dk, dv <- sums of the parts' planes
 cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
                              Lay kvl, cudaStream_t st);

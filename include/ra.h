@@ -438,8 +438,8 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
  *   kv_len  device array of B int32 (clamped to [0, N_kv]), or NULL: every key is there.
  *     Keys and values from kv_len[b] on may hold anything (infinities and NaN too).  A batch
  *     entry without keys has o = 0, lse = -inf.
- *   flags   RA_PRECISE (the backward pass of fp16 inputs takes it anyway; with d = 64 it
- *     carries dS in two terms for dq too).
+ *   flags   RA_PRECISE (P and dS in two terms, which the backward pass of fp16 inputs takes
+ *     anyway).
  *   A few queries (N_q Hq / Hkv <= 32; single tokens) run on a kernel bound by reading k
  *   and v once; where there are few query tiles the keys are split over the SMs and the parts
  *   joined.  P is rounded to fp16 (two terms with RA_PRECISE) against v in fp16 (bf16 v
@@ -455,7 +455,10 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
 /* Gradients of L = sum(o * dO): dq [B, N_q, Hq, d], dk, dv [B, N_kv, Hkv, d] in grad_dtype,
  * fully overwritten (rows from kv_len[b] on with zeros), by the formulas of ra_ring_bwd; o in
  * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  Operands are
- * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  P and dS are rounded to
+ * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  dO . o of an o in 16 bits
+ * is formed from q, k and v again for batch entries of up to 4 d keys (with RA_PRECISE of any
+ * number): the rounding of o would be the larger part of the errors of rows that few keys
+ * share, and stays in those of longer ones (pass o in RA_F32 to be without it).  P and dS are rounded to
  * fp16 times powers of two, dS by 1 (N_kv <= 1024) to 64 (N_kv > 32768): an element of dS past
  * 65504 divided by that overflows.  dq is summed over the key tiles in fp32 in an order that
  * varies; dk and dv do not vary from run to run. */

@@ -120,6 +120,47 @@ def test_forward(ra, case, dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("Nkv,d,lens,precise", [
+    (3, 128, None, False), (2, 64, None, False), (128, 128, None, False), (256, 64, None, False), (512, 128, None, False),
+    (700, 128, [700, 40, 0, 130], False), (1000, 64, [3, 1000, 256, 257], False), (900, 128, None, True),
+    (1500, 128, [9, 1500, 1200, 700], True)])
+def test_gradients_from_an_o_in_16_bits(ra, dtype, Nkv, d, lens, precise):
+    """o as the forward pass returns it in the inputs' type, rows that lean towards one key each.  In
+    the 2-norm, entry by entry: the gradients' own rounding (uniform within half a step of values
+    spread over a binade: at most u / sqrt(3), 0.58 u), for bf16 also that of P and dS to one fp16
+    term (2.8e-4 each at most), and 2e-5 for the rest.  An o rounded to 16 bits would leave up to three times u
+    where few keys share a row; past 4 d keys, without `precise`, it may leave another 0.58 u: |O| is
+    at most that of one value, and dP - D that of a difference of two."""
+    B, Nq, Hq, Hkv = (2 if lens is None else 4), 300, 4, 2
+    g = torch.Generator(device="cuda")
+    g.manual_seed(Nkv + d)
+    k, v, do = (torch.randn(s, generator=g, device="cuda") for s in ((B, Nkv, Hkv, d), (B, Nkv, Hkv, d), (B, Nq, Hq, d)))
+    q = torch.randn((B, Nq, Hq, d), generator=g, device="cuda")
+    for b in range(B):
+        n = Nkv if lens is None else max(lens[b], 1)
+        pick = torch.randint(0, n, (Nq, Hkv), generator=g, device="cuda")
+        at = k[b].gather(0, pick[..., None].expand(Nq, Hkv, d))
+        q[b] += 0.5 * torch.rand((Nq, Hq, 1), generator=g, device="cuda") * at.repeat_interleave(Hq // Hkv, dim=1)
+    q, k, v, do = (t.to(dtype) for t in (q, k, v, do))
+    kv_len = None if lens is None else torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = ra.cross_attention_fwd(q, k, v, kv_len, o_dtype=dtype)
+    got = ra.cross_attention_bwd(q, k, v, o, lse, do, kv_len, grad_dtype=dtype, precise=precise)
+    ra.ra_sync_status()
+    want = oracle.cross_attention(f64(q), f64(k), f64(v), d ** -0.5, lens or [Nkv] * B, f64(do))[2:]
+    u = torch.finfo(dtype).eps / 2
+    for b in range(B):
+        n = Nkv if lens is None else lens[b]
+        if n == 0:
+            assert not any(t[b].any() for t in got)
+            continue
+        limit = 0.58 * u + (5.6e-4 if dtype == torch.bfloat16 else 0) + 2e-5
+        for name, x, y in zip(("dq", "dk", "dv"), got, want):
+            lim = limit + (0.58 * u if n > 4 * d and not precise and name != "dv" else 0)
+            err = np.linalg.norm(f64(x)[b] - y[b]) / np.linalg.norm(y[b])
+            assert err <= lim, f"{name} of entry {b} ({n} keys): {err:.3g}, limit {lim:.3g}"
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("case", TILES + FEW)
 def test_backward(ra, case, dtype):
     B, Nq, Nkv, Hq, Hkv, d, lens = case
