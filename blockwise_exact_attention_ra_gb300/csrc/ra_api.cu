@@ -2330,11 +2330,13 @@ struct CrossPlan {
 
 // Parts of the keys, by what a call takes (us; measured): the waves of units, a tile of 128
 // keys `tile` and a unit's start and end `ends`, and the join, which reads every part's state.
-int cross_parts(long long units, long long tiles, double tile, double ends, double part_bytes, int most) {
+// Where batch entries differ in length about half of the work is there, and no wave is waited for.
+int cross_parts(long long units, long long tiles, double tile, double ends, double part_bytes, int most, bool ragged) {
   int best = 1;
   double least = 1e30;
   for (int s = 1; s <= most && s <= tiles; ++s) {
-    const double waves = (double)((units * s + kPlanSms - 1) / kPlanSms);
+    const double w = (double)(units * s) / kPlanSms, half = 0.5 * w + 0.25;
+    const double waves = !ragged ? ceil(w) : half < 1. ? 1. : half;
     const double t = waves * ((tiles + s - 1) / s * tile + ends) + (s > 1 ? 4. + s * part_bytes / 5e6 : 0.);
     if (t < least * 0.97) {
       least = t;
@@ -2380,8 +2382,8 @@ CrossPlan cross_plan(const Shape& s, int dtype, int flags, bool ragged) {
   } else {
     p.bf16_p = dtype == RA_BF16 && !(flags & RA_PRECISE) && (long long)s.Nq * group <= 512;
     const int pairs = ((s.Nq + 127) / 128 + 1) / 2;
-    const double tile = (s.Nq <= 128 ? 1.2 : 2.) * s.d / 128.;
-    p.splits = cross_parts((long long)s.B * s.Hq * pairs, tiles, tile, 4., 8. * s.B * s.Nq * s.Hq * s.d, 64);
+    const double tile = (s.Nq <= 128 ? 0.6 : 1.) * (s.d == 64 ? 1.5 : 1.9);
+    p.splits = cross_parts((long long)s.B * s.Hq * pairs, tiles, tile, 4., 8. * s.B * s.Nq * s.Hq * s.d, 64, false);
   }
   p.v16 = 256;
   p.parts = p.v16;
@@ -2408,14 +2410,15 @@ struct CrossBwdPlan {
   int Np, q_splits;
   size_t D, lse2, dq, sched, q16, do16, k16, v16, parts, total;
 };
-CrossBwdPlan cross_bwd_plan(const Shape& s, int dtype) {
+CrossBwdPlan cross_bwd_plan(const Shape& s, int dtype, bool ragged) {
   CrossBwdPlan p{};
   const long long nqt = (s.Nq + 127) / 128, nkt = (s.Nkv + 127) / 128, units = (long long)s.B * s.Hkv * nkt;
   const int group = s.Hq / s.Hkv;
   const size_t rows = (size_t)s.B * s.Hq * nqt * 128, qel = (size_t)s.B * s.Nq * s.Hq * s.d;
   const size_t kvel = (size_t)s.B * s.Nkv * s.Hkv * s.d;
   p.Np = (int)(nqt * 128);
-  const int most = cross_parts(units, nqt, 2.6 * group * s.d / 128., 5., 16. * kvel, 32);
+  const double tile = dtype == RA_F16 ? (s.d == 64 ? 3. : 4.5) : (s.d == 64 ? 2.5 : 3.);
+  const int most = cross_parts(units, nqt, tile * group, 5., 16. * kvel, 32, ragged);
   const long long per = (nqt + most - 1) / most;
   p.q_splits = (int)((nqt + per - 1) / per);  // none of them empty
   size_t off = 0;
@@ -2518,7 +2521,8 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
 size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape) {
   Shape s;
   if (check_cross(shape, dtype, 0, &s)) return 0;
-  return cross_bwd_plan(s, dtype).total;
+  const size_t a = cross_bwd_plan(s, dtype, false).total, b = cross_bwd_plan(s, dtype, true).total;
+  return a > b ? a : b;
 }
 
 int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype, const void* dO,
@@ -2532,7 +2536,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
       (rc = check_ptr(o, "o")) || (rc = check_ptr(dO, "dO")) || (rc = check_floats(lse, "lse")) ||
       (rc = check_ptr(dq, "dq")) || (rc = check_ptr(dk, "dk")) || (rc = check_ptr(dv, "dv")) || (rc = check_len(kv_len)))
     return rc;
-  const CrossBwdPlan p = cross_bwd_plan(s, dtype);
+  const CrossBwdPlan p = cross_bwd_plan(s, dtype, kv_len != nullptr);
   if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);

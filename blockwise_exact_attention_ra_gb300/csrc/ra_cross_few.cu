@@ -384,7 +384,7 @@ constexpr int kDotWarps = 8, kDotKeys = 64;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __grid_constant__ CrossDotArgs a) {
-  constexpr int kChunks = D / 8, kTile = kDotKeys * D * 2;
+  constexpr int kChunks = D / 8, kTile = kDotKeys * D * 2;  // K or V of a stage; two stages
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -401,7 +401,20 @@ __global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __gr
   }
   const T* kbase = static_cast<const T*>(a.k) + lay_at(a.kvl, b, 0, g);
   const T* vbase = static_cast<const T*>(a.v) + lay_at(a.kvl, b, 0, g);
-  const uint32_t kt = smem_u32(smem), vt = kt + kTile;
+  auto load = [&](int key0) {
+    const uint32_t stage = smem_u32(smem) + (key0 / kDotKeys & 1) * 2 * kTile;
+    const int keys = min(kDotKeys, (len - key0 + 15) & ~15);  // of whole products
+    for (int i = threadIdx.x; i < keys * kChunks; i += 32 * kDotWarps) {
+      const int r = i / kChunks, c = i - r * kChunks;
+      const bool there = key0 + r < len;
+      const long long at = (long long)(there ? key0 + r : 0) * a.kvl.rs + c * 8;
+      const uint32_t to = stage + r * (D * 2) + ((c ^ (r & 7)) << 4);
+      copy16(to, kbase + at, there);
+      copy16(to + kTile, vbase + at, there);
+    }
+    copy_commit();
+  };
+  load(0);
   uint32_t qf[D / 16][4], df[D / 16][4];
   float lse2[2], sum[2] = {0.f, 0.f};
 #pragma unroll
@@ -423,19 +436,11 @@ __global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __gr
   }
   const int mat = lane >> 3, mr = lane & 7;
   for (int key0 = 0; key0 < len; key0 += kDotKeys) {
-    if (key0) __syncthreads();
-    const int keys = min(kDotKeys, (len - key0 + 15) & ~15);  // of whole products
-    for (int i = threadIdx.x; i < keys * kChunks; i += 32 * kDotWarps) {
-      const int r = i / kChunks, c = i - r * kChunks;
-      const bool there = key0 + r < len;
-      const long long at = (long long)(there ? key0 + r : 0) * a.kvl.rs + c * 8;
-      const uint32_t to = r * (D * 2) + ((c ^ (r & 7)) << 4);
-      copy16(kt + to, kbase + at, there);
-      copy16(vt + to, vbase + at, there);
-    }
-    copy_commit();
     copy_wait<0>();
     __syncthreads();
+    if (key0 + kDotKeys < len) load(key0 + kDotKeys);  // into the place that the last turn read
+    const uint32_t kt = smem_u32(smem) + (key0 / kDotKeys & 1) * 2 * kTile, vt = kt + kTile;
+    const int keys = min(kDotKeys, (len - key0 + 15) & ~15);
     for (int j0 = 0; j0 < keys; j0 += 16) {
       float s[2][4], dp[2][4];
 #pragma unroll
@@ -478,9 +483,9 @@ __global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __gr
 
 cudaError_t launch_cross_dot(const CrossDotArgs& a, cudaStream_t st) {
   auto run = [&](auto kernel) {
-    const int smem = 2 * kDotKeys * a.d * 2;
-    const int blocks = a.B * a.Hq * ((a.Nq + 127) / 128);
-    const cudaError_t e = launch_pdl(kernel, blocks, 32 * kDotWarps, smem, st, a);
+    const int smem = 4 * kDotKeys * a.d * 2, blocks = a.B * a.Hq * ((a.Nq + 127) / 128);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_pdl(kernel, blocks, 32 * kDotWarps, smem, st, a);
     if (e == cudaSuccess) count_launch();
     return e;
   };
