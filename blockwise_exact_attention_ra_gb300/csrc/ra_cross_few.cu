@@ -380,6 +380,8 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
 // without o's rounding.  A block takes 128 query rows of a head, a warp 16 of them with all
 // keys, 64 at a time in shared memory for all warps; P from the saved lse, everything else as
 // above.  It runs beside the operand copies and waits for them only before it writes.
+// Measured: 8 x 512 queries of 16 heads of 64, 512 keys: 0.3 us more for the backward pass; 3 x 1924
+// of 32 heads of 128, 3 keys: 27 us more, reading q and dO (a forward pass for O: 37 and 64 us).
 constexpr int kDotWarps = 8, kDotKeys = 64;
 
 template <typename T, int D>
