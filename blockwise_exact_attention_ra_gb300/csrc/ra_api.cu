@@ -2405,10 +2405,10 @@ int check_len(const int* kv_len) {
 }
 
 // Backward workspace: D, lse2 [B, Hq, Np] fp32 | dq accumulator [B, Nq, Hq, d] fp32 | unit
-// counter | fp16 copies | planes of dK and dV.
+// counter | sizes of dO and v [B, Hkv] | fp16 copies | planes of dK and dV.
 struct CrossBwdPlan {
   int Np, q_splits;
-  size_t D, lse2, dq, sched, q16, do16, k16, v16, parts, total;
+  size_t D, lse2, dq, sched, range, q16, do16, k16, v16, parts, total;
 };
 CrossBwdPlan cross_bwd_plan(const Shape& s, int dtype, bool ragged) {
   CrossBwdPlan p{};
@@ -2426,6 +2426,7 @@ CrossBwdPlan cross_bwd_plan(const Shape& s, int dtype, bool ragged) {
   p.lse2 = off; off += align256(rows * 4);
   p.dq = off; off += align256(qel * 4);
   p.sched = off; off += 256;
+  p.range = off; off += align256((size_t)s.B * s.Hkv * sizeof(int2));
   if (dtype == RA_BF16) {
     p.q16 = off; off += align256(qel * 2);
     p.do16 = off; off += align256(qel * 2);
@@ -2546,16 +2547,14 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   memset(&r, 0, sizeof r);
   r.q = q; r.dO = dO; r.o = o; r.lse = lse;
   r.bf16 = bf; r.o_dtype = o_dtype;
-  r.B = s.B; r.Nq = s.Nq; r.Np = p.Np; r.Hq = s.Hq; r.d = s.d;
+  r.B = s.B; r.Nq = s.Nq; r.Np = p.Np; r.Hq = s.Hq; r.Hkv = s.Hkv; r.d = s.d;
   r.ql = s.ql;
   if (bf) {
     r.q16 = ws + p.q16;
     r.do16 = ws + p.do16;
   }
-  // dS times 2^m: a key's share of a row's probability is about 1 / Nkv, and a dS of 2^10 still fits
-  int m = 0;
-  while (m < 6 && (1ll << (m + 10)) < s.Nkv) ++m;
-  r.d_mul = ldexpf(1.f, m - kCrossP);
+  int2* const range = reinterpret_cast<int2*>(ws + p.range);
+  r.range = range;
   r.D = reinterpret_cast<float*>(ws + p.D);
   r.lse2 = reinterpret_cast<float*>(ws + p.lse2);
   r.dq_acc = reinterpret_cast<float*>(ws + p.dq);
@@ -2571,6 +2570,10 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   }
   const CrossKeysArgs keys{k, v, k16 == k ? nullptr : ws + p.k16, ws + p.v16, bf, s.B, s.Nkv, s.Hkv, s.d,
                            s.kvl, kv_len, st};
+  if ((e = cudaMemsetAsync(range, 0x80, (size_t)s.B * s.Hkv * sizeof(int2), cs)) != cudaSuccess)
+    return cuda_fail(e, "clear sizes");
+  CrossRangeArgs sizes{{{dO, s.ql, s.Hq, 0, 0}, {v, s.kvl, s.Hkv, 0, 0}}, bf, s.B, s.Nq, s.Nkv, s.Hkv, s.d, kv_len, range, 0};
+  if ((e = launch_cross_range(sizes, cs)) != cudaSuccess) return cuda_fail(e, "cross attention sizes launch");
   if ((e = launch_cross_prepare(r, keys, cs)) != cudaSuccess) return cuda_fail(e, "cross attention operands launch");
   // D = dO . O of rows that few keys share is formed again: the rounding of an o in 16 bits alone would
   // be up to three times that of dq and dk with 3 keys, 1.6 times with 200 (d 128, rows that lean
@@ -2578,7 +2581,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   const int dot_keys = flags & RA_PRECISE ? s.Nkv : 4 * s.d;
   if (o_dtype != RA_F32 && (kv_len || s.Nkv <= dot_keys)) {
     const CrossDotArgs f{q, k, v, dO, lse, bf, s.B, s.Nq, s.Nkv, p.Np, s.Hq, s.Hkv, s.d, dot_keys, s.ql, s.kvl,
-                         scale * 1.4426950408889634f, r.d_mul, kv_len, r.D};
+                         scale * 1.4426950408889634f, range, kv_len, r.D};
     if ((e = launch_cross_dot(f, cs)) != cudaSuccess) return cuda_fail(e, "cross attention dO . O launch");
   }
   TcBwdArgs a;
@@ -2594,7 +2597,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   a.scale_log2 = scale * 1.4426950408889634f;
   // fp16 gradients, whose own rounding is 2.1e-4, show that of P and dS to one fp16 term: 3.0e-4 in all
   a.precise = (flags & RA_PRECISE) != 0 || dtype == RA_F16;
-  a.dp_mul = r.d_mul; a.dk_mul = ldexpf(scale, -m); a.dv_mul = ldexpf(1.f, -kCrossP);
+  a.range = range; a.bf16_in = bf;
   a.lse = r.lse2; a.Dvec = r.D; a.dq_acc = r.dq_acc;
   a.dk = dk; a.dv = dv; a.grad_dtype = grad_dtype; a.kvl = s.kvl;
   a.status = st;
@@ -2610,7 +2613,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
   if (p.q_splits > 1 &&
       (e = launch_cross_sum(a.parts, p.q_splits, s.B, s.Nkv, s.Hkv, s.d, dk, dv, grad_dtype, s.kvl, cs)) != cudaSuccess)
     return cuda_fail(e, "cross attention gradient sum launch");
-  e = launch_cross_dq(r.dq_acc, a.dk_mul, s.B, s.Nq, s.Hq, s.d, dq, grad_dtype, s.ql, cs);
+  e = launch_cross_dq(r.dq_acc, scale, range, bf, s.B, s.Nq, s.Hq, s.Hkv, s.d, dq, grad_dtype, s.ql, cs);
   return e == cudaSuccess ? RA_OK : cuda_fail(e, "dq conversion launch");
 }
 

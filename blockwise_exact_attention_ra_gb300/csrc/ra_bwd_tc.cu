@@ -45,10 +45,11 @@
 // those columns after dK(i), which also leaves the next Q tile's load more
 // time; dQ(i) leaves TMEM while dK(i) and S(i+1) run, before dP(i+1) needs
 // its columns.
-// Cross attention (kLayoutCross): P and dS are held times 2^12 and 2^m, so that those of
-// long sequences (P about 1 / N) are normal fp16 numbers (131072 keys: dV within 1.3e-3
-// without, 3e-4 with): the first by adding to -LSE log2(e), the second by the factor that dP
-// and D enter dS with; dK, dV and dQ are scaled back.
+// Cross attention (kLayoutCross): P, dS and (where it is a copy) dO are held times powers of two, so
+// that those of long sequences (P about 1 / N) and of gradients of any size are normal fp16 numbers
+// (131072 keys: dV within 1.3e-3 without P's 2^12, 3e-4 with): P's by adding to -LSE log2(e), dS's,
+// which follows the sizes of dO and v (cross_scale), by the factor that dP and D enter dS with; dK, dV
+// and dQ are scaled back.
 // With PRECISE, dS enters the dK product as two fp16 terms (hi from shared
 // memory, lo = fp16(dS - hi) from TMEM columns of dP^T that have already been
 // read: [128+64h, 128+64h+32) for query half h), so its rounding drops from
@@ -602,6 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
         kvalid = host_len_at(a.host_len, j, a.ring_S) - (bu.jt - j * T) * 128;
       }
       if (CROSS) kvalid = (a.kv_len ? host_len_at(a.kv_len, bu.b, a.Nkv) : a.Nkv) - bu.jt * 128;
+      const float dp_mul = CROSS ? cross_scale(a.range, bu.b * a.Hkv + bu.g, a.bf16_in).mul : 1.f;
       // kq: position in the current query head's sweep, enough to place the
       // diagonal tiles without the query tile index
       int kq = 0;
@@ -709,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
             const float2 ndd = *reinterpret_cast<const float2*>(ndvec + c + j);
             // (CROSS: of D and P times powers of two, dS times another)
             const float2 dpj = make_float2(__uint_as_float(dp[j]), __uint_as_float(dp[j + 1]));
-            const float2 diff = CROSS ? __ffma2_rn(dpj, make_float2(a.dp_mul, a.dp_mul), ndd) : __fadd2_rn(dpj, ndd);
+            const float2 diff = CROSS ? __ffma2_rn(dpj, make_float2(dp_mul, dp_mul), ndd) : __fadd2_rn(dpj, ndd);
             const float2 ds = __fmul2_rn(make_float2(__uint_as_float(pr[c + j]), __uint_as_float(pr[c + j + 1])), diff);
             const float d0 = ds.x, d1 = ds.y;
             pk[j / 2] = pack_half2(d0, d1);
@@ -862,10 +864,16 @@ __global__ void __launch_bounds__(kThreads, 1) tc_bwd_kernel(const __grid_consta
       if (!ok) break;
       if (!mbar_wait(BAR_DKV_FULL, k & 1, abort_flag, a.status, lim)) { ok = false; break; }
       tc_fence_after();
+      float muls[2] = {a.scale, 1.f};
+      if (CROSS) {
+        const CrossScale sc = cross_scale(a.range, bu.b * a.Hkv + bu.g, a.bf16_in);
+        muls[0] = a.scale * sc.ds;
+        muls[1] = sc.dv;
+      }
 #pragma unroll
       for (int which = 0; which < 2; ++which) {
         const uint32_t src = (which == 0 ? T_DK : T_DV) + lane_off;
-        const float mul = which == 0 ? (CROSS ? a.dk_mul : a.scale) : (CROSS ? a.dv_mul : 1.f);
+        const float mul = muls[which];
 #pragma unroll
         for (int c = 0; c < D; c += 32) {
           uint32_t v[32];

@@ -1,6 +1,6 @@
 // The kernels around cross attention's products: the join of states over parts of the keys,
-// fp16 operand copies, the backward pass's row terms and its last conversions.  All are
-// bound by what they read and write.
+// the sizes of dO and v, fp16 operand copies, the backward pass's row terms and its last
+// conversions.  All are bound by what they read and write.
 #include <math.h>
 
 #include "ra_device.cuh"
@@ -190,38 +190,102 @@ __global__ void __launch_bounds__(kThreads) cross_keys_kernel(const __grid_const
   copy_keys(a, blockIdx.x, gridDim.x);
 }
 
+// Bounds of the norms of the rows of dO and of v for each key head (for cross_scale).  A lane
+// keeps the largest sum of squares of its eight columns over the rows that it reads of a head; the root of
+// the sum of these over a row's d / 8 lanes is at least every row's norm, and for values without a
+// pattern less than twice the largest.  No lane needs another until the end, so that reading
+// is what bounds it (the sums row by row take twice the time).  Sums that leave fp32's range are
+// left out, so that infinities and NaN, which lose their own gradients whatever the scale, leave the
+// others theirs; a lane that met some, or nothing else than zeros, reads its rows again at another scale.
+// It adds 6 us to 15 (77 queries, 590 keys, 8 heads of 128) and 28 to 648 (2 x 4096 x 4096, 16 heads of 128).
+__global__ void __launch_bounds__(kThreads) cross_range_kernel(const __grid_constant__ CrossRangeArgs a) {
+  pdl_trigger();
+  const bool values = (int)blockIdx.x >= a.blocks;
+  const CrossRangeArgs::Side& t = a.side[values];
+  const int G = a.d / 8, slots = kThreads / G, slot = threadIdx.x / G;
+  const int unit = (values ? blockIdx.x - a.blocks : blockIdx.x) / t.chunks, chunk = (values ? blockIdx.x - a.blocks : blockIdx.x) - unit * t.chunks;
+  const int tiles = (t.H + t.heads - 1) / t.heads, b = unit / tiles, h = (unit - b * tiles) * t.heads + slot % t.heads;
+  const int N = values ? len_at(a.kv_len, b, a.Nkv) : a.Nq, tokens = slots / t.heads, step = tokens * t.chunks;
+  const bool mine = slot / t.heads < tokens && h < t.H;
+  const int first = mine ? chunk * tokens + slot / t.heads : N;
+  const uint16_t* x = static_cast<const uint16_t*>(t.x) + lay_at(t.l, b, 0, mine ? h : 0) + threadIdx.x % G * 8;
+  bool left_out = false;
+  auto largest = [&](float by) {
+    float top = 0.f;
+    for (long long n = first; n < N; n += 4ll * step) {
+      uint4 v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[k] = n + (long long)k * step < N ? *reinterpret_cast<const uint4*>(x + (n + (long long)k * step) * t.l.rs) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float sum = 0.f;
+        const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 f = a.bf16 ? make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u)) : unpack_half2(w[j]);
+          f.x *= by;
+          f.y *= by;
+          sum = fmaf(f.y, f.y, fmaf(f.x, f.x, sum));
+        }
+        left_out |= !(sum < 1e37f);
+        if (sum < 1e37f) top = fmaxf(top, sum);
+      }
+    }
+    return top;
+  };
+  float top = largest(1.f), shift = 0.f;
+  if (left_out || top < 1e-30f) {
+    shift = left_out ? -70.f : 100.f;
+    top = largest(left_out ? 8.470329472543003e-22f : 1.2676506002282294e30f);
+  }
+  // log2 of the lanes' sums, joined
+  const float own = top > 0.f ? log2f(top) - 2.f * shift : -INFINITY;
+  float most = own;
+  for (int o = G >> 1; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  float sum = most == -INFINITY ? 0.f : exp2f(own - most);
+  for (int o = G >> 1; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (threadIdx.x % G || most == -INFINITY) return;
+  const int norm = (int)ceilf(8.f * (most + log2f(sum)) + 0.01f);
+  int2* const range = a.range + (long long)b * a.Hkv + h / (t.H / a.Hkv);
+  int* const to = values ? &range->y : &range->x;
+  if (norm > *static_cast<volatile int*>(to)) atomicMax(to, norm);
+}
+
 // What the backward kernel needs, the query side by the first row_blocks blocks (d / 8 lanes
 // a row (b, n, h), n up to Np), the key side by the others.
 __global__ void __launch_bounds__(kThreads) cross_prepare_kernel(const __grid_constant__ CrossRowsArgs a,
                                                                  const __grid_constant__ CrossKeysArgs keys, int row_blocks) {
   pdl_trigger();
+  pdl_wait();
   if ((int)blockIdx.x >= row_blocks) {
     copy_keys(keys, blockIdx.x - row_blocks, gridDim.x - row_blocks);
     return;
   }
   const int G = a.d / 8, lane = threadIdx.x % G, in_dtype = a.bf16 ? RA_BF16 : RA_F16;
-  const long long rows = (long long)a.B * a.Np * a.Hq, step = (long long)row_blocks * (kThreads / G);
+  const unsigned rows = (unsigned)a.B * a.Np * a.Hq, step = row_blocks * (kThreads / G);  // up to 2^31 rows
   if (blockIdx.x == 0 && threadIdx.x < 64) a.sched[threadIdx.x] = 0u;
   bool bad = false;
   // the warp's rows end together: its lanes meet in the sums
-  const long long first = (long long)blockIdx.x * (kThreads / G) + threadIdx.x / G;
-  for (long long base = first - (threadIdx.x % 32) / G; base < rows; base += step) {
-    const long long i = base + (threadIdx.x % 32) / G;
-    const int h = (int)(i % a.Hq);
-    const long long bn = i / a.Hq;
-    const int b = (int)(bn / a.Np), n = (int)(bn - (long long)b * a.Np);
-    const bool there = i < rows && n < a.Nq;
-    float dot = 0.f;
+  const unsigned first = blockIdx.x * (kThreads / G) + threadIdx.x / G, group = a.Hq / a.Hkv;
+  for (unsigned base = first - (threadIdx.x % 32) / G; base < rows; base += step) {
+    const unsigned i = base + (threadIdx.x % 32) / G, bn = i / a.Hq, h = i - bn * a.Hq, b = bn / a.Np, n = bn - b * a.Np;
+    const bool there = i < rows && (int)n < a.Nq;
+    float dot = 0.f, mul = 0.f;
     if (there) {
+      const CrossScale sc = cross_scale(a.range, b * a.Hkv + h / group, a.bf16);
+      mul = sc.mul;
       const long long src = lay_at(a.ql, b, n, h) + 8 * lane;
       const long long row = (((long long)b * a.Nq + n) * a.Hq + h) * a.d + 8 * lane;
       float f[8], g[8];
       get8(a.dO, in_dtype, src, f);
       get8(a.o, a.o_dtype, src, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dot = fmaf(f[j], g[j], dot);
+      for (int j = 0; j < 8; ++j) {
+        f[j] *= sc.copy;
+        dot = fmaf(f[j], g[j], dot);
+      }
       if (a.do16) {
-        bad |= past_fp16(f);
         put8(a.do16, RA_F16, row, f);
         get8(a.q, in_dtype, src, g);
         bad |= past_fp16(g);
@@ -235,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) cross_prepare_kernel(const __grid_co
       const long long at = ((long long)b * a.Hq + h) * a.Np + n;
       const float lse = there ? a.lse[((long long)b * a.Hq + h) * a.Nq + n] : -INFINITY;
       const bool seen = lse != -INFINITY;
-      a.D[at] = seen ? -dot * a.d_mul : 0.f;
+      a.D[at] = seen ? -dot * mul : 0.f;
       a.lse2[at] = seen ? (float)kCrossP - lse * kLog2e : -INFINITY;  // P = 0
     }
   }
@@ -264,19 +328,18 @@ __global__ void __launch_bounds__(kThreads) cross_sum_kernel(const float* parts,
   }
 }
 
-__global__ void __launch_bounds__(kThreads) cross_dq_kernel(const float* acc, float mul, int B, int Nq, int Hq, int d, void* dq,
-                                                            int dtype, Lay ql) {
+__global__ void __launch_bounds__(kThreads) cross_dq_kernel(const float* acc, float scale, const int2* range, int bf16, int B,
+                                                            int Nq, int Hq, int Hkv, int d, void* dq, int dtype, Lay ql) {
   pdl_wait();
-  const int per_row = Hq * d / 8;
-  const long long total = (long long)B * Nq * per_row;
-  for (long long t = (long long)blockIdx.x * kThreads + threadIdx.x; t < total; t += (long long)gridDim.x * kThreads) {
-    const long long bn = t / per_row;
-    const int e = (int)(t - bn * per_row) * 8, h = e / d, b = (int)(bn / Nq), n = (int)(bn - (long long)b * Nq);
+  const unsigned G = d / 8, lane = threadIdx.x % G * 8, per = kThreads / G, rows = (unsigned)B * Nq * Hq, group = Hq / Hkv;
+  for (unsigned i = blockIdx.x * per + threadIdx.x / G; i < rows; i += gridDim.x * per) {
+    const unsigned bn = i / Hq, h = i - bn * Hq, b = bn / Nq, n = bn - b * Nq;
     float f[8];
-    get8(acc, RA_F32, t * 8, f);
+    get8(acc, RA_F32, (long long)i * d + lane, f);
+    const float mul = scale * cross_scale(range, b * Hkv + h / group, bf16).ds;
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] *= mul;
-    put8(dq, dtype, lay_at(ql, b, n, h) + (e - h * d), f);
+    put8(dq, dtype, lay_at(ql, b, n, h) + lane, f);
   }
 }
 
@@ -305,12 +368,36 @@ cudaError_t launch_cross_keys(const CrossKeysArgs& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+cudaError_t launch_cross_range(CrossRangeArgs& a, cudaStream_t st) {
+  // a block's rows lie together: of heads where those do, else of tokens; four blocks an SM in all
+  // (16 x 4000 keys of 2 heads of 128, 64 queries: the backward pass takes 111 us, with eight 117, with two 113)
+  const int slots = kThreads / (a.d / 8);
+  long long units[2], most[2], all = 0;
+  for (int i = 0; i < 2; ++i) {
+    CrossRangeArgs::Side& t = a.side[i];
+    const int N = i ? a.Nkv : a.Nq;
+    t.heads = t.l.hs > t.l.rs ? 1 : t.H < slots ? t.H : slots;
+    units[i] = (long long)a.B * ((t.H + t.heads - 1) / t.heads);
+    const long long tokens = 4 * (slots / t.heads);
+    most[i] = (N + tokens - 1) / tokens;
+    all += units[i] * most[i];
+  }
+  for (int i = 0; i < 2; ++i) {
+    const long long want = most[i] * 152 * 4 / all + 1;
+    a.side[i].chunks = (int)(want < most[i] ? want : most[i]);
+  }
+  a.blocks = (int)(units[0] * a.side[0].chunks);
+  cross_range_kernel<<<(unsigned)(a.blocks + units[1] * a.side[1].chunks), kThreads, 0, st>>>(a);
+  count_launch();
+  return cudaGetLastError();
+}
+
 cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& keys, cudaStream_t st) {
   const unsigned rows = blocks_for((long long)a.B * a.Np * a.Hq * a.d / 8);
   const unsigned more = keys.k16 ? blocks_for((long long)keys.B * keys.Nkv * keys.Hkv * keys.d / 8) : 0;
-  cross_prepare_kernel<<<rows + more, kThreads, 0, st>>>(a, keys, (int)rows);
-  count_launch();
-  return cudaGetLastError();
+  const cudaError_t e = launch_pdl(cross_prepare_kernel, (int)(rows + more), kThreads, 0, st, a, keys, (int)rows);
+  if (e == cudaSuccess) count_launch();
+  return e;
 }
 
 cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
@@ -321,10 +408,10 @@ cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int
   return e;
 }
 
-cudaError_t launch_cross_dq(const float* dq_acc, float mul, int B, int Nq, int Hq, int d, void* dq, int dtype, Lay ql,
-                            cudaStream_t st) {
+cudaError_t launch_cross_dq(const float* dq_acc, float scale, const int2* range, int bf16, int B, int Nq, int Hq, int Hkv, int d,
+                            void* dq, int dtype, Lay ql, cudaStream_t st) {
   const cudaError_t e = launch_pdl(cross_dq_kernel, (int)blocks_for((long long)B * Nq * Hq * d / 8), kThreads, 0, st, dq_acc,
-                                   mul, B, Nq, Hq, d, dq, dtype, ql);
+                                   scale, range, bf16, B, Nq, Hq, Hkv, d, dq, dtype, ql);
   if (e == cudaSuccess) count_launch();
   return e;
 }

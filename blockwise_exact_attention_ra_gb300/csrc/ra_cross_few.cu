@@ -473,13 +473,14 @@ __global__ void __launch_bounds__(32 * kDotWarps, 2) cross_dot_kernel(const __gr
     }
   }
   pdl_wait();
+  const CrossScale sc = cross_scale(a.range, b * a.Hkv + g, std::is_same<T, __nv_bfloat16>::value);
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
     float v = sum[half];
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
     const int n = row0 + half * 8 + (lane >> 2);
-    if ((lane & 3) == 0 && n < a.Nq && lse2[half] != -INFINITY) a.D[((long long)b * a.Hq + h) * a.Np + n] = -v * a.d_mul;
+    if ((lane & 3) == 0 && n < a.Nq && lse2[half] != -INFINITY) a.D[((long long)b * a.Hq + h) * a.Np + n] = -v * sc.copy * sc.mul;
   }
 }
 

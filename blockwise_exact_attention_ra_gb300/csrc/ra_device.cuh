@@ -78,6 +78,32 @@ inline cudaError_t launch_pdl(void (*kernel)(Params...), int grid, int block, si
 }
 
 // ---------------------------------------------------------------------------
+// Powers of two of cross attention's backward pass, for a key head of a batch entry.  Its
+// fp16 operands are a copy of dO (bf16 inputs; fp16 ones are taken as they are) and dS, whose
+// sizes go with the loss (1e-8 and 1e4 are ordinary).  With X and Y above the largest norms of
+// a row of dO and of v, |dP| <= X Y, and |dS| = P |dP - D| <= P (1 - P) 2 X Y <= X Y / 2: dO times
+// 2^a with X 2^a <= 2^14 and dS times 2^s with X Y 2^s <= 2^16 do not overflow, with a factor of
+// two for what rounding adds.  Rows that lean to nothing have dS = X Y / (30 N) or so, of which
+// 2^16 leaves normal numbers for N of 131072 keys and rows of dO 2^-8 of the largest.
+// ---------------------------------------------------------------------------
+struct CrossScale {
+  float copy;   // 2^a, of dO's copy
+  float mul;    // what dP of that copy, and dO . O of it, enter dS' / P' with: 2^(s - a - kCrossP)
+  float ds;     // 2^-s
+  float dv;     // 2^(-a - kCrossP)
+};
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((e + 127) << 23); }  // -126 to 127
+__device__ __forceinline__ CrossScale cross_scale(const int2* range, int head, int bf16) {
+  const int2 r = range[head];
+  const int x = r.x == kCrossNone ? 0 : r.x, y = r.y == kCrossNone ? 0 : r.y;
+  // v is an fp16 number: norms from 2^-24 to 2^20.  The limits on a and s keep every factor a
+  // normal number; they are met by norms of dO outside 2^-72 to 2^100
+  const int a = bf16 ? min(max(14 - ((x + 15) >> 4), -110), 110) : 0;
+  const int s = min(max(16 - ((x + min(max(y, -24 * 16), 20 * 16) + 15) >> 4), -104), 112);
+  return {power_of_two(a), power_of_two(s - a - kCrossP), power_of_two(-s), power_of_two(-a - kCrossP)};
+}
+
+// ---------------------------------------------------------------------------
 // mbarrier
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

@@ -179,7 +179,8 @@ struct TcBwdArgs {
   int cross, Nkv, Np, q_splits;
   const int* kv_len;    // optional: keys per batch entry (device)
   float* parts;         // q_splits > 1: dK then dV [q_splits][B, Nkv, Hkv, d]
-  float dp_mul, dk_mul, dv_mul;  // lse is larger by kCrossP, Dvec is times dp_mul = 2^(m - kCrossP), dS times 2^m
+  const int2* range;    // cross_scale's [B, Hkv]: lse is larger by kCrossP, Dvec and dS times powers of two
+  int bf16_in;          // of the inputs' type, before the copies
   const float* lse;   // [B, Hq, N]: -LSE * log2(e)
   const float* Dvec;  // [B, Hq, N]: -D
   float* dq_acc;      // packed fp32 [B, N, Hq, d], pre-zeroed, reduce-added
@@ -203,6 +204,22 @@ struct CrossState {   // [splits][B, Nq, Hq, d], [splits][B, Hq, Nq] (natural-lo
 };
 constexpr int kCrossFewRows = 32;
 constexpr int kCrossP = 12;  // backward: P is held times 2^kCrossP
+// Backward: bounds of the norms of the rows of dO (x) and of v (y) that a key head of a batch
+// entry meets, as 16 log2 rounded up; kCrossNone: all are zero.
+constexpr int kCrossNone = (int)0x80808080;  // what bytes of 0x80 are
+struct CrossRangeArgs {
+  struct Side {
+    const void* x;
+    Lay l;
+    int H;
+    int heads, chunks;  // set by the launch: heads of a block, and blocks that share their rows
+  } side[2];            // dO, v
+  int bf16, B, Nq, Nkv, Hkv, d;
+  const int* kv_len;
+  int2* range;  // [B, Hkv], kCrossNone before
+  int blocks;   // of dO; set by the launch
+};
+cudaError_t launch_cross_range(CrossRangeArgs& a, cudaStream_t st);
 struct CrossFewArgs {
   const void *q, *k, *v;
   int bf16, B, Nq, Nkv, Hq, Hkv, d;
@@ -230,28 +247,30 @@ struct CrossKeysArgs {
   int* status;
 };
 cudaError_t launch_cross_keys(const CrossKeysArgs& a, cudaStream_t st);
-// what the backward kernel needs of the query side: lse2 = kCrossP - lse log2(e), D = -d_mul
-// dO . O (rows of Np; -inf and 0 where there is no row or it saw no key), fp16 copies of q and dO (bf16
-// inputs), dq_acc = 0 and the unit counter; and the key side as above where k16 is not NULL
+// what the backward kernel needs of the query side: lse2 = kCrossP - lse log2(e), D = -dO . O
+// times its power of two (rows of Np; -inf and 0 where there is no row or it saw no key), fp16 copies of q
+// and, times another, of dO (bf16 inputs), dq_acc = 0 and the unit counter; and the key side as above
+// where k16 is not NULL
 struct CrossRowsArgs {
   const void *q, *dO, *o;
   const float* lse;
-  int bf16, o_dtype, B, Nq, Np, Hq, d;
+  int bf16, o_dtype, B, Nq, Np, Hq, Hkv, d;
   Lay ql;
-  float d_mul;
+  const int2* range;
   void *q16, *do16;  // NULL for fp16 inputs
   float *D, *lse2, *dq_acc;
   unsigned int* sched;
   int* status;
 };
 cudaError_t launch_cross_prepare(const CrossRowsArgs& a, const CrossKeysArgs& keys, cudaStream_t st);
-// D (as above) <- -d_mul sum_j P_ij dO_i . v_j for the rows of batch entries with up to max_keys keys
+// D (as above) <- -sum_j P_ij dO_i . v_j for the rows of batch entries with up to max_keys keys
 struct CrossDotArgs {
   const void *q, *k, *v, *dO;
   const float* lse;
   int bf16, B, Nq, Nkv, Np, Hq, Hkv, d, max_keys;
   Lay ql, kvl;
-  float scale_log2, d_mul;
+  float scale_log2;
+  const int2* range;
   const int* kv_len;
   float* D;
 };
@@ -259,9 +278,9 @@ cudaError_t launch_cross_dot(const CrossDotArgs& a, cudaStream_t st);
 // dk, dv <- sums of the parts' planes
 cudaError_t launch_cross_sum(const float* parts, int splits, int B, int Nkv, int Hkv, int d, void* dk, void* dv, int dtype,
                              Lay kvl, cudaStream_t st);
-// out (dtype, layout) <- mul x (packed fp32)
-cudaError_t launch_cross_dq(const float* dq_acc, float mul, int B, int Nq, int Hq, int d, void* dq, int dtype, Lay ql,
-                            cudaStream_t st);
+// dq (dtype, layout) <- dq_acc (packed fp32) times scale, without the head's power of two
+cudaError_t launch_cross_dq(const float* dq_acc, float scale, const int2* range, int bf16, int B, int Nq, int Hq, int Hkv, int d,
+                            void* dq, int dtype, Lay ql, cudaStream_t st);
 
 // Counts kernel launches (ra_launch_count).
 void count_launch(unsigned n = 1);

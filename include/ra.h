@@ -454,13 +454,15 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
 
 /* Gradients of L = sum(o * dO): dq [B, N_q, Hq, d], dk, dv [B, N_kv, Hkv, d] in grad_dtype,
  * fully overwritten (rows from kv_len[b] on with zeros), by the formulas of ra_ring_bwd; o in
- * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  Operands are
- * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros).  dO . o of an o in 16 bits
+ * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  q, k and v are
+ * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros), dO times a power of two.  dO . o of an o in 16 bits
  * is formed from q, k and v again for batch entries of up to 4 d keys (with RA_PRECISE of any
  * number): the rounding of o would be the larger part of the errors of rows that few keys
  * share, and stays in those of longer ones (pass o in RA_F32 to be without it).  P and dS are rounded to
- * fp16 times powers of two, dS by 1 (N_kv <= 1024) to 64 (N_kv > 32768): an element of dS past
- * 65504 divided by that overflows.  dq is summed over the key tiles in fp32 in an order that
+ * fp16 times powers of two.  Those of dO and dS follow, for each batch entry and key head, the largest
+ * rows of dO and v, so that dO may have any size (the largest rows' norm from 2^-72 to 2^100) and no element
+ * overflows; rows of dO far below the largest lose digits of their own dq, from 2^-8 at N_kv = 131072
+ * (2^-15 at 1024) on.  dq is summed over the key tiles in fp32 in an order that
  * varies; dk and dv do not vary from run to run. */
 size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape);
 int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype,
