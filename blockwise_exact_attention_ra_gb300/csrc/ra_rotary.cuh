@@ -6,9 +6,9 @@
 //   (x, y) -> A (x cos - y sin, x sin + y cos),
 // columns (i, i + rot/2) or (2i, 2i+1).  A frequency is held as F = round(2^64 f / 2 pi),
 // the 64-bit fixed-point fraction of a turn per position; p F mod 2^64 is the phase, so
-// that whole turns fall away by the wrap-around of an integer product and positions of any
-// size keep an error of at most |p| 2^-56 turns (a double's rounding of f / 2 pi) plus
-// 2^-33.  No table is read.
+// that whole turns fall away by the wrap-around of an integer product.  f / 2 pi is formed in two
+// doubles, so that F is off by its own rounding alone: the angle of position p by |p| 2^-64
+// turns, and by 2^-28 for the phase's rounding to fp32.  No table is read.
 //
 // Organisation.  A lane holds two pieces of eight columns (16 bytes of a 16-bit type) of a
 // row, so chosen that they hold whole pairs where rot/2 is a multiple of 8 (or pairs are
@@ -121,7 +121,7 @@ __device__ __forceinline__ float load_any(const void* p, int dtype, int i) {
 
 // cos and sin of the phase (top 32 bits of position x frequency), times `amplitude`.  The
 // phase is brought within an eighth of a turn in integers, so that its conversion to fp32
-// loses nothing that matters.  FAST, for rows of 16-bit types: the hardware's sine and
+// is off by 2^-28 turns at most.  FAST, for rows of 16-bit types: the hardware's sine and
 // cosine, within 5e-7 there, a five-hundredth of fp16's rounding.
 template <bool FAST>
 __device__ __forceinline__ float2 turn(unsigned long long freq, long long pos, float amplitude) {
@@ -141,10 +141,14 @@ __device__ __forceinline__ float2 turn(unsigned long long freq, long long pos, f
   return quadrant & 2u ? make_float2(-a * amplitude, -b * amplitude) : make_float2(a * amplitude, b * amplitude);
 }
 
-// F of a frequency in radians per position.
+// F of a frequency in radians per position: f times 1 / 2 pi in two doubles, whole turns of
+// each taken away, the upper 32 bits of the fraction, then the lower ones with what the product lost.
 __device__ __forceinline__ unsigned long long fixed_turns(double f) {
-  const double t = f * 0.15915494309189535;  // 1 / 2 pi
-  return __double2ull_rn((t - floor(t)) * 18446744073709551616.0);
+  constexpr double kInv = 0.15915494309189535, kInvLow = -9.839338337591243e-18;  // 1 / 2 pi
+  const double hi = f * kInv, lo = fma(f, kInv, -hi) + f * kInvLow;
+  const double turns = (hi - rint(hi)) * 4294967296.0, upper = rint(turns);
+  const double lower = rint((turns - upper + (lo - rint(lo)) * 4294967296.0) * 4294967296.0);
+  return ((unsigned long long)(long long)upper << 32) + (unsigned long long)(long long)lower;
 }
 
 __device__ __forceinline__ long long rot_position(const RotaryArgs& a, long long b, int n) {

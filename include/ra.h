@@ -477,7 +477,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
  * rot on are copied.  q and k of one call go through one launch, between the projections
  * and ra_ring_fwd (backward: between ra_ring_bwd and the projections' gradients).
  *   freq       device array of rot / 2 doubles, radians per position (ra_rotary_frequencies
- *              makes some); angles keep an error of at most 2^-31 + |p| 2^-56 turns.
+ *              makes some); angles keep an error of at most 2^-28 + |p| 2^-64 turns.
  *   positions  device array of 64-bit integers, element (b, n) at b * pos_bstride + n (0:
  *              every batch has the same N), any values; or NULL: row n is at pos_off + n,
  *              or with RA_STRIPED, where row i S + l (S = N / P) is the l-th of virtual host
