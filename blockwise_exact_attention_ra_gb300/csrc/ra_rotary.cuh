@@ -121,7 +121,7 @@ __device__ __forceinline__ float load_any(const void* p, int dtype, int i) {
 
 // cos and sin of the phase (top 32 bits of position x frequency), times `amplitude`.  The
 // phase is brought within an eighth of a turn in integers, so that its conversion to fp32
-// is off by 2^-28 turns at most.  FAST, for rows of 16-bit types: the hardware's sine and
+// is off by 2^-28 turns at most.  FAST, for results of 16-bit types: the hardware's sine and
 // cosine, within 5e-7 there, a five-hundredth of fp16's rounding.
 template <bool FAST>
 __device__ __forceinline__ float2 turn(unsigned long long freq, long long pos, float amplitude) {

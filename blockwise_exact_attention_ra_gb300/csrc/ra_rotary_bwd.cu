@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kRotThreads, kBlocks) norm_rotary_bwd_kernel(c
     const long long tile = a.parts == 1 ? unit : unit / a.parts;
     const int part = (int)(unit - tile * a.parts);
     const long long t0 = tile * a.tile;
-    rot_factors<EX, sizeof(T) == 2, -1, false>(a, freq, nullptr, t0, factors);
+    rot_factors<EX, sizeof(TO) == 2, -1, false>(a, freq, nullptr, t0, factors);
     const bool token = t0 + l.token < a.tokens;
     const long long t = token ? t0 + l.token : t0;
     long long b, n;
