@@ -1924,6 +1924,83 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
 #pragma GCC visibility pop
 }  // extern "C"
 
+// ------------------------------------------------ tensors that overlap
+namespace ra {
+namespace {
+
+// A [B, N, H, d] tensor of a call (NULL: none); `pair` names what it may be written over.
+struct Rows {
+  const char* name;
+  const void* p;
+  int dtype;
+  Lay l;
+  long long N;
+  int H, pair;
+};
+
+// Whether some integers x_i in [lo_i, hi_i] bring delta + sum x_i stride_i within (-d, d).  The
+// axes come with falling strides, of which each steps past the axes within it but for a few steps.
+struct Axis {
+  long long stride, lo, hi;
+};
+bool offsets_meet(long long delta, const Axis* a, int n, long long d) {
+  if (n == 0) return delta > -d && delta < d;
+  long long reach = d;
+  for (int i = 1; i < n; ++i) reach += a[i].stride * (a[i].hi > -a[i].lo ? a[i].hi : -a[i].lo);
+  const long long s = a[0].stride;
+  long long x = (-delta - reach) / s - 1;
+  const long long last = (-delta + reach) / s + 1;
+  for (x = x < a[0].lo ? a[0].lo : x; x <= last && x <= a[0].hi; ++x)
+    if (offsets_meet(delta + x * s, a + 1, n - 1, d)) return true;
+  return false;
+}
+
+// Whether two tensors share an element: exactly, where they step alike (slices of one buffer, say);
+// else tensors that lie within each other count as sharing some.
+bool rows_meet(const Rows& a, const Rows& b, int B, int d) {
+  for (const Rows* t : {&a, &b})  // no memory is that large; what follows does not overflow
+    if ((double)B * t->l.bs + (double)t->N * t->l.rs + (double)t->H * t->l.hs > 1e17) return true;
+  const long long sa = (long long)dtype_size(a.dtype), sb = (long long)dtype_size(b.dtype);
+  const long long pa = (long long)reinterpret_cast<uintptr_t>(a.p), pb = (long long)reinterpret_cast<uintptr_t>(b.p);
+  const long long ea = pa + ((B - 1) * a.l.bs + (a.N - 1) * a.l.rs + (a.H - 1) * a.l.hs + d) * sa;
+  const long long eb = pb + ((B - 1) * b.l.bs + (b.N - 1) * b.l.rs + (b.H - 1) * b.l.hs + d) * sb;
+  if (ea <= pb || eb <= pa) return false;
+  if (sa != sb || (pb - pa) % sa) return true;
+  const long long na[3] = {B, a.N, a.H}, nb[3] = {B, b.N, b.H};
+  const long long la[3] = {a.l.bs, a.l.rs, a.l.hs}, lb[3] = {b.l.bs, b.l.rs, b.l.hs};
+  Axis axes[3];
+  int n = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (na[i] == 1 && nb[i] == 1) continue;
+    if (na[i] > 1 && nb[i] > 1 && la[i] != lb[i]) return true;
+    axes[n++] = Axis{na[i] > 1 ? la[i] : lb[i], 1 - na[i], nb[i] - 1};
+  }
+  std::sort(axes, axes + n, [](const Axis& x, const Axis& y) { return x.stride > y.stride; });
+  return offsets_meet((pb - pa) / sa, axes, n, d);
+}
+
+bool same_rows(const Rows& a, const Rows& b, int B) {
+  return a.p == b.p && a.dtype == b.dtype && a.N == b.N && a.H == b.H && (B == 1 || a.l.bs == b.l.bs) &&
+         (a.N == 1 || a.l.rs == b.l.rs) && (a.H == 1 || a.l.hs == b.l.hs);
+}
+
+// No result overlaps another, nor an input, but for one of its pair that it is written over row by row.
+int check_overlap(const Rows* outs, int n_out, const Rows* ins, int n_in, int B, int d) {
+  for (int i = 0; i < n_out; ++i) {
+    if (!outs[i].p) continue;
+    for (int j = 0; j < i; ++j)
+      if (outs[j].p && rows_meet(outs[i], outs[j], B, d))
+        return fail(RA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, outs[j].name);
+    for (int j = 0; j < n_in; ++j)
+      if (ins[j].p && !(outs[i].pair == ins[j].pair && same_rows(outs[i], ins[j], B)) && rows_meet(outs[i], ins[j], B, d))
+        return fail(RA_ERR_INVALID_ARG, "%s overlaps %s", outs[i].name, ins[j].name);
+  }
+  return RA_OK;
+}
+
+}  // namespace
+}  // namespace ra
+
 // ------------------------------------------------ rotary positions, norms of heads
 namespace ra {
 namespace {
@@ -2014,6 +2091,10 @@ int rotary_call(const void* q, const void* k, int dtype, const ra_shape& shape, 
       (rc = check_pair(q, k, k, "q", "k")) || (rc = check_pair(q_out, k_out, k, "the result of q", "the result of k")))
     return rc;
   if (norm && (rc = check_norm(qw, kw, w_dtype, eps))) return rc;
+  const Rows ins[] = {{"q", q, dtype, s.ql, s.Nq, s.Hq, 0}, {"k", k, dtype, s.kvl, s.Nq, s.Hkv, 1}};
+  const Rows outs[] = {{"the result of q", q_out, out_dtype, o.ql, s.Nq, s.Hq, 0},
+                       {"the result of k", k_out, out_dtype, o.kvl, s.Nq, s.Hkv, 1}};
+  if ((rc = check_overlap(outs, 2, ins, 2, s.B, s.d))) return rc;
   int* st;
   if ((rc = status_ptr(&st))) return rc;
   a.side[0].x = q; a.side[0].y = q_out; a.side[0].w = qw; a.side[0].xl = s.ql; a.side[0].yl = o.ql;
@@ -2104,6 +2185,10 @@ int ra_norm_rotary_bwd(const void* q, const void* k, ra_dtype dtype, ra_shape sh
       (rc = check_workspace(workspace, ws_bytes, ra_norm_rotary_bwd_workspace_bytes(s.d))))
     return rc;
   if (dk_weight && !k) return fail(RA_ERR_INVALID_ARG, "dk_weight is given but k is NULL");
+  const Rows ins[] = {{"q", q, dtype, s.ql, s.Nq, s.Hq, 0}, {"k", k, dtype, s.kvl, s.Nq, s.Hkv, 1},
+                      {"dq_out", dq_out, dout_dtype, g.ql, s.Nq, s.Hq, 0}, {"dk_out", dk_out, dout_dtype, g.kvl, s.Nq, s.Hkv, 1}};
+  const Rows outs[] = {{"dq", dq, grad_dtype, o.ql, s.Nq, s.Hq, 0}, {"dk", dk, grad_dtype, o.kvl, s.Nq, s.Hkv, 1}};
+  if ((rc = check_overlap(outs, 2, ins, 4, s.B, s.d))) return rc;
   int* st;
   if ((rc = status_ptr(&st))) return rc;
   a.side[0].x = q; a.side[0].dy = dq_out; a.side[0].y = dq; a.side[0].w = q_weight;
@@ -2462,7 +2547,9 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
       (rc = check_ptr(o, "o")) || (rc = check_floats(lse, "lse")) || (rc = check_len(kv_len)))
     return rc;
   const CrossPlan p = cross_plan(s, dtype, flags, kv_len != nullptr);
-  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
+  const Rows ins[] = {{"q", q, dtype, s.ql, s.Nq, s.Hq, 1}, {"k", k, dtype, s.kvl, s.Nkv, s.Hkv, 1}, {"v", v, dtype, s.kvl, s.Nkv, s.Hkv, 1}};
+  const Rows out{"o", o, o_dtype, s.ql, s.Nq, s.Hq, 0};
+  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = check_overlap(&out, 1, ins, 3, s.B, s.d)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const CrossState part{reinterpret_cast<float*>(ws + p.parts), reinterpret_cast<float*>(ws + p.m),
@@ -2538,7 +2625,13 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
       (rc = check_ptr(dq, "dq")) || (rc = check_ptr(dk, "dk")) || (rc = check_ptr(dv, "dv")) || (rc = check_len(kv_len)))
     return rc;
   const CrossBwdPlan p = cross_bwd_plan(s, dtype, kv_len != nullptr);
-  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
+  const Rows ins[] = {{"q", q, dtype, s.ql, s.Nq, s.Hq, 1}, {"k", k, dtype, s.kvl, s.Nkv, s.Hkv, 1},
+                      {"v", v, dtype, s.kvl, s.Nkv, s.Hkv, 1}, {"dO", dO, dtype, s.ql, s.Nq, s.Hq, 1}};
+  const Rows outs[] = {{"dk", dk, grad_dtype, s.kvl, s.Nkv, s.Hkv, 0}, {"dv", dv, grad_dtype, s.kvl, s.Nkv, s.Hkv, 0},
+                       {"dq", dq, grad_dtype, s.ql, s.Nq, s.Hq, 0}};
+  // dq is written when nothing else is read any more
+  if ((rc = check_workspace(workspace, ws_bytes, p.total)) || (rc = check_overlap(outs, 2, ins, 4, s.B, s.d)) ||
+      (rc = check_overlap(outs, 3, nullptr, 0, s.B, s.d)) || (rc = status_ptr(&st)) || (rc = check_tc(s, dtype))) return rc;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
   const int bf = dtype == RA_BF16;

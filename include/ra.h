@@ -455,15 +455,16 @@ int ra_cross_fwd(const void* q, const void* k, const void* v, ra_dtype dtype, ra
 /* Gradients of L = sum(o * dO): dq [B, N_q, Hq, d], dk, dv [B, N_kv, Hkv, d] in grad_dtype,
  * fully overwritten (rows from kv_len[b] on with zeros), by the formulas of ra_ring_bwd; o in
  * o_dtype, dO in dtype, lse from ra_cross_fwd with the same kv_len and scale.  q, k and v are
- * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros), dO times a power of two.  dO . o of an o in 16 bits
- * is formed from q, k and v again for batch entries of up to 4 d keys (with RA_PRECISE of any
- * number): the rounding of o would be the larger part of the errors of rows that few keys
- * share, and stays in those of longer ones (pass o in RA_F32 to be without it).  P and dS are rounded to
- * fp16 times powers of two.  Those of dO and dS follow, for each batch entry and key head, the largest
- * rows of dO and v, so that dO may have any size (the largest rows' norm from 2^-72 to 2^100) and no element
- * overflows; rows of dO far below the largest lose digits of their own dq, from 2^-8 at N_kv = 131072
- * (2^-15 at 1024) on.  dq is summed over the key tiles in fp32 in an order that
- * varies; dk and dv do not vary from run to run. */
+ * copied to fp16 as for ra_ring_bwd (those past kv_len[b] as zeros), dO times a power of two.
+ * dO . o of an o in 16 bits is formed from q, k and v again for batch entries of up to 4 d keys
+ * (with RA_PRECISE of any number): the rounding of o would be the larger part of the errors of
+ * rows that few keys share, and stays in those of longer ones (pass o in RA_F32 to be without it).
+ * P and dS are rounded to fp16 times powers of two.  Those of dO and dS follow, for each batch
+ * entry and key head, the largest rows of dO and v, so that dO may have any size (the largest
+ * rows' norm from 2^-72 to 2^100) and no element overflows; rows of dO far below the largest lose
+ * digits of their own dq, from 2^-8 at N_kv = 131072 (2^-15 at 1024) on.  dq is summed over the
+ * key tiles in fp32 in an order that varies; dk and dv do not vary from run to run.  dk and dv
+ * overlap none of q, k, v and dO, and no gradient another. */
 size_t ra_cross_bwd_workspace_bytes(ra_dtype dtype, ra_shape shape);
 int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_dtype o_dtype,
                  const void* dO, const float* lse, ra_dtype dtype, ra_shape shape,
@@ -513,7 +514,8 @@ int ra_rotary_frequencies(int rot, double base, double scale, int method, double
 /* q [B, N, Hq, d], k [B, N, Hkv, d] (shape.N_q = shape.N_kv = N) -> q_out, k_out, same type,
  * at the strides of out_shape (whose extents are those of shape).  k and k_out may both be
  * NULL: q alone.  q_out may be q itself (and k_out k) where the strides agree; otherwise
- * outputs overlap no input.  flags: RA_INTERLEAVED, RA_STRIPED.
+ * outputs overlap no input, nor each other.  (Refused; tensors of different strides or
+ * types that lie within each other count as overlapping.)  flags: RA_INTERLEAVED, RA_STRIPED.
  *   Sizes: d a multiple of 8 up to 256; rows start on 16-byte boundaries.  Any dtype; sums
  *   and products fp32, rounded once; sine and cosine to fp32's last bits for results in fp32,
  *   within 5e-7 for results (backward: dq, dk) in 16 bits.  Columns from rot on are copied bit for bit. */
@@ -544,7 +546,7 @@ int ra_norm_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape sh
  *   q, k the inputs of the forward pass (dtype, shape); dq_out, dk_out the gradients of its
  *   results in dout_dtype (dtype or RA_F32) at the strides of dout_shape; dq, dk in
  *   grad_dtype (dtype or RA_F32) at the strides of grad_shape, which may be dq_out, dk_out
- *   (or q, k) themselves where type and strides agree; dq_weight, dk_weight [d] fp32,
+ *   (or q, k) themselves where type and strides agree, and otherwise overlap none; dq_weight, dk_weight [d] fp32,
  *   overwritten, NULL where not wanted.  Results do not vary from run to run.
  *   workspace: device memory, 256-byte aligned, ra_norm_rotary_bwd_workspace_bytes(d)
  *   bytes.  It must not be in use by work that overlaps the call on the GPU. */
