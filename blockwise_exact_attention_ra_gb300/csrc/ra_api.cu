@@ -2048,6 +2048,8 @@ int rot_common(const ra_shape& sh, const Shape& s, const ra_rotary& r, int flags
       return fail(RA_ERR_INVALID_ARG, "RA_STRIPED does not combine with given positions");
     if (r.positions && r.pos_bstride != 0 && (r.pos_bstride < s.Nq || r.pos_bstride > (1ll << 50)))
       return fail(RA_ERR_INVALID_ARG, "pos_bstride must be 0 or at least N=%d (got %lld)", s.Nq, r.pos_bstride);
+    if (r.positions && r.pos_off)
+      return fail(RA_ERR_INVALID_ARG, "pos_off=%lld does not combine with given positions", r.pos_off);
     if ((flags & RA_STRIPED) && (r.P < 1 || s.Nq % r.P))
       return fail(RA_ERR_INVALID_ARG, "P=%d must divide N=%d", r.P, s.Nq);
     a->freq = r.freq;

@@ -480,7 +480,7 @@ int ra_cross_bwd(const void* q, const void* k, const void* v, const void* o, ra_
  *   freq       device array of rot / 2 doubles, radians per position (ra_rotary_frequencies
  *              makes some); angles keep an error of at most 2^-28 + |p| 2^-64 turns.
  *   positions  device array of 64-bit integers, element (b, n) at b * pos_bstride + n (0:
- *              every batch has the same N), any values; or NULL: row n is at pos_off + n,
+ *              every batch has the same N), any values (pos_off is 0); or NULL: row n is at pos_off + n,
  *              or with RA_STRIPED, where row i S + l (S = N / P) is the l-th of virtual host
  *              i, at pos_off + l P + i.  (Per-host lengths: pass positions.)
  *   P          with RA_STRIPED the number of hosts, which divides N; ignored otherwise. */
