@@ -437,7 +437,8 @@ int ra_newton_schulz(const void* g, ra_dtype g_dtype, int batch, int rows, int c
  *   RA_F16), d 64 or 128; o in o_dtype, lse [B, Hq, N_q] fp32.  Strides as in ra_shape.
  *   kv_len  device array of B int32 (clamped to [0, N_kv]), or NULL: every key is there.
  *     Keys and values from kv_len[b] on may hold anything (infinities and NaN too).  A batch
- *     entry without keys has o = 0, lse = -inf.
+ *     entry without keys has o = 0, lse = -inf.  So has a row whose scores are all -inf (a key with
+ *     one counts as not there); one with a score of +inf or NaN is NaN in o and lse.
  *   flags   RA_PRECISE (P and dS in two terms, which the backward pass of fp16 inputs takes
  *     anyway).
  *   A few queries (N_q Hq / Hkv <= 32; single tokens) run on a kernel bound by reading k
