@@ -381,9 +381,9 @@ __global__ void __launch_bounds__(kThreads) cross_few_kernel(const __grid_consta
 // keys, 64 at a time in shared memory for all warps; P from the saved lse, everything else as
 // above.  It runs beside the operand copies and waits for them only before it writes.
 // Measured, beside the rest of the backward pass (bf16, d 128): 2 x 4096 queries of 16 heads, 400
-// keys: 81 us of 240, 330 TFLOP/s, bound by what shared memory gives to products of 16 rows (operands
-// a product ahead: the same); 8192 queries, 128 keys: 35 of 146; 3 x 1924 queries of 32 heads, 3 keys:
-// 27 of 177, reading q and dO (64 with O from a forward pass on tcgen05).
+// keys: 80 us of 257, 330 TFLOP/s, bound by what shared memory gives to products of 16 rows (operands
+// a product ahead: the same); 8192 queries, 128 keys: 36 of 163; 3 x 1924 queries of 32 heads, 3 keys:
+// 29 of 197, reading q and dO (64 with O from a forward pass on tcgen05).
 constexpr int kDotWarps = 8, kDotKeys = 64;
 
 template <typename T, int D>

@@ -20,7 +20,8 @@
 // once for a token, in shared memory, from where each row's lanes read them: held in
 // registers they took a third of those, and of the warps that cover DRAM's latency.
 // Arithmetic is on pairs of fp32 (packed operations).  The kernels are bound by reading and
-// writing the rows, next to which issuing their instructions takes about as long.
+// writing the rows, those of the norm by the warps that cover DRAM's latency (half of the issue
+// slots stay free).
 #pragma once
 
 #include "ra_device.cuh"

@@ -11,8 +11,8 @@
 namespace ra {
 namespace {
 
-// Blocks of an SM: 128 registers a thread.  (131072 tokens of 16 + 4 heads of 128, bf16: 430
-// us, 4.7 TB/s; with three, whose 80 registers spill, 519.)
+// Blocks of an SM: 128 registers a thread.  (131072 tokens of 16 + 4 heads of 128, bf16: 466
+// us with the sum of dw's parts, 4.3 TB/s; with three, whose 80 registers spill, 593.)
 constexpr int kBlocks = 2;
 
 template <typename T, typename TG, typename TO, int EX, bool ALL>

@@ -519,7 +519,8 @@ int ra_rotary_frequencies(int rot, double base, double scale, int method, double
  * types that lie within each other count as overlapping.)  flags: RA_INTERLEAVED, RA_STRIPED.
  *   Sizes: d a multiple of 8 up to 256; rows start on 16-byte boundaries.  Any dtype; sums
  *   and products fp32, rounded once; sine and cosine to fp32's last bits for results in fp32,
- *   within 5e-7 for results (backward: dq, dk) in 16 bits.  Columns from rot on are copied bit for bit. */
+ *   within 5e-7 for results (backward: dq, dk) in 16 bits.  Columns from rot on are copied, bit for bit
+ *   but for what a NaN holds. */
 int ra_rotary_fwd(const void* q, const void* k, ra_dtype dtype, ra_shape shape, ra_rotary rotary,
                   int flags, void* q_out, void* k_out, ra_shape out_shape, void* stream);
 
