@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) cross_keys_kernel(const __grid_const
 // by row took 29 us instead of 23 for 67 MB, bound by instructions; what is left (16 us for 34 MB, 2 TB/s) are two
 // or three rounds of loads behind the latency of a launch.  Sums that leave fp32's range are
 // left out, so that infinities and NaN, which lose their own gradients whatever the scale, leave the
-// others theirs; a lane that met some, or nothing else than zeros, reads its rows again at another scale.
+// others theirs; a lane that met some, or nothing larger than 2^-50, reads its rows again at another scale.
 // It adds 6 us to 15 (77 queries, 590 keys, 8 heads of 128) and 28 to 648 (2 x 4096 x 4096, 16 heads of 128).
 __global__ void __launch_bounds__(kThreads) cross_range_kernel(const __grid_constant__ CrossRangeArgs a) {
   pdl_trigger();
@@ -235,13 +235,11 @@ __global__ void __launch_bounds__(kThreads) cross_range_kernel(const __grid_cons
     }
     return top;
   };
-  float top = largest(1.f), shift = 0.f;
-  if (left_out || top < 1e-30f) {
-    shift = left_out ? -70.f : 100.f;
-    top = largest(left_out ? 8.470329472543003e-22f : 1.2676506002282294e30f);
-  }
-  // log2 of the lanes' sums, joined
-  const float own = top > 0.f ? log2f(top) - 2.f * shift : -INFINITY;
+  // log2 of the largest sum; of those past fp32's range too, or of small ones where there is no other
+  float own = log2f(largest(1.f));
+  if (left_out) own = fmaxf(own, log2f(largest(8.470329472543003e-22f)) + 140.f);
+  if (own < -99.f) own = fmaxf(own, log2f(largest(1.2676506002282294e30f)) - 200.f);
+  // the lanes' sums, joined
   float most = own;
   for (int o = G >> 1; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   float sum = most == -INFINITY ? 0.f : exp2f(own - most);

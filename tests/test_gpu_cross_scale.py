@@ -152,3 +152,23 @@ def test_large_bf16_gradients_set_no_status(ra):
     ra.cross_attention_bwd(q, k, v, o, lse, do.to(BF))
     with pytest.raises(ra.RAError, match="RANGE"):
         ra.ra_sync_status()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("exponent", [-80, -30, 0, 90])
+@pytest.mark.parametrize("Nq", [2, 200])
+def test_rows_beside_a_lost_one(ra, Nq, exponent, bad):
+    """Rows of dO without a finite element leave the others, of any size, their dq.  (Each reader of
+    rows meets lost ones before it meets others.)"""
+    q, k, v, do = inputs(1, Nq, 300, 2, 1, 64, BF, 10)
+    do = do * 2.0 ** exponent
+    o, lse = ra.cross_attention_fwd(q, k, v)
+    want = oracle.cross_attention(f64(q), f64(k), f64(v), 0.125, None, f64(do))[2]
+    lost = do.clone()
+    lost[0, :Nq // 2] = bad
+    dq, _, _ = ra.cross_attention_bwd(q, k, v, o, lse, lost.to(BF))
+    ra.ra_sync_status()
+    assert not dq[0, :Nq // 2].isfinite().any()
+    G, V = np.abs(f64(do)), np.abs(f64(v))
+    delta = 0.125 * 16 * 2.0 ** -23 * G.reshape(-1, 64).max(axis=0) @ V.reshape(-1, 64).max(axis=0)
+    near("dq", dq[0, Nq // 2:], want[0, Nq // 2:], Nq ** 0.5 * delta * np.linalg.norm(f64(k), axis=-1).max())
